@@ -516,6 +516,147 @@ moe_status_t moe_union_cost(const uint64_t *bitmaps, int32_t nodes, int32_t L, i
                             int32_t *size, double *R, double *T, int32_t *best, void *ws, size_t ws_bytes,
                             moe_stream_t s);
 
+/* ---------------------------------------------------------------- attention side of the pass
+ *
+ * What a verification pass runs before its expert operation: rotary positions, the write of the
+ * pass's keys and values into a paged cache, and attention of the drafted tokens (a chain or a
+ * tree) over the cache.  The pages take these as given; the formulas are stated here.
+ *
+ * Device-only problems (a position beyond the table, a slot or page beyond the cache, a length
+ * that does not fit the page table) are recorded as MOE_ERR_BAD_ID in the error word of ws (the
+ * first 256 bytes of any workspace) when ws is not NULL, and read with moe_last_device_error.
+ */
+
+/* [tokens, heads, dim] rows, the channels of a row contiguous; strides in elements.  dtype
+ * MOE_F32 or MOE_BF16.  Pointers are aligned to their element; strides may be any number that
+ * keeps rows apart (rows that are read may overlap or repeat). */
+typedef struct {
+    void *ptr;                        /* [dev] */
+    int64_t token_stride, head_stride;
+    int32_t heads, dtype;
+} moe_heads_t;
+
+/*
+ * A paged cache of keys and values: position `r` of page `b`, head h, starts at element
+ * b * page_stride + r * token_stride + h * head_stride of k and of v.  Slot s of the cache is
+ * row s % page of page s / page.
+ *   dtype  MOE_F32, MOE_BF16, or MOE_E4M3: codes with one fp32 scale per row of one head,
+ *          k_scale and v_scale [pages, heads, page] (contiguous); NULL for the other types.
+ * k and v 16-byte aligned, strides multiples of 16 bytes, 1 <= dim <= 256, dim * element size a
+ * multiple of 16, page >= 1, heads >= 1, pages * page < 2^31.
+ */
+typedef struct {
+    void *k, *v;                      /* [dev] */
+    float *k_scale, *v_scale;         /* [dev] */
+    int64_t page_stride, token_stride, head_stride;
+    int32_t dtype, heads, dim, page, pages;
+    int32_t reserved;                 /* 0 */
+} moe_kv_cache_t;
+
+/*
+ * Rotary positions: table [dev] fp32 [table_positions][rot / 2][2] of m cos(p w_i), m sin(p w_i)
+ * (8-byte aligned), positions [dev] int32 [tokens].  The pair (a, b) of channels (i, i + rot/2),
+ * or (2i, 2i + 1) when interleaved != 0, becomes (a c - b s, b c + a s); channels from rot on are
+ * copied.  inverse != 0 applies the transposed matrix, (a c + b s, b c - a s): the gradient with
+ * respect to the input of a forward rotation.  rot even, 2 <= rot <= dim.
+ */
+typedef struct {
+    const float *table;               /* [dev] */
+    const int32_t *positions;         /* [dev] */
+    int32_t table_positions, rot, interleaved, inverse;
+} moe_rotary_t;
+
+/* Frequency scaling for contexts longer than the trained one (moe_rope_frequencies). */
+#define MOE_ROPE_PLAIN 0      /* w_i = base^(-2i/rot) */
+#define MOE_ROPE_LINEAR 1     /* w_i / factor: positions interpolated */
+#define MOE_ROPE_BASE 2       /* base * factor^(rot/(rot-2)): the slowest frequency is divided by factor */
+#define MOE_ROPE_BY_PARTS 3   /* interpolated below beta_slow turns over the original context, kept above
+                                 beta_fast, a linear ramp over i between; m = 0.1 ln(factor) + 1 */
+
+/*
+ * The rot / 2 frequencies and the magnitude m of a rotary table, in double.
+ *   w [host] double [rot/2] out, magnitude [host] double out (1 except by parts).
+ * By parts: i(t) = rot ln(original / (2 pi t)) / (2 ln base) is the index whose frequency makes t
+ * turns over `original` positions; ramp_i = clamp((i - lo) / (hi - lo), 0, 1) with
+ * lo = max(floor(i(beta_fast)), 0), hi = min(ceil(i(beta_slow)), rot - 1) (at least lo + 0.001),
+ * and w_i = base^(-2i/rot) (ramp_i / factor + 1 - ramp_i).
+ * rot even in [2, 256], base > 1, factor >= 1; by parts also original >= 1 and
+ * beta_fast > beta_slow > 0.  Host only.
+ */
+moe_status_t moe_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, int32_t original,
+                                  double beta_fast, double beta_slow, double *w, double *magnitude);
+
+/* The table of positions 0 .. positions-1: angles p * w_i, cosines and sines in double, rounded to
+ * fp32 once.  w [host] double [half], 1 <= half <= 128; table [dev] fp32 [positions][half][2],
+ * 8-byte aligned.  Asynchronous on s (w is copied before the call returns). */
+moe_status_t moe_rope_table(const double *w, int32_t half, double magnitude, int32_t positions, float *table,
+                            moe_stream_t s);
+
+/*
+ * Rotates the rows of q and of k (either may be NULL) into q_out and k_out, in fp32, rounded once
+ * to the output's type.  An output may be its input itself (in place), but may not overlap it
+ * otherwise.  A token whose position is outside [0, table_positions) is recorded and its rows are
+ * not written.  1 <= dim <= 256; tokens >= 0 (0 enqueues nothing).  ws may be NULL.  Asynchronous
+ * on s.
+ */
+moe_status_t moe_rope(const moe_heads_t *q, const moe_heads_t *q_out, const moe_heads_t *k, const moe_heads_t *k_out,
+                      int32_t tokens, int32_t dim, const moe_rotary_t *rotary, void *ws, moe_stream_t s);
+
+/*
+ * Writes the keys and values of `tokens` tokens into cache slots[t] (int32 [dev]).  A negative
+ * slot takes nothing; one beyond the cache is recorded and takes nothing; slots that are not
+ * negative must differ.  With rotary, the keys are rotated in fp32 before they are rounded to the
+ * cache's type, and, when q is not NULL, the rows of q are rotated into q_out in the same launch
+ * (for every token, whatever its slot); a token whose position is outside the table is recorded
+ * and nothing of it is written.  e4m3: scale = amax / 448 over the row (1 where that is 0; NaN
+ * elements do not count), codes of the fp32 quotient x / scale, rounded to nearest, ties to even.
+ * tokens >= 0; k and v [tokens, cache heads, cache dim].  ws may be NULL.  Asynchronous on s.
+ */
+moe_status_t moe_kv_write(const moe_kv_cache_t *cache, const moe_heads_t *k, const moe_heads_t *v,
+                          const int32_t *slots, int32_t tokens, const moe_rotary_t *rotary, const moe_heads_t *q,
+                          const moe_heads_t *q_out, void *ws, moe_stream_t s);
+
+/*
+ * Reads the rows of slots[t] back into k_out and v_out: cache values times their scales, rounded
+ * once to the output's type; zeros for a negative slot, and for one beyond the cache, which is
+ * recorded.  tokens >= 0; slots may repeat.  ws may be NULL.  Asynchronous on s.
+ */
+moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int32_t tokens, const moe_heads_t *k_out,
+                         const moe_heads_t *v_out, void *ws, moe_stream_t s);
+
+/* Largest number of drafted tokens of one sequence (the bits of a tree mask). */
+#define MOE_MAX_TREE_TOKENS 64
+
+/* Bytes of device workspace moe_tree_attention needs (zero it once with moe_workspace_init):
+ * 256 bytes with the error word, and the partial results of sequences that several CTAs share. */
+size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t tokens, int32_t seqs, int32_t q_heads);
+
+/*
+ * Attention of the drafted tokens of `seqs` sequences over the cache.  Sequence b has the tokens
+ * q_start[b] .. q_start[b+1]-1 of q (n_b <= max_tokens of them) and ctx[b] cached positions before
+ * them; its position p is row p % page of page page_table[b][p / page].  The drafted tokens' own
+ * keys and values are in the cache already, at positions ctx[b] + j (moe_kv_write).  Token i sees
+ * position p < ctx[b], and ctx[b] + j (j < n_b) where bit j of mask[q_start[b] + i] is set; without
+ * a mask, j <= i (a chain).  Query head h reads cache head h / (q heads / cache heads).
+ *     s_p = scale * <q, k_p>,  lse = ln sum_p e^(s_p),  out = sum_p e^(s_p - lse) v_p
+ * over the positions seen; a token that sees none gets out = 0, lse = -inf.  What stands in a
+ * position that a token does not see, infinities and NaN included, does not reach it.
+ *   q_start [dev] int32 [seqs + 1] (non-decreasing, 0 .. tokens), ctx [dev] int32 [seqs],
+ *   page_table [dev] int32 [seqs, max_pages], mask [dev] uint64 [tokens] or NULL, scale > 0,
+ *   q and out [tokens, q heads, dim] of one type; lse [dev] fp32 [tokens, q heads] or NULL.
+ * A page outside the cache is recorded and reads as zeros.  A sequence whose lengths do not fit
+ * (ctx < 0, n_b outside [0, max_tokens], ctx + n_b > max_pages * page, tokens beyond q) is recorded
+ * and its rows are not written.
+ * bf16 q over a bf16 or e4m3 cache with dim <= 128 runs on the tensor cores when q is 16-byte
+ * aligned with strides that are multiples of 8 elements and page is a multiple of 8; all else on
+ * the CUDA cores in fp32.  tokens >= 0; 1 <= max_tokens <= 64; q heads a multiple of the cache's,
+ * at most 64 times as many.  Asynchronous on s.
+ */
+moe_status_t moe_tree_attention(const moe_kv_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,
+                                const int32_t *q_start, const int32_t *ctx, const int32_t *page_table,
+                                const uint64_t *mask, int32_t seqs, int32_t tokens, int32_t max_tokens,
+                                int32_t max_pages, float scale, void *ws, size_t ws_bytes, moe_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -54,6 +54,26 @@ class WeightScales(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
 
 
+class Heads(ctypes.Structure):
+    """moe_heads_t: [tokens, heads, dim] rows (element strides)."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class CacheDesc(ctypes.Structure):
+    """moe_kv_cache_t."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_int32) for f in ("dtype", "heads", "dim", "page", "pages", "reserved")]
+
+
+class Rotary(ctypes.Structure):
+    """moe_rotary_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p)] + \
+               [(f, ctypes.c_int32) for f in ("table_positions", "rot", "interleaved", "inverse")]
+
+
 class ThresholdIn(ctypes.Structure):
     _fields_ = [(f, ctypes.c_double) for f in ("mW", "B_k", "beta_1", "tau_1", "dD_over_betaD", "dphi")]
 
@@ -71,7 +91,9 @@ EXPORTED = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_wor
             "moe_error_bounds", "moe_kstar_separated", "moe_fit_op_times", "moe_expert_op_perslot_fp8",
             "moe_expert_op_dedup_fp8", "moe_quantize_rows_e4m3", "moe_spec_accept",
             "moe_union_cost_workspace_bytes", "moe_union_cost", "moe_expert_op_dedup_ids",
-            "moe_expert_op_dedup_ids_fp8", "moe_read_probe", "moe_set_wait_limit")
+            "moe_expert_op_dedup_ids_fp8", "moe_read_probe", "moe_set_wait_limit", "moe_rope_frequencies",
+            "moe_rope_table", "moe_rope", "moe_kv_write", "moe_kv_read", "moe_tree_attention_workspace_bytes",
+            "moe_tree_attention")
 
 _lib = None
 
@@ -127,6 +149,14 @@ def lib():
         "moe_union_cost_workspace_bytes": ([I32], SZ),
         "moe_read_probe": ([P, SZ, P, P], I32),
         "moe_union_cost": ([P, I32, I32, I32, P, I32, P, P, D, P, P, P, P, P, P, SZ, P], I32),
+        "moe_rope_frequencies": ([I32, D, I32, D, I32, D, D, P, P], I32),
+        "moe_rope_table": ([P, I32, D, I32, P, P], I32),
+        # descriptors go as plain addresses (byref): one conversion less per argument
+        "moe_rope": ([P, P, P, P, I32, I32, P, P, P], I32),
+        "moe_kv_write": ([P, P, P, P, I32, P, P, P, P, P], I32),
+        "moe_kv_read": ([P, P, I32, P, P, P, P], I32),
+        "moe_tree_attention_workspace_bytes": ([P, I32, I32, I32], SZ),
+        "moe_tree_attention": ([P, P, P, P, P, P, P, P, I32, I32, I32, I32, ctypes.c_float, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -538,3 +568,207 @@ def read_probe(buf: torch.Tensor, ws: torch.Tensor) -> int:
     _check(lib().moe_read_probe(ctypes.c_void_p(buf.data_ptr()), nbytes, ctypes.c_void_p(ws.data_ptr()),
                                 _stream(buf.device)), "moe_read_probe")
     return nbytes // 32768 * 32768
+
+
+# ---------------------------------------------------------------- attention side of the pass
+ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+MAX_TREE_TOKENS = 64
+_HEAD_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_CACHE_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_E4M3}
+
+
+def _heads(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int) -> Heads:
+    """The descriptor of a [tokens, heads, dim] CUDA tensor: any token and head strides, dense channels."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = _HEAD_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if tuple(t.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} must have shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1 and dim > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return Heads(t.data_ptr(), st, sh, heads, code)
+
+
+def _like(x: torch.Tensor) -> torch.Tensor:
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _same_device(ref: torch.Tensor, **named):
+    for name, t in named.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """moe_rope_frequencies: (rot / 2 frequencies as float64, magnitude) of a rotary table; scaling
+    "plain", "linear", "base" or "by_parts" (the last needs `original`, the trained context)."""
+    w = np.zeros(max(rot // 2, 1), np.float64)
+    mag = ctypes.c_double(0.0)
+    _check(lib().moe_rope_frequencies(int(rot), float(base), ROPE_SCALING[scaling], float(factor), int(original),
+                                      float(beta_fast), float(beta_slow), ctypes.c_void_p(w.ctypes.data),
+                                      ctypes.byref(mag)), "moe_rope_frequencies")
+    return w, mag.value
+
+
+def rope_table(positions: int, w, magnitude: float = 1.0, device=None) -> torch.Tensor:
+    """moe_rope_table: fp32 [positions, rot / 2, 2] of m cos(p w_i), m sin(p w_i)."""
+    w = np.ascontiguousarray(np.asarray(w, dtype=np.float64))
+    table = torch.empty((positions, w.size, 2), dtype=torch.float32, device=device or "cuda")
+    _check(lib().moe_rope_table(ctypes.c_void_p(w.ctypes.data), w.size, float(magnitude), int(positions),
+                                ctypes.c_void_p(table.data_ptr()), _stream(table.device)), "moe_rope_table")
+    return table
+
+
+def _rotary(table: torch.Tensor, positions: torch.Tensor, tokens: int, interleaved: bool, inverse: bool) -> Rotary:
+    if table.dim() != 3 or table.shape[2] != 2:
+        raise ValueError(f"table must have shape (positions, rot / 2, 2), got {tuple(table.shape)}")
+    return Rotary(_dev(table, "table", torch.float32), _dev(positions, "positions", torch.int32, (tokens,)),
+                  table.shape[0], 2 * table.shape[1], 1 if interleaved else 0, 1 if inverse else 0)
+
+
+def rope(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False, inverse: bool = False,
+         q_out=None, k_out=None, ws=None):
+    """moe_rope: rotates the rows of q [tokens, q heads, dim] and k [tokens, k heads, dim] (either may be
+    None) by their positions; inverse gives the gradient's direction.  Returns (q_out, k_out); an output
+    may be its input.  ws (any workspace) records positions beyond the table."""
+    ref = q if q is not None else k
+    tokens, _, dim = ref.shape
+    desc = []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            desc += [None, None]
+            continue
+        hx = _heads(x, name, tokens, x.shape[1], dim)
+        y = _like(x) if y is None else y
+        hy = _heads(y, name + "_out", tokens, x.shape[1], dim)
+        if name == "q":
+            q_out = y
+        else:
+            k_out = y
+        desc += [ctypes.byref(hx), ctypes.byref(hy)]
+    _same_device(ref, k=k, positions=positions, table=table, q_out=q_out, k_out=k_out, ws=ws)
+    _check(lib().moe_rope(*desc, tokens, dim, ctypes.byref(_rotary(table, positions, tokens, interleaved, inverse)),
+                          None if ws is None else ws.data_ptr(), _stream(ref.device)), "moe_rope")
+    return q_out, k_out
+
+
+class KVCache:
+    """A paged key/value cache (moe_kv_cache_t) over tensors the caller owns: k and v
+    [pages, page, heads, dim] (fp32, bf16, or uint8 e4m3 codes; equal strides, dense channels), and
+    for codes the scales fp32 [pages, heads, page]."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale=None, v_scale=None):
+        if not k.is_cuda or not v.is_cuda:
+            raise TypeError("k and v must be CUDA tensors")
+        code = _CACHE_TYPES.get(k.dtype)
+        if code is None or v.dtype != k.dtype:
+            raise TypeError(f"k and v must be float32, bfloat16 or uint8 alike, got {k.dtype} and {v.dtype}")
+        if k.dim() != 4 or v.shape != k.shape or v.stride() != k.stride() or (k.stride(3) != 1 and k.shape[3] > 1):
+            raise ValueError("k and v must have one shape (pages, page, heads, dim), equal strides and dense channels")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page, self.heads, self.dim = k.shape
+        ks = vs = None
+        if code == MOE_E4M3:
+            shape = (self.pages, self.heads, self.page)
+            ks = _dev(k_scale, "k_scale", torch.float32, shape)
+            vs = _dev(v_scale, "v_scale", torch.float32, shape)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("scales belong to a cache of e4m3 codes")
+        _same_device(k, v=v, k_scale=k_scale, v_scale=v_scale)
+        self.desc = CacheDesc(k.data_ptr(), v.data_ptr(), ks, vs, *k.stride()[:3], code, self.heads, self.dim,
+                              self.page, self.pages, 0)
+        self.device = k.device
+
+
+def kv_cache(pages: int, page: int, heads: int, dim: int, dtype: str = "bf16", device=None) -> KVCache:
+    """A zeroed cache of `pages` pages of `page` tokens: dtype "bf16", "f32" or "e4m3" (codes and scales)."""
+    t = {"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.uint8}[dtype]
+    k, v = (torch.zeros((pages, page, heads, dim), dtype=t, device=device or "cuda") for _ in range(2))
+    if dtype != "e4m3":
+        return KVCache(k, v)
+    return KVCache(k, v, *(torch.ones((pages, heads, page), dtype=torch.float32, device=k.device) for _ in range(2)))
+
+
+def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, q=None, positions=None, table=None,
+             interleaved: bool = False, q_out=None, ws=None):
+    """moe_kv_write: the rows k, v [tokens, heads, dim] into the cache's slots int32 [tokens] (a negative
+    slot takes nothing), quantised for an e4m3 cache.  With positions and table the keys are rotated
+    before, and q [tokens, q heads, dim], when given, is rotated into q_out, which is returned (None
+    without q).  ws (any workspace) records slots and positions out of range."""
+    tokens = k.shape[0]
+    hk = _heads(k, "k", tokens, cache.heads, cache.dim)
+    hv = _heads(v, "v", tokens, cache.heads, cache.dim)
+    rot = dq = dqo = None
+    if (table is None) != (positions is None):
+        raise ValueError("rotation takes both positions and table")
+    if table is not None:
+        rot = ctypes.byref(_rotary(table, positions, tokens, interleaved, False))
+    if q is not None:
+        if table is None:
+            raise ValueError("q is only rotated: it takes positions and table")
+        q_out = _like(q) if q_out is None else q_out
+        dq = ctypes.byref(_heads(q, "q", tokens, q.shape[1], cache.dim))
+        dqo = ctypes.byref(_heads(q_out, "q_out", tokens, q.shape[1], cache.dim))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _same_device(cache.k, k=k, v=v, slots=slots, q=q, q_out=q_out, positions=positions, table=table, ws=ws)
+    _check(lib().moe_kv_write(ctypes.byref(cache.desc), ctypes.byref(hk), ctypes.byref(hv),
+                              _dev(slots, "slots", torch.int32, (tokens,)), tokens, rot, dq, dqo,
+                              None if ws is None else ws.data_ptr(), _stream(cache.device)), "moe_kv_write")
+    return q_out
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None, ws=None):
+    """moe_kv_read: the cache's rows of slots int32 [tokens] as (k, v) [tokens, heads, dim], fp32 or bf16;
+    zeros for a negative slot."""
+    tokens = slots.shape[0]
+    shape = (tokens, cache.heads, cache.dim)
+    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+    hk, hv = _heads(k_out, "k_out", *shape), _heads(v_out, "v_out", *shape)
+    _same_device(cache.k, slots=slots, k_out=k_out, v_out=v_out, ws=ws)
+    _check(lib().moe_kv_read(ctypes.byref(cache.desc), _dev(slots, "slots", torch.int32, (tokens,)), tokens,
+                             ctypes.byref(hk), ctypes.byref(hv), None if ws is None else ws.data_ptr(),
+                             _stream(cache.device)), "moe_kv_read")
+    return k_out, v_out
+
+
+def tree_attention_workspace(cache: KVCache, tokens: int, seqs: int, q_heads: int) -> torch.Tensor:
+    """A zeroed workspace for tree_attention calls of up to this many tokens and sequences."""
+    nbytes = int(lib().moe_tree_attention_workspace_bytes(ctypes.byref(cache.desc), tokens, seqs, q_heads))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    _check(lib().moe_workspace_init(ws.data_ptr(), nbytes, _stream(cache.device)), "moe_workspace_init")
+    return ws
+
+
+def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: torch.Tensor, page_table: torch.Tensor,
+                   mask=None, scale=None, max_tokens: int = MAX_TREE_TOKENS, out=None, lse=None,
+                   return_lse: bool = False, ws=None):
+    """moe_tree_attention: attention of drafted tokens over the cache.  q [tokens, q heads, dim] holds the
+    tokens of all sequences, q_start int32 [seqs + 1] their bounds, ctx int32 [seqs] the cached positions
+    before them, page_table int32 [seqs, max pages]; mask int64 [tokens], bit j of a token's word set
+    where it sees drafted token j of its sequence (None: a chain); scale defaults to dim^-0.5.  Returns
+    out, or (out, lse) with return_lse."""
+    tokens, heads = q.shape[0], q.shape[1]
+    seqs = ctx.shape[0]
+    hq = _heads(q, "q", tokens, heads, cache.dim)
+    out = _like(q) if out is None else out
+    ho = _heads(out, "out", tokens, heads, cache.dim)
+    if return_lse and lse is None:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device)
+    ws = ws if ws is not None else tree_attention_workspace(cache, tokens, seqs, heads)
+    if page_table.dim() != 2 or page_table.shape[0] != seqs:
+        raise ValueError(f"page_table must have shape ({seqs}, max pages), got {tuple(page_table.shape)}")
+    _same_device(cache.k, q=q, q_start=q_start, ctx=ctx, page_table=page_table, mask=mask, out=out, lse=lse, ws=ws)
+    _check(lib().moe_tree_attention(
+        ctypes.byref(cache.desc), ctypes.byref(hq), ctypes.byref(ho),
+        None if lse is None else _dev(lse, "lse", torch.float32, (tokens, heads)),
+        _dev(q_start, "q_start", torch.int32, (seqs + 1,)), _dev(ctx, "ctx", torch.int32),
+        _dev(page_table, "page_table", torch.int32), None if mask is None else _dev(mask, "mask", torch.int64, (tokens,)),
+        seqs, tokens, max_tokens, page_table.shape[1], cache.dim ** -0.5 if scale is None else scale,
+        ws.data_ptr(), ws.numel(), _stream(cache.device)), "moe_tree_attention")
+    return (out, lse) if return_lse else out
