@@ -17,6 +17,7 @@
 
 namespace moe {
 cudaError_t launch_read_probe(const void *buf, size_t bytes, int32_t *err, cudaStream_t s);
+long long current_wait_limit();
 }
 
 namespace moe {
@@ -37,6 +38,15 @@ constexpr bool kUsePdl = true;
 // Cycles a device pipeline wait of the expert kernels may take (0: kWaitLimitCycles); set
 // with moe_set_wait_limit.
 std::atomic<long long> g_wait_limit{0};
+
+}  // namespace
+
+long long moe::current_wait_limit() {
+    const long long wl = g_wait_limit.load(std::memory_order_relaxed);
+    return wl > 0 ? wl : kWaitLimitCycles;
+}
+
+namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // ids, gates, logits and groupings are read one element at a time: 4-byte alignment suffices
@@ -102,8 +112,7 @@ ExpertArgs make_args(const moe_layer_t *L, const void *wg, const void *wu, const
     a.mode = mode;
     a.w_dtype = L->w_dtype;
     a.x_dtype = L->x_dtype;
-    const long long wl = g_wait_limit.load(std::memory_order_relaxed);
-    a.wait_limit = wl > 0 ? wl : kWaitLimitCycles;
+    a.wait_limit = current_wait_limit();
     return a;
 }
 

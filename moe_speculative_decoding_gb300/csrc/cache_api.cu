@@ -184,7 +184,8 @@ moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int3
 
 size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t tokens, int32_t seqs, int32_t q_heads) {
     if (cache == nullptr || tokens < 0 || seqs < 0 || q_heads < 1) return 0;
-    return kWorkspaceBytes;
+    const bool parts = (cache->dtype == MOE_BF16 || cache->dtype == MOE_E4M3) && cache->dim <= 128;
+    return kWorkspaceBytes + (parts ? tree_attn_part_bytes(cache->dim) : 0);
 }
 
 moe_status_t moe_tree_attention(const moe_kv_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,
@@ -224,7 +225,13 @@ moe_status_t moe_tree_attention(const moe_kv_cache_t *cache, const moe_heads_t *
     a.max_pages = max_pages;
     a.group = q->heads / cache->heads;
     a.scale_log2 = scale * 1.44269504088896341f;
-    return status_of(launch_tree_simt(a, reinterpret_cast<cudaStream_t>(s), kUsePdl));
+    a.wait_limit = current_wait_limit();
+    const cudaStream_t st_ = reinterpret_cast<cudaStream_t>(s);
+    if (tree_attn_supports(*cache, *q, *out)) {
+        const cudaError_t e = launch_tree_attn(a, st_, kUsePdl);
+        if (e != cudaErrorNotSupported) return status_of(e);
+    }
+    return status_of(launch_tree_simt(a, st_, kUsePdl));
 }
 
 }  // extern "C"

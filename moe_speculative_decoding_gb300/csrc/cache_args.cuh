@@ -48,5 +48,11 @@ cudaError_t launch_rope_table(const double *w, int half, double magnitude, int p
 cudaError_t launch_rows(const RowArgs &a, cudaStream_t s, bool pdl);
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s, bool pdl);
 cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t s, bool pdl);
+// The tensor-core kernel: whether it takes these operands, its workspace after the header, the
+// launch (cudaErrorNotSupported: strides that no tensor map describes).
+bool tree_attn_supports(const moe_kv_cache_t &c, const moe_heads_t &q, const moe_heads_t &out);
+size_t tree_attn_part_bytes(int dim);
+cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t s, bool pdl);
+long long current_wait_limit();   // moe_set_wait_limit's, or the default
 
 }  // namespace moe
