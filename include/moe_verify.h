@@ -648,7 +648,8 @@ size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t t
  * (ctx < 0, n_b outside [0, max_tokens], ctx + n_b > max_pages * page, tokens beyond q) is recorded
  * and its rows are not written.
  * bf16 q over a bf16 or e4m3 cache with dim <= 128 runs on the tensor cores when q is 16-byte
- * aligned with strides that are multiples of 8 elements and page is a multiple of 8; all else on
+ * aligned with strides that are multiples of 8 elements, as out, page is a multiple of 8 and the
+ * scales are 16-byte aligned; all else on
  * the CUDA cores in fp32.  tokens >= 0; 1 <= max_tokens <= 64; q heads a multiple of the cache's,
  * at most 64 times as many.  Asynchronous on s.
  */

@@ -1,0 +1,617 @@
+// tree_common.cuh -- what the tensor-core attention kernels share: tcgen05 and TMA pieces, the
+// work list over (sequence, cache head) items and position tiles, tree masks, and the host's tensor
+// maps.
+#pragma once
+
+#include <algorithm>
+#include <mutex>
+
+#include "cache_args.cuh"
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 128;                      // positions of a K/V tile, lanes of an accumulator
+constexpr long long kDrain = 400000000ll;       // about 0.2 s
+constexpr int kMaxCtas = 256;
+constexpr float kLazy = 8.0f;                   // log2 growth of a maximum that O is rescaled for
+constexpr float kWeightUp = 128.0f;             // fp16 weights: at most 2^8 * 2^7, flushed below 2^-31
+
+// ------------------------------------------------------------------ tcgen05, TMA and arithmetic pieces
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,"
+        "%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+        "%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit A and B, fp32 D.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// An MN-major operand with the 128-byte swizzle: blocks of 64 16-bit elements (128 bytes) by 8 rows
+// of K (1024 bytes), the next 8 rows 1024 bytes on, the next 64 elements `block` bytes on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t block) {
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16 |
+           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+// kind::f16, fp32 D, B MN-major; fmt 0: fp16, 1: bf16
+__host__ __device__ constexpr uint32_t idesc_pv(int N, uint32_t fmt) {
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);
+}
+// kind::f8f6f4, A e5m2 (format 1), B e4m3 (0), both K-major
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N) { return idesc_e4m3_f32(M, N) | (1u << 7); }
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1,
+                                            int32_t c2, int32_t c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two fp32 operations in one instruction.
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ void f2_get(F2 x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float ninf() { return -__int_as_float(0x7f800000); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool f16) {
+    uint32_t r;
+    if (f16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Barrier over the 256 softmax threads that also ORs a predicate, so that all of them leave a loop
+// together.
+__device__ __forceinline__ bool softmax_any(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
+// Bounded warp-wide wait until *p has reached v, under mbar_wait's rules.
+__device__ __forceinline__ bool wait_count(const volatile uint32_t *p, uint32_t v, volatile int32_t *abort, int32_t *err,
+                                           long long limit) {
+    const long long t0 = clock64();
+    while (!__all_sync(0xFFFFFFFFu, static_cast<int32_t>(*p - v) >= 0)) {
+        const bool late = clock64() - t0 > limit;
+        if (__any_sync(0xFFFFFFFFu, late || *abort != 0)) {
+            if (late) {
+                *abort = 1;
+                record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+            }
+            return false;
+        }
+    }
+    __threadfence_block();
+    return true;
+}
+
+// ------------------------------------------------------------------ the work list
+struct Seq {
+    int t0, n, ctx, len, tiles, pairs;
+    bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
+    Seq s;
+    s.t0 = a.q_start[b];
+    const long long n = static_cast<long long>(a.q_start[b + 1]) - s.t0;
+    s.ctx = a.ctx[b];
+    const long long len = s.ctx + n;
+    s.bad = s.ctx < 0 || n < 0 || n > a.max_tokens || s.t0 < 0 || s.t0 > a.tokens - n ||
+            len > static_cast<long long>(a.max_pages) * a.cache.page;
+    s.n = s.bad ? 0 : static_cast<int>(n);
+    s.len = s.bad ? 0 : static_cast<int>(len);
+    s.tiles = (s.len + kTile - 1) / kTile;
+    s.pairs = (s.n * a.group + 2 * kTile - 1) / (2 * kTile);
+    return s;
+}
+__device__ __forceinline__ long long seq_work(const TreeArgs &a, const Seq &s) {
+    return static_cast<long long>(a.cache.heads) * s.pairs * s.tiles;
+}
+// The list is cut for at most as many CTAs as it has tiles, so that no range is empty (the join
+// reads a part of every CTA between an item's first and last).
+__device__ __forceinline__ int used_ctas(long long W, int ctas) { return static_cast<int>(min(W, static_cast<long long>(ctas))); }
+// First tile of CTA c's range, and the CTA whose range holds tile x.
+__device__ __forceinline__ long long range_lo(long long W, int c, int C) { return W * c / C; }
+__device__ __forceinline__ int range_of(long long W, long long x, int C) {
+    return static_cast<int>(((x + 1) * C - 1) / W);
+}
+
+// A CTA's walk over its range: item by item, the part [lo, hi) of the item's position tiles.
+struct Walk {
+    Seq s;
+    long long at, end, item0;   // next tile of the list, the range's end, the item's first tile
+    int b, hk, pair, lo, hi;
+    bool whole;                 // the item lies in this CTA alone
+    int index;                  // items walked before
+};
+// The whole warp calls these; the outcome is uniform.
+__device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool report) {
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    long long total = 0;
+    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
+        long long x = 0;
+        if (b0 + lane < a.seqs) {
+            const Seq s = load_seq(a, b0 + lane);
+            if (s.bad && report) record_error(a.err, MOE_ERR_BAD_ID);
+            x = seq_work(a, s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        total += x;
+    }
+    const int C = used_ctas(total, gridDim.x), c = static_cast<int>(blockIdx.x);
+    w.at = c < C ? range_lo(total, c, C) : 0;
+    w.end = c < C ? range_lo(total, c + 1, C) : 0;
+    w.index = -1;
+    w.b = 0;
+    w.hk = 0;
+    w.pair = 0;
+    w.item0 = 0;
+    if (w.at >= w.end) return;
+    long long before = 0;   // tiles of the sequences before
+    for (int b0 = 0;; b0 += 32) {
+        long long x = 0;
+        if (b0 + lane < a.seqs) x = seq_work(a, load_seq(a, b0 + lane));
+        long long incl = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + incl > w.at);
+        if (past != 0) {
+            const int l = __ffs(past) - 1;
+            w.b = b0 + l;
+            before += __shfl_sync(0xFFFFFFFFu, incl - x, l);
+            break;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    w.s = load_seq(a, w.b);
+    const long long item = (w.at - before) / w.s.tiles;
+    w.item0 = before + item * w.s.tiles;
+    w.hk = static_cast<int>(item / w.s.pairs);
+    w.pair = static_cast<int>(item % w.s.pairs);
+}
+// Sets the next item's part; false at the end of the range.
+__device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
+    if (w.at >= w.end) return false;
+    if (w.index >= 0) {   // step to the item at w.at
+        w.item0 += w.s.tiles;
+        if (++w.pair == w.s.pairs) {
+            w.pair = 0;
+            if (++w.hk == a.cache.heads) {
+                w.hk = 0;
+                do {
+                    w.s = load_seq(a, ++w.b);
+                } while (w.s.tiles == 0 || w.s.pairs == 0);   // there is work left, so one follows
+            }
+        }
+    }
+    ++w.index;
+    w.lo = static_cast<int>(w.at - w.item0);
+    const long long stop = min(w.end, w.item0 + w.s.tiles);
+    w.hi = static_cast<int>(stop - w.item0);
+    w.whole = w.lo == 0 && w.hi == w.s.tiles;
+    w.at = stop;
+    return true;
+}
+
+// Partial results: per CTA two slots (its first item, its last), each [2 M tiles][DP / 4][128
+// rows][4] fp32 of unnormalised output, then, after all slots, [slot][2][128] (maximum, sum).
+template <int DP>
+__device__ __forceinline__ float4 *part_out(const TreeArgs &a, int slot, int mt) {
+    return reinterpret_cast<float4 *>(a.part) + (static_cast<size_t>(slot) * 2 + mt) * (DP / 4) * kTile;
+}
+template <int DP>
+__device__ __forceinline__ float2 *part_ml(const TreeArgs &a, int ctas, int slot, int mt) {
+    return reinterpret_cast<float2 *>(reinterpret_cast<float4 *>(a.part) + static_cast<size_t>(ctas) * 4 * (DP / 4) * kTile) +
+           (static_cast<size_t>(slot) * 2 + mt) * kTile;
+}
+
+// Element offset of the row of position pos of sequence b, head hk; -1 for a page outside the cache.
+__device__ __forceinline__ int64_t row_offset(const TreeArgs &a, int b, int hk, int pos, int &page, int &at) {
+    page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / a.cache.page];
+    at = pos % a.cache.page;
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return -1;
+    return page * a.cache.page_stride + at * a.cache.token_stride + hk * a.cache.head_stride;
+}
+
+// Which of the 128 positions of tile tt a row sees: bit j of word j / 32.  M: the row's tree mask.
+__device__ __forceinline__ void seen_bits(uint64_t M, const Seq &s, int tt, uint32_t (&w)[4]) {
+    if (s.n < 64) M &= (1ull << s.n) - 1ull;
+    const int base = tt * kTile - s.ctx;   // drafted token of the tile's first position
+    uint64_t lo, hi = 0;
+    if (base >= 0) {
+        lo = base < 64 ? M >> base : 0ull;
+    } else {
+        const int sh = -base;
+        if (sh < 64) {
+            lo = M << sh | ((1ull << sh) - 1ull);
+            hi = M >> (64 - sh);
+        } else {
+            lo = ~0ull;
+            hi = sh >= 128 ? ~0ull : (M << (sh - 64) | ((1ull << (sh - 64)) - 1ull));
+        }
+    }
+    w[0] = static_cast<uint32_t>(lo);
+    w[1] = static_cast<uint32_t>(lo >> 32);
+    w[2] = static_cast<uint32_t>(hi);
+    w[3] = static_cast<uint32_t>(hi >> 32);
+}
+
+__device__ __forceinline__ float f16_of(uint32_t h) {
+    float r;
+    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
+    return h;
+}
+
+// ------------------------------------------------------------------ roles
+// L gives the places in shared memory: oK, oV, oS (V codes landing), oSSc (their scales), oBad,
+// oScale, oSigma, ring sizes NK, NV, NS, barriers bKF ... at oBar.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The producer warp: K, then V of each tile, a lane per box of box_rows positions.  Boxes beyond the
+// length are not copied.  An e4m3 cache's scales (contiguous over a page's rows) land with V's codes.
+template <typename L, bool F8, int DP>
+__device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
+                                        uint8_t *smem, int box_rows, volatile int32_t *abort_flag,
+                                        volatile uint32_t *v_issued) {
+    const uint32_t base = smem_u32(smem);
+    auto bar = [&](int i) { return base + L::oBar + 8u * i; };
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int boxes = kTile / box_rows;   // at most 16
+    const moe_kv_cache_t &kc = a.cache;
+    constexpr uint32_t NV = F8 ? L::NS : L::NV;
+    uint32_t cnt = 0, k_cnt = 0;
+    bool ok = true;
+    while (ok && walk_next(a, w)) {
+        const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
+        auto page_of = [&](int tt) {   // the lane's box of tile tt: its page (0 beyond the length)
+            const int pos = tt * kTile + lane * box_rows;
+            return tt < w.hi && lane < boxes && pos < w.s.len ? __ldg(table + pos / kc.page) : 0;
+        };
+        int next = page_of(w.lo);
+        for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
+            const int pos = tt * kTile + lane * box_rows, row = pos % kc.page;
+            const bool mine = lane < boxes && pos < w.s.len;
+            int page = next;
+            next = page_of(tt + 1);   // in flight during this tile
+            const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(kc.pages);
+            if (mine && !good) {
+                record_error(a.err, MOE_ERR_BAD_ID);
+                page = kc.pages;   // beyond the tensor: the copy writes zeros
+            }
+            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, mine)), n_good = __popc(__ballot_sync(0xFFFFFFFFu, mine && good));
+            const uint32_t bytes = n * box_rows * (F8 ? 128u : DP * 2u);
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t slot = v ? cnt % NV : cnt % L::NK, use = v ? cnt / NV : cnt / L::NK;
+                const uint32_t full = bar((v ? (F8 ? L::bSF : L::bVF) : L::bKF) + slot);
+                const uint32_t empty = bar((v ? (F8 ? L::bSE : L::bVE) : L::bKE) + slot);
+                const uint32_t dst = base + (v ? (F8 ? L::oS + slot * L::kStage : L::oV + slot * L::kVSlot)
+                                               : L::oK + slot * L::kKSlot);
+                if (!warp_wait(empty, (use & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) {
+                    ok = false;
+                    break;
+                }
+                if (F8 && v && mine && !good) {   // no scales to copy: zeros
+                    float *const sc = reinterpret_cast<float *>(smem + L::oSSc + slot * 1024) + lane * box_rows;
+                    for (int i = 0; i < box_rows; ++i) sc[i] = sc[128 + i] = 0.0f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes + (F8 && v ? n_good * box_rows * 8u : 0u));
+                __syncwarp();
+                if (mine) {
+                    const CUtensorMap *tm = v ? tm_v : tm_k;
+                    const uint32_t d = dst + static_cast<uint32_t>(lane * box_rows) * 128u;
+                    tma_load_4d(d, tm, full, 0, row, w.hk, page);
+                    if (!F8 && DP == 128) tma_load_4d(d + kTile * 128u, tm, full, 64, row, w.hk, page);
+                    if (F8 && v && good) {
+                        const int64_t o = (static_cast<int64_t>(page) * kc.heads + w.hk) * kc.page + row;
+                        const uint32_t sd = base + L::oSSc + slot * 1024 + lane * box_rows * 4u;
+                        bulk_load(sd, kc.k_scale + o, box_rows * 4u, full);
+                        bulk_load(sd + 512, kc.v_scale + o, box_rows * 4u, full);
+                    }
+                }
+                __syncwarp();
+                if (v == 0) ++k_cnt;
+            }
+            if (!ok) break;
+            if (!F8 && lane == 0) {
+                __threadfence_block();
+                *v_issued = cnt + 1;
+            }
+        }
+    }
+    if (*abort_flag != 0) {   // copies nobody waited for must land before the CTA leaves
+        for (uint32_t j = k_cnt > L::NK ? k_cnt - L::NK : 0; j < k_cnt; ++j)
+            mbar_wait_drain(bar(L::bKF + j % L::NK), (j / L::NK) & 1u, kDrain);
+        for (uint32_t j = cnt > NV ? cnt - NV : 0; j < cnt; ++j)
+            mbar_wait_drain(bar((F8 ? L::bSF : L::bVF) + j % NV), (j / NV) & 1u, kDrain);
+    }
+}
+
+// bf16: V's cleaner, one warp, over the tiles that reach past the context.  Positions beyond the
+// length become zeros (their weights are 0, what the cache holds there may be anything), and so do
+// non-finite elements of drafted tokens: a row that does not see such a token must not meet it in
+// the product.  Rows that do get it added at the end of the item (bad bits).
+template <typename L, int DP>
+__device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t *smem, volatile int32_t *abort_flag,
+                                             const volatile uint32_t *v_issued) {
+    const uint32_t base = smem_u32(smem);
+    auto bar = [&](int i) { return base + L::oBar + 8u * i; };
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    uint32_t cnt = 0, fixes = 0;
+    bool ok = true;
+    while (ok && walk_next(a, w)) {
+        uint32_t *const bad = reinterpret_cast<uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
+        if (lane < 8) bad[lane] = 0;
+        __syncwarp();
+        for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
+            if ((tt + 1) * kTile <= w.s.ctx) continue;
+            const uint32_t slot = cnt % L::NV;
+            // only the last tiles are waited for here, so the slot may be some uses behind: its
+            // parity tells this use from the one before once this one was issued
+            if (!wait_count(v_issued, cnt + 1, abort_flag, a.err, a.wait_limit) ||
+                !warp_wait(bar(L::bVF + slot), (cnt / L::NV) & 1u, abort_flag, a.err, a.wait_limit)) {
+                ok = false;
+                break;
+            }
+            uint8_t *const v = smem + L::oV + slot * L::kVSlot;
+            constexpr int C = DP / 8;   // 16-byte chunks of a row; 32 / C rows at a time
+            const int c = lane % C;
+            const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
+            for (int r0 = first / (32 / C) * (32 / C); r0 < kTile; r0 += 32 / C) {
+                const int r = r0 + lane / C;
+                uint4 *const p = reinterpret_cast<uint4 *>(v + (c / 8) * (kTile * 128) + r * 128 + (c % 8) * 16);
+                if (r >= stop) {
+                    *p = make_uint4(0, 0, 0, 0);
+                } else if (r >= first) {
+                    uint4 x = *p;
+                    uint32_t *const q = reinterpret_cast<uint32_t *>(&x);
+                    bool hit = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if ((q[i] & 0x7F80u) == 0x7F80u) {
+                            q[i] &= 0xFFFF0000u;
+                            hit = true;
+                        }
+                        if ((q[i] & 0x7F800000u) == 0x7F800000u) {
+                            q[i] &= 0x0000FFFFu;
+                            hit = true;
+                        }
+                    }
+                    if (hit) {
+                        *p = x;
+                        atomicOr(&bad[(tt & 1) * 4 + r / 32], 1u << (r & 31));
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __threadfence_block();
+            warp_arrive(bar(L::bFix + (fixes & 3u)));   // the ring of V keeps this at most NV ahead
+            ++fixes;
+        }
+    }
+}
+
+// e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
+// layout, the scales into the softmax's double buffer.  The value scales there are relative to
+// sigma, a power of two at or above all of the item's finite ones so far, times kWeightUp.  What
+// clean_values does for bf16 is done on the way.
+template <typename L, int DP>
+__device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw,
+                                               volatile int32_t *abort_flag) {
+    const uint32_t base = smem_u32(smem);
+    auto bar = [&](int i) { return base + L::oBar + 8u * i; };
+    const int lane = static_cast<int>(threadIdx.x & 31), j = cw * 32 + lane;
+    float *const scale_s = reinterpret_cast<float *>(smem + L::oScale);
+    volatile float *const sigma_s = reinterpret_cast<volatile float *>(smem + L::oSigma);
+    const float kMax = 3.4028234e38f;
+    uint32_t cnt = 0;
+    bool ok = true;
+    while (ok && walk_next(a, w)) {
+        uint32_t *const bad = reinterpret_cast<uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
+        if (lane < 2) bad[lane * 4 + cw] = 0;   // a warp's words are its own
+        __syncwarp();
+        float sigma = 7.888609e-31f;   // 2^-100: below any value scale that counts
+        for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
+            const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
+            const uint32_t ss = cnt % L::NS, slot = cnt % L::NV, sb = cnt & 1u;
+            if (!(ok = warp_wait(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
+            const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
+            float top = 0.0f, ks = 0.0f, vs = 0.0f;   // every warp forms the tile's largest: no barrier
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float v = k * 32 + lane < stop ? land[128 + k * 32 + lane] : 0.0f;
+                if (fabsf(v) <= kMax) top = fmaxf(top, fabsf(v));
+                if (k == cw) vs = v;
+            }
+            if (j < stop) ks = land[j];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            if (top > sigma)   // the power of two at or above it
+                sigma = __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000));
+            const bool odd_scale = j >= first && j < stop && !(fabsf(vs) <= kMax);
+            if (!(ok = warp_wait(bar(L::bCE + sb), ((cnt >> 1) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
+            scale_s[sb * 256 + j] = ks;
+            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
+            if (lane == 0) sigma_s[sb] = sigma;   // the same from every warp
+            if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
+            warp_arrive(bar(L::bCF + sb));
+            if (!(ok = warp_wait(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
+            const uint8_t *const src = smem + L::oS + ss * L::kStage;
+            uint8_t *const dst = smem + L::oV + slot * L::kVSlot;
+            // 4 (8) rows of 128 (64) codes a step: 16 codes per lane
+            constexpr int C = DP / 16, RS = 32 / C;
+            const int c = lane % C;
+#pragma unroll 4
+            for (int i = 0; i < 32 / RS; ++i) {
+                const int r = cw * 32 + i * RS + lane / C;
+                uint4 x = *reinterpret_cast<const uint4 *>(src + r * 128 + c * 16);
+                if (r >= first) {   // the tile's part past the context
+                    uint32_t *const q = reinterpret_cast<uint32_t *>(&x);
+                    if (r >= stop) {
+                        x = make_uint4(0, 0, 0, 0);
+                    } else {
+                        bool hit = false;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                if ((q[k] >> (8 * y) & 0x7Fu) == 0x7Fu) {
+                                    q[k] &= ~(0xFFu << (8 * y));
+                                    hit = true;
+                                }
+                        if (hit) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << (r & 31));
+                    }
+                }
+                const uint4 lo = make_uint4(e4m3x2_to_f16x2(x.x & 0xFFFFu), e4m3x2_to_f16x2(x.x >> 16),
+                                            e4m3x2_to_f16x2(x.y & 0xFFFFu), e4m3x2_to_f16x2(x.y >> 16));
+                const uint4 hi = make_uint4(e4m3x2_to_f16x2(x.z & 0xFFFFu), e4m3x2_to_f16x2(x.z >> 16),
+                                            e4m3x2_to_f16x2(x.w & 0xFFFFu), e4m3x2_to_f16x2(x.w >> 16));
+                // 64-channel halves; the halves' lanes store their two chunks in opposite order, so
+                // that a step's eight lanes of a row meet eight bank groups
+                uint8_t *const row = dst + (c / 4) * (kTile * 128) + r * 128;
+                const int u = (c % 4) * 2, sw = c / 4;
+                *reinterpret_cast<uint4 *>(row + (((u + sw) ^ (r & 7)) * 16)) = sw ? hi : lo;
+                *reinterpret_cast<uint4 *>(row + (((u + 1 - sw) ^ (r & 7)) * 16)) = sw ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __threadfence_block();
+            warp_arrive(bar(L::bSE + ss));
+            warp_arrive(bar(L::bVF + slot));
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
+                                  CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                  CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// The cache as a 4-D tensor (channel, row of a page, head, page); boxes of box_rows rows and 128
+// bytes.  Channels beyond dim and pages beyond the cache read as zeros.
+bool encode(CUtensorMap *map, const moe_kv_cache_t &c, const void *ptr, int box_rows, bool swizzle) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const uint64_t es = c.dtype == MOE_BF16 ? 2 : 1;
+    // a dimension of one element has no step; any valid stride will do
+    auto stride = [&](int64_t st, int extent) { return extent == 1 ? 16u * 1024u : static_cast<cuuint64_t>(st) * es; };
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page), static_cast<cuuint64_t>(c.heads),
+                          static_cast<cuuint64_t>(c.pages)};
+    cuuint64_t strides[3] = {stride(c.token_stride, c.page), stride(c.head_stride, c.heads), stride(c.page_stride, c.pages)};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr),
+              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int box_rows_of(int page) {   // the largest power of two that divides a page, at most a tile
+    int b = 8;
+    while (b < kTile && page % (2 * b) == 0) b *= 2;
+    return b;
+}
+
+int dim_padded(int dim) { return dim <= 64 ? 64 : 128; }
+
+}  // namespace
+}  // namespace moe
