@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libmoeverify.so")
 SOURCES = ("api.cu", "route.cu", "group.cu", "expert_simt.cu", "expert_tc.cu", "noalloc.cu", "quant.cu", "spec.cu", "probe.cu",
-           "cache_api.cu", "rope_kv.cu", "tree_attn_simt.cu", "tree_attn.cu")
+           "cache_api.cu", "rope_kv.cu", "tree_attn_simt.cu", "tree_attn.cu", "tree_attn_narrow.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -39,6 +39,10 @@
 #include "tree_common.cuh"
 
 namespace moe {
+
+cudaError_t launch_tree_narrow(const TreeArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_v, cudaStream_t s, bool pdl);
+
 namespace {
 
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kAuxWarp = 11;   // two product warps, one per softmax warpgroup
@@ -62,9 +66,9 @@ struct Lay {
     static constexpr uint32_t oSSc = oS + NS * kStage;             // F8: float [NS][ks, vs][128], landing
     static constexpr uint32_t oBar = oSSc + NS * 1024;
     // barriers: k_full, k_empty, v_full, v_empty, st_full, st_empty, sc_full[2], sc_empty[2],
-    // s_full[2], p_ready[2], q_ready, o_full, o_free, v_fix[4], drain
+    // s_full[2], p_ready[2], q_ready, o_full, v_fix[4], drain
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
-                         bCE = bCF + 2, bS = bCE + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bOF = bO + 1, bFix = bOF + 1,
+                         bCE = bCF + 2, bS = bCE + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
                          bDrain = bFix + 4, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
     static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
@@ -169,6 +173,13 @@ __device__ __forceinline__ float tile_weights(uint32_t s_addr, const float *ks, 
     return s0 + s1;
 }
 
+// o[i] += x with i known only at run time, o staying in registers
+__device__ __forceinline__ void add_at(float (&o)[32], int i, float x) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        if (k == i) o[k] += x;
+}
+
 // ------------------------------------------------------------------ the kernel
 template <bool F8, int DP>
 __global__ void __launch_bounds__(Lay<F8, DP>::kThreads, 1)
@@ -205,7 +216,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         mbar_init(bar(L::bQ), 8);
         mbar_init(bar(L::bO), 2);
-        mbar_init(bar(L::bOF), 8);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
         *abort_flag = 0;
@@ -281,8 +291,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     const uint32_t f = base_fix + (tt - edge0);
                     ok = warp_wait(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
                 }
-                // O of the previous item has been read
-                if (ok && u == g && items > 0) ok = warp_wait(bar(L::bOF), (items - 1) & 1u, abort_flag, a.err, limit);
                 ok = ok && warp_wait(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 ++pc;
@@ -344,36 +352,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         x = *reinterpret_cast<const uint4 *>(
                             static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
                             static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
-                    uint8_t *const q = smem + mt * L::kQTile;
-                    if (!F8) {
-                        *reinterpret_cast<uint4 *>(q + (c / 8) * (kTile * 128) + lr * 128 + (((c % 8) ^ (lr & 7)) * 16)) = x;
-                    } else {
-                        // the row's largest exponent over its C lanes (bf16 magnitudes order as integers)
-                        const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) top = max(top, max(wd[k] & 0x7FFFu, wd[k] >> 16 & 0x7FFFu));
-#pragma unroll
-                        for (int o = C / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                        const int e = static_cast<int>(top >> 7);   // biased exponent; 255: not finite
-                        // up = 2^(7 - (e - 127)): the largest lands in [128, 256); exponents of the two
-                        // factors stay in range by going to at most 2^126
-                        const int ub = min(max(127 + 134 - e, 1), 253);
-                        const float up = __int_as_float(ub << 23);
-                        if (c == 0) qs[mt * 128 + lr] = e == 255 ? __int_as_float(0x7fffffff) : __int_as_float((254 - ub) << 23);
-                        uint16_t hi[4], lo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x0 = bf16_lo(wd[k]) * up, x1 = bf16_hi(wd[k]) * up;
-                            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi[k]) : "f"(x1), "f"(x0));
-                            const uint32_t h = e4m3x2_to_f16x2(hi[k]);
-                            const float r0 = x0 - f16_of(h), r1 = x1 - f16_of(h >> 16);
-                            asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo[k]) : "f"(r1), "f"(r0));
-                        }
-                        uint8_t *const p = q + lr * 128 + (((c / 2) ^ (lr & 7)) * 16) + (c & 1) * 8;
-                        *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0] | static_cast<uint32_t>(hi[1]) << 16, hi[2] | static_cast<uint32_t>(hi[3]) << 16);
-                        *reinterpret_cast<uint2 *>(p + 16384) = make_uint2(lo[0] | static_cast<uint32_t>(lo[1]) << 16, lo[2] | static_cast<uint32_t>(lo[3]) << 16);
-                    }
+                    float unscale;
+                    store_query<F8, DP>(smem + mt * L::kQTile, kTile, lr, c, x, unscale);
+                    if (F8 && c == 0) qs[mt * 128 + lr] = unscale;
                 }
                 fence_proxy_async_smem();
             }
@@ -489,16 +470,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         seen_bits(M, w.s, tt, see);
                         for (int j = 0; j < kTile; ++j) {
                             if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u) || !(see[j / 32] >> (j & 31) & 1u)) continue;
-                            int page, at;
-                            const int64_t off = row_offset(a, w.b, w.hk, tt * kTile + j, page, at);
-                            if (off < 0) continue;
-                            const float vsc = F8 ? a.cache.v_scale[(static_cast<int64_t>(page) * a.cache.heads + w.hk) * a.cache.page + at] : 1.0f;
-#pragma unroll
+#pragma unroll 1
                             for (int i = 0; i < 32; ++i) {
-                                if (c + i >= a.cache.dim) continue;
-                                const float x = F8 ? f16_of(e4m3x2_to_f16x2(static_cast<const uint8_t *>(a.cache.v)[off + c + i])) * vsc
-                                                   : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.cache.v)[off + c + i]) << 16);
-                                if (!(fabsf(x) <= 3.4028234e38f)) o[i] += x;
+                                const float x = c + i < a.cache.dim ? value_at<F8>(a, w.b, w.hk, tt * kTile + j, c + i) : 0.0f;
+                                if (!(fabsf(x) <= 3.4028234e38f)) add_at(o, i, x);
                             }
                         }
                     }
@@ -517,9 +492,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     for (int i = 0; i < 32; i += 4) po[static_cast<size_t>((c + i) / 4) * kTile] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                 }
             }
-            __syncwarp();
-            tc_fence_before();
-            warp_arrive(bar(L::bOF));
+            tc_fence_before();   // the next item's products follow this warp's arrival on bQ
             if (live && (two || g == 0)) {
                 if (w.whole) {
                     if (a.lse != nullptr)
@@ -539,18 +512,26 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // ------------------------------------------------------------------ joining the parts
-// One CTA per 32 rows of a (sequence, cache head): for an item that several CTAs of the first
-// kernel shared, out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its parts in order.
+// For an item that several CTAs of the first kernel shared: out = sum_i 2^(m_i - m) O_i /
+// sum_i 2^(m_i - m) l_i over its parts in order.  The parts lie in L2, so what counts is how many
+// loads are in flight: a CTA takes 1024 / DP rows, a thread four channels of one row, its first
+// parts on their way while a warp per row forms the weights, a lane per part.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 32;
 
-template <int DP>
+template <bool NARROW, int DP>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
+    constexpr int Q = DP / 4, ROWS = kJoinThreads / Q, AHEAD = 8;
     __shared__ long long red[2][kJoinThreads / 32];
-    __shared__ float wt[kMaxCtas + 1][kJoinRows];
+    __shared__ float wt[kMaxCtas][ROWS], inv_s[ROWS];
     const int b = blockIdx.z, hk = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the lengths are no product of the first kernel, which waited for what came before it
+    const Seq s = load_seq(a, b);
+    const int row0 = blockIdx.x * ROWS, R = s.n * a.group;
+    if (row0 >= R) {
+        pdl_wait();
+        return;
+    }
     long long before = 0, total = 0;
     for (int i = threadIdx.x; i < a.seqs; i += kJoinThreads) {
         const long long x = seq_work(a, load_seq(a, i));
@@ -572,63 +553,76 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         before += red[0][i];
         total += red[1][i];
     }
-    const Seq s = load_seq(a, b);
-    const int row0 = blockIdx.x * kJoinRows, R = s.n * a.group;
-    pdl_wait();
-    pdl_trigger();
-    if (row0 >= R) return;
     const int pair = row0 / (2 * kTile), mt = row0 / kTile % 2, r0 = row0 % kTile;
     const long long first = before + (static_cast<long long>(hk) * s.pairs + pair) * s.tiles;
     const int C = used_ctas(total, ctas);
     const int ca = range_of(total, first, C), cb = range_of(total, first + s.tiles - 1, C);
+    pdl_wait();
+    pdl_trigger();
     if (ca == cb) return;
     const bool head_slot = range_lo(total, ca, C) == first;   // the item begins its first CTA's range
-    auto slot = [&](int c) { return 2 * c + (c == ca && !head_slot ? 1 : 0); };
+    auto slot = [&](int i) { return 2 * (ca + i) + (i == 0 && !head_slot ? 1 : 0); };
     const int parts = cb - ca + 1;
-    if (warp == 0) {   // a lane per row: the weights of its parts
-        const bool live = row0 + lane < R;
+    // neighbouring threads read neighbouring 16 bytes of either layout
+    const int rr = NARROW ? threadIdx.x / Q : threadIdx.x % ROWS, quad = NARROW ? threadIdx.x % Q : threadIdx.x / ROWS;
+    const bool live = row0 + rr < R && quad * 4 < a.cache.dim;
+    auto part = [&](int i) {
+        return NARROW ? *reinterpret_cast<const float4 *>(narrow_out<DP>(a, slot(i)) + (r0 + rr) * DP + quad * 4)
+                      : part_out<DP>(a, slot(i), mt)[static_cast<size_t>(quad) * kTile + r0 + rr];
+    };
+    float4 x[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+        if (live && i < parts) x[i] = part(i);
+    for (int r = warp; r < ROWS; r += kJoinThreads / 32) {
+        if (row0 + r >= R) continue;
+        auto ml = [&](int i) { return NARROW ? narrow_ml<DP>(a, ctas, slot(i))[r0 + r] : part_ml<DP>(a, ctas, slot(i), mt)[r0 + r]; };
         float m = ninf(), l = 0.0f;
-        for (int i = 0; i < parts; ++i)
-            if (live) m = fmaxf(m, part_ml<DP>(a, ctas, slot(ca + i), mt)[r0 + lane].x);
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml(i).x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float ref = m == ninf() ? 0.0f : m;
-        for (int i = 0; i < parts; ++i) {
-            float k = 0.0f;
-            if (live) {
-                const float2 ml = part_ml<DP>(a, ctas, slot(ca + i), mt)[r0 + lane];
-                k = ex2(ml.x - ref);
-                l += ml.y * k;
-            }
-            wt[i][lane] = k;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 y = ml(i);
+            const float k = ex2(y.x - ref);
+            l += y.y * k;
+            wt[i][r] = k;
         }
-        const bool none = m == ninf() && l == 0.0f;
-        wt[parts][lane] = none ? 0.0f : 1.0f / l;
-        if (live && a.lse != nullptr) {
-            const int row = row0 + lane;
-            a.lse[static_cast<int64_t>(s.t0 + row / a.group) * a.q.heads + hk * a.group + row % a.group] =
-                none ? ninf() : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0) {
+            const bool none = m == ninf() && l == 0.0f;
+            inv_s[r] = none ? 0.0f : 1.0f / l;
+            const int row = row0 + r;
+            if (a.lse != nullptr)
+                a.lse[static_cast<int64_t>(s.t0 + row / a.group) * a.q.heads + hk * a.group + row % a.group] =
+                    none ? ninf() : (m + log2f(l)) * 0.69314718055994531f;
         }
     }
     __syncthreads();
-    // 8 channel quads x 4 rows per warp and step
-    for (int i = threadIdx.x; i < kJoinRows * (DP / 4); i += kJoinThreads) {
-        const int q8 = i / 32, quad = (q8 % (DP / 32)) * 8 + lane % 8, rr = (q8 / (DP / 32)) * 4 + lane / 8;
-        const int row = row0 + rr;
-        if (row >= R || quad * 4 >= a.cache.dim) continue;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-            const float4 x = part_out<DP>(a, slot(ca + p), mt)[static_cast<size_t>(quad) * kTile + r0 + rr];
-            const float k = wt[p][rr];
-            o.x = fmaf(x.x, k, o.x);
-            o.y = fmaf(x.y, k, o.y);
-            o.z = fmaf(x.z, k, o.z);
-            o.w = fmaf(x.w, k, o.w);
+    if (!live) return;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < parts; i0 += AHEAD) {
+        if (i0 > 0) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i0 + i < parts) x[i] = part(i0 + i);
         }
-        const float inv = wt[parts][rr];
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out.ptr) + static_cast<int64_t>(s.t0 + row / a.group) * a.out.token_stride +
-                                   static_cast<int64_t>(hk * a.group + row % a.group) * a.out.head_stride + quad * 4) =
-            make_uint2(pack2(o.x * inv, o.y * inv, false), pack2(o.z * inv, o.w * inv, false));
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) {
+            if (i0 + i >= parts) continue;
+            const float k = wt[i0 + i][rr];
+            o.x = fmaf(x[i].x, k, o.x);
+            o.y = fmaf(x[i].y, k, o.y);
+            o.z = fmaf(x[i].z, k, o.z);
+            o.w = fmaf(x[i].w, k, o.w);
+        }
     }
+    const float inv = inv_s[rr];
+    const int row = row0 + rr;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out.ptr) + static_cast<int64_t>(s.t0 + row / a.group) * a.out.token_stride +
+                               static_cast<int64_t>(hk * a.group + row % a.group) * a.out.head_stride + quad * 4) =
+        make_uint2(pack2(o.x * inv, o.y * inv, false), pack2(o.z * inv, o.w * inv, false));
 }
 
 // ------------------------------------------------------------------ host side
@@ -646,7 +640,8 @@ int sm_count(int dev) {
 }
 
 template <bool F8, int DP>
-cudaError_t launch(const TreeArgs &a, int dev, cudaStream_t s, bool pdl) {
+cudaError_t launch_wide(const TreeArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                        cudaStream_t s, bool pdl) {
     using L = Lay<F8, DP>;
     {
         std::lock_guard<std::mutex> lock(g_mu);
@@ -657,16 +652,6 @@ cudaError_t launch(const TreeArgs &a, int dev, cudaStream_t s, bool pdl) {
             set = true;
         }
     }
-    const int sms = sm_count(dev);
-    if (sms < 1) return cudaErrorInvalidDevice;
-    const int rows = box_rows_of(a.cache.page);
-    CUtensorMap tm_k, tm_v;
-    if (!encode(&tm_k, a.cache, a.cache.k, rows, true) || !encode(&tm_v, a.cache, a.cache.v, rows, !F8))
-        return cudaErrorNotSupported;
-    // no more CTAs than the page tables could fill with tiles
-    const long long most = static_cast<long long>(a.seqs) * a.cache.heads * ((a.max_tokens * a.group + 2 * kTile - 1) / (2 * kTile)) *
-                           ((static_cast<long long>(a.max_pages) * a.cache.page + kTile - 1) / kTile);
-    const int ctas = static_cast<int>(std::min<long long>(sms, most));
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
@@ -677,12 +662,22 @@ cudaError_t launch(const TreeArgs &a, int dev, cudaStream_t s, bool pdl) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, tree_attn_kernel<F8, DP>, tm_k, tm_v, a, rows);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((a.max_tokens * a.group + kJoinRows - 1) / kJoinRows, a.cache.heads, a.seqs);
+    return cudaLaunchKernelEx(&cfg, tree_attn_kernel<F8, DP>, tm_k, tm_v, a, rows);
+}
+
+template <bool NARROW, int DP>
+cudaError_t launch_join(const TreeArgs &a, int ctas, cudaStream_t s, bool pdl) {
+    constexpr int ROWS = kJoinThreads / (DP / 4);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.max_tokens * a.group + ROWS - 1) / ROWS, a.cache.heads, a.seqs);
     cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, tree_join_kernel<DP>, a, ctas);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel<NARROW, DP>, a, ctas);
 }
 
 bool wide16(const moe_heads_t &h) {
@@ -711,11 +706,30 @@ size_t tree_attn_part_bytes(int dim) {
 
 cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t s, bool pdl) {
     int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const bool f8 = a.cache.dtype == MOE_E4M3;
-    if (dim_padded(a.cache.dim) == 64) return f8 ? launch<true, 64>(a, dev, s, pdl) : launch<false, 64>(a, dev, s, pdl);
-    return f8 ? launch<true, 128>(a, dev, s, pdl) : launch<false, 128>(a, dev, s, pdl);
+    const int sms = sm_count(dev);
+    if (sms < 1) return cudaErrorInvalidDevice;
+    const bool f8 = a.cache.dtype == MOE_E4M3, wide_head = a.cache.dim > 64;
+    const int rows = box_rows_of(a.cache.page);
+    CUtensorMap tm_k, tm_v;
+    if (!encode(&tm_k, a.cache, a.cache.k, rows, true) || !encode(&tm_v, a.cache, a.cache.v, rows, !f8))
+        return cudaErrorNotSupported;
+    // no more CTAs than the page tables could fill with tiles
+    const long long most = static_cast<long long>(a.seqs) * a.cache.heads * ((a.max_tokens * a.group + 2 * kTile - 1) / (2 * kTile)) *
+                           ((static_cast<long long>(a.max_pages) * a.cache.page + kTile - 1) / kTile);
+    const int ctas = static_cast<int>(std::min<long long>(sms, most));
+    if (a.max_tokens * a.group <= kNarrowRows) {
+        e = launch_tree_narrow(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+        if (e != cudaSuccess) return e;
+        return wide_head ? launch_join<true, 128>(a, ctas, s, pdl) : launch_join<true, 64>(a, ctas, s, pdl);
+    }
+    if (wide_head)
+        e = f8 ? launch_wide<true, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : launch_wide<false, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+    else
+        e = f8 ? launch_wide<true, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : launch_wide<false, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+    if (e != cudaSuccess) return e;
+    return wide_head ? launch_join<false, 128>(a, ctas, s, pdl) : launch_join<false, 64>(a, ctas, s, pdl);
 }
 
 }  // namespace moe

@@ -1,0 +1,602 @@
+// tree_attn_narrow.cu -- tree attention on the tensor cores for up to 64 rows (token, query head of
+// the group) of a cache head: the ordinary verification pass, and single tokens.
+//
+// Bound: the cache's bytes; 4 * dim flops per position, row and head leave the tensor cores far from
+// their limit, so what counts is that nothing else of a tile costs its rows twice: padding 8 or 20
+// rows to the 128 lanes of the kernel for many rows (tree_attn.cu) makes every product and every
+// exponential 128 wide.  Here the products are the other way round: positions are the M = 128
+// operand and rows the N = NT columns (16, 32 or 64),
+//
+//     S^T = K Q^T [128 positions x NT],  O^T += V^T P^T [128 channels x NT],
+//
+// K and V^T taken as they lie in the cache (V^T MN-major), Q and the weights P in shared memory.  A
+// thread of a softmax warpgroup owns a position, so a tile costs it NT exponentials, and the key and
+// value scales of an e4m3 cache are one number per thread.  The row maxima are columns' maxima over
+// 128 threads, which is dear, so they are not formed per tile: a tile is weighed against the maxima
+// so far, and only when some score lies above its row's by more than 2^8 (a vote of the warpgroup)
+// are they formed anew and O rescaled.  The sums stay with the threads until the end of an item.
+//
+// The two warpgroups take alternate tiles, each with its own maxima, sums and O^T, joined at the
+// item's end.  S^T of a warpgroup's next tile is formed while it weighs the present one.  Work list,
+// copies, value cleaning and conversion, parts and their join are those of tree_attn.cu.
+#include "tree_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kAuxWarp = 11;
+
+template <bool F8, int DP, int NT>
+struct Lay {
+    static constexpr int kThreads = (kAuxWarp + (F8 ? 4 : 1)) * 32;
+    static constexpr uint32_t kKSlot = F8 ? 16384 : 128 * DP * 2;
+    static constexpr uint32_t kVSlot = 128 * DP * 2;
+    static constexpr uint32_t kStage = F8 ? 16384 : 0;
+    static constexpr uint32_t kQ = F8 ? 2 * NT * 128 : DP / 64 * NT * 128;
+    static constexpr uint32_t kP = 128 * NT * 2;   // weights of a tile: a row of NT per position
+    // even rings: a product warp takes every other tile, all uses of its slots
+    static constexpr int NK = F8 || DP == 64 ? 4 : 2, NV = !F8 && DP == 64 ? 4 : 2;
+    static constexpr int NS = !F8 ? 0 : (NT == 64 && DP == 128 ? 2 : 4);
+    static constexpr int kUsers = 1, kVReaders = F8 ? 4 : 1;
+    static constexpr uint32_t oK = 0, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot, oP = oS + NS * kStage,
+                              oQ = oP + 2 * kP, oSSc = oQ + kQ, oBar = oSSc + NS * 1024;
+    static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
+                         bCE = bCF + 2, bS = bCE + 2, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
+                         bO = bQ + 1, bFix = bO + 1, bDrain = bFix + 4, kBars = bDrain + 1;
+    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
+    static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
+    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
+    static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);   // F8: float [2]
+    static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // float [NT]: score to log2 units
+    static constexpr uint32_t oM = oCs + NT * 4;                   // float [2][NT]: maxima of a warpgroup
+    static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
+    static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
+    static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
+    static constexpr uint32_t kSmem = oMask + NT * 8;
+    static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+// The weights' operand [128 positions][NT], MN-major, rows of NT * 2 = 32, 64 or 128 bytes with the
+// swizzle of that width: 16-byte chunk ^= the row's index within an atom of 8, at that granularity.
+template <int NT>
+__device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
+    constexpr uint64_t mode = NT == 64 ? 2 : (NT == 32 ? 4 : 6);
+    constexpr uint32_t atom = 8 * NT * 2;   // 8 positions
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
+           static_cast<uint64_t>(atom >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | mode << 61;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t p_chunk(int row, int chunk) {   // byte offset of a 16-byte chunk
+    const int x = NT == 64 ? row & 7 : (NT == 32 ? row >> 1 & 3 : row >> 2 & 1);
+    return static_cast<uint32_t>(row * NT * 2 + ((chunk ^ x) << 4));
+}
+// kind::f16, A (V^T) and B (P^T) MN-major; fmt 0: fp16, 1: bf16
+__host__ __device__ constexpr uint32_t idesc_vp(int N, uint32_t fmt) { return idesc_pv(N, fmt) | (1u << 15); }
+// kind::f8f6f4, A e4m3, B e5m2
+__host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N) { return idesc_e4m3_f32(M, N) | (1u << 10); }
+
+__device__ __forceinline__ void mma_ss_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    tc_mma_bf16(d, a, b, idesc, acc);   // kind::f16; the descriptor names the formats
+}
+
+template <int NT>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t addr, uint32_t (&x)[NT]) {
+    if constexpr (NT == 16) {
+        tmem_ld_16_async(addr, x);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NT / 32; ++c) tmem_ld32(addr + 32 * c, reinterpret_cast<uint32_t(&)[32]>(x[32 * c]));
+    }
+}
+template <int NT>
+__device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t (&x)[NT]) {
+    if constexpr (NT == 16) {
+        tmem_st16(addr, x);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NT / 32; ++c) tmem_st32(addr + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(x[32 * c]));
+    }
+}
+
+__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
+// Sums v[c] over the warp's lanes: afterwards lane l holds in v[0 .. NT/32) the sums of columns
+// l * NT/32 + i (NT = 16: of column l / 2 in v[0]).  The order of additions is fixed.
+template <int NT>
+__device__ __forceinline__ void warp_columns(float (&v)[NT], int lane) {
+#pragma unroll
+    for (int o = 16, n = NT; o > 0; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = (lane & o) != 0;
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) {
+                if (i < n) {
+                    const float send = up ? v[i] : v[i + n], kept = up ? v[i + n] : v[i];
+                    v[i] = kept + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+                }
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        }
+    }
+}
+
+template <bool F8, int DP, int NT>
+__global__ void __launch_bounds__(Lay<F8, DP, NT>::kThreads, 1)
+tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                   const __grid_constant__ TreeArgs a, int box_rows) {
+    using L = Lay<F8, DP, NT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    auto bar = [&](int i) { return base + L::oBar + 8u * i; };
+    volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8);
+    const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const long long limit = a.wait_limit;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::NK; ++i) {
+            mbar_init(bar(L::bKF + i), 1);
+            mbar_init(bar(L::bKE + i), L::kUsers);
+        }
+        for (int i = 0; i < L::NV; ++i) {
+            mbar_init(bar(L::bVF + i), L::kVReaders);
+            mbar_init(bar(L::bVE + i), L::kUsers);
+        }
+        for (int i = 0; i < L::NS; ++i) {
+            mbar_init(bar(L::bSF + i), 1);
+            mbar_init(bar(L::bSE + i), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::bCF + i), 4);
+            mbar_init(bar(L::bCE + i), 4);
+            mbar_init(bar(L::bS + i), 1);
+            mbar_init(bar(L::bSFree + i), 4);
+            mbar_init(bar(L::bP + i), 4);
+            mbar_init(bar(L::bPV + i), 1);
+        }
+        mbar_init(bar(L::bQ), 8);
+        mbar_init(bar(L::bO), 2);
+        for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
+        mbar_init(bar(L::bDrain), 2);
+        *abort_flag = 0;
+        *v_issued = 0;
+        fence_mbar_init();
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(base + L::oMisc, L::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
+    pdl_wait();
+    pdl_trigger();
+
+    Walk w;
+    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
+    const int G = a.group;
+
+    if (warp == kProducerWarp) {
+        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, v_issued);
+    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+        // ---------------------------------------------------------------- products
+        const int g = warp - kMmaWarp;
+        const uint32_t s_col = tmem + g * NT, o_col = tmem + (2 + g) * NT;
+        const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ), p_desc = desc_p<NT>(base + L::oP + g * L::kP);
+        uint32_t base_tile = 0, base_fix = 0, pc = 0, sc = 0, items = 0;
+        bool ok = true;
+        while (ok && walk_next(a, w)) {
+            const int T = w.hi - w.lo;
+            const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
+            ok = warp_wait(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
+            auto qk = [&](int t) {
+                const uint32_t c = base_tile + t, slot = c % L::NK;
+                // the warpgroup has taken this buffer's previous scores
+                ok = (sc == 0 || warp_wait(bar(L::bSFree + g), (sc - 1) & 1u, abort_flag, a.err, limit)) &&
+                     warp_wait(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
+                if (!ok) return;
+                ++sc;
+                tc_fence_after();
+                const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
+                if (elect_one()) {
+                    if (F8) {
+#pragma unroll
+                        for (int i = 0; i < DP / 32; ++i)
+                            tc_mma_f8(s_col, k_desc + 2 * i, q_desc + 2 * i, idesc_e4m3_f32(128, NT), i > 0);
+#pragma unroll
+                        for (int i = 0; i < DP / 32; ++i)
+                            tc_mma_f8(s_col, k_desc + 2 * i, q_desc + NT * 8 + 2 * i, idesc_e4m3_e5m2(128, NT), 1);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i)   // 64-channel halves
+                            tc_mma_bf16(s_col, k_desc + (i / 4) * 1024 + (i % 4) * 2, q_desc + (i / 4) * (NT * 8) + (i % 4) * 2,
+                                        idesc_bf16_f32(128, NT), i > 0);
+                    }
+                    tc_commit(bar(L::bKE + slot));
+                    tc_commit(bar(L::bS + g));
+                }
+                __syncwarp();
+            };
+            if (ok && g < T) qk(g);
+            for (int t = g; ok && t < T; t += 2) {
+                if (t + 2 < T) qk(t + 2);   // while the warpgroup weighs tile t
+                if (!ok) break;
+                const uint32_t c = base_tile + t, slot = c % L::NV;
+                ok = warp_wait(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
+                if (!F8 && ok && w.lo + t >= edge0) {   // V's cleaner has been over it
+                    const uint32_t f = base_fix + (w.lo + t - edge0);
+                    ok = warp_wait(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
+                }
+                ok = ok && warp_wait(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
+                if (!ok) break;
+                ++pc;
+                tc_fence_after();
+                const uint64_t v_desc = desc_mn_sw128(base + L::oV + slot * L::kVSlot, DP == 128 ? kTile * 128u : 0u);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)   // 16 positions: 2 KB of V's blocks, 2 atoms of P
+                        mma_ss_f16(o_col, v_desc + 128 * i, p_desc + (16 * NT * 2 / 16) * i, idesc_vp(NT, F8 ? 0 : 1),
+                                   t >= 2 || i > 0);
+                    tc_commit(bar(L::bVE + slot));
+                    tc_commit(bar(L::bPV + g));
+                }
+                __syncwarp();
+            }
+            if (ok && elect_one()) tc_commit(bar(L::bO));
+            __syncwarp();
+            base_tile += T;
+            base_fix += max(0, w.hi - edge0);
+            ++items;
+        }
+        // every product is done before the CTA leaves
+        if (elect_one()) tc_commit(bar(L::bDrain));
+        __syncwarp();
+        mbar_wait_drain(bar(L::bDrain), 0, kDrain);
+        __syncwarp();
+    } else if (warp >= kAuxWarp) {
+        if constexpr (F8)
+            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag);
+        else
+            clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
+    } else {
+        // ---------------------------------------------------------------- softmax, two warpgroups
+        const int g = warp >> 2, q4 = warp & 3, p = q4 * 32 + lane;   // this thread's position of a tile, and channel of O
+        const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + g * NT, o_addr = tmem + lanes + (2 + g) * NT;
+        float *const cs_s = reinterpret_cast<float *>(smem + L::oCs);
+        float *const m_s = reinterpret_cast<float *>(smem + L::oM) + g * NT;
+        float *const alpha_s = reinterpret_cast<float *>(smem + L::oAlpha) + g * NT;
+        float *const red_s = reinterpret_cast<float *>(smem + L::oRed) + g * 4 * NT;
+        uint64_t *const mask_s = reinterpret_cast<uint64_t *>(smem + L::oMask);
+        const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
+        const volatile float *const sigma_s = reinterpret_cast<const volatile float *>(smem + L::oSigma);
+        uint8_t *const p_buf = smem + L::oP + g * L::kP;
+        uint32_t sc = 0, tiles = 0;   // this warpgroup's tiles; all tiles
+        bool dead = false;            // a wait gave up: only the barriers are kept
+        while (true) {
+            const bool more = walk_next(a, w);
+            // the previous item's shared words have been read; everybody leaves together
+            if (bar_any(1, 256, dead || *abort_flag != 0) || !more) break;
+            const int R = w.s.n * G, T = w.hi - w.lo;
+            {   // Q rows, zeros beyond them; row factors and masks
+                constexpr int C = DP / 8;
+                for (int i = static_cast<int>(threadIdx.x); i < NT * C; i += 256) {
+                    const int c = i % C, row = i / C;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (row < R && c * 8 < a.cache.dim)
+                        x = *reinterpret_cast<const uint4 *>(
+                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
+                            static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+                    float unscale;
+                    store_query<F8, DP>(smem + L::oQ, NT, row, c, x, unscale);
+                    if (c == 0) {
+                        cs_s[row] = a.scale_log2 * unscale;
+                        uint64_t M = 0;
+                        if (row < R) M = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
+                        if (w.s.n < 64) M &= (1ull << w.s.n) - 1ull;
+                        mask_s[row] = M;
+                    }
+                }
+                if (p < NT) m_s[p] = ninf();
+                fence_proxy_async_smem();
+            }
+            warp_arrive(bar(L::bQ));
+            named_barrier(4, 256);
+            float l[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) l[c] = 0.0f;
+            float sigma = 1.0f;
+            for (int t = g; t < T; t += 2) {
+                const int tt = w.lo + t, pos = tt * kTile + p;
+                const bool edge = (tt + 1) * kTile > w.s.ctx;
+                const uint32_t no = tiles + t, sb = no & 1u;
+                float ks = 1.0f, vs = 1.0f, sigma_new = 1.0f;
+                uint32_t x[NT];
+                if (F8 && !dead) dead = !warp_wait(bar(L::bCF + sb), (no >> 1) & 1u, abort_flag, a.err, limit);
+                if (!dead) dead = !warp_wait(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
+                tc_fence_after();
+                tmem_ld_cols<NT>(s_addr, x);
+                if (F8) {
+                    ks = scale_s[sb * 256 + p];
+                    vs = scale_s[sb * 256 + 128 + p];
+                    sigma_new = sigma_s[sb];
+                }
+                tmem_wait_ld();
+                tc_fence_before();
+                if (!dead) {
+                    warp_arrive(bar(L::bSFree + g));
+                    if (F8) warp_arrive(bar(L::bCE + sb));
+                }
+                // scores in log2 units; what a row does not see is -inf
+#pragma unroll
+                for (int c = 0; c < NT; c += 4) {
+                    const float4 k = *reinterpret_cast<const float4 *>(cs_s + c);
+                    const F2 ks2 = f2(ks, ks);
+                    F2 s0 = f2(x[c], x[c + 1]), s1 = f2(x[c + 2], x[c + 3]);
+                    if (F8) {
+                        s0 = f2_mul(s0, ks2);
+                        s1 = f2_mul(s1, ks2);
+                    }
+                    s0 = f2_mul(s0, f2(k.x, k.y));
+                    s1 = f2_mul(s1, f2(k.z, k.w));
+                    float s[4];
+                    f2_get(s0, s[0], s[1]);
+                    f2_get(s1, s[2], s[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[c + i] = __float_as_uint(s[i]);
+                }
+                if (edge) {
+                    const int d = pos - w.s.ctx;   // drafted token; masks have no bits beyond n
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        if (d >= 0 && (d >= 64 || !(mask_s[c] >> d & 1ull))) x[c] = __float_as_uint(ninf());
+                }
+                // any score far above its row's maximum so far?
+                float over = ninf();
+#pragma unroll
+                for (int c = 0; c < NT; c += 4) {
+                    const float4 m = *reinterpret_cast<const float4 *>(m_s + c);
+                    over = fmaxf(fmaxf(over, __uint_as_float(x[c]) - m.x), __uint_as_float(x[c + 1]) - m.y);
+                    over = fmaxf(fmaxf(over, __uint_as_float(x[c + 2]) - m.z), __uint_as_float(x[c + 3]) - m.w);
+                }
+                const bool move = t < 2 || over > kLazy || (F8 && sigma_new != sigma);
+                if (bar_any(2 + g, 128, move)) {
+                    // the columns' maxima over the 128 positions: per warp by reduction of ordered
+                    // integers (NaN, above every number there, is left out), then over the four
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        const float s = __uint_as_float(x[c]);
+                        const int b = static_cast<int>(x[c]);
+                        int key = b ^ (b >> 31 & 0x7fffffff);
+                        if (s != s) key = 0x807fffff;   // as -inf
+                        key = __reduce_max_sync(0xFFFFFFFFu, key);
+                        if (lane == (c & 31)) red_s[q4 * NT + c] = __int_as_float(key ^ (key >> 31 & 0x7fffffff));
+                    }
+                    named_barrier(2 + g, 128);
+                    if (p < NT) {
+                        const float old = m_s[p];
+                        const float mn = fmaxf(fmaxf(old, fmaxf(red_s[p], red_s[NT + p])), fmaxf(red_s[2 * NT + p], red_s[3 * NT + p]));
+                        m_s[p] = mn;
+                        alpha_s[p] = mn == ninf() ? 1.0f : ex2(old - mn);
+                    }
+                    named_barrier(2 + g, 128);
+                    if (t >= 2) {
+                        // O so far is complete when the previous product is
+                        if (!dead) dead = !warp_wait(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
+                        tc_fence_after();
+                        const float f = F8 ? sigma / sigma_new : 1.0f;
+                        uint32_t o[NT];
+                        tmem_ld_cols<NT>(o_addr, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < NT; ++c) {
+                            const float k = alpha_s[c];
+                            l[c] *= k;
+                            o[c] = __float_as_uint(__uint_as_float(o[c]) * (k * f));
+                        }
+                        tmem_st_cols<NT>(o_addr, o);
+                        tmem_wait_st();
+                    }
+                    sigma = sigma_new;
+                }
+                // the weights' buffer is free when the previous product has read it
+                if (t >= 2 && !dead) dead = !warp_wait(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
+#pragma unroll
+                for (int c8 = 0; c8 < NT / 8; ++c8) {
+                    uint32_t out[4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int c = c8 * 8 + h * 4;
+                        const float4 m = *reinterpret_cast<const float4 *>(m_s + c);
+                        // a row that has seen nothing yet: every weight is 0
+                        const float r0 = m.x == ninf() ? 0.0f : m.x, r1 = m.y == ninf() ? 0.0f : m.y;
+                        const float r2 = m.z == ninf() ? 0.0f : m.z, r3 = m.w == ninf() ? 0.0f : m.w;
+                        float w0 = ex2(__uint_as_float(x[c]) - r0), w1 = ex2(__uint_as_float(x[c + 1]) - r1);
+                        float w2 = ex2(__uint_as_float(x[c + 2]) - r2), w3 = ex2(__uint_as_float(x[c + 3]) - r3);
+                        l[c] += w0;
+                        l[c + 1] += w1;
+                        l[c + 2] += w2;
+                        l[c + 3] += w3;
+                        if (F8) {
+                            w0 *= vs;
+                            w1 *= vs;
+                            w2 *= vs;
+                            w3 *= vs;
+                        }
+                        out[2 * h] = pack2(w0, w1, F8);
+                        out[2 * h + 1] = pack2(w2, w3, F8);
+                    }
+                    *reinterpret_cast<uint4 *>(p_buf + p_chunk<NT>(p, c8)) = make_uint4(out[0], out[1], out[2], out[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                if (!dead) warp_arrive(bar(L::bP + g));
+                ++sc;
+            }
+            // ------------------------------------------------------------ the item's end
+            if (!dead) dead = !warp_wait(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
+            tc_fence_after();
+            tiles += T;
+            warp_columns<NT>(l, lane);
+            if constexpr (NT == 16) {
+                if ((lane & 1) == 0) red_s[q4 * NT + lane / 2] = l[0];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NT / 32; ++i) red_s[q4 * NT + lane * (NT / 32) + i] = l[i];
+            }
+            if (lane == 0 && q4 == 0) cs_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // the accumulator's unit
+            named_barrier(4, 256);
+            const bool second = T > 1;   // the second warpgroup had a tile
+            const float *const m0_s = reinterpret_cast<const float *>(smem + L::oM), *const m1_s = m0_s + NT;
+            const float *const red0 = reinterpret_cast<const float *>(smem + L::oRed), *const red1 = red0 + 4 * NT;
+            float *const w0_s = reinterpret_cast<float *>(smem + L::oAlpha), *const w1_s = w0_s + NT;
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
+            if (threadIdx.x < NT) {
+                const int c = static_cast<int>(threadIdx.x);
+                const float ma = m0_s[c], mb = second ? m1_s[c] : ninf();
+                const float mm = fmaxf(ma, mb), ref = mm == ninf() ? 0.0f : mm;
+                const float ka = ex2(ma - ref), kb = ex2(mb - ref);
+                float ll = (red0[c] + red0[NT + c] + red0[2 * NT + c] + red0[3 * NT + c]) * ka;
+                if (second) ll += (red1[c] + red1[NT + c] + red1[2 * NT + c] + red1[3 * NT + c]) * kb;
+                const bool none = mm == ninf() && ll == 0.0f;
+                const float inv = !w.whole ? 1.0f : (none ? 0.0f : 1.0f / ll);
+                w0_s[c] = ka * cs_s[0] * inv;
+                w1_s[c] = second ? kb * cs_s[1] * inv : 0.0f;
+                if (c < R) {
+                    if (!w.whole)
+                        narrow_ml<DP>(a, gridDim.x, slot)[c] = make_float2(mm, ll);
+                    else if (a.lse != nullptr)
+                        a.lse[static_cast<int64_t>(w.s.t0 + c / G) * a.q.heads + w.hk * G + c % G] =
+                            none ? ninf() : (mm + log2f(ll)) * 0.69314718055994531f;
+                }
+            }
+            named_barrier(4, 256);
+            // a warpgroup writes half of the rows, a thread one channel of them
+            constexpr int H = NT / 2;
+            uint32_t oa[H], ob[H];
+            if constexpr (H == 8) {
+                tmem_ld8(tmem + lanes + 2 * NT + g * H, oa);
+                tmem_ld8(tmem + lanes + 3 * NT + g * H, ob);
+            } else {
+                tmem_ld_cols<H>(tmem + lanes + 2 * NT + g * H, oa);
+                tmem_ld_cols<H>(tmem + lanes + 3 * NT + g * H, ob);
+            }
+            tmem_wait_ld();
+            tc_fence_before();   // the next item's products follow this warp's arrival on bQ
+            const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
+            uint32_t any_bad = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+            if (p < a.cache.dim) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int c = g * H + i;
+                    float o = __uint_as_float(oa[i]) * w0_s[c];
+                    if (second) o = fmaf(__uint_as_float(ob[i]), w1_s[c], o);
+                    oa[i] = __float_as_uint(o);
+                }
+                if (any_bad != 0) {   // non-finite values of drafted tokens, for the rows that see them
+                    for (int tt = max(w.lo, w.s.ctx / kTile); tt < w.hi; ++tt)
+                        for (int j = 0; j < kTile; ++j) {
+                            if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u)) continue;
+                            const float v = value_at<F8>(a, w.b, w.hk, tt * kTile + j, p);
+                            if (fabsf(v) <= 3.4028234e38f) continue;
+                            const int d = tt * kTile + j - w.s.ctx;   // only drafted tokens are marked
+#pragma unroll
+                            for (int i = 0; i < H; ++i)
+                                if (mask_s[g * H + i] >> d & 1ull) oa[i] = __float_as_uint(__uint_as_float(oa[i]) + v);
+                        }
+                }
+                if (w.whole) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        const int c = g * H + i;
+                        if (c < R)
+                            static_cast<__nv_bfloat16 *>(a.out.ptr)[static_cast<int64_t>(w.s.t0 + c / G) * a.out.token_stride +
+                                                                    static_cast<int64_t>(w.hk * G + c % G) * a.out.head_stride + p] =
+                                __float2bfloat16_rn(__uint_as_float(oa[i]));
+                    }
+                } else {
+                    float *const po = narrow_out<DP>(a, slot) + p;
+#pragma unroll
+                    for (int i = 0; i < H; ++i)
+                        if (g * H + i < R) po[(g * H + i) * DP] = __uint_as_float(oa[i]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmem);
+    }
+}
+
+std::mutex g_mu;
+bool g_set[64][12];
+
+template <bool F8, int DP, int NT>
+cudaError_t launch(const TreeArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                   cudaStream_t s, bool pdl) {
+    using L = Lay<F8, DP, NT>;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        bool &set = g_set[dev & 63][(F8 ? 6 : 0) + (DP == 128 ? 3 : 0) + (NT == 16 ? 0 : NT / 32)];
+        if (!set) {
+            const cudaError_t e = cudaFuncSetAttribute(tree_narrow_kernel<F8, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+            if (e != cudaSuccess) return e;
+            set = true;
+        }
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_narrow_kernel<F8, DP, NT>, tm_k, tm_v, a, rows);
+}
+
+template <bool F8, int DP>
+cudaError_t by_rows(const TreeArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                    cudaStream_t s, bool pdl) {
+    const int R = a.max_tokens * a.group;
+    if (R <= 16) return launch<F8, DP, 16>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+    if (R <= 32) return launch<F8, DP, 32>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+    return launch<F8, DP, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_narrow(const TreeArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_k,
+                               const CUtensorMap &tm_v, cudaStream_t s, bool pdl) {
+    const bool f8 = a.cache.dtype == MOE_E4M3;
+    if (a.cache.dim <= 64)
+        return f8 ? by_rows<true, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : by_rows<false, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+    return f8 ? by_rows<true, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : by_rows<false, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
+}
+
+}  // namespace moe

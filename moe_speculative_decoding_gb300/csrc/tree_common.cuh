@@ -50,6 +50,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit A and B, fp32 D.
@@ -280,12 +286,16 @@ __device__ __forceinline__ float2 *part_ml(const TreeArgs &a, int ctas, int slot
            (static_cast<size_t>(slot) * 2 + mt) * kTile;
 }
 
-// Element offset of the row of position pos of sequence b, head hk; -1 for a page outside the cache.
-__device__ __forceinline__ int64_t row_offset(const TreeArgs &a, int b, int hk, int pos, int &page, int &at) {
-    page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / a.cache.page];
-    at = pos % a.cache.page;
-    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return -1;
-    return page * a.cache.page_stride + at * a.cache.token_stride + hk * a.cache.head_stride;
+// The kernel for few rows: [slot][64 rows][DP] fp32, then [slot][64] (maximum, sum).
+constexpr int kNarrowRows = 64;
+template <int DP>
+__device__ __forceinline__ float *narrow_out(const TreeArgs &a, int slot) {
+    return static_cast<float *>(a.part) + static_cast<size_t>(slot) * kNarrowRows * DP;
+}
+template <int DP>
+__device__ __forceinline__ float2 *narrow_ml(const TreeArgs &a, int ctas, int slot) {
+    return reinterpret_cast<float2 *>(static_cast<float *>(a.part) + static_cast<size_t>(ctas) * 2 * kNarrowRows * DP) +
+           static_cast<size_t>(slot) * kNarrowRows;
 }
 
 // Which of the 128 positions of tile tt a row sees: bit j of word j / 32.  M: the row's tree mask.
@@ -320,6 +330,57 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(codes)));
     return h;
+}
+
+// Channel ch of the value at position pos of sequence b, cache head hk, as the cache has it (0 for a
+// page outside the cache).
+template <bool F8>
+__device__ __forceinline__ float value_at(const TreeArgs &a, int b, int hk, int pos, int ch) {
+    const moe_kv_cache_t &c = a.cache;
+    const int page = a.page_table[static_cast<int64_t>(b) * a.max_pages + pos / c.page], at = pos % c.page;
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(c.pages)) return 0.0f;
+    const int64_t off = page * c.page_stride + at * c.token_stride + hk * c.head_stride + ch;
+    if (F8)
+        return f16_of(e4m3x2_to_f16x2(static_cast<const uint8_t *>(c.v)[off])) *
+               c.v_scale[(static_cast<int64_t>(page) * c.heads + hk) * c.page + at];
+    return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(c.v)[off]) << 16);
+}
+
+// Stores chunk c (8 channels) of a query row into a K-major operand of `rows` rows.  bf16: blocks of
+// 64 channels, rows * 128 bytes each.  F8: the row, scaled by a power of two to at most 256, as an
+// e4m3 operand and, rows * 128 bytes on, the e5m2 remainder; unscale is the inverse factor (NaN for
+// a row that is not finite).  The DP / 8 lanes of a row call together.
+template <bool F8, int DP>
+__device__ __forceinline__ void store_query(uint8_t *q, int rows, int row, int c, uint4 x, float &unscale) {
+    unscale = 1.0f;
+    if (!F8) {
+        *reinterpret_cast<uint4 *>(q + (c / 8) * (rows * 128) + row * 128 + (((c % 8) ^ (row & 7)) * 16)) = x;
+        return;
+    }
+    // the row's largest exponent (bf16 magnitudes order as integers)
+    const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = max(top, max(wd[k] & 0x7FFFu, wd[k] >> 16 & 0x7FFFu));
+#pragma unroll
+    for (int o = DP / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const int e = static_cast<int>(top >> 7);   // biased exponent; 255: not finite
+    // up = 2^(7 - (e - 127)): the largest lands in [128, 256); both factors' exponents in range
+    const int ub = min(max(261 - e, 1), 253);
+    const float up = __int_as_float(ub << 23);
+    unscale = e == 255 ? __int_as_float(0x7fffffff) : __int_as_float((254 - ub) << 23);
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float x0 = bf16_lo(wd[k]) * up, x1 = bf16_hi(wd[k]) * up;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi[k]) : "f"(x1), "f"(x0));
+        const uint32_t h = e4m3x2_to_f16x2(hi[k]);
+        const float r0 = x0 - f16_of(h), r1 = x1 - f16_of(h >> 16);
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo[k]) : "f"(r1), "f"(r0));
+    }
+    uint8_t *const p = q + row * 128 + (((c / 2) ^ (row & 7)) * 16) + (c & 1) * 8;
+    *reinterpret_cast<uint2 *>(p) = make_uint2(hi[0] | static_cast<uint32_t>(hi[1]) << 16, hi[2] | static_cast<uint32_t>(hi[3]) << 16);
+    *reinterpret_cast<uint2 *>(p + rows * 128) = make_uint2(lo[0] | static_cast<uint32_t>(lo[1]) << 16, lo[2] | static_cast<uint32_t>(lo[3]) << 16);
 }
 
 // ------------------------------------------------------------------ roles

@@ -241,7 +241,10 @@ def test_device_errors(cache):
     out = torch.full_like(args["q"], 5.0)
     api.tree_attention(**args, out=out, ws=ws, max_tokens=6)
     assert api.last_device_error(ws) == 5
-    assert bool((out[:10] == 5).all()) and torch.equal(out[10:], base[10:])
+    # a smaller bound may run on the kernel for few rows: the others are held to the reference
+    ref, _, ob, _ = p.reference(weight_eps(p), True)
+    assert bool((out[:10] == 5).all())
+    assert_within("out", out[10:], ref[10:], ob[10:])
     for bad in (-3, 10 ** 6):
         table = args["page_table"].clone()
         table[0, 2] = bad
