@@ -65,10 +65,10 @@ struct Lay {
     static constexpr uint32_t oK = 2 * kQTile, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot;
     static constexpr uint32_t oSSc = oS + NS * kStage;             // F8: float [NS][ks, vs][128], landing
     static constexpr uint32_t oBar = oSSc + NS * 1024;
-    // barriers: k_full, k_empty, v_full, v_empty, st_full, st_empty, sc_full[2], sc_empty[2],
+    // barriers: k_full, k_empty, v_full, v_empty, st_full, st_empty, sc_full[2],
     // s_full[2], p_ready[2], q_ready, o_full, v_fix[4], drain
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
-                         bCE = bCF + 2, bS = bCE + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
+                         bS = bCF + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
                          bDrain = bFix + 4, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
     static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
@@ -190,7 +190,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8);
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 1;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -210,7 +210,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::bCF + i), 4);
-            mbar_init(bar(L::bCE + i), 8);
             mbar_init(bar(L::bS + i), 1);
             mbar_init(bar(L::bP + i), 4);
         }
@@ -220,6 +219,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(L::bDrain), 2);
         *abort_flag = 0;
         *v_issued = 0;
+        *k_issued = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -240,7 +240,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int G = a.group;
 
     if (warp == kProducerWarp) {
-        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, v_issued);
+        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in
@@ -253,11 +253,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const bool two = w.s.n * G - w.pair * 2 * kTile > kTile;
             const int T = w.hi - w.lo, U = two ? 2 * T : T;
             const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
-            ok = warp_wait(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
+            ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
             const uint64_t q_desc = desc_kmajor_sw128(base + (two ? g : 0) * L::kQTile);
             auto qk = [&](int u) {
                 const uint32_t c = base_tile + (two ? u >> 1 : u), slot = c % L::NK;
-                ok = warp_wait(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
+                ok = wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
@@ -286,12 +286,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int u = g; ok && u < U; u += 2) {
                 const int t = two ? u >> 1 : u, tt = w.lo + t;
                 const uint32_t c = base_tile + t, slot = c % L::NV;
-                ok = warp_wait(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
+                ok = wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
                 if (!F8 && ok && tt >= edge0) {   // V's cleaner has been over it
                     const uint32_t f = base_fix + (tt - edge0);
-                    ok = warp_wait(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
+                    ok = wait_for(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
                 }
-                ok = ok && warp_wait(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
+                ok = ok && wait_for(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 ++pc;
                 tc_fence_after();
@@ -319,7 +319,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         __syncwarp();
     } else if (warp >= kAuxWarp) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag);
+            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag, v_issued);
         else
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
     } else {
@@ -374,8 +374,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (edge) seen_bits(M, w.s, tt, see);
                 const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no & 1u;
                 const float *const ks = scale_s + sb * 256, *const vs = ks + 128;
-                if (F8 && !(ok = warp_wait(bar(L::bCF + sb), (tile_no >> 1) & 1u, abort_flag, a.err, limit))) break;
-                if (!(ok = warp_wait(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
+                if (F8 && !(ok = wait_for(bar(L::bCF + sb), (tile_no >> 1) & 1u, abort_flag, a.err, limit))) break;
+                if (!(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
                 ++sc;
                 tc_fence_after();
                 float mx = edge ? tile_max<F8, true>(s_addr, ks, see) : tile_max<F8, false>(s_addr, ks, see);
@@ -409,10 +409,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(bar(L::bP + g));
-                if (F8) warp_arrive_cnt(bar(L::bCE + sb), two ? 1 : 2);
             }
             // ------------------------------------------------------------ the item's end
-            ok = ok && warp_wait(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
+            ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             scnt += T;
             const float gain = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator

@@ -24,7 +24,7 @@
 namespace moe {
 namespace {
 
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kAuxWarp = 11;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 11, kAuxWarp = 12;
 
 template <bool F8, int DP, int NT>
 struct Lay {
@@ -34,31 +34,38 @@ struct Lay {
     static constexpr uint32_t kStage = F8 ? 16384 : 0;
     static constexpr uint32_t kQ = F8 ? 2 * NT * 128 : DP / 64 * NT * 128;
     static constexpr uint32_t kP = 128 * NT * 2;   // weights of a tile: a row of NT per position
-    // even rings: a product warp takes every other tile, all uses of its slots
-    static constexpr int NK = F8 || DP == 64 ? 4 : 2, NV = !F8 && DP == 64 ? 4 : 2;
-    static constexpr int NS = !F8 ? 0 : (NT == 64 && DP == 128 ? 2 : 4);
+    // What fits.  A product warp takes every other tile, so within an item, with an even ring, the
+    // slots it waits for are its own and their parities name the use.  An item's first tiles, and a
+    // ring of 3, may wait on a slot the other warp is not done with: there k_issued and v_issued,
+    // which the filler sets when the previous use is over, are waited for first.
+    static constexpr int NK = DP == 64 ? 4 : (F8 && NT < 64 ? 4 : 2);
+    static constexpr int NV = F8 ? 2 : (DP == 64 ? 4 : (NT < 64 ? 3 : 2));
+    static constexpr int NS = !F8 ? 0 : (DP == 64 ? 4 : 3) - (NT < 64 ? 0 : 1);
     static constexpr int kUsers = 1, kVReaders = F8 ? 4 : 1;
     static constexpr uint32_t oK = 0, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot, oP = oS + NS * kStage,
-                              oQ = oP + 2 * kP, oSSc = oQ + kQ, oBar = oSSc + NS * 1024;
+                              oQ = oP + 2 * kP, oSSc = oQ + 2 * kQ, oBar = oSSc + NS * 1024;
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
-                         bCE = bCF + 2, bS = bCE + 2, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
-                         bO = bQ + 1, bFix = bO + 1, bDrain = bFix + 4, kBars = bDrain + 1;
+                         bS = bCF + 2, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
+                         bQE = bQ + 2, bO = bQE + 2, bOF = bO + 1, bFix = bOF + 1, bDrain = bFix + 4, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
     static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);   // F8: float [2]
-    static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // float [NT]: score to log2 units
-    static constexpr uint32_t oM = oCs + NT * 4;                   // float [2][NT]: maxima of a warpgroup
+    static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // F8: float [2 items][NT]: score to log2 units
+    static constexpr uint32_t oM = oCs + (F8 ? 2 * NT * 4 : 0);    // float [2][NT]: minus the maxima of a warpgroup
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
     static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
-    static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
-    static constexpr uint32_t kSmem = oMask + NT * 8;
+    static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [2 items][NT]: the rows' tree masks
+    static constexpr uint32_t oUnit = oMask + 2 * NT * 8;          // float [2]: a warpgroup's accumulator unit
+    static constexpr uint32_t kSmem = oUnit + 16;
     static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
 // The weights' operand [128 positions][NT], MN-major, rows of NT * 2 = 32, 64 or 128 bytes with the
 // swizzle of that width: 16-byte chunk ^= the row's index within an atom of 8, at that granularity.
+constexpr float kNone = -3.0e38f;   // the maximum of a row that has seen nothing: below every score, finite
+
 template <int NT>
 __device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
     constexpr uint64_t mode = NT == 64 ? 2 : (NT == 32 ? 4 : 6);
@@ -143,7 +150,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8);
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 1;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -163,18 +170,22 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::bCF + i), 4);
-            mbar_init(bar(L::bCE + i), 4);
             mbar_init(bar(L::bS + i), 1);
             mbar_init(bar(L::bSFree + i), 4);
             mbar_init(bar(L::bP + i), 4);
             mbar_init(bar(L::bPV + i), 1);
         }
-        mbar_init(bar(L::bQ), 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::bQ + i), 1);
+            mbar_init(bar(L::bQE + i), 8);
+        }
+        mbar_init(bar(L::bOF), 8);
         mbar_init(bar(L::bO), 2);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
         *abort_flag = 0;
         *v_issued = 0;
+        *k_issued = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -195,23 +206,25 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int G = a.group;
 
     if (warp == kProducerWarp) {
-        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, v_issued);
+        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         const int g = warp - kMmaWarp;
         const uint32_t s_col = tmem + g * NT, o_col = tmem + (2 + g) * NT;
-        const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ), p_desc = desc_p<NT>(base + L::oP + g * L::kP);
+        const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
         uint32_t base_tile = 0, base_fix = 0, pc = 0, sc = 0, items = 0;
         bool ok = true;
         while (ok && walk_next(a, w)) {
             const int T = w.hi - w.lo;
             const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
-            ok = warp_wait(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
+            const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ + (items & 1u) * L::kQ);
+            ok = wait_for(bar(L::bQ + (items & 1u)), (items >> 1) & 1u, abort_flag, a.err, limit);
             auto qk = [&](int t) {
                 const uint32_t c = base_tile + t, slot = c % L::NK;
                 // the warpgroup has taken this buffer's previous scores
-                ok = (sc == 0 || warp_wait(bar(L::bSFree + g), (sc - 1) & 1u, abort_flag, a.err, limit)) &&
-                     warp_wait(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
+                ok = (sc == 0 || wait_for(bar(L::bSFree + g), (sc - 1) & 1u, abort_flag, a.err, limit)) &&
+                     (t >= L::NK || wait_count(k_issued, c + 1, abort_flag, a.err, limit)) &&
+                     wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
                 if (!ok) return;
                 ++sc;
                 tc_fence_after();
@@ -240,12 +253,16 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (t + 2 < T) qk(t + 2);   // while the warpgroup weighs tile t
                 if (!ok) break;
                 const uint32_t c = base_tile + t, slot = c % L::NV;
-                ok = warp_wait(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
+                ok = ((L::NV % 2 == 0 && t >= L::NV) || wait_count(v_issued, c + 1, abort_flag, a.err, limit)) &&
+                     wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
                 if (!F8 && ok && w.lo + t >= edge0) {   // V's cleaner has been over it
                     const uint32_t f = base_fix + (w.lo + t - edge0);
-                    ok = warp_wait(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
+                    ok = wait_for(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
                 }
-                ok = ok && warp_wait(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
+                // O of the previous item has been read (both product warps pass here or in an item's
+                // first weights, which the same warpgroups form later)
+                if (ok && t == g && items > 0) ok = wait_for(bar(L::bOF), (items - 1) & 1u, abort_flag, a.err, limit);
+                ok = ok && wait_for(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 ++pc;
                 tc_fence_after();
@@ -271,9 +288,51 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         __syncwarp();
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
+    } else if (warp == kQueryWarp) {
+        // ---------------------------------------------------------------- queries, an item ahead
+        uint64_t *const mask_all = reinterpret_cast<uint64_t *>(smem + L::oMask);
+        float *const cs_all = reinterpret_cast<float *>(smem + L::oCs);
+        bool ok = true;
+        while (ok && walk_next(a, w)) {
+            const uint32_t qb = w.index & 1u;
+            const int R = w.s.n * G;
+            constexpr int C = DP / 8, PER = 32 / C;   // lanes of a row, rows of a step
+            const int c = lane % C;
+            uint4 x[NT / PER];
+#pragma unroll
+            for (int i = 0; i < NT / PER; ++i) {   // in flight before the buffer is free
+                const int row = i * PER + lane / C;
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (row < R && c * 8 < a.cache.dim)
+                    x[i] = *reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
+                        static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+            }
+            uint64_t M[(NT + 31) / 32];
+#pragma unroll
+            for (int i = 0; i < (NT + 31) / 32; ++i) {
+                const int row = i * 32 + lane;
+                M[i] = 0;
+                if (row < R) M[i] = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
+                if (w.s.n < 64) M[i] &= (1ull << w.s.n) - 1ull;
+            }
+            if (!(ok = wait_for(bar(L::bQE + qb), ((w.index >> 1) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
+#pragma unroll
+            for (int i = 0; i < NT / PER; ++i) {
+                const int row = i * PER + lane / C;
+                float unscale;
+                store_query<F8, DP>(smem + L::oQ + qb * L::kQ, NT, row, c, x[i], unscale);
+                if (F8 && c == 0) cs_all[qb * NT + row] = a.scale_log2 * unscale;
+            }
+#pragma unroll
+            for (int i = 0; i < (NT + 31) / 32; ++i)
+                if (i * 32 + lane < NT) mask_all[qb * NT + i * 32 + lane] = M[i];
+            fence_proxy_async_smem();
+            warp_arrive(bar(L::bQ + qb));
+        }
     } else if (warp >= kAuxWarp) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag);
+            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag, v_issued);
         else
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
     } else {
@@ -281,13 +340,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const int g = warp >> 2, q4 = warp & 3, p = q4 * 32 + lane;   // this thread's position of a tile, and channel of O
         const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t s_addr = tmem + lanes + g * NT, o_addr = tmem + lanes + (2 + g) * NT;
-        float *const cs_s = reinterpret_cast<float *>(smem + L::oCs);
-        float *const m_s = reinterpret_cast<float *>(smem + L::oM) + g * NT;
+        float *const nm_s = reinterpret_cast<float *>(smem + L::oM) + g * NT;
         float *const alpha_s = reinterpret_cast<float *>(smem + L::oAlpha) + g * NT;
         float *const red_s = reinterpret_cast<float *>(smem + L::oRed) + g * 4 * NT;
-        uint64_t *const mask_s = reinterpret_cast<uint64_t *>(smem + L::oMask);
         const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
         const volatile float *const sigma_s = reinterpret_cast<const volatile float *>(smem + L::oSigma);
+        float *const unit_s = reinterpret_cast<float *>(smem + L::oUnit);
         uint8_t *const p_buf = smem + L::oP + g * L::kP;
         uint32_t sc = 0, tiles = 0;   // this warpgroup's tiles; all tiles
         bool dead = false;            // a wait gave up: only the barriers are kept
@@ -296,33 +354,15 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             // the previous item's shared words have been read; everybody leaves together
             if (bar_any(1, 256, dead || *abort_flag != 0) || !more) break;
             const int R = w.s.n * G, T = w.hi - w.lo;
-            {   // Q rows, zeros beyond them; row factors and masks
-                constexpr int C = DP / 8;
-                for (int i = static_cast<int>(threadIdx.x); i < NT * C; i += 256) {
-                    const int c = i % C, row = i / C;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < R && c * 8 < a.cache.dim)
-                        x = *reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
-                            static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
-                    float unscale;
-                    store_query<F8, DP>(smem + L::oQ, NT, row, c, x, unscale);
-                    if (c == 0) {
-                        cs_s[row] = a.scale_log2 * unscale;
-                        uint64_t M = 0;
-                        if (row < R) M = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
-                        if (w.s.n < 64) M &= (1ull << w.s.n) - 1ull;
-                        mask_s[row] = M;
-                    }
-                }
-                if (p < NT) m_s[p] = ninf();
-                fence_proxy_async_smem();
-            }
-            warp_arrive(bar(L::bQ));
-            named_barrier(4, 256);
-            float l[NT];
+            const uint32_t qb = w.index & 1u;
+            const float *const cs_s = reinterpret_cast<const float *>(smem + L::oCs) + qb * NT;
+            const uint64_t *const mask_s = reinterpret_cast<const uint64_t *>(smem + L::oMask) + qb * NT;
+            if (p < NT) nm_s[p] = -kNone;
+            dead = !wait_for(bar(L::bQ + qb), (w.index >> 1) & 1u, abort_flag, a.err, limit);
+            named_barrier(2 + g, 128);
+            F2 l2[NT / 2];
 #pragma unroll
-            for (int c = 0; c < NT; ++c) l[c] = 0.0f;
+            for (int c = 0; c < NT / 2; ++c) l2[c] = f2(0.0f, 0.0f);
             float sigma = 1.0f;
             for (int t = g; t < T; t += 2) {
                 const int tt = w.lo + t, pos = tt * kTile + p;
@@ -330,33 +370,30 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint32_t no = tiles + t, sb = no & 1u;
                 float ks = 1.0f, vs = 1.0f, sigma_new = 1.0f;
                 uint32_t x[NT];
-                if (F8 && !dead) dead = !warp_wait(bar(L::bCF + sb), (no >> 1) & 1u, abort_flag, a.err, limit);
-                if (!dead) dead = !warp_wait(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
+                if (F8 && !dead) dead = !wait_for(bar(L::bCF + sb), (no >> 1) & 1u, abort_flag, a.err, limit);
+                if (!dead) dead = !wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
                 tc_fence_after();
                 tmem_ld_cols<NT>(s_addr, x);
                 if (F8) {
                     ks = scale_s[sb * 256 + p];
                     vs = scale_s[sb * 256 + 128 + p];
                     sigma_new = sigma_s[sb];
+                } else {
+                    ks = a.scale_log2;
                 }
                 tmem_wait_ld();
                 tc_fence_before();
-                if (!dead) {
-                    warp_arrive(bar(L::bSFree + g));
-                    if (F8) warp_arrive(bar(L::bCE + sb));
-                }
+                if (!dead) warp_arrive(bar(L::bSFree + g));
                 // scores in log2 units; what a row does not see is -inf
+                const F2 ks2 = f2(ks, ks);
 #pragma unroll
                 for (int c = 0; c < NT; c += 4) {
-                    const float4 k = *reinterpret_cast<const float4 *>(cs_s + c);
-                    const F2 ks2 = f2(ks, ks);
-                    F2 s0 = f2(x[c], x[c + 1]), s1 = f2(x[c + 2], x[c + 3]);
+                    F2 s0 = f2_mul(f2(x[c], x[c + 1]), ks2), s1 = f2_mul(f2(x[c + 2], x[c + 3]), ks2);
                     if (F8) {
-                        s0 = f2_mul(s0, ks2);
-                        s1 = f2_mul(s1, ks2);
+                        const float4 k = *reinterpret_cast<const float4 *>(cs_s + c);
+                        s0 = f2_mul(s0, f2(k.x, k.y));
+                        s1 = f2_mul(s1, f2(k.z, k.w));
                     }
-                    s0 = f2_mul(s0, f2(k.x, k.y));
-                    s1 = f2_mul(s1, f2(k.z, k.w));
                     float s[4];
                     f2_get(s0, s[0], s[1]);
                     f2_get(s1, s[2], s[3]);
@@ -365,19 +402,27 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 if (edge) {
                     const int d = pos - w.s.ctx;   // drafted token; masks have no bits beyond n
+                    if (d >= 0) {
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        if (d >= 0 && (d >= 64 || !(mask_s[c] >> d & 1ull))) x[c] = __float_as_uint(ninf());
+                        for (int c = 0; c < NT; ++c)
+                            if (d >= 64 || !(mask_s[c] >> d & 1ull)) x[c] = __float_as_uint(ninf());
+                    }
                 }
-                // any score far above its row's maximum so far?
-                float over = ninf();
+                // any score far above its row's maximum so far?  (That is kNone before a row has
+                // seen anything, so that its first finite score is.)
+                bool move = t < 2 || (F8 && sigma_new != sigma);
+                if (t >= 2) {
+                    float over = ninf();
 #pragma unroll
-                for (int c = 0; c < NT; c += 4) {
-                    const float4 m = *reinterpret_cast<const float4 *>(m_s + c);
-                    over = fmaxf(fmaxf(over, __uint_as_float(x[c]) - m.x), __uint_as_float(x[c + 1]) - m.y);
-                    over = fmaxf(fmaxf(over, __uint_as_float(x[c + 2]) - m.z), __uint_as_float(x[c + 3]) - m.w);
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 n = *reinterpret_cast<const float4 *>(nm_s + c);
+                        float d0, d1, d2, d3;
+                        f2_get(f2_add(f2(x[c], x[c + 1]), f2(n.x, n.y)), d0, d1);
+                        f2_get(f2_add(f2(x[c + 2], x[c + 3]), f2(n.z, n.w)), d2, d3);
+                        over = fmaxf(fmaxf(over, d0), fmaxf(d1, fmaxf(d2, d3)));
+                    }
+                    move = move || over > kLazy;
                 }
-                const bool move = t < 2 || over > kLazy || (F8 && sigma_new != sigma);
                 if (bar_any(2 + g, 128, move)) {
                     // the columns' maxima over the 128 positions: per warp by reduction of ordered
                     // integers (NaN, above every number there, is left out), then over the four
@@ -386,61 +431,63 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         const float s = __uint_as_float(x[c]);
                         const int b = static_cast<int>(x[c]);
                         int key = b ^ (b >> 31 & 0x7fffffff);
-                        if (s != s) key = 0x807fffff;   // as -inf
+                        if (s != s) key = static_cast<int>(0x807fffffu);   // as -inf
                         key = __reduce_max_sync(0xFFFFFFFFu, key);
                         if (lane == (c & 31)) red_s[q4 * NT + c] = __int_as_float(key ^ (key >> 31 & 0x7fffffff));
                     }
                     named_barrier(2 + g, 128);
                     if (p < NT) {
-                        const float old = m_s[p];
+                        const float old = -nm_s[p];
                         const float mn = fmaxf(fmaxf(old, fmaxf(red_s[p], red_s[NT + p])), fmaxf(red_s[2 * NT + p], red_s[3 * NT + p]));
-                        m_s[p] = mn;
-                        alpha_s[p] = mn == ninf() ? 1.0f : ex2(old - mn);
+                        nm_s[p] = -mn;
+                        alpha_s[p] = ex2(old - mn);
                     }
                     named_barrier(2 + g, 128);
                     if (t >= 2) {
                         // O so far is complete when the previous product is
-                        if (!dead) dead = !warp_wait(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
+                        if (!dead) dead = !wait_for(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
                         tc_fence_after();
                         const float f = F8 ? sigma / sigma_new : 1.0f;
-                        uint32_t o[NT];
-                        tmem_ld_cols<NT>(o_addr, o);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < NT; ++c) {
-                            const float k = alpha_s[c];
-                            l[c] *= k;
-                            o[c] = __float_as_uint(__uint_as_float(o[c]) * (k * f));
+                        for (int c0 = 0; c0 < NT; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld_16_async(o_addr + c0, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 16; c += 2) {
+                                const float2 k = *reinterpret_cast<const float2 *>(alpha_s + c0 + c);
+                                l2[(c0 + c) / 2] = f2_mul(l2[(c0 + c) / 2], f2(k.x, k.y));
+                                o[c] = __float_as_uint(__uint_as_float(o[c]) * (k.x * f));
+                                o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * (k.y * f));
+                            }
+                            tmem_st16(o_addr + c0, o);
                         }
-                        tmem_st_cols<NT>(o_addr, o);
                         tmem_wait_st();
                     }
                     sigma = sigma_new;
                 }
                 // the weights' buffer is free when the previous product has read it
-                if (t >= 2 && !dead) dead = !warp_wait(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
+                if (t >= 2 && !dead) dead = !wait_for(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
+                const F2 vs2 = f2(vs, vs);
 #pragma unroll
                 for (int c8 = 0; c8 < NT / 8; ++c8) {
                     uint32_t out[4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int c = c8 * 8 + h * 4;
-                        const float4 m = *reinterpret_cast<const float4 *>(m_s + c);
-                        // a row that has seen nothing yet: every weight is 0
-                        const float r0 = m.x == ninf() ? 0.0f : m.x, r1 = m.y == ninf() ? 0.0f : m.y;
-                        const float r2 = m.z == ninf() ? 0.0f : m.z, r3 = m.w == ninf() ? 0.0f : m.w;
-                        float w0 = ex2(__uint_as_float(x[c]) - r0), w1 = ex2(__uint_as_float(x[c + 1]) - r1);
-                        float w2 = ex2(__uint_as_float(x[c + 2]) - r2), w3 = ex2(__uint_as_float(x[c + 3]) - r3);
-                        l[c] += w0;
-                        l[c + 1] += w1;
-                        l[c + 2] += w2;
-                        l[c + 3] += w3;
+                        const float4 n = *reinterpret_cast<const float4 *>(nm_s + c);
+                        float w0, w1, w2, w3;
+                        f2_get(f2_add(f2(x[c], x[c + 1]), f2(n.x, n.y)), w0, w1);
+                        f2_get(f2_add(f2(x[c + 2], x[c + 3]), f2(n.z, n.w)), w2, w3);
+                        F2 a0 = f2(ex2(w0), ex2(w1)), a1 = f2(ex2(w2), ex2(w3));
+                        l2[c / 2] = f2_add(l2[c / 2], a0);
+                        l2[c / 2 + 1] = f2_add(l2[c / 2 + 1], a1);
                         if (F8) {
-                            w0 *= vs;
-                            w1 *= vs;
-                            w2 *= vs;
-                            w3 *= vs;
+                            a0 = f2_mul(a0, vs2);
+                            a1 = f2_mul(a1, vs2);
                         }
+                        f2_get(a0, w0, w1);
+                        f2_get(a1, w2, w3);
                         out[2 * h] = pack2(w0, w1, F8);
                         out[2 * h + 1] = pack2(w2, w3, F8);
                     }
@@ -452,9 +499,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 ++sc;
             }
             // ------------------------------------------------------------ the item's end
-            if (!dead) dead = !warp_wait(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
+            if (!dead) dead = !wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             tiles += T;
+            float l[NT];
+#pragma unroll
+            for (int c = 0; c < NT; c += 2) f2_get(l2[c / 2], l[c], l[c + 1]);
             warp_columns<NT>(l, lane);
             if constexpr (NT == 16) {
                 if ((lane & 1) == 0) red_s[q4 * NT + lane / 2] = l[0];
@@ -462,7 +512,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < NT / 32; ++i) red_s[q4 * NT + lane * (NT / 32) + i] = l[i];
             }
-            if (lane == 0 && q4 == 0) cs_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // the accumulator's unit
+            if (lane == 0 && q4 == 0) unit_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
             named_barrier(4, 256);
             const bool second = T > 1;   // the second warpgroup had a tile
             const float *const m0_s = reinterpret_cast<const float *>(smem + L::oM), *const m1_s = m0_s + NT;
@@ -471,15 +521,15 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
             if (threadIdx.x < NT) {
                 const int c = static_cast<int>(threadIdx.x);
-                const float ma = m0_s[c], mb = second ? m1_s[c] : ninf();
-                const float mm = fmaxf(ma, mb), ref = mm == ninf() ? 0.0f : mm;
-                const float ka = ex2(ma - ref), kb = ex2(mb - ref);
+                const float ma = -m0_s[c], mb = second ? -m1_s[c] : kNone;
+                const float mx = fmaxf(ma, mb), ka = ex2(ma - mx), kb = ex2(mb - mx);
+                const float mm = mx == kNone ? ninf() : mx;
                 float ll = (red0[c] + red0[NT + c] + red0[2 * NT + c] + red0[3 * NT + c]) * ka;
                 if (second) ll += (red1[c] + red1[NT + c] + red1[2 * NT + c] + red1[3 * NT + c]) * kb;
                 const bool none = mm == ninf() && ll == 0.0f;
                 const float inv = !w.whole ? 1.0f : (none ? 0.0f : 1.0f / ll);
-                w0_s[c] = ka * cs_s[0] * inv;
-                w1_s[c] = second ? kb * cs_s[1] * inv : 0.0f;
+                w0_s[c] = ka * unit_s[0] * inv;
+                w1_s[c] = second ? kb * unit_s[1] * inv : 0.0f;
                 if (c < R) {
                     if (!w.whole)
                         narrow_ml<DP>(a, gridDim.x, slot)[c] = make_float2(mm, ll);
@@ -500,7 +550,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 tmem_ld_cols<H>(tmem + lanes + 3 * NT + g * H, ob);
             }
             tmem_wait_ld();
-            tc_fence_before();   // the next item's products follow this warp's arrival on bQ
+            tc_fence_before();
+            warp_arrive(bar(L::bOF));   // the next item's products may begin
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
             uint32_t any_bad = 0;
 #pragma unroll
@@ -541,6 +592,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         if (g * H + i < R) po[(g * H + i) * DP] = __uint_as_float(oa[i]);
                 }
             }
+            __syncwarp();
+            warp_arrive(bar(L::bQE + qb));   // masks and queries of this item are done with
         }
     }
     tc_fence_before();

@@ -144,6 +144,16 @@ __device__ __forceinline__ bool softmax_any(bool v) {
     return r != 0;
 }
 
+// warp_wait with its loop out of line: the kernels have many waits, and their code should stay in
+// the instruction caches.
+__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *err, long long limit) {
+    return mbar_wait(bar, parity, abort, err, limit);
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *err, long long limit) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xFFFFFFFFu, wait_loop(bar, parity, abort, err, limit));
+}
+
 // Bounded warp-wide wait until *p has reached v, under mbar_wait's rules.
 __device__ __forceinline__ bool wait_count(const volatile uint32_t *p, uint32_t v, volatile int32_t *abort, int32_t *err,
                                            long long limit) {
@@ -397,7 +407,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <typename L, bool F8, int DP>
 __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                         uint8_t *smem, int box_rows, volatile int32_t *abort_flag,
-                                        volatile uint32_t *v_issued) {
+                                        volatile uint32_t *k_issued, volatile uint32_t *v_issued) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -432,7 +442,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
                 const uint32_t empty = bar((v ? (F8 ? L::bSE : L::bVE) : L::bKE) + slot);
                 const uint32_t dst = base + (v ? (F8 ? L::oS + slot * L::kStage : L::oV + slot * L::kVSlot)
                                                : L::oK + slot * L::kKSlot);
-                if (!warp_wait(empty, (use & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) {
+                if (!wait_for(empty, (use & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) {
                     ok = false;
                     break;
                 }
@@ -456,13 +466,15 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
                     }
                 }
                 __syncwarp();
+                // once a tile is announced, its slot's previous use is over, and the slot's parity
+                // tells this use from that one
                 if (v == 0) ++k_cnt;
+                if (lane == 0 && (v == 0 || !F8)) {
+                    __threadfence_block();
+                    *(v ? v_issued : k_issued) = cnt + 1;
+                }
             }
             if (!ok) break;
-            if (!F8 && lane == 0) {
-                __threadfence_block();
-                *v_issued = cnt + 1;
-            }
         }
     }
     if (*abort_flag != 0) {   // copies nobody waited for must land before the CTA leaves
@@ -495,7 +507,7 @@ __device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t
             // only the last tiles are waited for here, so the slot may be some uses behind: its
             // parity tells this use from the one before once this one was issued
             if (!wait_count(v_issued, cnt + 1, abort_flag, a.err, a.wait_limit) ||
-                !warp_wait(bar(L::bVF + slot), (cnt / L::NV) & 1u, abort_flag, a.err, a.wait_limit)) {
+                !wait_for(bar(L::bVF + slot), (cnt / L::NV) & 1u, abort_flag, a.err, a.wait_limit)) {
                 ok = false;
                 break;
             }
@@ -537,13 +549,19 @@ __device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t
     }
 }
 
+// All ones in the bytes of four codes that are not NaN (0x7f, 0xff).
+__device__ __forceinline__ uint32_t finite_codes(uint32_t x) {
+    const uint32_t nan = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of such a byte
+    return ~((nan >> 7) * 0xFFu);
+}
+
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
 // layout, the scales into the softmax's double buffer.  The value scales there are relative to
 // sigma, a power of two at or above all of the item's finite ones so far, times kWeightUp.  What
 // clean_values does for bf16 is done on the way.
 template <typename L, int DP>
 __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw,
-                                               volatile int32_t *abort_flag) {
+                                               volatile int32_t *abort_flag, volatile uint32_t *v_issued) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31), j = cw * 32 + lane;
@@ -559,8 +577,8 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
         float sigma = 7.888609e-31f;   // 2^-100: below any value scale that counts
         for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
-            const uint32_t ss = cnt % L::NS, slot = cnt % L::NV, sb = cnt & 1u;
-            if (!(ok = warp_wait(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
+            const uint32_t ss = cnt % L::NS, slot = cnt % L::NV;
+            if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
             const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
             float top = 0.0f, ks = 0.0f, vs = 0.0f;   // every warp forms the tile's largest: no barrier
 #pragma unroll
@@ -575,49 +593,51 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             if (top > sigma)   // the power of two at or above it
                 sigma = __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000));
             const bool odd_scale = j >= first && j < stop && !(fabsf(vs) <= kMax);
-            if (!(ok = warp_wait(bar(L::bCE + sb), ((cnt >> 1) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
-            scale_s[sb * 256 + j] = ks;
-            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
-            if (lane == 0) sigma_s[sb] = sigma;   // the same from every warp
+            // the V slot is free when its previous product is done, and that came after the softmax
+            // had read the scales of that tile: the scales' buffer goes with the slot
+            if (!(ok = wait_for(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
+            if (cw == 0 && lane == 0) *v_issued = cnt + 1;   // the slot's previous use is over
+            scale_s[slot * 256 + j] = ks;
+            scale_s[slot * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
+            if (lane == 0) sigma_s[slot] = sigma;   // the same from every warp
             if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
-            warp_arrive(bar(L::bCF + sb));
-            if (!(ok = warp_wait(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
-            const uint8_t *const src = smem + L::oS + ss * L::kStage;
+            warp_arrive(bar(L::bCF + slot));
+            uint8_t *const src = smem + L::oS + ss * L::kStage;
             uint8_t *const dst = smem + L::oV + slot * L::kVSlot;
             // 4 (8) rows of 128 (64) codes a step: 16 codes per lane
-            constexpr int C = DP / 16, RS = 32 / C;
-            const int c = lane % C;
-#pragma unroll 4
-            for (int i = 0; i < 32 / RS; ++i) {
-                const int r = cw * 32 + i * RS + lane / C;
-                uint4 x = *reinterpret_cast<const uint4 *>(src + r * 128 + c * 16);
-                if (r >= first) {   // the tile's part past the context
-                    uint32_t *const q = reinterpret_cast<uint32_t *>(&x);
+            constexpr int C = DP / 16, RS = 32 / C, STEPS = 32 / RS;
+            const int c = lane % C, row0 = cw * 32 + lane / C;
+            if (min(first, stop) < kTile) {   // the tile reaches past the context
+#pragma unroll 1
+                for (int i = 0; i < STEPS; ++i) {
+                    const int r = row0 + i * RS;
+                    uint4 *const q = reinterpret_cast<uint4 *>(src + r * 128 + c * 16);
                     if (r >= stop) {
-                        x = make_uint4(0, 0, 0, 0);
-                    } else {
-                        bool hit = false;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                if ((q[k] >> (8 * y) & 0x7Fu) == 0x7Fu) {
-                                    q[k] &= ~(0xFFu << (8 * y));
-                                    hit = true;
-                                }
-                        if (hit) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << (r & 31));
+                        *q = make_uint4(0, 0, 0, 0);
+                    } else if (r >= first) {
+                        const uint4 x = *q;
+                        const uint4 keep = make_uint4(finite_codes(x.x), finite_codes(x.y), finite_codes(x.z), finite_codes(x.w));
+                        if ((keep.x & keep.y & keep.z & keep.w) != 0xFFFFFFFFu) {
+                            atomicOr(&bad[(tt & 1) * 4 + cw], 1u << (r & 31));
+                            *q = make_uint4(x.x & keep.x, x.y & keep.y, x.z & keep.z, x.w & keep.w);
+                        }
                     }
                 }
+            }
+            // 64-channel halves; the halves' lanes store their two chunks in opposite order, so that a
+            // step's eight lanes of a row meet eight bank groups
+            uint8_t *const half = dst + (c / 4) * (kTile * 128);
+            const int u = (c % 4) * 2, sw = c / 4;
+#pragma unroll 2
+            for (int i = 0; i < STEPS; ++i) {
+                const int r = row0 + i * RS;
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + r * 128 + c * 16);
                 const uint4 lo = make_uint4(e4m3x2_to_f16x2(x.x & 0xFFFFu), e4m3x2_to_f16x2(x.x >> 16),
                                             e4m3x2_to_f16x2(x.y & 0xFFFFu), e4m3x2_to_f16x2(x.y >> 16));
                 const uint4 hi = make_uint4(e4m3x2_to_f16x2(x.z & 0xFFFFu), e4m3x2_to_f16x2(x.z >> 16),
                                             e4m3x2_to_f16x2(x.w & 0xFFFFu), e4m3x2_to_f16x2(x.w >> 16));
-                // 64-channel halves; the halves' lanes store their two chunks in opposite order, so
-                // that a step's eight lanes of a row meet eight bank groups
-                uint8_t *const row = dst + (c / 4) * (kTile * 128) + r * 128;
-                const int u = (c % 4) * 2, sw = c / 4;
-                *reinterpret_cast<uint4 *>(row + (((u + sw) ^ (r & 7)) * 16)) = sw ? hi : lo;
-                *reinterpret_cast<uint4 *>(row + (((u + 1 - sw) ^ (r & 7)) * 16)) = sw ? lo : hi;
+                *reinterpret_cast<uint4 *>(half + r * 128 + (((u + sw) ^ (r & 7)) * 16)) = sw ? hi : lo;
+                *reinterpret_cast<uint4 *>(half + r * 128 + (((u + 1 - sw) ^ (r & 7)) * 16)) = sw ? lo : hi;
             }
             fence_proxy_async_smem();
             __threadfence_block();

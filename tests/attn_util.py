@@ -101,6 +101,20 @@ class Pass:
                 see[i, self.ctx[b] + j] = bool((bits >> j) & 1)
         return see
 
+    def reference_heads(self, heads, p_eps, out_bf16):
+        """{query head: (out, lse, out bound, lse bound)} of some heads only."""
+        found = {}
+        for h in heads:
+            one = Pass.__new__(Pass)
+            one.__dict__.update(self.__dict__)
+            hk = h // self.group
+            one.q, one.group = self.q[:, h:h + 1], 1
+            cut = lambda x, d: None if x is None else x.narrow(d, hk, 1)
+            one.k, one.v = cut(self.k, 2), cut(self.v, 2)
+            one.k_scale, one.v_scale = cut(self.k_scale, 1), cut(self.v_scale, 1)
+            found[h] = tuple(x[:, 0] for x in one.reference(p_eps, out_bf16))
+        return found
+
     def reference(self, p_eps, out_bf16, scale=None):
         """(out, lse, out bound, lse bound) in float64.  With s off by ds = (dim + 4) 2^-24 scale
         sum|q||k| (fp32 products summed in any order) a weight is off by 2 ds relative; exponential,

@@ -281,6 +281,26 @@ def test_long_context():
         _check(Pass([40001], [3], 2, 1, 128, 64, cache, seed=15))
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,dim", [(2, 128), (7, 128), (15, 128), (2, 64), (14, 64), (30, 128), (64, 64)])
+def test_every_cta_walks_many_tiles(n, dim, cache):
+    """Long ragged contexts over many heads: each CTA streams tens of tiles through its rings and
+    crosses from one item to the next, with odd tile counts, on both kernels and every row width."""
+    ctx = [9001, 4000, 6500, 130, 7777]
+    p = Pass(ctx, [n, 1, n, n, max(1, n - 1)], 32, 8, dim, 64, cache, seed=n)
+    args = p.device(api)
+    ws = api.tree_attention_workspace(args["cache"], int(p.starts[-1]), 5, 32)
+    out, lse = api.tree_attention(**args, max_tokens=n, return_lse=True, ws=ws)
+    again = api.tree_attention(**args, max_tokens=n, ws=ws)
+    assert api.last_device_error(ws) == 0
+    assert torch.equal(out, again)
+    heads = [0, 5, 31]   # the reference of every eighth cache head or so
+    full = p.reference_heads(heads, weight_eps(p), True)
+    for h in heads:
+        assert_within(f"lse {h}", lse[:, h], full[h][1], full[h][3])
+        assert_within(f"out {h}", out[:, h], full[h][0], full[h][2])
+
+
 def test_empty_call():
     c = api.kv_cache(1, 16, 2, 64)
     e = torch.empty((0, 4, 64), dtype=torch.bfloat16, device=DEV)
