@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -575,31 +576,60 @@ ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
 MAX_TREE_TOKENS = 64
 _HEAD_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 _CACHE_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_E4M3}
+# Descriptors of these calls, which run once per layer and pass, are packed as bytes and passed by
+# address: a fraction of a ctypes structure's cost.
+_pack_heads = struct.Struct("@Pqqii").pack      # moe_heads_t
+_pack_rotary = struct.Struct("@PPiiii").pack    # moe_rotary_t
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _heads(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int) -> Heads:
-    """The descriptor of a [tokens, heads, dim] CUDA tensor: any token and head strides, dense channels."""
+def _device_of(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _heads(t: torch.Tensor, name: str, tokens: int, heads: int, dim: int, device: int) -> bytes:
+    """The descriptor of a [tokens, heads, dim] tensor on `device`: any token and head strides, dense channels."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
     code = _HEAD_TYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-    if tuple(t.shape) != (tokens, heads, dim):
+    if t.shape != (tokens, heads, dim):
         raise ValueError(f"{name} must have shape {(tokens, heads, dim)}, got {tuple(t.shape)}")
     st, sh, sd = t.stride()
     if sd != 1 and dim > 1:
         raise ValueError(f"{name} must have contiguous channels")
-    return Heads(t.data_ptr(), st, sh, heads, code)
+    return _pack_heads(t.data_ptr(), st, sh, heads, code)
 
 
-def _like(x: torch.Tensor) -> torch.Tensor:
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+def _flat(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous tensor of this type and shape on `device`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(ref: torch.Tensor, **named):
-    for name, t in named.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} must be on {ref.device}, got {t.device}")
+def _new_heads(x: torch.Tensor, tokens: int, heads: int, dim: int):
+    """A dense [tokens, heads, dim] tensor of x's type beside it, and its descriptor."""
+    y = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+    return y, _pack_heads(y.data_ptr(), heads * dim, dim, heads, _HEAD_TYPES[x.dtype])
+
+
+def _ws_ptr(ws, device: int):
+    if ws is None:
+        return None
+    if ws.get_device() != device:
+        raise TypeError(f"ws must be a CUDA tensor on device {device}")
+    return ws.data_ptr()
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -623,11 +653,13 @@ def rope_table(positions: int, w, magnitude: float = 1.0, device=None) -> torch.
     return table
 
 
-def _rotary(table: torch.Tensor, positions: torch.Tensor, tokens: int, interleaved: bool, inverse: bool) -> Rotary:
-    if table.dim() != 3 or table.shape[2] != 2:
-        raise ValueError(f"table must have shape (positions, rot / 2, 2), got {tuple(table.shape)}")
-    return Rotary(_dev(table, "table", torch.float32), _dev(positions, "positions", torch.int32, (tokens,)),
-                  table.shape[0], 2 * table.shape[1], 1 if interleaved else 0, 1 if inverse else 0)
+def _rotary(table: torch.Tensor, positions: torch.Tensor, tokens: int, interleaved: bool, inverse: bool, device: int) -> bytes:
+    shape = table.shape
+    if len(shape) != 3 or shape[2] != 2:
+        raise ValueError(f"table must have shape (positions, rot / 2, 2), got {tuple(shape)}")
+    return _pack_rotary(_flat(table, "table", torch.float32, shape, device),
+                        _flat(positions, "positions", torch.int32, (tokens,), device),
+                        shape[0], 2 * shape[1], 1 if interleaved else 0, 1 if inverse else 0)
 
 
 def rope(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False, inverse: bool = False,
@@ -636,23 +668,28 @@ def rope(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool =
     None) by their positions; inverse gives the gradient's direction.  Returns (q_out, k_out); an output
     may be its input.  ws (any workspace) records positions beyond the table."""
     ref = q if q is not None else k
+    device = _device_of(ref, "q" if q is not None else "k")
     tokens, _, dim = ref.shape
-    desc = []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            desc += [None, None]
-            continue
-        hx = _heads(x, name, tokens, x.shape[1], dim)
-        y = _like(x) if y is None else y
-        hy = _heads(y, name + "_out", tokens, x.shape[1], dim)
-        if name == "q":
-            q_out = y
+    dq = dqo = dk = dko = None
+    if q is not None:
+        heads = q.shape[1]
+        dq = _heads(q, "q", tokens, heads, dim, device)
+        if q_out is None:
+            q_out, dqo = _new_heads(q, tokens, heads, dim)
         else:
-            k_out = y
-        desc += [ctypes.byref(hx), ctypes.byref(hy)]
-    _same_device(ref, k=k, positions=positions, table=table, q_out=q_out, k_out=k_out, ws=ws)
-    _check(lib().moe_rope(*desc, tokens, dim, ctypes.byref(_rotary(table, positions, tokens, interleaved, inverse)),
-                          None if ws is None else ws.data_ptr(), _stream(ref.device)), "moe_rope")
+            dqo = _heads(q_out, "q_out", tokens, heads, dim, device)
+    if k is not None:
+        heads = k.shape[1]
+        dk = _heads(k, "k", tokens, heads, dim, device)
+        if k_out is None:
+            k_out, dko = _new_heads(k, tokens, heads, dim)
+        else:
+            dko = _heads(k_out, "k_out", tokens, heads, dim, device)
+    code = (_lib or lib()).moe_rope(dq, dqo, dk, dko, tokens, dim,
+                                    _rotary(table, positions, tokens, interleaved, inverse, device),
+                                    _ws_ptr(ws, device), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_rope")
     return q_out, k_out
 
 
@@ -678,10 +715,13 @@ class KVCache:
             vs = _dev(v_scale, "v_scale", torch.float32, shape)
         elif k_scale is not None or v_scale is not None:
             raise ValueError("scales belong to a cache of e4m3 codes")
-        _same_device(k, v=v, k_scale=k_scale, v_scale=v_scale)
+        for name, t in (("v", v), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"{name} must be on {k.device}, got {t.device}")
         self.desc = CacheDesc(k.data_ptr(), v.data_ptr(), ks, vs, *k.stride()[:3], code, self.heads, self.dim,
                               self.page, self.pages, 0)
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self.address = ctypes.addressof(self.desc)
 
 
 def kv_cache(pages: int, page: int, heads: int, dim: int, dtype: str = "bf16", device=None) -> KVCache:
@@ -699,47 +739,54 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     slot takes nothing), quantised for an e4m3 cache.  With positions and table the keys are rotated
     before, and q [tokens, q heads, dim], when given, is rotated into q_out, which is returned (None
     without q).  ws (any workspace) records slots and positions out of range."""
+    device, dim = cache.index, cache.dim
     tokens = k.shape[0]
-    hk = _heads(k, "k", tokens, cache.heads, cache.dim)
-    hv = _heads(v, "v", tokens, cache.heads, cache.dim)
+    dk = _heads(k, "k", tokens, cache.heads, dim, device)
+    dv = _heads(v, "v", tokens, cache.heads, dim, device)
     rot = dq = dqo = None
     if (table is None) != (positions is None):
         raise ValueError("rotation takes both positions and table")
     if table is not None:
-        rot = ctypes.byref(_rotary(table, positions, tokens, interleaved, False))
+        rot = _rotary(table, positions, tokens, interleaved, False, device)
     if q is not None:
         if table is None:
             raise ValueError("q is only rotated: it takes positions and table")
-        q_out = _like(q) if q_out is None else q_out
-        dq = ctypes.byref(_heads(q, "q", tokens, q.shape[1], cache.dim))
-        dqo = ctypes.byref(_heads(q_out, "q_out", tokens, q.shape[1], cache.dim))
+        heads = q.shape[1]
+        dq = _heads(q, "q", tokens, heads, dim, device)
+        if q_out is None:
+            q_out, dqo = _new_heads(q, tokens, heads, dim)
+        else:
+            dqo = _heads(q_out, "q_out", tokens, heads, dim, device)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _same_device(cache.k, k=k, v=v, slots=slots, q=q, q_out=q_out, positions=positions, table=table, ws=ws)
-    _check(lib().moe_kv_write(ctypes.byref(cache.desc), ctypes.byref(hk), ctypes.byref(hv),
-                              _dev(slots, "slots", torch.int32, (tokens,)), tokens, rot, dq, dqo,
-                              None if ws is None else ws.data_ptr(), _stream(cache.device)), "moe_kv_write")
+    code = (_lib or lib()).moe_kv_write(cache.address, dk, dv, _flat(slots, "slots", torch.int32, (tokens,), device), tokens,
+                                        rot, dq, dqo, _ws_ptr(ws, device), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_kv_write")
     return q_out
 
 
 def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=None, v_out=None, ws=None):
     """moe_kv_read: the cache's rows of slots int32 [tokens] as (k, v) [tokens, heads, dim], fp32 or bf16;
     zeros for a negative slot."""
+    device = cache.index
     tokens = slots.shape[0]
     shape = (tokens, cache.heads, cache.dim)
-    k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
-    hk, hv = _heads(k_out, "k_out", *shape), _heads(v_out, "v_out", *shape)
-    _same_device(cache.k, slots=slots, k_out=k_out, v_out=v_out, ws=ws)
-    _check(lib().moe_kv_read(ctypes.byref(cache.desc), _dev(slots, "slots", torch.int32, (tokens,)), tokens,
-                             ctypes.byref(hk), ctypes.byref(hv), None if ws is None else ws.data_ptr(),
-                             _stream(cache.device)), "moe_kv_read")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    code = (_lib or lib()).moe_kv_read(cache.address, _flat(slots, "slots", torch.int32, (tokens,), device), tokens,
+                                       _heads(k_out, "k_out", *shape, device), _heads(v_out, "v_out", *shape, device),
+                                       _ws_ptr(ws, device), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_kv_read")
     return k_out, v_out
 
 
 def tree_attention_workspace(cache: KVCache, tokens: int, seqs: int, q_heads: int) -> torch.Tensor:
     """A zeroed workspace for tree_attention calls of up to this many tokens and sequences."""
-    nbytes = int(lib().moe_tree_attention_workspace_bytes(ctypes.byref(cache.desc), tokens, seqs, q_heads))
+    nbytes = int(lib().moe_tree_attention_workspace_bytes(cache.address, tokens, seqs, q_heads))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
     _check(lib().moe_workspace_init(ws.data_ptr(), nbytes, _stream(cache.device)), "moe_workspace_init")
     return ws
@@ -753,22 +800,26 @@ def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: 
     before them, page_table int32 [seqs, max pages]; mask int64 [tokens], bit j of a token's word set
     where it sees drafted token j of its sequence (None: a chain); scale defaults to dim^-0.5.  Returns
     out, or (out, lse) with return_lse."""
+    device, dim = cache.index, cache.dim
     tokens, heads = q.shape[0], q.shape[1]
-    seqs = ctx.shape[0]
-    hq = _heads(q, "q", tokens, heads, cache.dim)
-    out = _like(q) if out is None else out
-    ho = _heads(out, "out", tokens, heads, cache.dim)
+    seqs, max_pages = page_table.shape
+    dq = _heads(q, "q", tokens, heads, dim, device)
+    if out is None:
+        out, do = _new_heads(q, tokens, heads, dim)
+    else:
+        do = _heads(out, "out", tokens, heads, dim, device)
     if return_lse and lse is None:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device)
-    ws = ws if ws is not None else tree_attention_workspace(cache, tokens, seqs, heads)
-    if page_table.dim() != 2 or page_table.shape[0] != seqs:
-        raise ValueError(f"page_table must have shape ({seqs}, max pages), got {tuple(page_table.shape)}")
-    _same_device(cache.k, q=q, q_start=q_start, ctx=ctx, page_table=page_table, mask=mask, out=out, lse=lse, ws=ws)
-    _check(lib().moe_tree_attention(
-        ctypes.byref(cache.desc), ctypes.byref(hq), ctypes.byref(ho),
-        None if lse is None else _dev(lse, "lse", torch.float32, (tokens, heads)),
-        _dev(q_start, "q_start", torch.int32, (seqs + 1,)), _dev(ctx, "ctx", torch.int32),
-        _dev(page_table, "page_table", torch.int32), None if mask is None else _dev(mask, "mask", torch.int64, (tokens,)),
-        seqs, tokens, max_tokens, page_table.shape[1], cache.dim ** -0.5 if scale is None else scale,
-        ws.data_ptr(), ws.numel(), _stream(cache.device)), "moe_tree_attention")
+    if ws is None:
+        ws = tree_attention_workspace(cache, tokens, seqs, heads)
+    code = (_lib or lib()).moe_tree_attention(
+        cache.address, dq, do,
+        None if lse is None else _flat(lse, "lse", torch.float32, (tokens, heads), device),
+        _flat(q_start, "q_start", torch.int32, (seqs + 1,), device), _flat(ctx, "ctx", torch.int32, (seqs,), device),
+        _flat(page_table, "page_table", torch.int32, (seqs, max_pages), device),
+        None if mask is None else _flat(mask, "mask", torch.int64, (tokens,), device),
+        seqs, tokens, max_tokens, max_pages, dim ** -0.5 if scale is None else scale,
+        _ws_ptr(ws, device), ws.numel(), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_tree_attention")
     return (out, lse) if return_lse else out

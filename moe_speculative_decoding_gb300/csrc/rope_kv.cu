@@ -10,6 +10,7 @@
 #include "common.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -105,6 +106,28 @@ __device__ __forceinline__ float row_scale(float amax) {
     return s > 0.0f ? s : 1.0f;
 }
 
+// x / s, correctly rounded, from r = 1 / s rounded to nearest: q = x r, and one step with the exact
+// remainder x - q s (Markstein's theorem, IBM J. Res. Dev. 34 (1990)): three operations where a
+// division takes a dozen.  s within 2^+-100, so that neither r nor the remainder leaves the range
+// that matters (a quotient below 2^-11 is code 0 whatever its last bit).
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+// The chunk's eight codes for scale s.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
+    float q[8];
+    if (s >= 7.888609e-31f && s <= 1.2676506e30f) {
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s, r);
+    } else {   // also infinite and NaN
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = x[i] / s;
+    }
+    return make_uint2(pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7]));
+}
+
 // ------------------------------------------------------------------ where a row comes from and goes
 struct Row {
     const void *src;
@@ -169,85 +192,192 @@ __device__ __forceinline__ Row locate(const RowArgs &a, uint32_t g, uint32_t row
     return w;
 }
 
-// A row on T threads (a power of two, T * 16 >= dim), 16 channels each in two chunks of 8: both
-// halves of 8 pairs of the half layout, or 16 consecutive channels.
-template <int T>
-__global__ void __launch_bounds__(kThreads) rows_vec_kernel(const __grid_constant__ RowArgs a, uint32_t rows, uint32_t total) {
+// The streaming kernels take a token's rows together, because a row alone costs more instructions
+// for finding its place than for its channels (16381 tokens x 40 heads of 128: 76 us with a row per
+// thread group and all of its address arithmetic, 96 us with two): `share` groups of T threads (a
+// power of two, T * 16 >= dim) share a token, find its position, table row and cache slot once, and
+// step through its heads by pointer.  A thread holds 16 channels of a row, in two chunks of 8: both
+// halves of 8 pairs of the half layout, or 16 consecutive channels; the token's 8 cosines and sines
+// stay in its registers, and the next row's loads are on their way while it works on one.
+
+// 16 channels as they come from memory
+template <typename E>
+struct Raw {
+    uint4 v[sizeof(E)];   // 2 bytes: two chunks of 16; 4 bytes: two of 32
+};
+template <typename E>
+__device__ __forceinline__ void load_raw(const E *p, int o1, Raw<E> &r) {
+    if constexpr (sizeof(E) == 2) {
+        r.v[0] = *reinterpret_cast<const uint4 *>(p);
+        r.v[1] = *reinterpret_cast<const uint4 *>(p + o1);
+    } else {
+        r.v[0] = *reinterpret_cast<const uint4 *>(p);
+        r.v[1] = *reinterpret_cast<const uint4 *>(p + 4);
+        r.v[2] = *reinterpret_cast<const uint4 *>(p + o1);
+        r.v[3] = *reinterpret_cast<const uint4 *>(p + o1 + 4);
+    }
+}
+template <typename E>
+__device__ __forceinline__ void from_raw(const Raw<E> &r, float (&x)[8], float (&y)[8]) {
+    if constexpr (sizeof(E) == 2) {
+        const uint32_t a[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w}, b[4] = {r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf16_lo(a[i]);
+            x[2 * i + 1] = bf16_hi(a[i]);
+            y[2 * i] = bf16_lo(b[i]);
+            y[2 * i + 1] = bf16_hi(b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 a = r.v[h], b = r.v[2 + h];
+            x[4 * h] = __uint_as_float(a.x);
+            x[4 * h + 1] = __uint_as_float(a.y);
+            x[4 * h + 2] = __uint_as_float(a.z);
+            x[4 * h + 3] = __uint_as_float(a.w);
+            y[4 * h] = __uint_as_float(b.x);
+            y[4 * h + 1] = __uint_as_float(b.y);
+            y[4 * h + 2] = __uint_as_float(b.z);
+            y[4 * h + 3] = __uint_as_float(b.w);
+        }
+    }
+}
+
+// One rotation of the thread's pairs.  cs: 8 (cos, sin); a thread with unrotated channels holds
+// (1, 0) there and skips nothing: x * 1 - y * 0 would turn an infinity into NaN, so `turn` decides.
+__device__ __forceinline__ void turn16(float (&x)[8], float (&y)[8], const float (&cs)[16], bool adjacent) {
+    if (adjacent) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
+            x[2 * i] = a * cs[2 * i] - b * cs[2 * i + 1];
+            x[2 * i + 1] = b * cs[2 * i] + a * cs[2 * i + 1];
+            y[2 * i] = c * cs[8 + 2 * i] - d * cs[8 + 2 * i + 1];
+            y[2 * i + 1] = d * cs[8 + 2 * i] + c * cs[8 + 2 * i + 1];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = x[i], b = y[i];
+            x[i] = a * cs[2 * i] - b * cs[2 * i + 1];
+            y[i] = b * cs[2 * i] + a * cs[2 * i + 1];
+        }
+    }
+}
+
+// IN: the rows' type, also of dense outputs.  CT: the cache's type, or -1 for no cache.  ROT: with
+// rotation.  At least four CTAs an SM: what is in flight covers the memory's latency.
+template <typename IN, int CT, int T, bool ROT>
+__global__ void __launch_bounds__(kThreads, 4) rows_vec_kernel(const __grid_constant__ RowArgs a, int share) {
+    constexpr int kInType = sizeof(IN) == 2 ? MOE_BF16 : MOE_F32;
     pdl_wait();
     pdl_trigger();
-    const int c = static_cast<int>(threadIdx.x) % T;
-    const uint32_t g = blockIdx.x * (kThreads / T) + threadIdx.x / T;
-    const bool on = g < total && 16 * c < a.dim;
-    float x[8], y[8];
-    Row w;
-    w.dst = nullptr;
-    w.scale = nullptr;
-    w.dst_type = MOE_F32;
-    int o0 = 16 * c, o1 = 16 * c + 8;
-    if (on) {
-        w = locate(a, g, rows);
-        const bool turn = w.cs != nullptr && 16 * c < a.rot.rot;
-        if (turn && !a.rot.interleaved) {
-            o0 = 8 * c;
-            o1 = (a.rot.rot >> 1) + 8 * c;
-        }
-        if (w.dst != nullptr) {
-            load8(w.src, w.src_type, w.src_off + o0, x);
-            load8(w.src, w.src_type, w.src_off + o1, y);
-            if (turn) {
-                float2 cs[8];
+    const int c = static_cast<int>(threadIdx.x) % T, group = static_cast<int>(threadIdx.x) / T, sub = group % share;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / T / share) + group / share;
+    const bool here = t < a.tokens && 16 * c < a.dim;
+    float cs[16];
+    bool turn = false, live = here;
+    int o0 = 16 * c, o1 = 8;   // first chunk, and the second's distance from it
+    if (ROT && here) {
+        const int p = __ldg(a.rot.positions + t);
+        live = static_cast<uint32_t>(p) < static_cast<uint32_t>(a.rot.table_positions);
+        if (!live) {
+            record_error(a.err, MOE_ERR_BAD_ID);
+        } else if (16 * c < a.rot.rot) {
+            turn = true;
+            const float4 *const k = reinterpret_cast<const float4 *>(a.rot.table + static_cast<int64_t>(p) * a.rot.rot) + 4 * c;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    cs[i] = __ldg(w.cs + 8 * c + i);
-                    if (a.rot.inverse) cs[i].y = -cs[i].y;
-                }
-                if (a.rot.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p = x[2 * i], q = x[2 * i + 1], u = y[2 * i], v = y[2 * i + 1];
-                        x[2 * i] = p * cs[i].x - q * cs[i].y;
-                        x[2 * i + 1] = q * cs[i].x + p * cs[i].y;
-                        y[2 * i] = u * cs[i + 4].x - v * cs[i + 4].y;
-                        y[2 * i + 1] = v * cs[i + 4].x + u * cs[i + 4].y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p = x[i], q = y[i];
-                        x[i] = p * cs[i].x - q * cs[i].y;
-                        y[i] = q * cs[i].x + p * cs[i].y;
-                    }
-                }
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = __ldg(k + i);
+                cs[4 * i] = v.x;
+                cs[4 * i + 1] = a.rot.inverse ? -v.y : v.y;
+                cs[4 * i + 2] = v.z;
+                cs[4 * i + 3] = a.rot.inverse ? -v.w : v.w;
             }
         }
     }
-    const bool quant = w.dst != nullptr && w.dst_type == MOE_E4M3;
-    if (__any_sync(0xFFFFFFFFu, quant)) {   // the row's T threads share a warp
-        float mx = 0.0f;
-        if (quant) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x[i]), fabsf(y[i])));
-        }
-#pragma unroll
-        for (int off = T / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, off));
-        if (quant) {
-            const float sc = row_scale(mx);
-            if (c == 0) *w.scale = sc;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] /= sc;
-                y[i] /= sc;
-            }
-            uint8_t *const d = static_cast<uint8_t *>(w.dst) + w.dst_off;
-            *reinterpret_cast<uint2 *>(d + o0) =
-                make_uint2(pack_e4m3x4(x[0], x[1], x[2], x[3]), pack_e4m3x4(x[4], x[5], x[6], x[7]));
-            *reinterpret_cast<uint2 *>(d + o1) =
-                make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+    const bool split = ROT && 16 * c < a.rot.rot && !a.rot.interleaved;
+    const int q0 = split ? 8 * c : o0, q1 = split ? a.rot.rot >> 1 : o1;   // chunks of rotated rows
+
+    // dense rows: q, and k where there is no cache
+    const int dense = a.q.heads + (CT < 0 ? a.k.heads : 0);
+    if (live && sub < dense) {
+        auto src = [&](int r) {
+            const bool q = CT >= 0 || r < a.q.heads;
+            const moe_heads_t &h = q ? a.q : a.k;
+            return static_cast<const IN *>(h.ptr) + t * h.token_stride + (q ? r : r - a.q.heads) * h.head_stride + q0;
+        };
+        Raw<IN> next;
+        load_raw(src(sub), q1, next);
+        for (int r = sub; r < dense; r += share) {
+            float x[8], y[8];
+            from_raw(next, x, y);
+            if (r + share < dense) load_raw(src(r + share), q1, next);
+            if (ROT && turn) turn16(x, y, cs, a.rot.interleaved);
+            const bool q = CT >= 0 || r < a.q.heads;
+            const moe_heads_t &h = q ? a.q_out : a.k_out;
+            const int64_t off = t * h.token_stride + (q ? r : r - a.q.heads) * h.head_stride + q0;
+            store8(h.ptr, kInType, off, x);
+            store8(h.ptr, kInType, off + q1, y);
         }
     }
-    if (w.dst != nullptr && !quant) {
-        store8(w.dst, w.dst_type, w.dst_off + o0, x);
-        store8(w.dst, w.dst_type, w.dst_off + o1, y);
+    if constexpr (CT >= 0) {
+        // cache rows: k (rotated), then v
+        const moe_kv_cache_t &kc = a.cache;
+        const int n = 2 * kc.heads;
+        const int slot = live ? __ldg(a.slots + t) : -1;
+        auto src = [&](int r) {
+            const bool k = r < kc.heads;
+            const moe_heads_t &h = k ? a.k : a.v;
+            return static_cast<const IN *>(h.ptr) + t * h.token_stride + (k ? r : r - kc.heads) * h.head_stride + (k ? q0 : o0);
+        };
+        Raw<IN> next;
+        if (live && sub < n) load_raw(src(sub), sub < kc.heads ? q1 : o1, next);   // beside the slot's load
+        int64_t at = -1, sc_at = 0;
+        if (slot >= 0) {
+            const int page = slot / kc.page, row = slot - page * kc.page;
+            if (page >= kc.pages) {
+                record_error(a.err, MOE_ERR_BAD_ID);
+            } else {
+                at = page * kc.page_stride + row * kc.token_stride;
+                sc_at = static_cast<int64_t>(page) * kc.heads * kc.page + row;
+            }
+        }
+        // every group of a warp takes the same number of turns: the lanes of a row meet in shuffles
+        for (int r = sub; r - sub < n; r += share) {
+            const bool on = at >= 0 && r < n, k = r < kc.heads;
+            float x[8] = {}, y[8] = {};
+            if (on) {
+                from_raw(next, x, y);
+                if (r + share < n) load_raw(src(r + share), r + share < kc.heads ? q1 : o1, next);
+                if (ROT && turn && k) turn16(x, y, cs, a.rot.interleaved);
+            }
+            const int h = k ? r : r - kc.heads, d0 = k ? q0 : o0, d1 = k ? q1 : o1;
+            const int64_t off = at + h * kc.head_stride + d0;
+            if constexpr (CT == MOE_E4M3) {
+                float mx = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x[i]), fabsf(y[i])));
+#pragma unroll
+                for (int o = T / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+                if (on) {
+                    const float sc = row_scale(mx);
+                    if (c == 0) (k ? kc.k_scale : kc.v_scale)[sc_at + static_cast<int64_t>(h) * kc.page] = sc;
+                    uint8_t *const d = static_cast<uint8_t *>(k ? kc.k : kc.v) + off;
+                    const uint2 lo = codes8(x, sc), hi = codes8(y, sc);
+                    if (d1 == 8) {
+                        *reinterpret_cast<uint4 *>(d) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+                    } else {
+                        *reinterpret_cast<uint2 *>(d) = lo;
+                        *reinterpret_cast<uint2 *>(d + d1) = hi;
+                    }
+                }
+            } else if (on) {
+                store8(k ? kc.k : kc.v, CT, off, x);
+                store8(k ? kc.k : kc.v, CT, off + d1, y);
+            }
+        }
     }
 }
 
@@ -311,68 +441,122 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
 }
 
 // ------------------------------------------------------------------ read back
-// 16 channels per thread (VEC, dim a multiple of 16 and aligned outputs) or one.
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ ReadArgs a, uint32_t per_row, uint64_t total) {
+// Row r of the read: token r / (2 heads), then head, keys before values.
+struct Back {
+    const void *src;   // null: zeros
+    int64_t src_off, dst_off;
+    float scale;
+    bool is_v;
+};
+__device__ __forceinline__ Back locate_back(const ReadArgs &a, uint32_t r) {
+    const moe_kv_cache_t &c = a.cache;
+    const uint32_t th = r >> 1;
+    const int64_t t = th / static_cast<uint32_t>(c.heads);
+    const int h = static_cast<int>(th - static_cast<uint32_t>(t) * c.heads);
+    Back w;
+    w.is_v = r & 1u;
+    w.src = nullptr;
+    w.src_off = 0;
+    w.scale = 1.0f;
+    const moe_heads_t &o = w.is_v ? a.v_out : a.k_out;
+    w.dst_off = t * o.token_stride + h * o.head_stride;
+    const int slot = __ldg(a.slots + t);
+    if (slot < 0) return w;
+    const int page = slot / c.page, at = slot - page * c.page;
+    if (page >= c.pages) {
+        record_error(a.err, MOE_ERR_BAD_ID);
+        return w;
+    }
+    w.src = w.is_v ? c.v : c.k;
+    w.src_off = page * c.page_stride + at * c.token_stride + h * c.head_stride;
+    if (c.dtype == MOE_E4M3) w.scale = __ldg((w.is_v ? c.v_scale : c.k_scale) + (static_cast<int64_t>(page) * c.heads + h) * c.page + at);
+    return w;
+}
+
+// Tokens shared as by the rows above: the slot is found once, the heads are stepped through, the
+// next row's loads on their way.
+template <int CT, typename OUT, int T>
+__global__ void __launch_bounds__(kThreads) read_vec_kernel(const __grid_constant__ ReadArgs a, int share) {
+    constexpr int kOutType = sizeof(OUT) == 2 ? MOE_BF16 : MOE_F32;
     pdl_wait();
     pdl_trigger();
-    const moe_kv_cache_t &c = a.cache;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x; i < total;
-         i += static_cast<uint64_t>(gridDim.x) * kThreads) {
-        const uint64_t row = i / per_row;
-        const int ch = static_cast<int>(i - row * per_row) * (VEC ? 16 : 1);
-        const uint64_t th = row >> 1;
-        const bool is_v = row & 1;
-        const int64_t t = static_cast<int64_t>(th / c.heads);
-        const int h = static_cast<int>(th - t * c.heads);
-        const int slot = a.slots[t];
-        int page = 0, at = 0;
-        bool live = slot >= 0;
-        if (live) {
-            page = slot / c.page;
-            at = slot - page * c.page;
-            if (page >= c.pages) {
-                live = false;
-                record_error(a.err, MOE_ERR_BAD_ID);
-            }
-        }
-        const void *src = is_v ? c.v : c.k;
-        const int64_t so = page * c.page_stride + at * c.token_stride + h * c.head_stride + ch;
-        const float sc = live && c.dtype == MOE_E4M3
-                             ? (is_v ? c.v_scale : c.k_scale)[(static_cast<int64_t>(page) * c.heads + h) * c.page + at]
-                             : 1.0f;
-        const moe_heads_t &o = is_v ? a.v_out : a.k_out;
-        const int64_t off = t * o.token_stride + h * o.head_stride + ch;
-        if (VEC) {
-            float x[8] = {}, y[8] = {};
-            if (live) {
-                if (c.dtype == MOE_E4M3) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) + so);
-                    const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 lo = unpack_e4m3x2(static_cast<uint16_t>(wd[j] & 0xFFFFu));
-                        const float2 hi = unpack_e4m3x2(static_cast<uint16_t>(wd[j] >> 16));
-                        float *const d = j < 2 ? x + 4 * j : y + 4 * (j - 2);
-                        d[0] = lo.x * sc;
-                        d[1] = lo.y * sc;
-                        d[2] = hi.x * sc;
-                        d[3] = hi.y * sc;
-                    }
-                } else {
-                    load8(src, c.dtype, so, x);
-                    load8(src, c.dtype, so + 8, y);
-                }
-            }
-            store8(o.ptr, o.dtype, off, x);
-            store8(o.ptr, o.dtype, off + 8, y);
+    const moe_kv_cache_t &kc = a.cache;
+    const int ch = static_cast<int>(threadIdx.x) % T * 16, group = static_cast<int>(threadIdx.x) / T, sub = group % share;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / T / share) + group / share;
+    if (t >= a.tokens || ch >= kc.dim) return;
+    const int slot = __ldg(a.slots + t);
+    int64_t at = -1, sc_at = 0;
+    if (slot >= 0) {
+        const int page = slot / kc.page, row = slot - page * kc.page;
+        if (page >= kc.pages) {
+            record_error(a.err, MOE_ERR_BAD_ID);
         } else {
-            float v = 0.0f;
-            if (live)
-                v = c.dtype == MOE_E4M3 ? unpack_e4m3x2(static_cast<const uint8_t *>(src)[so]).x * sc
-                                        : load1(src, c.dtype, so);
-            store1(o.ptr, o.dtype, off, v);
+            at = page * kc.page_stride + row * kc.token_stride + ch;
+            sc_at = static_cast<int64_t>(page) * kc.heads * kc.page + row;
         }
+    }
+    using E = typename std::conditional<CT == MOE_F32, float, uint16_t>::type;   // of a cache that is not codes
+    struct Next {
+        uint4 q;
+        float scale;
+        Raw<E> raw;
+    } next;
+    auto fetch = [&](int r) {
+        const bool k = r < kc.heads;
+        const int h = k ? r : r - kc.heads;
+        const int64_t off = at + h * kc.head_stride;
+        if constexpr (CT == MOE_E4M3) {
+            next.q = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(k ? kc.k : kc.v) + off);
+            next.scale = __ldg((k ? kc.k_scale : kc.v_scale) + sc_at + static_cast<int64_t>(h) * kc.page);
+        } else {
+            load_raw(static_cast<const E *>(k ? kc.k : kc.v) + off, 8, next.raw);
+        }
+    };
+    const int n = 2 * kc.heads;
+    if (at >= 0 && sub < n) fetch(sub);
+    for (int r = sub; r < n; r += share) {
+        float x[8] = {}, y[8] = {};
+        if (at >= 0) {
+            if constexpr (CT == MOE_E4M3) {
+                const uint32_t wd[4] = {next.q.x, next.q.y, next.q.z, next.q.w};
+                const float sc = next.scale;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 lo = unpack_e4m3x2(static_cast<uint16_t>(wd[j] & 0xFFFFu));
+                    const float2 hi = unpack_e4m3x2(static_cast<uint16_t>(wd[j] >> 16));
+                    float(&d)[8] = j < 2 ? x : y;
+                    d[4 * (j & 1)] = lo.x * sc;
+                    d[4 * (j & 1) + 1] = lo.y * sc;
+                    d[4 * (j & 1) + 2] = hi.x * sc;
+                    d[4 * (j & 1) + 3] = hi.y * sc;
+                }
+            } else {
+                from_raw(next.raw, x, y);
+            }
+            if (r + share < n) fetch(r + share);
+        }
+        const bool k = r < kc.heads;
+        const moe_heads_t &o = k ? a.k_out : a.v_out;
+        const int64_t off = t * o.token_stride + (k ? r : r - kc.heads) * o.head_stride + ch;
+        store8(o.ptr, kOutType, off, x);
+        store8(o.ptr, kOutType, off + 8, y);
+    }
+}
+
+// Any dim and output strides: a warp per row.
+__global__ void __launch_bounds__(kThreads) read_any_kernel(const __grid_constant__ ReadArgs a, uint32_t total) {
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t r = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (r >= total) return;
+    const Back w = locate_back(a, r);
+    const moe_heads_t &o = w.is_v ? a.v_out : a.k_out;
+    for (int ch = static_cast<int>(threadIdx.x & 31); ch < a.cache.dim; ch += 32) {
+        float v = 0.0f;
+        if (w.src != nullptr)
+            v = a.cache.dtype == MOE_E4M3 ? unpack_e4m3x2(static_cast<const uint8_t *>(w.src)[w.src_off + ch]).x * w.scale
+                                          : load1(w.src, a.cache.dtype, w.src_off + ch);
+        store1(o.ptr, o.dtype, w.dst_off + ch, v);
     }
 }
 
@@ -408,25 +592,75 @@ cudaError_t launch_rope_table(const double *w, int half, double magnitude, int p
     return cudaGetLastError();
 }
 
+namespace {
+
+// Groups of threads that share a token: one token to a CTA while that leaves SMs free, so that a
+// short call is short; else eight groups (or as many as the token has rows), whose lanes then all
+// have work and load the token's table row once for several heads.
+int share_of(int groups, int64_t tokens, int rows) {
+    int share = groups;
+    while (share > 8 && tokens * share > 152ll * groups * 4) share /= 2;
+    while (share > 1 && share / 2 >= rows) share /= 2;
+    return share;
+}
+
+template <typename IN, int CT, int T>
+cudaError_t launch_vec(const RowArgs &a, int rows, cudaStream_t s, bool pdl) {
+    const int share = share_of(kThreads / T, a.tokens, rows), per = kThreads / T / share;
+    const unsigned grid = static_cast<unsigned>((a.tokens + per - 1) / per);
+    if constexpr (CT >= 0)
+        if (a.rot.rot == 0) return launch_flat(rows_vec_kernel<IN, CT, T, false>, grid, s, pdl, a, share);
+    return launch_flat(rows_vec_kernel<IN, CT, T, true>, grid, s, pdl, a, share);
+}
+template <typename IN, int CT>
+cudaError_t by_dim(const RowArgs &a, int rows, cudaStream_t s, bool pdl) {
+    if (a.dim > 128) return launch_vec<IN, CT, 16>(a, rows, s, pdl);
+    return a.dim > 64 ? launch_vec<IN, CT, 8>(a, rows, s, pdl) : launch_vec<IN, CT, 4>(a, rows, s, pdl);
+}
+template <typename IN>
+cudaError_t by_cache(const RowArgs &a, int rows, cudaStream_t s, bool pdl) {
+    if (!a.cached) return by_dim<IN, -1>(a, rows, s, pdl);
+    if (a.cache.dtype == MOE_E4M3) return by_dim<IN, MOE_E4M3>(a, rows, s, pdl);
+    return a.cache.dtype == MOE_BF16 ? by_dim<IN, MOE_BF16>(a, rows, s, pdl) : by_dim<IN, MOE_F32>(a, rows, s, pdl);
+}
+
+template <int CT, typename OUT, int T>
+cudaError_t launch_read(const ReadArgs &a, cudaStream_t s, bool pdl) {
+    const int share = share_of(kThreads / T, a.tokens, 2 * a.cache.heads), per = kThreads / T / share;
+    return launch_flat(read_vec_kernel<CT, OUT, T>, static_cast<unsigned>((a.tokens + per - 1) / per), s, pdl, a, share);
+}
+template <int CT, typename OUT>
+cudaError_t read_by_dim(const ReadArgs &a, cudaStream_t s, bool pdl) {
+    if (a.cache.dim > 128) return launch_read<CT, OUT, 16>(a, s, pdl);
+    return a.cache.dim > 64 ? launch_read<CT, OUT, 8>(a, s, pdl) : launch_read<CT, OUT, 4>(a, s, pdl);
+}
+template <typename OUT>
+cudaError_t read_by_cache(const ReadArgs &a, cudaStream_t s, bool pdl) {
+    if (a.cache.dtype == MOE_E4M3) return read_by_dim<MOE_E4M3, OUT>(a, s, pdl);
+    return a.cache.dtype == MOE_BF16 ? read_by_dim<MOE_BF16, OUT>(a, s, pdl) : read_by_dim<MOE_F32, OUT>(a, s, pdl);
+}
+
+}  // namespace
+
 cudaError_t launch_rows(const RowArgs &a, cudaStream_t s, bool pdl) {
     const uint32_t rows = a.q.heads + a.k.heads + a.v.heads;
     const uint32_t total = rows * static_cast<uint32_t>(a.tokens);   // the caller keeps it below 2^31
-    const bool vec = a.dim % 16 == 0 && a.rot.rot % 16 == 0 && vec_rows(a.q) && vec_rows(a.q_out) && vec_rows(a.k) &&
-                     vec_rows(a.k_out) && vec_rows(a.v);
-    auto grid = [&](int per) { return (total + per - 1) / per; };
-    if (!vec) return launch_flat(rows_any_kernel, grid(kThreads / 32), s, pdl, a, rows, total);
-    if (a.dim > 128) return launch_flat(rows_vec_kernel<16>, grid(kThreads / 16), s, pdl, a, rows, total);
-    if (a.dim > 64) return launch_flat(rows_vec_kernel<8>, grid(kThreads / 8), s, pdl, a, rows, total);
-    return launch_flat(rows_vec_kernel<4>, grid(kThreads / 4), s, pdl, a, rows, total);
+    // the streaming kernel: 16-byte pieces, one type of rows (an absent q has type 0 = fp32, and no say)
+    const int type = a.k.heads > 0 ? a.k.dtype : a.q.dtype;
+    auto same = [&](const moe_heads_t &h) { return h.heads == 0 || h.dtype == type; };
+    const bool vec = a.dim % 16 == 0 && a.rot.rot % 16 == 0 && (reinterpret_cast<uintptr_t>(a.rot.table) & 15u) == 0 &&
+                     vec_rows(a.q) && vec_rows(a.q_out) && vec_rows(a.k) && vec_rows(a.k_out) && vec_rows(a.v) &&
+                     same(a.q) && same(a.q_out) && same(a.k) && same(a.k_out) && same(a.v);
+    if (!vec) return launch_flat(rows_any_kernel, (total + kThreads / 32 - 1) / (kThreads / 32), s, pdl, a, rows, total);
+    return type == MOE_BF16 ? by_cache<uint16_t>(a, static_cast<int>(rows), s, pdl) : by_cache<float>(a, static_cast<int>(rows), s, pdl);
 }
 
 cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t s, bool pdl) {
-    const bool vec = a.cache.dim % 16 == 0 && vec_rows(a.k_out) && vec_rows(a.v_out);
-    const uint32_t per_row = vec ? a.cache.dim / 16 : a.cache.dim;
-    const uint64_t total = 2ull * a.tokens * a.cache.heads * per_row;
-    const unsigned grid = static_cast<unsigned>(std::min<uint64_t>((total + kThreads - 1) / kThreads, 1u << 30));
-    return vec ? launch_flat(read_kernel<true>, grid, s, pdl, a, per_row, total)
-               : launch_flat(read_kernel<false>, grid, s, pdl, a, per_row, total);
+    if (a.cache.dim % 16 != 0 || !vec_rows(a.k_out) || !vec_rows(a.v_out) || a.k_out.dtype != a.v_out.dtype) {
+        const uint32_t total = 2u * static_cast<uint32_t>(a.tokens) * static_cast<uint32_t>(a.cache.heads);   // below 2^31
+        return launch_flat(read_any_kernel, (total + kThreads / 32 - 1) / (kThreads / 32), s, pdl, a, total);
+    }
+    return a.k_out.dtype == MOE_BF16 ? read_by_cache<uint16_t>(a, s, pdl) : read_by_cache<float>(a, s, pdl);
 }
 
 }  // namespace moe

@@ -150,4 +150,4 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         api.KVCache(torch.zeros((2, 4, 1, 64)), torch.zeros((2, 4, 1, 64)))
     with pytest.raises(TypeError):
-        api._heads(x, "q", 2, 2, 64)
+        api._heads(x, "q", 2, 2, 64, 0)
