@@ -45,14 +45,17 @@ cudaError_t launch_tree_narrow(const TreeArgs &a, int dev, int ctas, int rows, c
 
 namespace {
 
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kAuxWarp = 11;   // two product warps, one per softmax warpgroup
+constexpr int kProducerWarp = 8, kMmaWarp = 9;   // two product warps, one per softmax warpgroup
 constexpr uint32_t kTmemCols = 512;
 
 // DP: the head's channels rounded up to 64 or 128.
 template <bool F8, int DP>
 struct Lay {
-    static constexpr int kAuxWarps = F8 ? 4 : 1;   // V converters; the cleaner of V's last tiles
-    static constexpr int kThreads = (kAuxWarp + kAuxWarps) * 32;
+    static constexpr int kAux = F8 ? 12 : 11;      // V's four converters; the cleaner of its last tiles
+    static constexpr int kThreads = F8 ? 512 : 384, kGroups = 1;
+    // a thread's registers: the softmax's hold a row's 128 scores; the sum is what is launched with
+    static constexpr int kOther = 56, kSoft = F8 ? 200 : 224;
+    static constexpr int kRegs = 256 * kSoft + (kThreads - 256) * kOther;
     static constexpr uint32_t kQTile = F8 ? 2 * 16384 : 128 * DP * 2;
     static constexpr uint32_t kKSlot = F8 ? 16384 : 128 * DP * 2;
     static constexpr uint32_t kVSlot = 128 * DP * 2;
@@ -71,7 +74,7 @@ struct Lay {
                          bS = bCF + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
                          bDrain = bFix + 4, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
-    static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
+    static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);    // F8: float [2], the running power of two
     static constexpr uint32_t oQs = oSigma + (F8 ? 32 : 0);         // F8: float [2][128], row factors
@@ -190,7 +193,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 1;
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -218,8 +221,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
         *abort_flag = 0;
-        *v_issued = 0;
-        *k_issued = 0;
+        *v_issued = *k_issued = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -232,13 +234,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
-    pdl_wait();
-    pdl_trigger();
-
-    Walk w;
-    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     const int G = a.group;
 
+    if (warp >= 8) {
+    regs_down<L::kOther>();
+    pdl_wait();
+    pdl_trigger();
+    Walk w;
+    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     if (warp == kProducerWarp) {
         produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -317,13 +320,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         __syncwarp();
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
-    } else if (warp >= kAuxWarp) {
+    } else if (warp >= L::kAux) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag, v_issued);
+            convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, v_issued);
         else
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
+    }
     } else {
         // ---------------------------------------------------------------- softmax, two warpgroups
+        regs_up<L::kSoft>();
+        Walk w;
         const int g = warp >> 2, r = (warp & 3) * 32 + lane;   // lane quarter = warp % 4
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + g * kTile, o_addr = tmem + lanes + 256 + g * DP;
@@ -333,10 +339,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         float4 *const exch = reinterpret_cast<float4 *>(smem);   // [2][128], over Q when Q is done with
         uint32_t sc = 0, scnt = 0;
         bool ok = true;
+        // The first item is a dry one, as in the kernel for few rows: no waits, no arrivals, no rows.
+        bool dry = true;
+        w.s.n = w.s.t0 = 0;
+        w.s.ctx = kTile;
+        w.b = w.hk = w.pair = w.lo = w.index = 0;
+        w.hi = 5;
+        w.whole = true;
         while (true) {
-            const bool more = walk_next(a, w);
+            const bool more = dry || walk_next(a, w);
             // the previous item's exchange has been read; everybody leaves together
-            if (softmax_any(!ok || *abort_flag != 0) || !more) break;
+            if (softmax_any(!dry && (!ok || *abort_flag != 0)) || !more) break;
             const int R = w.s.n * G, row0 = w.pair * 2 * kTile;
             const bool two = R - row0 > kTile;
             const int T = w.hi - w.lo, U = two ? 2 * T : T;
@@ -363,7 +376,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int token = live ? w.s.t0 + row / G : 0, head = w.hk * G + (live ? row % G : 0);
             uint64_t M = 0;
             if (live) M = a.mask != nullptr ? a.mask[token] : (2ull << (row / G)) - 1ull;
-            warp_arrive(bar(L::bQ));
+            if (!dry) warp_arrive(bar(L::bQ));
             if (F8) named_barrier(3, 256);   // the row factors, before other threads' are read
             const float cs = F8 ? a.scale_log2 * qs[mt * 128 + r] : a.scale_log2;
             float m = ninf(), l = 0.0f, sigma = 1.0f;
@@ -374,14 +387,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (edge) seen_bits(M, w.s, tt, see);
                 const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no & 1u;
                 const float *const ks = scale_s + sb * 256, *const vs = ks + 128;
-                if (F8 && !(ok = wait_for(bar(L::bCF + sb), (tile_no >> 1) & 1u, abort_flag, a.err, limit))) break;
-                if (!(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
+                if (F8 && !dry && !(ok = wait_for(bar(L::bCF + sb), (tile_no >> 1) & 1u, abort_flag, a.err, limit))) break;
+                if (!dry && !(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
                 ++sc;
                 tc_fence_after();
                 float mx = edge ? tile_max<F8, true>(s_addr, ks, see) : tile_max<F8, false>(s_addr, ks, see);
                 mx *= cs;   // cs > 0; -inf stays
                 float keep = 1.0f;
-                bool move = u < 2 || mx - m > kLazy;
+                bool move = u < 2 || dry || mx - m > kLazy;
                 const float sigma_new = F8 ? sigma_s[sb] : 1.0f;   // the tile's value scales are relative to it
                 if (F8 && sigma_new != sigma) move = true;
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -408,10 +421,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                           : tile_weights<F8, false>(s_addr, ks, vs, cs, ref, see);
                 tmem_wait_st();
                 tc_fence_before();
-                warp_arrive(bar(L::bP + g));
+                if (!dry) warp_arrive(bar(L::bP + g));
             }
             // ------------------------------------------------------------ the item's end
-            ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
+            if (!dry) ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             scnt += T;
             const float gain = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
@@ -436,9 +449,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const float inv = none ? 0.0f : 1.0f / ll;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
-            uint32_t any_bad = 0;
+            uint32_t any_bad = 0;   // of parts that reach past the context: there the products waited for the words
+            if (!dry && w.hi * kTile > w.s.ctx) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+                for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+            }
             const int64_t out_off = static_cast<int64_t>(token) * a.out.token_stride + static_cast<int64_t>(head) * a.out.head_stride;
             for (int c = c0; c < c1; c += 32) {
                 __syncwarp();
@@ -499,6 +514,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 } else {
                     part_ml<DP>(a, gridDim.x, slot, mt)[r] = make_float2(mm, ll);
                 }
+            }
+            if (dry) {
+                dry = false;
+                sc = scnt = 0;
+                pdl_wait();
+                pdl_trigger();
+                walk_begin(a, w, false);
             }
         }
     }
@@ -646,7 +668,8 @@ cudaError_t launch_wide(const TreeArgs &a, int dev, int ctas, int rows, const CU
         std::lock_guard<std::mutex> lock(g_mu);
         bool &set = g_dev[dev & 63].set[(F8 ? 2 : 0) + (DP == 128 ? 1 : 0)];
         if (!set) {
-            const cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<F8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+            cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<F8, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+            if (e == cudaSuccess) e = check_registers(tree_attn_kernel<F8, DP>, L::kThreads, L::kRegs);
             if (e != cudaSuccess) return e;
             set = true;
         }

@@ -28,7 +28,11 @@ constexpr int kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 11, kAuxWarp = 12;
 
 template <bool F8, int DP, int NT>
 struct Lay {
-    static constexpr int kThreads = (kAuxWarp + (F8 ? 4 : 1)) * 32;
+    // bf16: a cleaner (and three idle warps of its warpgroup); F8: two groups of four converters
+    static constexpr int kThreads = F8 ? 640 : 512, kGroups = F8 ? 2 : 1;
+    // a thread's registers: the softmax's hold a position's NT scores and NT sums
+    static constexpr int kOther = F8 ? 48 : 56, kSoft = F8 ? 168 : 200;
+    static constexpr int kRegs = 256 * kSoft + (kThreads - 256) * kOther;
     static constexpr uint32_t kKSlot = F8 ? 16384 : 128 * DP * 2;
     static constexpr uint32_t kVSlot = 128 * DP * 2;
     static constexpr uint32_t kStage = F8 ? 16384 : 0;
@@ -38,9 +42,9 @@ struct Lay {
     // slots it waits for are its own and their parities name the use.  An item's first tiles, and a
     // ring of 3, may wait on a slot the other warp is not done with: there k_issued and v_issued,
     // which the filler sets when the previous use is over, are waited for first.
-    static constexpr int NK = DP == 64 ? 4 : (F8 && NT < 64 ? 4 : 2);
+    static constexpr int NK = DP == 64 ? 4 : (F8 ? 3 : 2);
     static constexpr int NV = F8 ? 2 : (DP == 64 ? 4 : (NT < 64 ? 3 : 2));
-    static constexpr int NS = !F8 ? 0 : (DP == 64 ? 4 : 3) - (NT < 64 ? 0 : 1);
+    static constexpr int NS = !F8 ? 0 : (NT < 64 ? 4 : 2);   // even: a slot is one converter group's
     static constexpr int kUsers = 1, kVReaders = F8 ? 4 : 1;
     static constexpr uint32_t oK = 0, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot, oP = oS + NS * kStage,
                               oQ = oP + 2 * kP, oSSc = oQ + 2 * kQ, oBar = oSSc + NS * 1024;
@@ -48,7 +52,7 @@ struct Lay {
                          bS = bCF + 2, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
                          bQE = bQ + 2, bO = bQE + 2, bOF = bO + 1, bFix = bOF + 1, bDrain = bFix + 4, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
-    static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
+    static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);   // F8: float [2]
     static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // F8: float [2 items][NT]: score to log2 units
@@ -150,7 +154,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 1;
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2;   // v_issued: one word per converter group
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -184,8 +188,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
         *abort_flag = 0;
-        *v_issued = 0;
-        *k_issued = 0;
+        v_issued[0] = v_issued[1] = *k_issued = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -198,13 +201,14 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
-    pdl_wait();
-    pdl_trigger();
-
-    Walk w;
-    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     const int G = a.group;
 
+    if (warp >= 8) {
+    regs_down<L::kOther>();
+    pdl_wait();
+    pdl_trigger();
+    Walk w;
+    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     if (warp == kProducerWarp) {
         produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
@@ -223,7 +227,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const uint32_t c = base_tile + t, slot = c % L::NK;
                 // the warpgroup has taken this buffer's previous scores
                 ok = (sc == 0 || wait_for(bar(L::bSFree + g), (sc - 1) & 1u, abort_flag, a.err, limit)) &&
-                     (t >= L::NK || wait_count(k_issued, c + 1, abort_flag, a.err, limit)) &&
+                     ((L::NK % 2 == 0 && t >= L::NK) || wait_count(k_issued, c + 1, abort_flag, a.err, limit)) &&
                      wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
                 if (!ok) return;
                 ++sc;
@@ -253,7 +257,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (t + 2 < T) qk(t + 2);   // while the warpgroup weighs tile t
                 if (!ok) break;
                 const uint32_t c = base_tile + t, slot = c % L::NV;
-                ok = ((L::NV % 2 == 0 && t >= L::NV) || wait_count(v_issued, c + 1, abort_flag, a.err, limit)) &&
+                ok = ((L::NV % 2 == 0 && t >= L::NV) || wait_count(v_issued + (F8 ? c & 1u : 0u), c + 1, abort_flag, a.err, limit)) &&
                      wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
                 if (!F8 && ok && w.lo + t >= edge0) {   // V's cleaner has been over it
                     const uint32_t f = base_fix + (w.lo + t - edge0);
@@ -298,45 +302,55 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const int R = w.s.n * G;
             constexpr int C = DP / 8, PER = 32 / C;   // lanes of a row, rows of a step
             const int c = lane % C;
-            uint4 x[NT / PER];
+            // Rows beyond R are zeros: their columns go nowhere, but their scores have a say in when O
+            // is rescaled.  Four steps' loads at a time, in a loop: this code runs once an item, and
+            // what runs once should be short.
+#pragma unroll 1
+            for (int r0 = 0; r0 < NT; r0 += 4 * PER) {
+                uint4 x[4];
 #pragma unroll
-            for (int i = 0; i < NT / PER; ++i) {   // in flight before the buffer is free
-                const int row = i * PER + lane / C;
-                x[i] = make_uint4(0, 0, 0, 0);
-                if (row < R && c * 8 < a.cache.dim)
-                    x[i] = *reinterpret_cast<const uint4 *>(
-                        static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
-                        static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r0 + i * PER + lane / C;
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (row < R && c * 8 < a.cache.dim)
+                        x[i] = *reinterpret_cast<const uint4 *>(
+                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
+                            static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+                }
+                if (r0 == 0) ok = wait_for(bar(L::bQE + qb), ((w.index >> 1) & 1u) ^ 1u, abort_flag, a.err, limit);
+                if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int row = r0 + i * PER + lane / C;
+                    const uint4 y = i == 0 ? x[0] : (i == 1 ? x[1] : (i == 2 ? x[2] : x[3]));
+                    float unscale;
+                    if (row - lane / C < NT) {   // the step lies within the operand
+                        store_query<F8, DP>(smem + L::oQ + qb * L::kQ, NT, row, c, y, unscale);
+                        if (F8 && c == 0) cs_all[qb * NT + row] = a.scale_log2 * unscale;
+                    }
+                }
             }
-            uint64_t M[(NT + 31) / 32];
-#pragma unroll
-            for (int i = 0; i < (NT + 31) / 32; ++i) {
-                const int row = i * 32 + lane;
-                M[i] = 0;
-                if (row < R) M[i] = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
-                if (w.s.n < 64) M[i] &= (1ull << w.s.n) - 1ull;
+            if (!ok) break;
+#pragma unroll 1
+            for (int row = lane; row < NT; row += 32) {
+                uint64_t M = 0;
+                if (row < R) M = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
+                if (w.s.n < 64) M &= (1ull << w.s.n) - 1ull;
+                mask_all[qb * NT + row] = M;
             }
-            if (!(ok = wait_for(bar(L::bQE + qb), ((w.index >> 1) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
-#pragma unroll
-            for (int i = 0; i < NT / PER; ++i) {
-                const int row = i * PER + lane / C;
-                float unscale;
-                store_query<F8, DP>(smem + L::oQ + qb * L::kQ, NT, row, c, x[i], unscale);
-                if (F8 && c == 0) cs_all[qb * NT + row] = a.scale_log2 * unscale;
-            }
-#pragma unroll
-            for (int i = 0; i < (NT + 31) / 32; ++i)
-                if (i * 32 + lane < NT) mask_all[qb * NT + i * 32 + lane] = M[i];
             fence_proxy_async_smem();
             warp_arrive(bar(L::bQ + qb));
         }
     } else if (warp >= kAuxWarp) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - kAuxWarp, abort_flag, v_issued);
-        else
+            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, v_issued);
+        else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
+    }
     } else {
         // ---------------------------------------------------------------- softmax, two warpgroups
+        regs_up<L::kSoft>();
+        Walk w;
         const int g = warp >> 2, q4 = warp & 3, p = q4 * 32 + lane;   // this thread's position of a tile, and channel of O
         const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
         const uint32_t s_addr = tmem + lanes + g * NT, o_addr = tmem + lanes + (2 + g) * NT;
@@ -348,17 +362,26 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         float *const unit_s = reinterpret_cast<float *>(smem + L::oUnit);
         uint8_t *const p_buf = smem + L::oP + g * L::kP;
         uint32_t sc = 0, tiles = 0;   // this warpgroup's tiles; all tiles
-        bool dead = false;            // a wait gave up: only the barriers are kept
+        bool dead = true;             // no waits, no arrivals: a wait gave up, or the dry item
+        // The first item is a dry one: every path once, on whatever shared memory and TMEM hold,
+        // without rows to write, while the previous kernel ends and the first tiles are on their way.
+        // It brings the code into the instruction caches (8 us of a short call otherwise).
+        bool dry = true;
+        w.s.n = w.s.t0 = 0;
+        w.s.ctx = kTile;
+        w.b = w.hk = w.lo = w.index = 0;
+        w.hi = 3;
+        w.whole = true;
         while (true) {
-            const bool more = walk_next(a, w);
+            const bool more = dry || walk_next(a, w);
             // the previous item's shared words have been read; everybody leaves together
-            if (bar_any(1, 256, dead || *abort_flag != 0) || !more) break;
+            if (bar_any(1, 256, !dry && (dead || *abort_flag != 0)) || !more) break;
             const int R = w.s.n * G, T = w.hi - w.lo;
             const uint32_t qb = w.index & 1u;
             const float *const cs_s = reinterpret_cast<const float *>(smem + L::oCs) + qb * NT;
             const uint64_t *const mask_s = reinterpret_cast<const uint64_t *>(smem + L::oMask) + qb * NT;
             if (p < NT) nm_s[p] = -kNone;
-            dead = !wait_for(bar(L::bQ + qb), (w.index >> 1) & 1u, abort_flag, a.err, limit);
+            if (!dry) dead = !wait_for(bar(L::bQ + qb), (w.index >> 1) & 1u, abort_flag, a.err, limit);
             named_barrier(2 + g, 128);
             F2 l2[NT / 2];
 #pragma unroll
@@ -410,7 +433,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 // any score far above its row's maximum so far?  (That is kNone before a row has
                 // seen anything, so that its first finite score is.)
-                bool move = t < 2 || (F8 && sigma_new != sigma);
+                bool move = t < 2 || dry || (F8 && sigma_new != sigma);
                 if (t >= 2) {
                     float over = ninf();
 #pragma unroll
@@ -551,11 +574,13 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             tmem_wait_ld();
             tc_fence_before();
-            warp_arrive(bar(L::bOF));   // the next item's products may begin
+            if (!dry) warp_arrive(bar(L::bOF));   // the next item's products may begin
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
-            uint32_t any_bad = 0;
+            uint32_t any_bad = 0;   // of parts that reach past the context: there the products waited for the words
+            if (!dry && w.hi * kTile > w.s.ctx) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+                for (int i = 0; i < 8; ++i) any_bad |= bad[i];
+            }
             if (p < a.cache.dim) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
@@ -593,7 +618,15 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             __syncwarp();
-            warp_arrive(bar(L::bQE + qb));   // masks and queries of this item are done with
+            if (!dry) {
+                warp_arrive(bar(L::bQE + qb));   // masks and queries of this item are done with
+            } else {
+                dry = dead = false;
+                sc = tiles = 0;
+                pdl_wait();
+                pdl_trigger();
+                walk_begin(a, w, false);
+            }
         }
     }
     tc_fence_before();
@@ -615,7 +648,8 @@ cudaError_t launch(const TreeArgs &a, int dev, int ctas, int rows, const CUtenso
         std::lock_guard<std::mutex> lock(g_mu);
         bool &set = g_set[dev & 63][(F8 ? 6 : 0) + (DP == 128 ? 3 : 0) + (NT == 16 ? 0 : NT / 32)];
         if (!set) {
-            const cudaError_t e = cudaFuncSetAttribute(tree_narrow_kernel<F8, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+            cudaError_t e = cudaFuncSetAttribute(tree_narrow_kernel<F8, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+            if (e == cudaSuccess) e = check_registers(tree_narrow_kernel<F8, DP, NT>, L::kThreads, L::kRegs);
             if (e != cudaSuccess) return e;
             set = true;
         }

@@ -94,6 +94,16 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Registers of a warpgroup's threads from here on (all its warps call).
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Two fp32 operations in one instruction.
 struct F2 {
     uint64_t v;
@@ -144,14 +154,22 @@ __device__ __forceinline__ bool softmax_any(bool v) {
     return r != 0;
 }
 
-// warp_wait with its loop out of line: the kernels have many waits, and their code should stay in
-// the instruction caches.
-__device__ __noinline__ bool wait_loop(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *err, long long limit) {
-    return mbar_wait(bar, parity, abort, err, limit);
-}
+// warp_wait with less code: the kernels have many waits, and their code should stay in the
+// instruction caches.  (Out of line it cannot be: a function call ends the register shares.)
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int32_t *abort, int32_t *err, long long limit) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xFFFFFFFFu, wait_loop(bar, parity, abort, err, limit));
+    bool ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xFFFFFFFFu, ok)) return true;
+    const long long t0 = clock64();
+    do {
+        const bool late = clock64() - t0 > limit;
+        if (__any_sync(0xFFFFFFFFu, late || *abort != 0)) {
+            *abort = 1;
+            if (late) record_error(err, MOE_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+        if (!ok) ok = mbar_try_wait(bar, parity);
+    } while (!__all_sync(0xFFFFFFFFu, ok));
+    return true;
 }
 
 // Bounded warp-wide wait until *p has reached v, under mbar_wait's rules.
@@ -214,51 +232,59 @@ struct Walk {
 // The whole warp calls these; the outcome is uniform.
 __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool report) {
     const int lane = static_cast<int>(threadIdx.x & 31);
-    long long total = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-        long long x = 0;
-        if (b0 + lane < a.seqs) {
-            const Seq s = load_seq(a, b0 + lane);
-            if (s.bad && report) record_error(a.err, MOE_ERR_BAD_ID);
-            x = seq_work(a, s);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
-        total += x;
-    }
-    const int C = used_ctas(total, gridDim.x), c = static_cast<int>(blockIdx.x);
-    w.at = c < C ? range_lo(total, c, C) : 0;
-    w.end = c < C ? range_lo(total, c + 1, C) : 0;
     w.index = -1;
-    w.b = 0;
-    w.hk = 0;
-    w.pair = 0;
-    w.item0 = 0;
-    if (w.at >= w.end) return;
-    long long before = 0;   // tiles of the sequences before
-    for (int b0 = 0;; b0 += 32) {
-        long long x = 0;
-        if (b0 + lane < a.seqs) x = seq_work(a, load_seq(a, b0 + lane));
-        long long incl = x;
+    w.b = w.hk = w.pair = 0;
+    w.at = w.end = w.item0 = 0;
+    // tiles of the list, 32 sequences a step; the last step's stay in registers (all of them, when
+    // there is one step)
+    Seq mine;
+    long long total = 0, x = 0, incl = 0;
+    auto step = [&](int b0) {
+        x = 0;
+        if (b0 + lane < a.seqs) {
+            mine = load_seq(a, b0 + lane);
+            x = seq_work(a, mine);
+        }
+        incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
             if (lane >= o) incl += y;
         }
+    };
+    mine.bad = false;
+    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
+        step(b0);
+        if (b0 + lane < a.seqs && mine.bad && report) record_error(a.err, MOE_ERR_BAD_ID);
+        total += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    const int C = used_ctas(total, gridDim.x), c = static_cast<int>(blockIdx.x);
+    if (c >= C) return;
+    w.at = range_lo(total, c, C);
+    w.end = range_lo(total, c + 1, C);
+    long long before = 0;   // tiles of the sequences before
+    for (int b0 = 0;; b0 += 32) {
+        if (a.seqs > 32) step(b0);
         const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + incl > w.at);
         if (past != 0) {
             const int l = __ffs(past) - 1;
             w.b = b0 + l;
             before += __shfl_sync(0xFFFFFFFFu, incl - x, l);
+            w.s.t0 = __shfl_sync(0xFFFFFFFFu, mine.t0, l);
+            w.s.n = __shfl_sync(0xFFFFFFFFu, mine.n, l);
+            w.s.ctx = __shfl_sync(0xFFFFFFFFu, mine.ctx, l);
+            w.s.len = __shfl_sync(0xFFFFFFFFu, mine.len, l);
+            w.s.tiles = __shfl_sync(0xFFFFFFFFu, mine.tiles, l);
+            w.s.pairs = __shfl_sync(0xFFFFFFFFu, mine.pairs, l);
+            w.s.bad = false;
             break;
         }
         before += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    w.s = load_seq(a, w.b);
-    const long long item = (w.at - before) / w.s.tiles;
-    w.item0 = before + item * w.s.tiles;
-    w.hk = static_cast<int>(item / w.s.pairs);
-    w.pair = static_cast<int>(item % w.s.pairs);
+    const int item = static_cast<int>((w.at - before) / w.s.tiles);
+    w.item0 = before + static_cast<long long>(item) * w.s.tiles;
+    w.hk = item / w.s.pairs;
+    w.pair = item % w.s.pairs;
 }
 // Sets the next item's part; false at the end of the range.
 __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
@@ -558,9 +584,11 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t x) {
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
 // layout, the scales into the softmax's double buffer.  The value scales there are relative to
 // sigma, a power of two at or above all of the item's finite ones so far, times kWeightUp.  What
-// clean_values does for bf16 is done on the way.
+// clean_values does for bf16 is done on the way.  With two groups of four warps each takes every
+// other tile (of one softmax warpgroup, whose sigma it is; rings are even, so that a slot is one
+// group's).
 template <typename L, int DP>
-__device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw,
+__device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw, int group,
                                                volatile int32_t *abort_flag, volatile uint32_t *v_issued) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
@@ -572,10 +600,13 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
     bool ok = true;
     while (ok && walk_next(a, w)) {
         uint32_t *const bad = reinterpret_cast<uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
-        if (lane < 2) bad[lane * 4 + cw] = 0;   // a warp's words are its own
+        // a warp's words are its own: with two groups, the tiles of one parity
+        const int odd = L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(w.lo) ^ static_cast<uint32_t>(group)) & 1u) : 0;
+        if (lane < 2 && (L::kGroups == 1 || lane == odd)) bad[lane * 4 + cw] = 0;
         __syncwarp();
         float sigma = 7.888609e-31f;   // 2^-100: below any value scale that counts
         for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
+            if (L::kGroups == 2 && (cnt & 1u) != static_cast<uint32_t>(group)) continue;
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
             const uint32_t ss = cnt % L::NS, slot = cnt % L::NV;
             if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
@@ -596,7 +627,7 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             // the V slot is free when its previous product is done, and that came after the softmax
             // had read the scales of that tile: the scales' buffer goes with the slot
             if (!(ok = wait_for(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
-            if (cw == 0 && lane == 0) *v_issued = cnt + 1;   // the slot's previous use is over
+            if (cw == 0 && lane == 0) v_issued[L::kGroups == 2 ? group : 0] = cnt + 1;   // the slot's previous use is over
             scale_s[slot * 256 + j] = ks;
             scale_s[slot * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
             if (lane == 0) sigma_s[slot] = sigma;   // the same from every warp
@@ -648,6 +679,16 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
 }
 
 // ------------------------------------------------------------------ host side
+// The warpgroups' register shares must fit what a block is launched with: a larger share would be
+// waited for without end.
+template <typename K>
+cudaError_t check_registers(K kernel, int threads, int shares) {
+    cudaFuncAttributes at;
+    const cudaError_t e = cudaFuncGetAttributes(&at, kernel);
+    if (e != cudaSuccess) return e;
+    return at.numRegs * threads >= shares ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
