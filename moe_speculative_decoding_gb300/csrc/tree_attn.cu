@@ -62,23 +62,24 @@ struct Lay {
     static constexpr uint32_t kStage = F8 ? 16384 : 0;
     // A product warp waits only for its own tiles, every other one when the warpgroups alternate:
     // with two slots these are all of one slot's uses, so that the slot's parity names the use.
-    static constexpr int NK = 2, NV = 2, NS = F8 ? 3 : 0;
+    static constexpr int NK = 2, NV = 2, NS = F8 ? 3 : 0, NC = 4;
     static constexpr int kUsers = 2;               // products that release a slot
     static constexpr int kVReaders = F8 ? 4 : 1;   // arrivals that fill a V slot
     static constexpr uint32_t oK = 2 * kQTile, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot;
     static constexpr uint32_t oSSc = oS + NS * kStage;             // F8: float [NS][ks, vs][128], landing
     static constexpr uint32_t oBar = oSSc + NS * 1024;
-    // barriers: k_full, k_empty, v_full, v_empty, st_full, st_empty, sc_full[2],
+    // barriers: k_full, k_empty, v_full, v_empty, st_full, st_empty, sc_full[NC], sc_empty[NC],
     // s_full[2], p_ready[2], q_ready, o_full, v_fix[4], drain
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
-                         bS = bCF + 2, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
-                         bDrain = bFix + 4, kBars = bDrain + 1;
+                         bCE = bCF + NC, bS = bCE + NC, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
+                         bDrain = bFix + 4, bW = bDrain + 1, kBars = bW + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
-    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
-    static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);    // F8: float [2], the running power of two
+    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
+    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);    // F8: float [NC], the running power of two
     static constexpr uint32_t oQs = oSigma + (F8 ? 32 : 0);         // F8: float [2][128], row factors
-    static constexpr uint32_t kSmem = oQs + (F8 ? 1024 : 0);
+    static constexpr uint32_t oWalk = oQs + (F8 ? 1024 : 0);        // Walk
+    static constexpr uint32_t kSmem = oWalk + 128;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -211,8 +212,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             mbar_init(bar(L::bSF + i), 1);
             mbar_init(bar(L::bSE + i), 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::NC; ++i) {
             mbar_init(bar(L::bCF + i), 4);
+            mbar_init(bar(L::bCE + i), 8);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::bS + i), 1);
             mbar_init(bar(L::bP + i), 4);
         }
@@ -220,6 +224,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(L::bO), 2);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
+        mbar_init(bar(L::bW), 1);
         *abort_flag = 0;
         *v_issued = *k_issued = 0;
         fence_mbar_init();
@@ -234,6 +239,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
+    Walk *const walk_s = reinterpret_cast<Walk *>(smem + L::oWalk);
     const int G = a.group;
 
     if (warp >= 8) {
@@ -241,13 +247,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     pdl_wait();
     pdl_trigger();
     Walk w;
-    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     if (warp == kProducerWarp) {
+        walk_share(a, w, walk_s, bar(L::bW));
         produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in
         // line behind the other's, and its O += P V precedes the next S over the same columns.
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         const int g = warp - kMmaWarp;
         const uint32_t s_col = tmem + g * kTile, o_col = tmem + 256 + g * DP;
         uint32_t base_tile = 0, base_fix = 0, pc = 0, items = 0;
@@ -321,6 +328,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
     } else if (warp >= L::kAux) {
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         if constexpr (F8)
             convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, v_issued);
         else
@@ -385,9 +393,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 const bool edge = (tt + 1) * kTile > w.s.ctx;
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
                 if (edge) seen_bits(M, w.s, tt, see);
-                const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no & 1u;
+                const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no % L::NC;
                 const float *const ks = scale_s + sb * 256, *const vs = ks + 128;
-                if (F8 && !dry && !(ok = wait_for(bar(L::bCF + sb), (tile_no >> 1) & 1u, abort_flag, a.err, limit))) break;
+                if (F8 && !dry && !(ok = wait_for(bar(L::bCF + sb), (tile_no / L::NC) & 1u, abort_flag, a.err, limit))) break;
                 if (!dry && !(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
                 ++sc;
                 tc_fence_after();
@@ -421,7 +429,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                           : tile_weights<F8, false>(s_addr, ks, vs, cs, ref, see);
                 tmem_wait_st();
                 tc_fence_before();
-                if (!dry) warp_arrive(bar(L::bP + g));
+                if (!dry) {
+                    warp_arrive(bar(L::bP + g));
+                    if (F8) warp_arrive_cnt(bar(L::bCE + sb), two ? 1 : 2);   // the tile's scales are read
+                }
             }
             // ------------------------------------------------------------ the item's end
             if (!dry) ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
@@ -519,8 +530,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 dry = false;
                 sc = scnt = 0;
                 pdl_wait();
-                pdl_trigger();
-                walk_begin(a, w, false);
+                walk_take(a, w, walk_s, bar(L::bW), abort_flag);
             }
         }
     }

@@ -45,23 +45,24 @@ struct Lay {
     static constexpr int NK = DP == 64 ? 4 : (F8 ? 3 : 2);
     static constexpr int NV = F8 ? 2 : (DP == 64 ? 4 : (NT < 64 ? 3 : 2));
     static constexpr int NS = !F8 ? 0 : (NT < 64 ? 4 : 2);   // even: a slot is one converter group's
-    static constexpr int kUsers = 1, kVReaders = F8 ? 4 : 1;
+    static constexpr int NC = 4, kUsers = 1, kVReaders = F8 ? 4 : 1;
     static constexpr uint32_t oK = 0, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot, oP = oS + NS * kStage,
                               oQ = oP + 2 * kP, oSSc = oQ + 2 * kQ, oBar = oSSc + NS * 1024;
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
-                         bS = bCF + 2, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
-                         bQE = bQ + 2, bO = bQE + 2, bOF = bO + 1, bFix = bOF + 1, bDrain = bFix + 4, kBars = bDrain + 1;
+                         bCE = bCF + NC, bS = bCE + NC, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
+                         bQE = bQ + 2, bO = bQE + 2, bOF = bO + 1, bFix = bOF + 1, bW = bFix + 4, bDrain = bW + 1, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
-    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [2][ks, vs][128]
-    static constexpr uint32_t oSigma = oScale + (F8 ? 2048 : 0);   // F8: float [2]
+    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
+    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);   // F8: float [NC]
     static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // F8: float [2 items][NT]: score to log2 units
     static constexpr uint32_t oM = oCs + (F8 ? 2 * NT * 4 : 0);    // float [2][NT]: minus the maxima of a warpgroup
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
     static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
     static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [2 items][NT]: the rows' tree masks
     static constexpr uint32_t oUnit = oMask + 2 * NT * 8;          // float [2]: a warpgroup's accumulator unit
-    static constexpr uint32_t kSmem = oUnit + 16;
+    static constexpr uint32_t oWalk = oUnit + 16;                  // Walk
+    static constexpr uint32_t kSmem = oWalk + 128;
     static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -123,10 +124,12 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
     return r != 0;
 }
 
-// Sums v[c] over the warp's lanes: afterwards lane l holds in v[0 .. NT/32) the sums of columns
-// l * NT/32 + i (NT = 16: of column l / 2 in v[0]).  The order of additions is fixed.
-template <int NT>
+// Sums (or maxima of) v[c] over the warp's lanes: afterwards lane l holds in v[0 .. NT/32) those of
+// columns l * NT/32 + i (NT = 16: of column l / 2 in v[0]).  A halving exchange: about NT shuffles in
+// all, where a reduction instruction per column took 100 cycles each.  The order is fixed.
+template <int NT, bool MAX>
 __device__ __forceinline__ void warp_columns(float (&v)[NT], int lane) {
+    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
     for (int o = 16, n = NT; o > 0; o >>= 1) {
         if (n > 1) {
@@ -136,12 +139,21 @@ __device__ __forceinline__ void warp_columns(float (&v)[NT], int lane) {
             for (int i = 0; i < NT / 2; ++i) {
                 if (i < n) {
                     const float send = up ? v[i] : v[i + n], kept = up ? v[i + n] : v[i];
-                    v[i] = kept + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+                    v[i] = join(kept, __shfl_xor_sync(0xFFFFFFFFu, send, o));
                 }
             }
         } else {
-            v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+            v[0] = join(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
         }
+    }
+}
+template <int NT>
+__device__ __forceinline__ void store_columns(float *to, const float (&v)[NT], int lane) {
+    if constexpr (NT == 16) {
+        if ((lane & 1) == 0) to[lane / 2] = v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) to[lane * (NT / 32) + i] = v[i];
     }
 }
 
@@ -172,8 +184,11 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mbar_init(bar(L::bSF + i), 1);
             mbar_init(bar(L::bSE + i), 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::NC; ++i) {
             mbar_init(bar(L::bCF + i), 4);
+            mbar_init(bar(L::bCE + i), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::bS + i), 1);
             mbar_init(bar(L::bSFree + i), 4);
             mbar_init(bar(L::bP + i), 4);
@@ -187,6 +202,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_init(bar(L::bO), 2);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
+        mbar_init(bar(L::bW), 1);
         *abort_flag = 0;
         v_issued[0] = v_issued[1] = *k_issued = 0;
         fence_mbar_init();
@@ -201,6 +217,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
+    Walk *const walk_s = reinterpret_cast<Walk *>(smem + L::oWalk);
     const int G = a.group;
 
     if (warp >= 8) {
@@ -208,11 +225,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     pdl_wait();
     pdl_trigger();
     Walk w;
-    walk_begin(a, w, blockIdx.x == 0 && warp == kMmaWarp);
     if (warp == kProducerWarp) {
+        walk_share(a, w, walk_s, bar(L::bW));
         produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         const int g = warp - kMmaWarp;
         const uint32_t s_col = tmem + g * NT, o_col = tmem + (2 + g) * NT;
         const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
@@ -294,6 +312,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         __syncwarp();
     } else if (warp == kQueryWarp) {
         // ---------------------------------------------------------------- queries, an item ahead
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         uint64_t *const mask_all = reinterpret_cast<uint64_t *>(smem + L::oMask);
         float *const cs_all = reinterpret_cast<float *>(smem + L::oCs);
         bool ok = true;
@@ -342,6 +361,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             warp_arrive(bar(L::bQ + qb));
         }
     } else if (warp >= kAuxWarp) {
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         if constexpr (F8)
             convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, v_issued);
         else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
@@ -390,10 +410,10 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             for (int t = g; t < T; t += 2) {
                 const int tt = w.lo + t, pos = tt * kTile + p;
                 const bool edge = (tt + 1) * kTile > w.s.ctx;
-                const uint32_t no = tiles + t, sb = no & 1u;
+                const uint32_t no = tiles + t, sb = no % L::NC;
                 float ks = 1.0f, vs = 1.0f, sigma_new = 1.0f;
                 uint32_t x[NT];
-                if (F8 && !dead) dead = !wait_for(bar(L::bCF + sb), (no >> 1) & 1u, abort_flag, a.err, limit);
+                if (F8 && !dead) dead = !wait_for(bar(L::bCF + sb), (no / L::NC) & 1u, abort_flag, a.err, limit);
                 if (!dead) dead = !wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
                 tc_fence_after();
                 tmem_ld_cols<NT>(s_addr, x);
@@ -406,7 +426,10 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 tmem_wait_ld();
                 tc_fence_before();
-                if (!dead) warp_arrive(bar(L::bSFree + g));
+                if (!dead) {
+                    warp_arrive(bar(L::bSFree + g));
+                    if (F8) warp_arrive(bar(L::bCE + sb));
+                }
                 // scores in log2 units; what a row does not see is -inf
                 const F2 ks2 = f2(ks, ks);
 #pragma unroll
@@ -447,17 +470,13 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     move = move || over > kLazy;
                 }
                 if (bar_any(2 + g, 128, move)) {
-                    // the columns' maxima over the 128 positions: per warp by reduction of ordered
-                    // integers (NaN, above every number there, is left out), then over the four
+                    // the columns' maxima over the 128 positions (NaN left out): over the warp's lanes,
+                    // then over the four warps
+                    float top[NT];
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const float s = __uint_as_float(x[c]);
-                        const int b = static_cast<int>(x[c]);
-                        int key = b ^ (b >> 31 & 0x7fffffff);
-                        if (s != s) key = static_cast<int>(0x807fffffu);   // as -inf
-                        key = __reduce_max_sync(0xFFFFFFFFu, key);
-                        if (lane == (c & 31)) red_s[q4 * NT + c] = __int_as_float(key ^ (key >> 31 & 0x7fffffff));
-                    }
+                    for (int c = 0; c < NT; ++c) top[c] = __uint_as_float(x[c]);
+                    warp_columns<NT, true>(top, lane);
+                    store_columns<NT>(red_s + q4 * NT, top, lane);
                     named_barrier(2 + g, 128);
                     if (p < NT) {
                         const float old = -nm_s[p];
@@ -528,13 +547,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             float l[NT];
 #pragma unroll
             for (int c = 0; c < NT; c += 2) f2_get(l2[c / 2], l[c], l[c + 1]);
-            warp_columns<NT>(l, lane);
-            if constexpr (NT == 16) {
-                if ((lane & 1) == 0) red_s[q4 * NT + lane / 2] = l[0];
-            } else {
-#pragma unroll
-                for (int i = 0; i < NT / 32; ++i) red_s[q4 * NT + lane * (NT / 32) + i] = l[i];
-            }
+            warp_columns<NT, false>(l, lane);
+            store_columns<NT>(red_s + q4 * NT, l, lane);
             if (lane == 0 && q4 == 0) unit_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
             named_barrier(4, 256);
             const bool second = T > 1;   // the second warpgroup had a tile
@@ -624,8 +638,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 dry = dead = false;
                 sc = tiles = 0;
                 pdl_wait();
-                pdl_trigger();
-                walk_begin(a, w, false);
+                walk_take(a, w, walk_s, bar(L::bW), abort_flag);
             }
         }
     }

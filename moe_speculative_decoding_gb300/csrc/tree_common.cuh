@@ -216,8 +216,14 @@ __device__ __forceinline__ long long seq_work(const TreeArgs &a, const Seq &s) {
 // reads a part of every CTA between an item's first and last).
 __device__ __forceinline__ int used_ctas(long long W, int ctas) { return static_cast<int>(min(W, static_cast<long long>(ctas))); }
 // First tile of CTA c's range, and the CTA whose range holds tile x.
-__device__ __forceinline__ long long range_lo(long long W, int c, int C) { return W * c / C; }
+// (In 32 bits where they do: a 64-bit division is some hundred instructions.)
+__device__ __forceinline__ long long range_lo(long long W, int c, int C) {
+    if (W < (1ll << 23)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(C);
+    return W * c / C;
+}
 __device__ __forceinline__ int range_of(long long W, long long x, int C) {
+    if (W < (1ll << 23))
+        return static_cast<int>(((static_cast<uint32_t>(x) + 1) * static_cast<uint32_t>(C) - 1) / static_cast<uint32_t>(W));
     return static_cast<int>(((x + 1) * C - 1) / W);
 }
 
@@ -281,11 +287,25 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
         }
         before += __shfl_sync(0xFFFFFFFFu, incl, 31);
     }
-    const int item = static_cast<int>((w.at - before) / w.s.tiles);
+    const long long into = w.at - before;
+    const int item = into < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(w.s.tiles))
+                                        : static_cast<int>(into / w.s.tiles);
     w.item0 = before + static_cast<long long>(item) * w.s.tiles;
     w.hk = item / w.s.pairs;
     w.pair = item % w.s.pairs;
 }
+// One warp finds the CTA's range and leaves it to the others in shared memory (`bar` counts 1).
+__device__ __forceinline__ void walk_share(const TreeArgs &a, Walk &w, Walk *place, uint32_t bar) {
+    walk_begin(a, w, blockIdx.x == 0);
+    if ((threadIdx.x & 31) == 0) *place = w;
+    warp_arrive(bar);
+}
+__device__ __forceinline__ void walk_take(const TreeArgs &a, Walk &w, const Walk *place, uint32_t bar, volatile int32_t *abort_flag) {
+    wait_for(bar, 0, abort_flag, a.err, a.wait_limit);
+    w = *place;
+    if (*abort_flag != 0) w.at = w.end = 0;
+}
+
 // Sets the next item's part; false at the end of the range.
 __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
     if (w.at >= w.end) return false;
@@ -581,8 +601,16 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t x) {
     return ~((nan >> 7) * 0xFFu);
 }
 
+// Four codes to fp16, exact.  (Assembling the fp16 bits with integer operations, five or more for four
+// codes, made the integer pipe the kernel's bound.)
+__device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
+}
+
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
-// layout, the scales into the softmax's double buffer.  The value scales there are relative to
+// layout, the scales into a ring for the softmax.  The value scales there are relative to
 // sigma, a power of two at or above all of the item's finite ones so far, times kWeightUp.  What
 // clean_values does for bf16 is done on the way.  With two groups of four warps each takes every
 // other tile (of one softmax warpgroup, whose sigma it is; rings are even, so that a slot is one
@@ -624,15 +652,18 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             if (top > sigma)   // the power of two at or above it
                 sigma = __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000));
             const bool odd_scale = j >= first && j < stop && !(fabsf(vs) <= kMax);
-            // the V slot is free when its previous product is done, and that came after the softmax
-            // had read the scales of that tile: the scales' buffer goes with the slot
+            // The scales have a ring of their own, so that a tile can be weighed before its values are
+            // converted (with the V slot's, a tile waited for the product two before it: 4000 cycles
+            // for two tiles instead of 2700).
+            const uint32_t sb = cnt % L::NC;
+            if (!(ok = wait_for(bar(L::bCE + sb), ((cnt / L::NC) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
+            scale_s[sb * 256 + j] = ks;
+            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
+            if (lane == 0) sigma_s[sb] = sigma;   // the same from every warp
+            if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
+            warp_arrive(bar(L::bCF + sb));
             if (!(ok = wait_for(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
             if (cw == 0 && lane == 0) v_issued[L::kGroups == 2 ? group : 0] = cnt + 1;   // the slot's previous use is over
-            scale_s[slot * 256 + j] = ks;
-            scale_s[slot * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
-            if (lane == 0) sigma_s[slot] = sigma;   // the same from every warp
-            if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
-            warp_arrive(bar(L::bCF + slot));
             uint8_t *const src = smem + L::oS + ss * L::kStage;
             uint8_t *const dst = smem + L::oV + slot * L::kVSlot;
             // 4 (8) rows of 128 (64) codes a step: 16 codes per lane
@@ -655,20 +686,25 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
                     }
                 }
             }
-            // 64-channel halves; the halves' lanes store their two chunks in opposite order, so that a
-            // step's eight lanes of a row meet eight bank groups
-            uint8_t *const half = dst + (c / 4) * (kTile * 128);
-            const int u = (c % 4) * 2, sw = c / 4;
-#pragma unroll 2
+            // 64-channel halves.  The lanes of the second half take the neighbouring row, so that the
+            // eight lanes that store together meet eight bank groups.
+            const int rs = row0 ^ (c / 4);
+            const uint8_t *const from = src + rs * 128 + c * 16;
+            uint8_t *const to = dst + (c / 4) * (kTile * 128) + rs * 128;
+            // the row's swizzle; a step of four rows changes its bit 2, a step of eight nothing
+            const int o0 = (((c % 4) * 2) ^ (rs & 7)) * 16, o1 = o0 ^ 16;
+            // no branch in the loop: the steps' chains of dependent operations overlap
+#pragma unroll 4
             for (int i = 0; i < STEPS; ++i) {
-                const int r = row0 + i * RS;
-                const uint4 x = *reinterpret_cast<const uint4 *>(src + r * 128 + c * 16);
-                const uint4 lo = make_uint4(e4m3x2_to_f16x2(x.x & 0xFFFFu), e4m3x2_to_f16x2(x.x >> 16),
-                                            e4m3x2_to_f16x2(x.y & 0xFFFFu), e4m3x2_to_f16x2(x.y >> 16));
-                const uint4 hi = make_uint4(e4m3x2_to_f16x2(x.z & 0xFFFFu), e4m3x2_to_f16x2(x.z >> 16),
-                                            e4m3x2_to_f16x2(x.w & 0xFFFFu), e4m3x2_to_f16x2(x.w >> 16));
-                *reinterpret_cast<uint4 *>(half + r * 128 + (((u + sw) ^ (r & 7)) * 16)) = sw ? hi : lo;
-                *reinterpret_cast<uint4 *>(half + r * 128 + (((u + 1 - sw) ^ (r & 7)) * 16)) = sw ? lo : hi;
+                const int flip = RS == 4 ? (i & 1) * 64 : 0;
+                const uint4 x = *reinterpret_cast<const uint4 *>(from + i * RS * 128);
+                uint4 lo, hi;
+                codes_to_f16(x.x, lo.x, lo.y);
+                codes_to_f16(x.y, lo.z, lo.w);
+                codes_to_f16(x.z, hi.x, hi.y);
+                codes_to_f16(x.w, hi.z, hi.w);
+                *reinterpret_cast<uint4 *>(to + i * RS * 128 + (o0 ^ flip)) = lo;
+                *reinterpret_cast<uint4 *>(to + i * RS * 128 + (o1 ^ flip)) = hi;
             }
             fence_proxy_async_smem();
             __threadfence_block();
