@@ -24,7 +24,7 @@
 namespace moe {
 namespace {
 
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kQueryWarp = 11, kAuxWarp = 12;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 10, kQueryWarp = 11, kAuxWarp = 12;
 
 template <bool F8, int DP, int NT>
 struct Lay {
@@ -38,10 +38,7 @@ struct Lay {
     static constexpr uint32_t kStage = F8 ? 16384 : 0;
     static constexpr uint32_t kQ = F8 ? 2 * NT * 128 : DP / 64 * NT * 128;
     static constexpr uint32_t kP = 128 * NT * 2;   // weights of a tile: a row of NT per position
-    // What fits.  A product warp takes every other tile, so within an item, with an even ring, the
-    // slots it waits for are its own and their parities name the use.  An item's first tiles, and a
-    // ring of 3, may wait on a slot the other warp is not done with: there k_issued and v_issued,
-    // which the filler sets when the previous use is over, are waited for first.
+    // rings: what fits
     static constexpr int NK = DP == 64 ? 4 : (F8 ? 3 : 2);
     static constexpr int NV = F8 ? 2 : (DP == 64 ? 4 : (NT < 64 ? 3 : 2));
     static constexpr int NS = !F8 ? 0 : (NT < 64 ? 4 : 2);   // even: a slot is one converter group's
@@ -199,7 +196,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mbar_init(bar(L::bQE + i), 8);
         }
         mbar_init(bar(L::bOF), 8);
-        mbar_init(bar(L::bO), 2);
+        mbar_init(bar(L::bO), 1);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
         mbar_init(bar(L::bW), 1);
@@ -209,7 +206,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tmem_alloc(base + L::oMisc, L::kTmem);
         tmem_relinquish();
     }
@@ -228,27 +225,21 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     if (warp == kProducerWarp) {
         walk_share(a, w, walk_s, bar(L::bW));
         produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
-    } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-        // ---------------------------------------------------------------- products
+    } else if (warp == kScoreWarp) {
+        // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
         walk_take(a, w, walk_s, bar(L::bW), abort_flag);
-        const int g = warp - kMmaWarp;
-        const uint32_t s_col = tmem + g * NT, o_col = tmem + (2 + g) * NT;
-        const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
-        uint32_t base_tile = 0, base_fix = 0, pc = 0, sc = 0, items = 0;
+        uint32_t c = 0, sc[2] = {0, 0}, items = 0;
         bool ok = true;
         while (ok && walk_next(a, w)) {
-            const int T = w.hi - w.lo;
-            const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
             const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ + (items & 1u) * L::kQ);
             ok = wait_for(bar(L::bQ + (items & 1u)), (items >> 1) & 1u, abort_flag, a.err, limit);
-            auto qk = [&](int t) {
-                const uint32_t c = base_tile + t, slot = c % L::NK;
+            for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
+                const uint32_t slot = c % L::NK, g = t & 1, s_col = tmem + g * NT;
                 // the warpgroup has taken this buffer's previous scores
-                ok = (sc == 0 || wait_for(bar(L::bSFree + g), (sc - 1) & 1u, abort_flag, a.err, limit)) &&
-                     ((L::NK % 2 == 0 && t >= L::NK) || wait_count(k_issued, c + 1, abort_flag, a.err, limit)) &&
+                ok = (sc[g] == 0 || wait_for(bar(L::bSFree + g), (sc[g] - 1) & 1u, abort_flag, a.err, limit)) &&
                      wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
-                if (!ok) return;
-                ++sc;
+                if (!ok) break;
+                ++sc[g];
                 tc_fence_after();
                 const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
                 if (elect_one()) {
@@ -269,26 +260,37 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     tc_commit(bar(L::bS + g));
                 }
                 __syncwarp();
-            };
-            if (ok && g < T) qk(g);
-            for (int t = g; ok && t < T; t += 2) {
-                if (t + 2 < T) qk(t + 2);   // while the warpgroup weighs tile t
-                if (!ok) break;
-                const uint32_t c = base_tile + t, slot = c % L::NV;
-                ok = ((L::NV % 2 == 0 && t >= L::NV) || wait_count(v_issued + (F8 ? c & 1u : 0u), c + 1, abort_flag, a.err, limit)) &&
-                     wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
-                if (!F8 && ok && w.lo + t >= edge0) {   // V's cleaner has been over it
-                    const uint32_t f = base_fix + (w.lo + t - edge0);
-                    ok = wait_for(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
+            }
+            ++items;
+        }
+        // every product is done before the CTA leaves
+        if (elect_one()) tc_commit(bar(L::bDrain));
+        __syncwarp();
+        mbar_wait_drain(bar(L::bDrain), 0, kDrain);
+        __syncwarp();
+    } else if (warp == kOutWarp) {
+        // ---------------------------------------------------------------- O^T += V^T P^T, tile by tile
+        // (A warp of its own: a tile's K may come later than the weights of the tile before.)
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
+        uint32_t c = 0, fixes = 0, pc[2] = {0, 0}, items = 0;
+        bool ok = true;
+        while (ok && walk_next(a, w)) {
+            const int T = w.hi - w.lo;
+            for (int t = 0; ok && t < T; ++t, ++c) {
+                const uint32_t slot = c % L::NV, g = t & 1, o_col = tmem + (2 + g) * NT;
+                ok = wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
+                if (!F8 && ok && (w.lo + t + 1) * kTile > w.s.ctx) {   // V's cleaner has been over it
+                    ok = wait_for(bar(L::bFix + (fixes & 3u)), (fixes >> 2) & 1u, abort_flag, a.err, limit);
+                    ++fixes;
                 }
-                // O of the previous item has been read (both product warps pass here or in an item's
-                // first weights, which the same warpgroups form later)
-                if (ok && t == g && items > 0) ok = wait_for(bar(L::bOF), (items - 1) & 1u, abort_flag, a.err, limit);
-                ok = ok && wait_for(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
+                // O of the previous item has been read
+                if (ok && t == 0 && items > 0) ok = wait_for(bar(L::bOF), (items - 1) & 1u, abort_flag, a.err, limit);
+                ok = ok && wait_for(bar(L::bP + g), pc[g] & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
-                ++pc;
+                ++pc[g];
                 tc_fence_after();
                 const uint64_t v_desc = desc_mn_sw128(base + L::oV + slot * L::kVSlot, DP == 128 ? kTile * 128u : 0u);
+                const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
                 if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < kTile / 16; ++i)   // 16 positions: 2 KB of V's blocks, 2 atoms of P
@@ -296,16 +298,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                                    t >= 2 || i > 0);
                     tc_commit(bar(L::bVE + slot));
                     tc_commit(bar(L::bPV + g));
+                    if (t == T - 1) tc_commit(bar(L::bO));
                 }
                 __syncwarp();
             }
-            if (ok && elect_one()) tc_commit(bar(L::bO));
-            __syncwarp();
-            base_tile += T;
-            base_fix += max(0, w.hi - edge0);
             ++items;
         }
-        // every product is done before the CTA leaves
         if (elect_one()) tc_commit(bar(L::bDrain));
         __syncwarp();
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
@@ -644,7 +642,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmem);
     }

@@ -457,23 +457,39 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31);
-    const int boxes = kTile / box_rows;   // at most 16
+    const int boxes = kTile / box_rows;   // of a tile, at most 16
     const moe_kv_cache_t &kc = a.cache;
     constexpr uint32_t NV = F8 ? L::NS : L::NV;
+    constexpr int kNone = -2147483647;    // a box beyond the length
     uint32_t cnt = 0, k_cnt = 0;
     bool ok = true;
     while (ok && walk_next(a, w)) {
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
-        auto page_of = [&](int tt) {   // the lane's box of tile tt: its page (0 beyond the length)
-            const int pos = tt * kTile + lane * box_rows;
-            return tt < w.hi && lane < boxes && pos < w.s.len ? __ldg(table + pos / kc.page) : 0;
+        // The places of 32 boxes, a lane each, for 32 / boxes tiles; the next ones are on their way
+        // while these are used.
+        auto places = [&](int first, int &page, int &row) {
+            const int64_t pos = (static_cast<int64_t>(first) * boxes + lane) * box_rows;
+            page = kNone;
+            row = 0;
+            if (pos < w.s.len) {
+                page = __ldg(table + static_cast<int>(pos) / kc.page);
+                row = static_cast<int>(pos) % kc.page;
+            }
         };
-        int next = page_of(w.lo);
-        for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
-            const int pos = tt * kTile + lane * box_rows, row = pos % kc.page;
-            const bool mine = lane < boxes && pos < w.s.len;
-            int page = next;
-            next = page_of(tt + 1);   // in flight during this tile
+        const int per = 32 / boxes;
+        int page_now, row_now, page_next, row_next;
+        places(w.lo, page_now, row_now);
+        places(w.lo + per, page_next, row_next);
+        for (int tt = w.lo, k = 0; tt < w.hi; ++tt, ++cnt, ++k) {
+            if (k == per) {
+                k = 0;
+                page_now = page_next;
+                row_now = row_next;
+                places(tt + per, page_next, row_next);
+            }
+            int page = __shfl_sync(0xFFFFFFFFu, page_now, (k * boxes + lane) & 31);
+            const int row = __shfl_sync(0xFFFFFFFFu, row_now, (k * boxes + lane) & 31);
+            const bool mine = lane < boxes && page != kNone;
             const bool good = static_cast<uint32_t>(page) < static_cast<uint32_t>(kc.pages);
             if (mine && !good) {
                 record_error(a.err, MOE_ERR_BAD_ID);
@@ -759,7 +775,9 @@ bool encode(CUtensorMap *map, const moe_kv_cache_t &c, const void *ptr, int box_
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr),
               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+              // a head's row and no more: 256 bytes where a row has 128 would fetch the next head's too
+              c.dim * es > 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
