@@ -63,6 +63,7 @@ struct Lay {
     // A product warp waits only for its own tiles, every other one when the warpgroups alternate:
     // with two slots these are all of one slot's uses, so that the slot's parity names the use.
     static constexpr int NK = 2, NV = 2, NS = F8 ? 3 : 0, NC = 4;
+    static constexpr bool kLandScales = F8;
     static constexpr int kUsers = 2;               // products that release a slot
     static constexpr int kVReaders = F8 ? 4 : 1;   // arrivals that fill a V slot
     static constexpr uint32_t oK = 2 * kQTile, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot;
@@ -249,7 +250,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     Walk w;
     if (warp == kProducerWarp) {
         walk_share(a, w, walk_s, bar(L::bW));
-        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
+        produce<L, F8, DP, 0, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in

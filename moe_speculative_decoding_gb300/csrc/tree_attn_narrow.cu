@@ -24,14 +24,15 @@
 namespace moe {
 namespace {
 
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 10, kQueryWarp = 11, kAuxWarp = 12;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 10, kValueWarp = 11, kAuxWarp = 12;
 
 template <bool F8, int DP, int NT>
 struct Lay {
-    // bf16: a cleaner (and three idle warps of its warpgroup); F8: two groups of four converters
-    static constexpr int kThreads = F8 ? 640 : 512, kGroups = F8 ? 2 : 1;
+    // bf16: a cleaner (and three idle warps of its warpgroup); F8: two groups of four converters, one
+    // for 64 rows, whose softmax needs the registers
+    static constexpr int kGroups = F8 && NT < 64 ? 2 : 1, kThreads = kGroups == 2 ? 640 : 512;
     // a thread's registers: the softmax's hold a position's NT scores and NT sums
-    static constexpr int kOther = F8 ? 48 : 56, kSoft = F8 ? 168 : 200;
+    static constexpr int kOther = kGroups == 2 ? 48 : 56, kSoft = kGroups == 2 ? 168 : 200;
     static constexpr int kRegs = 256 * kSoft + (kThreads - 256) * kOther;
     static constexpr uint32_t kKSlot = F8 ? 16384 : 128 * DP * 2;
     static constexpr uint32_t kVSlot = 128 * DP * 2;
@@ -42,22 +43,25 @@ struct Lay {
     static constexpr int NK = DP == 64 ? 4 : (F8 ? 3 : 2);
     static constexpr int NV = F8 ? 2 : (DP == 64 ? 4 : (NT < 64 ? 3 : 2));
     static constexpr int NS = !F8 ? 0 : (NT < 64 ? 4 : 2);   // even: a slot is one converter group's
+    // The converters load a position's scales themselves: two bulk copies a box, next to the codes,
+    // cost the producer 800 cycles a tile.
+    static constexpr bool kLandScales = false;
     static constexpr int NC = 4, kUsers = 1, kVReaders = F8 ? 4 : 1;
     static constexpr uint32_t oK = 0, oV = oK + NK * kKSlot, oS = oV + NV * kVSlot, oP = oS + NS * kStage,
-                              oQ = oP + 2 * kP, oSSc = oQ + 2 * kQ, oBar = oSSc + NS * 1024;
+                              oQ = oP + 2 * kP, oSSc = oQ + kQ, oBar = oSSc;
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
                          bCE = bCF + NC, bS = bCE + NC, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
-                         bQE = bQ + 2, bO = bQE + 2, bOF = bO + 1, bFix = bOF + 1, bW = bFix + 4, bDrain = bW + 1, kBars = bDrain + 1;
+                         bO = bQ + 1, bFix = bO + 1, bW = bFix + 4, bDrain = bW + 1, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
-    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);   // F8: float [NC]
-    static constexpr uint32_t oCs = oSigma + (F8 ? 32 : 0);        // F8: float [2 items][NT]: score to log2 units
-    static constexpr uint32_t oM = oCs + (F8 ? 2 * NT * 4 : 0);    // float [2][NT]: minus the maxima of a warpgroup
+    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);   // F8: float [NC][4], the warps' largest value scales
+    static constexpr uint32_t oCs = oSigma + (F8 ? NC * 16 : 0);        // F8: float [NT]: score to log2 units
+    static constexpr uint32_t oM = oCs + (F8 ? NT * 4 : 0);    // float [2][NT]: minus the maxima of a warpgroup
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
     static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
-    static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [2 items][NT]: the rows' tree masks
-    static constexpr uint32_t oUnit = oMask + 2 * NT * 8;          // float [2]: a warpgroup's accumulator unit
+    static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
+    static constexpr uint32_t oUnit = oMask + NT * 8;          // float [2]: a warpgroup's accumulator unit
     static constexpr uint32_t oWalk = oUnit + 16;                  // Walk
     static constexpr uint32_t kSmem = oWalk + 128;
     static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
@@ -191,11 +195,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             mbar_init(bar(L::bP + i), 4);
             mbar_init(bar(L::bPV + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(L::bQ + i), 1);
-            mbar_init(bar(L::bQE + i), 8);
-        }
-        mbar_init(bar(L::bOF), 8);
+        mbar_init(bar(L::bQ), 8);
         mbar_init(bar(L::bO), 1);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
@@ -224,15 +224,15 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     Walk w;
     if (warp == kProducerWarp) {
         walk_share(a, w, walk_s, bar(L::bW));
-        produce<L, F8, DP>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
+        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp == kScoreWarp) {
         // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
         walk_take(a, w, walk_s, bar(L::bW), abort_flag);
+        const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
         uint32_t c = 0, sc[2] = {0, 0}, items = 0;
         bool ok = true;
         while (ok && walk_next(a, w)) {
-            const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ + (items & 1u) * L::kQ);
-            ok = wait_for(bar(L::bQ + (items & 1u)), (items >> 1) & 1u, abort_flag, a.err, limit);
+            ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
             for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
                 const uint32_t slot = c % L::NK, g = t & 1, s_col = tmem + g * NT;
                 // the warpgroup has taken this buffer's previous scores
@@ -272,7 +272,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         // ---------------------------------------------------------------- O^T += V^T P^T, tile by tile
         // (A warp of its own: a tile's K may come later than the weights of the tile before.)
         walk_take(a, w, walk_s, bar(L::bW), abort_flag);
-        uint32_t c = 0, fixes = 0, pc[2] = {0, 0}, items = 0;
+        uint32_t c = 0, fixes = 0, pc[2] = {0, 0};
         bool ok = true;
         while (ok && walk_next(a, w)) {
             const int T = w.hi - w.lo;
@@ -283,8 +283,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     ok = wait_for(bar(L::bFix + (fixes & 3u)), (fixes >> 2) & 1u, abort_flag, a.err, limit);
                     ++fixes;
                 }
-                // O of the previous item has been read
-                if (ok && t == 0 && items > 0) ok = wait_for(bar(L::bOF), (items - 1) & 1u, abort_flag, a.err, limit);
+                // (the first weights of an item come after the previous item's O was read)
                 ok = ok && wait_for(bar(L::bP + g), pc[g] & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 ++pc[g];
@@ -302,62 +301,14 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 __syncwarp();
             }
-            ++items;
         }
         if (elect_one()) tc_commit(bar(L::bDrain));
         __syncwarp();
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
-    } else if (warp == kQueryWarp) {
-        // ---------------------------------------------------------------- queries, an item ahead
+    } else if (warp == kValueWarp) {
         walk_take(a, w, walk_s, bar(L::bW), abort_flag);
-        uint64_t *const mask_all = reinterpret_cast<uint64_t *>(smem + L::oMask);
-        float *const cs_all = reinterpret_cast<float *>(smem + L::oCs);
-        bool ok = true;
-        while (ok && walk_next(a, w)) {
-            const uint32_t qb = w.index & 1u;
-            const int R = w.s.n * G;
-            constexpr int C = DP / 8, PER = 32 / C;   // lanes of a row, rows of a step
-            const int c = lane % C;
-            // Rows beyond R are zeros: their columns go nowhere, but their scores have a say in when O
-            // is rescaled.  Four steps' loads at a time, in a loop: this code runs once an item, and
-            // what runs once should be short.
-#pragma unroll 1
-            for (int r0 = 0; r0 < NT; r0 += 4 * PER) {
-                uint4 x[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = r0 + i * PER + lane / C;
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (row < R && c * 8 < a.cache.dim)
-                        x[i] = *reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
-                            static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
-                }
-                if (r0 == 0) ok = wait_for(bar(L::bQE + qb), ((w.index >> 1) & 1u) ^ 1u, abort_flag, a.err, limit);
-                if (!ok) break;
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int row = r0 + i * PER + lane / C;
-                    const uint4 y = i == 0 ? x[0] : (i == 1 ? x[1] : (i == 2 ? x[2] : x[3]));
-                    float unscale;
-                    if (row - lane / C < NT) {   // the step lies within the operand
-                        store_query<F8, DP>(smem + L::oQ + qb * L::kQ, NT, row, c, y, unscale);
-                        if (F8 && c == 0) cs_all[qb * NT + row] = a.scale_log2 * unscale;
-                    }
-                }
-            }
-            if (!ok) break;
-#pragma unroll 1
-            for (int row = lane; row < NT; row += 32) {
-                uint64_t M = 0;
-                if (row < R) M = a.mask != nullptr ? a.mask[w.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
-                if (w.s.n < 64) M &= (1ull << w.s.n) - 1ull;
-                mask_all[qb * NT + row] = M;
-            }
-            fence_proxy_async_smem();
-            warp_arrive(bar(L::bQ + qb));
-        }
+        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
     } else if (warp >= kAuxWarp) {
         walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         if constexpr (F8)
@@ -390,26 +341,64 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         w.b = w.hk = w.lo = w.index = 0;
         w.hi = 3;
         w.whole = true;
+        float *const cs_s = reinterpret_cast<float *>(smem + L::oCs);
+        uint64_t *const mask_s = reinterpret_cast<uint64_t *>(smem + L::oMask);
+        // The next item's queries, 16 bytes a piece, are on their way while an item ends: the lanes of
+        // a row are C neighbouring threads.  Rows beyond R are zeros; their columns go nowhere, but
+        // their scores have a say in when O is rescaled.
+        constexpr int C = DP / 8, PIECES = (NT * C + 255) / 256;
+        uint4 queries[PIECES];
+        uint64_t next_mask = 0;
+        auto fetch = [&](const Walk &v) {
+            const int R = v.s.n * G;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int at = static_cast<int>(threadIdx.x) + 256 * i, row = at / C, c = at % C;
+                queries[i] = make_uint4(0, 0, 0, 0);
+                if (row < R && c * 8 < a.cache.dim)
+                    queries[i] = *reinterpret_cast<const uint4 *>(
+                        static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(v.s.t0 + row / G) * a.q.token_stride +
+                        static_cast<int64_t>(v.hk * G + row % G) * a.q.head_stride + c * 8);
+            }
+            next_mask = 0;
+            const int row = static_cast<int>(threadIdx.x);
+            if (row < NT && row < R) {
+                next_mask = a.mask != nullptr ? a.mask[v.s.t0 + row / G] : (2ull << (row / G)) - 1ull;
+                if (v.s.n < 64) next_mask &= (1ull << v.s.n) - 1ull;
+            }
+        };
+        Walk next = w;
+        bool more = true;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) queries[i] = make_uint4(0, 0, 0, 0);
         while (true) {
-            const bool more = dry || walk_next(a, w);
             // the previous item's shared words have been read; everybody leaves together
             if (bar_any(1, 256, !dry && (dead || *abort_flag != 0)) || !more) break;
+            w = next;
             const int R = w.s.n * G, T = w.hi - w.lo;
-            const uint32_t qb = w.index & 1u;
-            const float *const cs_s = reinterpret_cast<const float *>(smem + L::oCs) + qb * NT;
-            const uint64_t *const mask_s = reinterpret_cast<const uint64_t *>(smem + L::oMask) + qb * NT;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int at = static_cast<int>(threadIdx.x) + 256 * i, row = at / C, c = at % C;
+                if (NT * C >= 256 || at < NT * C) {   // whole warps
+                    float unscale;
+                    store_query<F8, DP>(smem + L::oQ, NT, row, c, queries[i], unscale);
+                    if (F8 && c == 0) cs_s[row] = a.scale_log2 * unscale;
+                }
+            }
+            if (threadIdx.x < NT) mask_s[threadIdx.x] = next_mask;
             if (p < NT) nm_s[p] = -kNone;
-            if (!dry) dead = !wait_for(bar(L::bQ + qb), (w.index >> 1) & 1u, abort_flag, a.err, limit);
-            named_barrier(2 + g, 128);
+            fence_proxy_async_smem();
+            if (!dry) warp_arrive(bar(L::bQ));
+            named_barrier(4, 256);
             F2 l2[NT / 2];
 #pragma unroll
             for (int c = 0; c < NT / 2; ++c) l2[c] = f2(0.0f, 0.0f);
-            float sigma = 1.0f;
+            float sigma = kSigmaLow;
             for (int t = g; t < T; t += 2) {
                 const int tt = w.lo + t, pos = tt * kTile + p;
                 const bool edge = (tt + 1) * kTile > w.s.ctx;
                 const uint32_t no = tiles + t, sb = no % L::NC;
-                float ks = 1.0f, vs = 1.0f, sigma_new = 1.0f;
+                float ks = 1.0f, vs = 1.0f, sigma_new = sigma;
                 uint32_t x[NT];
                 if (F8 && !dead) dead = !wait_for(bar(L::bCF + sb), (no / L::NC) & 1u, abort_flag, a.err, limit);
                 if (!dead) dead = !wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
@@ -418,7 +407,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (F8) {
                     ks = scale_s[sb * 256 + p];
                     vs = scale_s[sb * 256 + 128 + p];
-                    sigma_new = sigma_s[sb];
+                    sigma_new = sigma_above(sigma, fmaxf(fmaxf(sigma_s[sb * 4], sigma_s[sb * 4 + 1]), fmaxf(sigma_s[sb * 4 + 2], sigma_s[sb * 4 + 3])));
+                    vs *= kWeightUp / sigma_new;
                 } else {
                     ks = a.scale_log2;
                 }
@@ -539,6 +529,11 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 ++sc;
             }
             // ------------------------------------------------------------ the item's end
+            if (!dry) {
+                next = w;
+                more = walk_next(a, next);
+                if (more) fetch(next);
+            }
             if (!dead) dead = !wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             tiles += T;
@@ -586,7 +581,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             }
             tmem_wait_ld();
             tc_fence_before();
-            if (!dry) warp_arrive(bar(L::bOF));   // the next item's products may begin
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
             uint32_t any_bad = 0;   // of parts that reach past the context: there the products waited for the words
             if (!dry && w.hi * kTile > w.s.ctx) {
@@ -630,13 +624,13 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             __syncwarp();
-            if (!dry) {
-                warp_arrive(bar(L::bQE + qb));   // masks and queries of this item are done with
-            } else {
+            if (dry) {
                 dry = dead = false;
                 sc = tiles = 0;
                 pdl_wait();
-                walk_take(a, w, walk_s, bar(L::bW), abort_flag);
+                walk_take(a, next, walk_s, bar(L::bW), abort_flag);
+                more = walk_next(a, next);
+                if (more) fetch(next);
             }
         }
     }

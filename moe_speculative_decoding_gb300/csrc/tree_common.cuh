@@ -448,9 +448,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// The producer warp: K, then V of each tile, a lane per box of box_rows positions.  Boxes beyond the
-// length are not copied.  An e4m3 cache's scales (contiguous over a page's rows) land with V's codes.
-template <typename L, bool F8, int DP>
+// A producer warp: K (FIRST = 0), V (LAST = 1) or K, then V of each tile, a lane per box of box_rows
+// positions.  Boxes beyond the length are not copied.  An e4m3 cache's scales (contiguous over a
+// page's rows) land with V's codes where the converters want them there (kLandScales).
+template <typename L, bool F8, int DP, int FIRST, int LAST>
 __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                         uint8_t *smem, int box_rows, volatile int32_t *abort_flag,
                                         volatile uint32_t *k_issued, volatile uint32_t *v_issued) {
@@ -498,7 +499,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
             const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, mine)), n_good = __popc(__ballot_sync(0xFFFFFFFFu, mine && good));
             const uint32_t bytes = n * box_rows * (F8 ? 128u : DP * 2u);
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
+            for (int v = FIRST; v <= LAST; ++v) {
                 const uint32_t slot = v ? cnt % NV : cnt % L::NK, use = v ? cnt / NV : cnt / L::NK;
                 const uint32_t full = bar((v ? (F8 ? L::bSF : L::bVF) : L::bKF) + slot);
                 const uint32_t empty = bar((v ? (F8 ? L::bSE : L::bVE) : L::bKE) + slot);
@@ -508,19 +509,19 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
                     ok = false;
                     break;
                 }
-                if (F8 && v && mine && !good) {   // no scales to copy: zeros
+                if (L::kLandScales && v && mine && !good) {   // no scales to copy: zeros
                     float *const sc = reinterpret_cast<float *>(smem + L::oSSc + slot * 1024) + lane * box_rows;
                     for (int i = 0; i < box_rows; ++i) sc[i] = sc[128 + i] = 0.0f;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes + (F8 && v ? n_good * box_rows * 8u : 0u));
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes + (L::kLandScales && v ? n_good * box_rows * 8u : 0u));
                 __syncwarp();
                 if (mine) {
                     const CUtensorMap *tm = v ? tm_v : tm_k;
                     const uint32_t d = dst + static_cast<uint32_t>(lane * box_rows) * 128u;
                     tma_load_4d(d, tm, full, 0, row, w.hk, page);
                     if (!F8 && DP == 128) tma_load_4d(d + kTile * 128u, tm, full, 64, row, w.hk, page);
-                    if (F8 && v && good) {
+                    if (L::kLandScales && v && good) {
                         const int64_t o = (static_cast<int64_t>(page) * kc.heads + w.hk) * kc.page + row;
                         const uint32_t sd = base + L::oSSc + slot * 1024 + lane * box_rows * 4u;
                         bulk_load(sd, kc.k_scale + o, box_rows * 4u, full);
@@ -542,7 +543,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
     if (*abort_flag != 0) {   // copies nobody waited for must land before the CTA leaves
         for (uint32_t j = k_cnt > L::NK ? k_cnt - L::NK : 0; j < k_cnt; ++j)
             mbar_wait_drain(bar(L::bKF + j % L::NK), (j / L::NK) & 1u, kDrain);
-        for (uint32_t j = cnt > NV ? cnt - NV : 0; j < cnt; ++j)
+        for (uint32_t j = LAST == 0 || cnt <= NV ? 0 : cnt - NV; LAST == 1 && j < cnt; ++j)
             mbar_wait_drain(bar((F8 ? L::bSF : L::bVF) + j % NV), (j / NV) & 1u, kDrain);
     }
 }
@@ -617,6 +618,11 @@ __device__ __forceinline__ uint32_t finite_codes(uint32_t x) {
     return ~((nan >> 7) * 0xFFu);
 }
 
+constexpr float kSigmaLow = 7.888609e-31f;   // 2^-100: below any value scale that counts
+__device__ __forceinline__ float sigma_above(float sigma, float top) {   // the power of two at or above top
+    return top > sigma ? __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000)) : sigma;
+}
+
 // Four codes to fp16, exact.  (Assembling the fp16 bits with integer operations, five or more for four
 // codes, made the integer pipe the kernel's bound.)
 __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t &hi) {
@@ -626,8 +632,10 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 }
 
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
-// layout, the scales into a ring for the softmax.  The value scales there are relative to
-// sigma, a power of two at or above all of the item's finite ones so far, times kWeightUp.  What
+// layout, the scales into a ring for the softmax.  With kLandScales (a softmax thread owns a row) the
+// value scales there are relative to sigma, a power of two at or above all of the item's finite ones
+// so far, times kWeightUp; without (it owns a position) they are as the cache has them, with each
+// warp's largest, and sigma is the softmax's.  What
 // clean_values does for bf16 is done on the way.  With two groups of four warps each takes every
 // other tile (of one softmax warpgroup, whose sigma it is; rings are even, so that a slot is one
 // group's).
@@ -648,25 +656,50 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
         const int odd = L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(w.lo) ^ static_cast<uint32_t>(group)) & 1u) : 0;
         if (lane < 2 && (L::kGroups == 1 || lane == odd)) bad[lane * 4 + cw] = 0;
         __syncwarp();
-        float sigma = 7.888609e-31f;   // 2^-100: below any value scale that counts
+        float sigma = kSigmaLow;
+        // without landing scales: this thread's position of the group's tiles, the scales loaded a
+        // tile ahead and the page two
+        const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
+        auto page_at = [&](int tt) {
+            const int64_t pos = static_cast<int64_t>(tt) * kTile + j;
+            return !L::kLandScales && tt < w.hi && pos < w.s.len ? __ldg(table + static_cast<int>(pos) / a.cache.page) : -1;
+        };
+        auto scales_at = [&](int tt, int page, float &ks, float &vs) {
+            ks = vs = 0.0f;
+            if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return;
+            const int64_t o = (static_cast<int64_t>(page) * a.cache.heads + w.hk) * a.cache.page + (tt * kTile + j) % a.cache.page;
+            ks = __ldg(a.cache.k_scale + o);
+            vs = __ldg(a.cache.v_scale + o);
+        };
+        const int t0 = w.lo + (L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(group)) & 1u) : 0);
+        float ks_next = 0.0f, vs_next = 0.0f;
+        if (!L::kLandScales) scales_at(t0, page_at(t0), ks_next, vs_next);
+        int page_next = page_at(t0 + L::kGroups);
         for (int tt = w.lo; tt < w.hi; ++tt, ++cnt) {
             if (L::kGroups == 2 && (cnt & 1u) != static_cast<uint32_t>(group)) continue;
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
             const uint32_t ss = cnt % L::NS, slot = cnt % L::NV;
-            if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
-            const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
-            float top = 0.0f, ks = 0.0f, vs = 0.0f;   // every warp forms the tile's largest: no barrier
+            float top = 0.0f, ks = 0.0f, vs = 0.0f;
+            if (L::kLandScales) {
+                if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
+                const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float v = k * 32 + lane < stop ? land[128 + k * 32 + lane] : 0.0f;
-                if (fabsf(v) <= kMax) top = fmaxf(top, fabsf(v));
-                if (k == cw) vs = v;
+                for (int k = 0; k < 4; ++k) {   // every warp forms the tile's largest: no barrier
+                    const float v = k * 32 + lane < stop ? land[128 + k * 32 + lane] : 0.0f;
+                    if (fabsf(v) <= kMax) top = fmaxf(top, fabsf(v));
+                    if (k == cw) vs = v;
+                }
+                if (j < stop) ks = land[j];
+            } else {
+                ks = ks_next;
+                vs = vs_next;
+                if (fabsf(vs) <= kMax) top = fabsf(vs);
+                scales_at(tt + L::kGroups, page_next, ks_next, vs_next);   // in flight during this tile
+                page_next = page_at(tt + 2 * L::kGroups);
             }
-            if (j < stop) ks = land[j];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            if (top > sigma)   // the power of two at or above it
-                sigma = __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000));
+            if (L::kLandScales) sigma = sigma_above(sigma, top);
             const bool odd_scale = j >= first && j < stop && !(fabsf(vs) <= kMax);
             // The scales have a ring of their own, so that a tile can be weighed before its values are
             // converted (with the V slot's, a tile waited for the product two before it: 4000 cycles
@@ -674,10 +707,11 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             const uint32_t sb = cnt % L::NC;
             if (!(ok = wait_for(bar(L::bCE + sb), ((cnt / L::NC) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
             scale_s[sb * 256 + j] = ks;
-            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : vs * (kWeightUp / sigma);
-            if (lane == 0) sigma_s[sb] = sigma;   // the same from every warp
+            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : (L::kLandScales ? vs * (kWeightUp / sigma) : vs);
+            if (lane == 0) sigma_s[L::kLandScales ? sb : sb * 4 + cw] = L::kLandScales ? sigma : top;
             if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
             warp_arrive(bar(L::bCF + sb));
+            if (!L::kLandScales && !(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
             if (!(ok = wait_for(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
             if (cw == 0 && lane == 0) v_issued[L::kGroups == 2 ? group : 0] = cnt + 1;   // the slot's previous use is over
             uint8_t *const src = smem + L::oS + ss * L::kStage;
