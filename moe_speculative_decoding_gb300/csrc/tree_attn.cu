@@ -348,17 +348,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         float4 *const exch = reinterpret_cast<float4 *>(smem);   // [2][128], over Q when Q is done with
         uint32_t sc = 0, scnt = 0;
         bool ok = true;
-        // The first item is a dry one, as in the kernel for few rows: no waits, no arrivals, no rows.
-        bool dry = true;
-        w.s.n = w.s.t0 = 0;
-        w.s.ctx = kTile;
-        w.b = w.hk = w.pair = w.lo = w.index = 0;
-        w.hi = 5;
-        w.whole = true;
+        pdl_wait();
+        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         while (true) {
-            const bool more = dry || walk_next(a, w);
+            const bool more = walk_next(a, w);
             // the previous item's exchange has been read; everybody leaves together
-            if (softmax_any(!dry && (!ok || *abort_flag != 0)) || !more) break;
+            if (softmax_any(!ok || *abort_flag != 0) || !more) break;
             const int R = w.s.n * G, row0 = w.pair * 2 * kTile;
             const bool two = R - row0 > kTile;
             const int T = w.hi - w.lo, U = two ? 2 * T : T;
@@ -385,7 +380,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int token = live ? w.s.t0 + row / G : 0, head = w.hk * G + (live ? row % G : 0);
             uint64_t M = 0;
             if (live) M = a.mask != nullptr ? a.mask[token] : (2ull << (row / G)) - 1ull;
-            if (!dry) warp_arrive(bar(L::bQ));
+            warp_arrive(bar(L::bQ));
             if (F8) named_barrier(3, 256);   // the row factors, before other threads' are read
             const float cs = F8 ? a.scale_log2 * qs[mt * 128 + r] : a.scale_log2;
             float m = ninf(), l = 0.0f, sigma = 1.0f;
@@ -396,14 +391,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (edge) seen_bits(M, w.s, tt, see);
                 const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no % L::NC;
                 const float *const ks = scale_s + sb * 256, *const vs = ks + 128;
-                if (F8 && !dry && !(ok = wait_for(bar(L::bCF + sb), (tile_no / L::NC) & 1u, abort_flag, a.err, limit))) break;
-                if (!dry && !(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
+                if (F8 && !(ok = wait_for(bar(L::bCF + sb), (tile_no / L::NC) & 1u, abort_flag, a.err, limit))) break;
+                if (!(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
                 ++sc;
                 tc_fence_after();
                 float mx = edge ? tile_max<F8, true>(s_addr, ks, see) : tile_max<F8, false>(s_addr, ks, see);
                 mx *= cs;   // cs > 0; -inf stays
                 float keep = 1.0f;
-                bool move = u < 2 || dry || mx - m > kLazy;
+                bool move = u < 2 || mx - m > kLazy;
                 const float sigma_new = F8 ? sigma_s[sb] : 1.0f;   // the tile's value scales are relative to it
                 if (F8 && sigma_new != sigma) move = true;
                 if (__any_sync(0xFFFFFFFFu, move)) {
@@ -430,13 +425,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                           : tile_weights<F8, false>(s_addr, ks, vs, cs, ref, see);
                 tmem_wait_st();
                 tc_fence_before();
-                if (!dry) {
-                    warp_arrive(bar(L::bP + g));
-                    if (F8) warp_arrive_cnt(bar(L::bCE + sb), two ? 1 : 2);   // the tile's scales are read
-                }
+                warp_arrive(bar(L::bP + g));
+                if (F8) warp_arrive_cnt(bar(L::bCE + sb), two ? 1 : 2);   // the tile's scales are read
             }
             // ------------------------------------------------------------ the item's end
-            if (!dry) ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
+            ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             scnt += T;
             const float gain = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
@@ -462,7 +455,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
             uint32_t any_bad = 0;   // of parts that reach past the context: there the products waited for the words
-            if (!dry && w.hi * kTile > w.s.ctx) {
+            if (w.hi * kTile > w.s.ctx) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) any_bad |= bad[i];
             }
@@ -526,12 +519,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 } else {
                     part_ml<DP>(a, gridDim.x, slot, mt)[r] = make_float2(mm, ll);
                 }
-            }
-            if (dry) {
-                dry = false;
-                sc = scnt = 0;
-                pdl_wait();
-                walk_take(a, w, walk_s, bar(L::bW), abort_flag);
             }
         }
     }

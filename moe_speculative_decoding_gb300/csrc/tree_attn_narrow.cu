@@ -331,16 +331,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         float *const unit_s = reinterpret_cast<float *>(smem + L::oUnit);
         uint8_t *const p_buf = smem + L::oP + g * L::kP;
         uint32_t sc = 0, tiles = 0;   // this warpgroup's tiles; all tiles
-        bool dead = true;             // no waits, no arrivals: a wait gave up, or the dry item
-        // The first item is a dry one: every path once, on whatever shared memory and TMEM hold,
-        // without rows to write, while the previous kernel ends and the first tiles are on their way.
-        // It brings the code into the instruction caches (8 us of a short call otherwise).
-        bool dry = true;
-        w.s.n = w.s.t0 = 0;
-        w.s.ctx = kTile;
-        w.b = w.hk = w.lo = w.index = 0;
-        w.hi = 3;
-        w.whole = true;
+        bool dead = false;            // a wait gave up: only the barriers are kept
         float *const cs_s = reinterpret_cast<float *>(smem + L::oCs);
         uint64_t *const mask_s = reinterpret_cast<uint64_t *>(smem + L::oMask);
         // The next item's queries, 16 bytes a piece, are on their way while an item ends: the lanes of
@@ -367,13 +358,14 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (v.s.n < 64) next_mask &= (1ull << v.s.n) - 1ull;
             }
         };
-        Walk next = w;
-        bool more = true;
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i) queries[i] = make_uint4(0, 0, 0, 0);
+        pdl_wait();
+        Walk next;
+        walk_take(a, next, walk_s, bar(L::bW), abort_flag);
+        bool more = walk_next(a, next);
+        if (more) fetch(next);
         while (true) {
             // the previous item's shared words have been read; everybody leaves together
-            if (bar_any(1, 256, !dry && (dead || *abort_flag != 0)) || !more) break;
+            if (bar_any(1, 256, dead || *abort_flag != 0) || !more) break;
             w = next;
             const int R = w.s.n * G, T = w.hi - w.lo;
 #pragma unroll
@@ -388,7 +380,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             if (threadIdx.x < NT) mask_s[threadIdx.x] = next_mask;
             if (p < NT) nm_s[p] = -kNone;
             fence_proxy_async_smem();
-            if (!dry) warp_arrive(bar(L::bQ));
+            warp_arrive(bar(L::bQ));
             named_barrier(4, 256);
             F2 l2[NT / 2];
 #pragma unroll
@@ -444,7 +436,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
                 // any score far above its row's maximum so far?  (That is kNone before a row has
                 // seen anything, so that its first finite score is.)
-                bool move = t < 2 || dry || (F8 && sigma_new != sigma);
+                bool move = t < 2 || (F8 && sigma_new != sigma);
                 if (t >= 2) {
                     float over = ninf();
 #pragma unroll
@@ -529,11 +521,9 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 ++sc;
             }
             // ------------------------------------------------------------ the item's end
-            if (!dry) {
-                next = w;
-                more = walk_next(a, next);
-                if (more) fetch(next);
-            }
+            next = w;
+            more = walk_next(a, next);
+            if (more) fetch(next);
             if (!dead) dead = !wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             tiles += T;
@@ -583,7 +573,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             tc_fence_before();
             const uint32_t *const bad = reinterpret_cast<const uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
             uint32_t any_bad = 0;   // of parts that reach past the context: there the products waited for the words
-            if (!dry && w.hi * kTile > w.s.ctx) {
+            if (w.hi * kTile > w.s.ctx) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) any_bad |= bad[i];
             }
@@ -624,14 +614,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             __syncwarp();
-            if (dry) {
-                dry = dead = false;
-                sc = tiles = 0;
-                pdl_wait();
-                walk_take(a, next, walk_s, bar(L::bW), abort_flag);
-                more = walk_next(a, next);
-                if (more) fetch(next);
-            }
         }
     }
     tc_fence_before();
