@@ -73,14 +73,14 @@ struct Lay {
     // s_full[2], p_ready[2], q_ready, o_full, v_fix[4], drain
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
                          bCE = bCF + NC, bS = bCE + NC, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
-                         bDrain = bFix + 4, bW = bDrain + 1, kBars = bW + 1;
+                         bDrain = bFix + 4, bW = bDrain + 1, kBars = bW + kRecords;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);    // F8: float [NC], the running power of two
     static constexpr uint32_t oQs = oSigma + (F8 ? 32 : 0);         // F8: float [2][128], row factors
-    static constexpr uint32_t oWalk = oQs + (F8 ? 1024 : 0);        // Walk
-    static constexpr uint32_t kSmem = oWalk + 128;
+    static constexpr uint32_t oWalk = (oQs + (F8 ? 1024 : 0) + 7) & ~7u;   // records of walks
+    static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -225,7 +225,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(L::bO), 2);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
-        mbar_init(bar(L::bW), 1);
+        for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         *abort_flag = 0;
         *v_issued = *k_issued = 0;
         fence_mbar_init();
@@ -240,7 +240,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
-    Walk *const walk_s = reinterpret_cast<Walk *>(smem + L::oWalk);
+    Follow follow = {smem + L::oWalk, bar(L::bW), 0};
     const int G = a.group;
 
     if (warp >= 8) {
@@ -249,18 +249,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     pdl_trigger();
     Walk w;
     if (warp == kProducerWarp) {
-        walk_share(a, w, walk_s, bar(L::bW));
-        produce<L, F8, DP, 0, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
+        walk_begin(a, w, blockIdx.x == 0);
+        produce<L, F8, DP, 0, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in
         // line behind the other's, and its O += P V precedes the next S over the same columns.
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         const int g = warp - kMmaWarp;
         const uint32_t s_col = tmem + g * kTile, o_col = tmem + 256 + g * DP;
         uint32_t base_tile = 0, base_fix = 0, pc = 0, items = 0;
         bool ok = true;
-        while (ok && walk_next(a, w)) {
+        while (ok && walk_follow(a, w, follow, abort_flag)) {
             const bool two = w.s.n * G - w.pair * 2 * kTile > kTile;
             const int T = w.hi - w.lo, U = two ? 2 * T : T;
             const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
@@ -329,11 +328,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
     } else if (warp >= L::kAux) {
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, v_issued);
+            convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, v_issued, follow);
         else
-            clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
+            clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
     }
     } else {
         // ---------------------------------------------------------------- softmax, two warpgroups
@@ -349,9 +347,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         uint32_t sc = 0, scnt = 0;
         bool ok = true;
         pdl_wait();
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         while (true) {
-            const bool more = walk_next(a, w);
+            const bool more = walk_follow(a, w, follow, abort_flag);
             // the previous item's exchange has been read; everybody leaves together
             if (softmax_any(!ok || *abort_flag != 0) || !more) break;
             const int R = w.s.n * G, row0 = w.pair * 2 * kTile;

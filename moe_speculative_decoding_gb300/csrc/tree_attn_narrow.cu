@@ -51,7 +51,7 @@ struct Lay {
                               oQ = oP + 2 * kP, oSSc = oQ + kQ, oBar = oSSc;
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
                          bCE = bCF + NC, bS = bCE + NC, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
-                         bO = bQ + 1, bFix = bO + 1, bW = bFix + 4, bDrain = bW + 1, kBars = bDrain + 1;
+                         bO = bQ + 1, bFix = bO + 1, bW = bFix + 4, bDrain = bW + kRecords, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
@@ -61,9 +61,10 @@ struct Lay {
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
     static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
     static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
-    static constexpr uint32_t oUnit = oMask + NT * 8;          // float [2]: a warpgroup's accumulator unit
-    static constexpr uint32_t oWalk = oUnit + 16;                  // Walk
-    static constexpr uint32_t kSmem = oWalk + 128;
+    static constexpr uint32_t oTo = oMask + NT * 8;                // int64 [NT]: the rows' output offsets
+    static constexpr uint32_t oUnit = oTo + NT * 8;          // float [2]: a warpgroup's accumulator unit
+    static constexpr uint32_t oWalk = (oUnit + 16 + 7) & ~7u;   // records of walks
+    static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
     static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -199,7 +200,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_init(bar(L::bO), 1);
         for (int i = 0; i < 4; ++i) mbar_init(bar(L::bFix + i), 1);
         mbar_init(bar(L::bDrain), 2);
-        mbar_init(bar(L::bW), 1);
+        for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         *abort_flag = 0;
         v_issued[0] = v_issued[1] = *k_issued = 0;
         fence_mbar_init();
@@ -214,7 +215,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
-    Walk *const walk_s = reinterpret_cast<Walk *>(smem + L::oWalk);
+    Follow follow = {smem + L::oWalk, bar(L::bW), 0};
     const int G = a.group;
 
     if (warp >= 8) {
@@ -223,15 +224,14 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     pdl_trigger();
     Walk w;
     if (warp == kProducerWarp) {
-        walk_share(a, w, walk_s, bar(L::bW));
-        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
+        walk_begin(a, w, blockIdx.x == 0);
+        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
     } else if (warp == kScoreWarp) {
         // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
         uint32_t c = 0, sc[2] = {0, 0}, items = 0;
         bool ok = true;
-        while (ok && walk_next(a, w)) {
+        while (ok && walk_follow(a, w, follow, abort_flag)) {
             ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
             for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
                 const uint32_t slot = c % L::NK, g = t & 1, s_col = tmem + g * NT;
@@ -271,10 +271,9 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     } else if (warp == kOutWarp) {
         // ---------------------------------------------------------------- O^T += V^T P^T, tile by tile
         // (A warp of its own: a tile's K may come later than the weights of the tile before.)
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         uint32_t c = 0, fixes = 0, pc[2] = {0, 0};
         bool ok = true;
-        while (ok && walk_next(a, w)) {
+        while (ok && walk_follow(a, w, follow, abort_flag)) {
             const int T = w.hi - w.lo;
             for (int t = 0; ok && t < T; ++t, ++c) {
                 const uint32_t slot = c % L::NV, g = t & 1, o_col = tmem + (2 + g) * NT;
@@ -307,14 +306,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
     } else if (warp == kValueWarp) {
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
-        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued);
+        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
     } else if (warp >= kAuxWarp) {
-        walk_take(a, w, walk_s, bar(L::bW), abort_flag);
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, v_issued);
+            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, v_issued, follow);
         else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
-            clean_values<L, DP>(a, w, smem, abort_flag, v_issued);
+            clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
     }
     } else {
         // ---------------------------------------------------------------- softmax, two warpgroups
@@ -360,8 +357,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         };
         pdl_wait();
         Walk next;
-        walk_take(a, next, walk_s, bar(L::bW), abort_flag);
-        bool more = walk_next(a, next);
+        bool more = walk_follow(a, next, follow, abort_flag);
         if (more) fetch(next);
         while (true) {
             // the previous item's shared words have been read; everybody leaves together
@@ -521,8 +517,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 ++sc;
             }
             // ------------------------------------------------------------ the item's end
-            next = w;
-            more = walk_next(a, next);
+            more = walk_follow(a, next, follow, abort_flag);
             if (more) fetch(next);
             if (!dead) dead = !wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
@@ -537,6 +532,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             const bool second = T > 1;   // the second warpgroup had a tile
             const float *const m0_s = reinterpret_cast<const float *>(smem + L::oM), *const m1_s = m0_s + NT;
             const float *const red0 = reinterpret_cast<const float *>(smem + L::oRed), *const red1 = red0 + 4 * NT;
+            int64_t *const to_s = reinterpret_cast<int64_t *>(smem + L::oTo);
             float *const w0_s = reinterpret_cast<float *>(smem + L::oAlpha), *const w1_s = w0_s + NT;
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
             if (threadIdx.x < NT) {
@@ -550,6 +546,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 const float inv = !w.whole ? 1.0f : (none ? 0.0f : 1.0f / ll);
                 w0_s[c] = ka * unit_s[0] * inv;
                 w1_s[c] = second ? kb * unit_s[1] * inv : 0.0f;
+                to_s[c] = static_cast<int64_t>(w.s.t0 + c / G) * a.out.token_stride + static_cast<int64_t>(w.hk * G + c % G) * a.out.head_stride;
                 if (c < R) {
                     if (!w.whole)
                         narrow_ml<DP>(a, gridDim.x, slot)[c] = make_float2(mm, ll);
@@ -577,41 +574,45 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 8; ++i) any_bad |= bad[i];
             }
-            if (p < a.cache.dim) {
 #pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const int c = g * H + i;
-                    float o = __uint_as_float(oa[i]) * w0_s[c];
-                    if (second) o = fmaf(__uint_as_float(ob[i]), w1_s[c], o);
-                    oa[i] = __float_as_uint(o);
-                }
-                if (any_bad != 0) {   // non-finite values of drafted tokens, for the rows that see them
-                    for (int tt = max(w.lo, w.s.ctx / kTile); tt < w.hi; ++tt)
-                        for (int j = 0; j < kTile; ++j) {
-                            if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u)) continue;
-                            const float v = value_at<F8>(a, w.b, w.hk, tt * kTile + j, p);
-                            if (fabsf(v) <= 3.4028234e38f) continue;
-                            const int d = tt * kTile + j - w.s.ctx;   // only drafted tokens are marked
+            for (int i = 0; i < H; ++i) {
+                const int c = g * H + i;
+                float o = __uint_as_float(oa[i]) * w0_s[c];
+                if (second) o = fmaf(__uint_as_float(ob[i]), w1_s[c], o);
+                oa[i] = __float_as_uint(o);
+            }
+            if (any_bad != 0 && p < a.cache.dim) {   // non-finite values of drafted tokens, for the rows that see them
+#pragma unroll 1
+                for (int tt = max(w.lo, w.s.ctx / kTile); tt < w.hi; ++tt)
+#pragma unroll 1
+                    for (int j = 0; j < kTile; ++j) {
+                        if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u)) continue;
+                        const float v = value_at<F8>(a, w.b, w.hk, tt * kTile + j, p);
+                        if (fabsf(v) <= 3.4028234e38f) continue;
+                        const int d = tt * kTile + j - w.s.ctx;   // only drafted tokens are marked
 #pragma unroll
-                            for (int i = 0; i < H; ++i)
-                                if (mask_s[g * H + i] >> d & 1ull) oa[i] = __float_as_uint(__uint_as_float(oa[i]) + v);
-                        }
-                }
-                if (w.whole) {
-#pragma unroll
-                    for (int i = 0; i < H; ++i) {
-                        const int c = g * H + i;
-                        if (c < R)
-                            static_cast<__nv_bfloat16 *>(a.out.ptr)[static_cast<int64_t>(w.s.t0 + c / G) * a.out.token_stride +
-                                                                    static_cast<int64_t>(w.hk * G + c % G) * a.out.head_stride + p] =
-                                __float2bfloat16_rn(__uint_as_float(oa[i]));
+                        for (int i = 0; i < H; ++i)
+                            if (mask_s[g * H + i] >> d & 1ull) oa[i] = __float_as_uint(__uint_as_float(oa[i]) + v);
                     }
-                } else {
-                    float *const po = narrow_out<DP>(a, slot) + p;
+                __syncwarp();
+            }
+            if (w.whole) {
+                // two rows at a time: neighbouring lanes trade, and each stores two channels of one row
+                const int odd = lane & 1;
+                uint16_t *const out = static_cast<uint16_t *>(a.out.ptr) + (p & ~1);
 #pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        if (g * H + i < R) po[(g * H + i) * DP] = __uint_as_float(oa[i]);
+                for (int i = 0; i < H; i += 2) {
+                    const float mine = __uint_as_float(odd ? oa[i + 1] : oa[i]);
+                    const float other = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, odd ? oa[i] : oa[i + 1], 1));
+                    const int c = g * H + i + odd;
+                    if (c < R && p < a.cache.dim)
+                        *reinterpret_cast<uint32_t *>(out + to_s[c]) = odd ? pack2(other, mine, false) : pack2(mine, other, false);
                 }
+            } else if (p < a.cache.dim) {
+                float *const po = narrow_out<DP>(a, slot) + p;
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                    if (g * H + i < R) po[(g * H + i) * DP] = __uint_as_float(oa[i]);
             }
             __syncwarp();
         }

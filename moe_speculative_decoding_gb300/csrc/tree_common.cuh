@@ -294,18 +294,6 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
     w.hk = item / w.s.pairs;
     w.pair = item % w.s.pairs;
 }
-// One warp finds the CTA's range and leaves it to the others in shared memory (`bar` counts 1).
-__device__ __forceinline__ void walk_share(const TreeArgs &a, Walk &w, Walk *place, uint32_t bar) {
-    walk_begin(a, w, blockIdx.x == 0);
-    if ((threadIdx.x & 31) == 0) *place = w;
-    warp_arrive(bar);
-}
-__device__ __forceinline__ void walk_take(const TreeArgs &a, Walk &w, const Walk *place, uint32_t bar, volatile int32_t *abort_flag) {
-    wait_for(bar, 0, abort_flag, a.err, a.wait_limit);
-    w = *place;
-    if (*abort_flag != 0) w.at = w.end = 0;
-}
-
 // Sets the next item's part; false at the end of the range.
 __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
     if (w.at >= w.end) return false;
@@ -328,6 +316,37 @@ __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
     w.whole = w.lo == 0 && w.hi == w.s.tiles;
     w.at = stop;
     return true;
+}
+
+// The K producer, which runs ahead of all others, walks; the others follow it through a ring of
+// records in shared memory (finding an item's place takes a chain of global loads, microseconds
+// while the memory is busy).  Every role is less than kRecords items behind: K's ring holds at most
+// four tiles, and K of item i + 5 is not copied before item i + 1's queries are in place, that is
+// before the softmax has finished item i.
+constexpr int kRecords = 8;
+constexpr uint32_t kRecordBytes = 96;
+static_assert(sizeof(Walk) <= kRecordBytes, "a record holds a walk");
+struct Follow {
+    uint8_t *ring;      // [kRecords][kRecordBytes]
+    uint32_t bars;      // [kRecords]
+    uint32_t n;         // records published or taken
+};
+__device__ __forceinline__ bool walk_lead(const TreeArgs &a, Walk &w, Follow &f) {
+    const bool more = walk_next(a, w);
+    if ((threadIdx.x & 31) == 0) {
+        Walk *const r = reinterpret_cast<Walk *>(f.ring + (f.n % kRecords) * kRecordBytes);
+        *r = w;
+        if (!more) r->lo = -1;   // the end
+    }
+    warp_arrive(f.bars + 8u * (f.n % kRecords));
+    ++f.n;
+    return more;
+}
+__device__ __forceinline__ bool walk_follow(const TreeArgs &a, Walk &w, Follow &f, volatile int32_t *abort_flag) {
+    if (!wait_for(f.bars + 8u * (f.n % kRecords), (f.n / kRecords) & 1u, abort_flag, a.err, a.wait_limit)) return false;
+    w = *reinterpret_cast<const Walk *>(f.ring + (f.n % kRecords) * kRecordBytes);
+    ++f.n;
+    return w.lo >= 0;
 }
 
 // Partial results: per CTA two slots (its first item, its last), each [2 M tiles][DP / 4][128
@@ -454,7 +473,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <typename L, bool F8, int DP, int FIRST, int LAST>
 __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                         uint8_t *smem, int box_rows, volatile int32_t *abort_flag,
-                                        volatile uint32_t *k_issued, volatile uint32_t *v_issued) {
+                                        volatile uint32_t *k_issued, volatile uint32_t *v_issued, Follow f) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -464,7 +483,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
     constexpr int kNone = -2147483647;    // a box beyond the length
     uint32_t cnt = 0, k_cnt = 0;
     bool ok = true;
-    while (ok && walk_next(a, w)) {
+    while (ok && (FIRST == 0 ? walk_lead(a, w, f) : walk_follow(a, w, f, abort_flag))) {
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
         // The places of 32 boxes, a lane each, for 32 / boxes tiles; the next ones are on their way
         // while these are used.
@@ -554,13 +573,13 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
 // the product.  Rows that do get it added at the end of the item (bad bits).
 template <typename L, int DP>
 __device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t *smem, volatile int32_t *abort_flag,
-                                             const volatile uint32_t *v_issued) {
+                                             const volatile uint32_t *v_issued, Follow f) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31);
     uint32_t cnt = 0, fixes = 0;
     bool ok = true;
-    while (ok && walk_next(a, w)) {
+    while (ok && walk_follow(a, w, f, abort_flag)) {
         uint32_t *const bad = reinterpret_cast<uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
         if (lane < 8) bad[lane] = 0;
         __syncwarp();
@@ -641,7 +660,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 // group's).
 template <typename L, int DP>
 __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw, int group,
-                                               volatile int32_t *abort_flag, volatile uint32_t *v_issued) {
+                                               volatile int32_t *abort_flag, volatile uint32_t *v_issued, Follow f) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31), j = cw * 32 + lane;
@@ -650,7 +669,7 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
     const float kMax = 3.4028234e38f;
     uint32_t cnt = 0;
     bool ok = true;
-    while (ok && walk_next(a, w)) {
+    while (ok && walk_follow(a, w, f, abort_flag)) {
         uint32_t *const bad = reinterpret_cast<uint32_t *>(smem + L::oBad) + (w.index & 7) * 8;
         // a warp's words are its own: with two groups, the tiles of one parity
         const int odd = L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(w.lo) ^ static_cast<uint32_t>(group)) & 1u) : 0;
