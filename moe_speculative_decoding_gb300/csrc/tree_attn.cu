@@ -195,7 +195,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2;
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2, *const turn_s = v_issued + 3;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -227,7 +227,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(L::bDrain), 2);
         for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         *abort_flag = 0;
-        *v_issued = *k_issued = 0;
+        *v_issued = *k_issued = *turn_s = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -254,10 +254,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in
-        // line behind the other's, and its O += P V precedes the next S over the same columns.
+        // line behind the other's, and its O += P V precedes the next S over the same columns.  When
+        // the warpgroups share tiles (two M tiles), the warps take turns, O += P V of one tile and S of
+        // the next at a time: started together they stay together, and the tensor cores idle while
+        // both form weights (4,400 cycles for a K/V tile against 2,900 in turns).
         const int g = warp - kMmaWarp;
         const uint32_t s_col = tmem + g * kTile, o_col = tmem + 256 + g * DP;
-        uint32_t base_tile = 0, base_fix = 0, pc = 0, items = 0;
+        uint32_t base_tile = 0, base_fix = 0, pc = 0, items = 0, turns = 0;   // turns of both, before this item
         bool ok = true;
         while (ok && walk_follow(a, w, follow, abort_flag)) {
             const bool two = w.s.n * G - w.pair * 2 * kTile > kTile;
@@ -265,10 +268,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const int edge0 = max(w.lo, w.s.ctx / kTile);   // the first tile that V's cleaner goes over
             ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
             const uint64_t q_desc = desc_kmajor_sw128(base + (two ? g : 0) * L::kQTile);
+            auto k_ready = [&](int u) {
+                const uint32_t c = base_tile + (two ? u >> 1 : u);
+                return wait_for(bar(L::bKF + c % L::NK), (c / L::NK) & 1u, abort_flag, a.err, limit);
+            };
+            auto my_turn = [&](int k) { return !two || wait_count(turn_s, turns + k, abort_flag, a.err, limit); };
+            auto pass_turn = [&](int k) {
+                if (two && lane == 0) *turn_s = turns + k + 1;
+                __syncwarp();
+            };
             auto qk = [&](int u) {
                 const uint32_t c = base_tile + (two ? u >> 1 : u), slot = c % L::NK;
-                ok = wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
-                if (!ok) return;
                 tc_fence_after();
                 const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
                 if (elect_one()) {
@@ -292,7 +302,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
                 __syncwarp();
             };
-            if (ok && g < U) qk(g);
+            if (ok && g < U && (ok = k_ready(g) && my_turn(g))) {
+                qk(g);
+                pass_turn(g);
+            }
             for (int u = g; ok && u < U; u += 2) {
                 const int t = two ? u >> 1 : u, tt = w.lo + t;
                 const uint32_t c = base_tile + t, slot = c % L::NV;
@@ -301,7 +314,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     const uint32_t f = base_fix + (tt - edge0);
                     ok = wait_for(bar(L::bFix + (f & 3u)), (f >> 2) & 1u, abort_flag, a.err, limit);
                 }
-                ok = ok && wait_for(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
+                ok = ok && (!two || u + 2 >= U || k_ready(u + 2)) && my_turn(2 + u) &&
+                     wait_for(bar(L::bP + g), pc & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 ++pc;
                 tc_fence_after();
@@ -314,8 +328,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     if (!two) tc_commit(bar(L::bVE + slot));
                 }
                 __syncwarp();
-                if (u + 2 < U) qk(u + 2);
+                if (u + 2 < U && (two || (ok = k_ready(u + 2)))) qk(u + 2);
+                pass_turn(2 + u);
             }
+            if (two) turns += U + 2;
             if (ok && elect_one()) tc_commit(bar(L::bO));
             __syncwarp();
             base_tile += T;
@@ -537,7 +553,7 @@ constexpr int kJoinThreads = 256;
 template <bool NARROW, int DP>
 __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeArgs a, int ctas) {
     constexpr int Q = DP / 4, ROWS = kJoinThreads / Q, AHEAD = 8;
-    __shared__ long long red[2][kJoinThreads / 32];
+    __shared__ long long red[4][kJoinThreads / 32];
     __shared__ float wt[kMaxCtas][ROWS], inv_s[ROWS];
     const int b = blockIdx.z, hk = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -548,35 +564,43 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         pdl_wait();
         return;
     }
-    long long before = 0, total = 0;
+    Work before = {0, 0}, total = {0, 0};
     for (int i = threadIdx.x; i < a.seqs; i += kJoinThreads) {
-        const long long x = seq_work(a, load_seq(a, i));
-        total += x;
-        if (i < b) before += x;
+        const Work x = seq_work(a, load_seq(a, i));
+        total.tiles += x.tiles;
+        total.items += x.items;
+        if (i < b) {
+            before.tiles += x.tiles;
+            before.items += x.items;
+        }
     }
+    long long *const sums[4] = {&before.tiles, &before.items, &total.tiles, &total.items};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
-        total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
-    }
-    if (lane == 0) {
-        red[0][warp] = before;
-        red[1][warp] = total;
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) *sums[k] += __shfl_xor_sync(0xFFFFFFFFu, *sums[k], o);
+        if (lane == 0) red[k][warp] = *sums[k];
     }
     __syncthreads();
-    before = total = 0;
-    for (int i = 0; i < kJoinThreads / 32; ++i) {
-        before += red[0][i];
-        total += red[1][i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        *sums[k] = 0;
+        for (int i = 0; i < kJoinThreads / 32; ++i) *sums[k] += red[k][i];
     }
+    const int extra = item_cost(total, ctas);
+    const long long W = total.tiles + extra * total.items;
     const int pair = row0 / (2 * kTile), mt = row0 / kTile % 2, r0 = row0 % kTile;
-    const long long first = before + (static_cast<long long>(hk) * s.pairs + pair) * s.tiles;
-    const int C = used_ctas(total, ctas);
-    const int ca = range_of(total, first, C), cb = range_of(total, first + s.tiles - 1, C);
+    const long long item0 = before.tiles + extra * before.items +
+                            (static_cast<long long>(hk) * s.pairs + pair) * (s.tiles + extra);
+    const long long first = item0 + extra;   // the unit of the item's first tile
+    const int C = used_ctas(W, ctas);
+    const int ca = range_of(W, first, C), cb = range_of(W, first + s.tiles - 1, C);
     pdl_wait();
     pdl_trigger();
     if (ca == cb) return;
-    const bool head_slot = range_lo(total, ca, C) == first;   // the item begins its first CTA's range
+    // whether the item is the first with tiles in its first CTA's range (the unit before an item is
+    // the last tile of the one before)
+    const bool head_slot = range_lo(W, ca, C) >= item0;
     auto slot = [&](int i) { return 2 * (ca + i) + (i == 0 && !head_slot ? 1 : 0); };
     const int parts = cb - ca + 1;
     // neighbouring threads read neighbouring 16 bytes of either layout

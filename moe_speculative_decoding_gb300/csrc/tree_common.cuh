@@ -175,6 +175,7 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 // Bounded warp-wide wait until *p has reached v, under mbar_wait's rules.
 __device__ __forceinline__ bool wait_count(const volatile uint32_t *p, uint32_t v, volatile int32_t *abort, int32_t *err,
                                            long long limit) {
+    if (__all_sync(0xFFFFFFFFu, static_cast<int32_t>(*p - v) >= 0)) return true;
     const long long t0 = clock64();
     while (!__all_sync(0xFFFFFFFFu, static_cast<int32_t>(*p - v) >= 0)) {
         const bool late = clock64() - t0 > limit;
@@ -186,7 +187,6 @@ __device__ __forceinline__ bool wait_count(const volatile uint32_t *p, uint32_t 
             return false;
         }
     }
-    __threadfence_block();
     return true;
 }
 
@@ -209,13 +209,25 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
     s.pairs = (s.n * a.group + 2 * kTile - 1) / (2 * kTile);
     return s;
 }
-__device__ __forceinline__ long long seq_work(const TreeArgs &a, const Seq &s) {
-    return static_cast<long long>(a.cache.heads) * s.pairs * s.tiles;
+// The list is cut by cost, in tiles: an item costs its tiles and, when there are several tiles for
+// every CTA, kItemCost more, for its beginning and end (8,000-13,000 cycles against 1,500-4,000 of a
+// tile): before that, a CTA with parts of three items took 74,000 cycles where one with the same
+// number of tiles of one item took 43,000 (sixteen sequences of 800-4100 positions, 8 heads).
+// An item's extra units come first; a CTA whose range holds only such units has nothing to do.
+constexpr int kItemCost = 6;
+struct Work {
+    long long tiles, items;
+};
+__device__ __forceinline__ Work seq_work(const TreeArgs &a, const Seq &s) {
+    Work w;
+    w.items = s.tiles > 0 ? static_cast<long long>(a.cache.heads) * s.pairs : 0;
+    w.tiles = w.items * s.tiles;
+    return w;
 }
-// The list is cut for at most as many CTAs as it has tiles, so that no range is empty (the join
-// reads a part of every CTA between an item's first and last).
+__device__ __forceinline__ int item_cost(const Work &total, int ctas) { return total.tiles > 2ll * ctas ? kItemCost : 0; }
+// At most as many ranges as units, so that none is empty.
 __device__ __forceinline__ int used_ctas(long long W, int ctas) { return static_cast<int>(min(W, static_cast<long long>(ctas))); }
-// First tile of CTA c's range, and the CTA whose range holds tile x.
+// First unit of CTA c's range, and the CTA whose range holds unit x.
 // (In 32 bits where they do: a 64-bit division is some hundred instructions.)
 __device__ __forceinline__ long long range_lo(long long W, int c, int C) {
     if (W < (1ll << 23)) return static_cast<uint32_t>(W) * static_cast<uint32_t>(c) / static_cast<uint32_t>(C);
@@ -230,9 +242,11 @@ __device__ __forceinline__ int range_of(long long W, long long x, int C) {
 // A CTA's walk over its range: item by item, the part [lo, hi) of the item's position tiles.
 struct Walk {
     Seq s;
-    long long at, end, item0;   // next tile of the list, the range's end, the item's first tile
+    long long at, end, item0;   // next unit of the list, the range's end, the item's first unit
     int b, hk, pair, lo, hi;
+    int extra;                  // units of an item before its tiles
     bool whole;                 // the item lies in this CTA alone
+    bool first;                 // the range's first item has not been looked at
     int index;                  // items walked before
 };
 // The whole warp calls these; the outcome is uniform.
@@ -241,12 +255,13 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
     w.index = -1;
     w.b = w.hk = w.pair = 0;
     w.at = w.end = w.item0 = 0;
-    // tiles of the list, 32 sequences a step; the last step's stay in registers (all of them, when
-    // there is one step)
+    w.extra = 0;
+    w.first = true;
+    // 32 sequences a step; the last step's stay in registers (all of them, when there is one step)
     Seq mine;
-    long long total = 0, x = 0, incl = 0;
+    Work x = {0, 0}, incl = {0, 0}, total = {0, 0};
     auto step = [&](int b0) {
-        x = 0;
+        x.tiles = x.items = 0;
         if (b0 + lane < a.seqs) {
             mine = load_seq(a, b0 + lane);
             x = seq_work(a, mine);
@@ -254,28 +269,35 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
         incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += y;
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, incl.tiles, o), z = __shfl_up_sync(0xFFFFFFFFu, incl.items, o);
+            if (lane >= o) {
+                incl.tiles += y;
+                incl.items += z;
+            }
         }
     };
     mine.bad = false;
     for (int b0 = 0; b0 < a.seqs; b0 += 32) {
         step(b0);
         if (b0 + lane < a.seqs && mine.bad && report) record_error(a.err, MOE_ERR_BAD_ID);
-        total += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        total.tiles += __shfl_sync(0xFFFFFFFFu, incl.tiles, 31);
+        total.items += __shfl_sync(0xFFFFFFFFu, incl.items, 31);
     }
-    const int C = used_ctas(total, gridDim.x), c = static_cast<int>(blockIdx.x);
+    w.extra = item_cost(total, gridDim.x);
+    const long long W = total.tiles + w.extra * total.items;
+    const int C = used_ctas(W, gridDim.x), c = static_cast<int>(blockIdx.x);
     if (c >= C) return;
-    w.at = range_lo(total, c, C);
-    w.end = range_lo(total, c + 1, C);
-    long long before = 0;   // tiles of the sequences before
+    w.at = range_lo(W, c, C);
+    w.end = range_lo(W, c + 1, C);
+    long long before = 0;   // units of the sequences before
     for (int b0 = 0;; b0 += 32) {
         if (a.seqs > 32) step(b0);
-        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + incl > w.at);
+        const long long units = incl.tiles + w.extra * incl.items;
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + units > w.at);
         if (past != 0) {
             const int l = __ffs(past) - 1;
             w.b = b0 + l;
-            before += __shfl_sync(0xFFFFFFFFu, incl - x, l);
+            before += __shfl_sync(0xFFFFFFFFu, units - x.tiles - w.extra * x.items, l);
             w.s.t0 = __shfl_sync(0xFFFFFFFFu, mine.t0, l);
             w.s.n = __shfl_sync(0xFFFFFFFFu, mine.n, l);
             w.s.ctx = __shfl_sync(0xFFFFFFFFu, mine.ctx, l);
@@ -285,37 +307,44 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
             w.s.bad = false;
             break;
         }
-        before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        before += __shfl_sync(0xFFFFFFFFu, units, 31);
     }
     const long long into = w.at - before;
-    const int item = into < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(w.s.tiles))
-                                        : static_cast<int>(into / w.s.tiles);
-    w.item0 = before + static_cast<long long>(item) * w.s.tiles;
+    const int size = w.s.tiles + w.extra;
+    const int item = into < (1ll << 31) ? static_cast<int>(static_cast<uint32_t>(into) / static_cast<uint32_t>(size))
+                                        : static_cast<int>(into / size);
+    w.item0 = before + static_cast<long long>(item) * size;
     w.hk = item / w.s.pairs;
     w.pair = item % w.s.pairs;
+    w.first = true;
 }
 // Sets the next item's part; false at the end of the range.
 __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
-    if (w.at >= w.end) return false;
-    if (w.index >= 0) {   // step to the item at w.at
-        w.item0 += w.s.tiles;
-        if (++w.pair == w.s.pairs) {
-            w.pair = 0;
-            if (++w.hk == a.cache.heads) {
-                w.hk = 0;
-                do {
-                    w.s = load_seq(a, ++w.b);
-                } while (w.s.tiles == 0 || w.s.pairs == 0);   // there is work left, so one follows
+    while (w.at < w.end) {
+        if (!w.first) {   // step to the item at w.at
+            w.item0 += w.s.tiles + w.extra;
+            if (++w.pair == w.s.pairs) {
+                w.pair = 0;
+                if (++w.hk == a.cache.heads) {
+                    w.hk = 0;
+                    do {
+                        w.s = load_seq(a, ++w.b);
+                    } while (w.s.tiles == 0 || w.s.pairs == 0);   // there are units left, so one follows
+                }
             }
         }
+        w.first = false;
+        const long long tile0 = w.item0 + w.extra, past = tile0 + w.s.tiles, stop = min(w.end, past);
+        w.lo = static_cast<int>(max(w.at, tile0) - tile0);
+        w.hi = static_cast<int>(stop - tile0);
+        w.whole = w.lo == 0 && w.hi == w.s.tiles;
+        w.at = stop;
+        if (w.hi > w.lo) {
+            ++w.index;
+            return true;
+        }
     }
-    ++w.index;
-    w.lo = static_cast<int>(w.at - w.item0);
-    const long long stop = min(w.end, w.item0 + w.s.tiles);
-    w.hi = static_cast<int>(stop - w.item0);
-    w.whole = w.lo == 0 && w.hi == w.s.tiles;
-    w.at = stop;
-    return true;
+    return false;
 }
 
 // The K producer, which runs ahead of all others, walks; the others follow it through a ring of
@@ -324,7 +353,7 @@ __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
 // four tiles, and K of item i + 5 is not copied before item i + 1's queries are in place, that is
 // before the softmax has finished item i.
 constexpr int kRecords = 8;
-constexpr uint32_t kRecordBytes = 96;
+constexpr uint32_t kRecordBytes = 104;
 static_assert(sizeof(Walk) <= kRecordBytes, "a record holds a walk");
 struct Follow {
     uint8_t *ring;      // [kRecords][kRecordBytes]
