@@ -374,17 +374,27 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             {
                 constexpr int C = DP / 8;
                 const int tiles = two ? 2 : 1;
-                for (int i = static_cast<int>(threadIdx.x); i < tiles * kTile * C; i += 256) {
-                    const int c = i % C, rr = i / C, mt = rr / kTile, lr = rr % kTile;
-                    const int row = row0 + rr;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (row < R && c * 8 < a.cache.dim)
-                        x = *reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
-                            static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
-                    float unscale;
-                    store_query<F8, DP>(smem + mt * L::kQTile, kTile, lr, c, x, unscale);
-                    if (F8 && c == 0) qs[mt * 128 + lr] = unscale;
+                const int c = static_cast<int>(threadIdx.x) % C;   // 256 / C rows a step, eight steps' loads at a time
+#pragma unroll 1
+                for (int r0 = static_cast<int>(threadIdx.x) / C; r0 < tiles * kTile; r0 += 8 * (256 / C)) {
+                    uint4 x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = row0 + r0 + i * (256 / C);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (row < R && c * 8 < a.cache.dim)
+                            x[i] = *reinterpret_cast<const uint4 *>(
+                                static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
+                                static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = r0 + i * (256 / C), mt = rr / kTile, lr = rr % kTile;
+                        if (mt >= tiles) break;
+                        float unscale;
+                        store_query<F8, DP>(smem + mt * L::kQTile, kTile, lr, c, x[i], unscale);
+                        if (F8 && c == 0) qs[mt * 128 + lr] = unscale;
+                    }
                 }
                 fence_proxy_async_smem();
             }
@@ -473,6 +483,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 for (int i = 0; i < 8; ++i) any_bad |= bad[i];
             }
             const int64_t out_off = static_cast<int64_t>(token) * a.out.token_stride + static_cast<int64_t>(head) * a.out.head_stride;
+#pragma unroll 1
             for (int c = c0; c < c1; c += 32) {
                 __syncwarp();
                 float o[32];
@@ -497,9 +508,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
                 if (any_bad != 0) {
                     // non-finite values of drafted tokens, for the rows that see them
+#pragma unroll 1
                     for (int tt = max(w.lo, w.s.ctx / kTile); tt < w.hi; ++tt) {
                         uint32_t see[4];
                         seen_bits(M, w.s, tt, see);
+#pragma unroll 1
                         for (int j = 0; j < kTile; ++j) {
                             if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u) || !(see[j / 32] >> (j & 31) & 1u)) continue;
 #pragma unroll 1

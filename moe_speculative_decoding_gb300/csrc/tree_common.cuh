@@ -622,36 +622,30 @@ __device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t
                 ok = false;
                 break;
             }
-            uint8_t *const v = smem + L::oV + slot * L::kVSlot;
-            constexpr int C = DP / 8;   // 16-byte chunks of a row; 32 / C rows at a time
-            const int c = lane % C;
+            constexpr int C = DP / 8, ROWS = 32 / C, BATCH = 4;   // 16-byte chunks of a row; rows at a time
+            uint8_t *const v = smem + L::oV + slot * L::kVSlot + (lane % C / 8) * (kTile * 128) + (lane % 8) * 16;
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
-            for (int r0 = first / (32 / C) * (32 / C); r0 < kTile; r0 += 32 / C) {
-                const int r = r0 + lane / C;
-                uint4 *const p = reinterpret_cast<uint4 *>(v + (c / 8) * (kTile * 128) + r * 128 + (c % 8) * 16);
-                if (r >= stop) {
-                    *p = make_uint4(0, 0, 0, 0);
-                } else if (r >= first) {
-                    uint4 x = *p;
-                    uint32_t *const q = reinterpret_cast<uint32_t *>(&x);
-                    bool hit = false;
+#pragma unroll 1
+            for (int r0 = first + lane / C; r0 < stop; r0 += BATCH * ROWS) {
+                uint4 x[BATCH];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if ((q[i] & 0x7F80u) == 0x7F80u) {
-                            q[i] &= 0xFFFF0000u;
-                            hit = true;
-                        }
-                        if ((q[i] & 0x7F800000u) == 0x7F800000u) {
-                            q[i] &= 0x0000FFFFu;
-                            hit = true;
-                        }
-                    }
-                    if (hit) {
-                        *p = x;
-                        atomicOr(&bad[(tt & 1) * 4 + r / 32], 1u << (r & 31));
-                    }
+                for (int i = 0; i < BATCH; ++i)
+                    if (r0 + i * ROWS < stop) x[i] = *reinterpret_cast<const uint4 *>(v + (r0 + i * ROWS) * 128);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = r0 + i * ROWS;
+                    uint32_t *const q = reinterpret_cast<uint32_t *>(&x[i]);
+                    // bit 15 of a half whose exponent is all ones
+                    auto over = [](uint32_t y) { return ((y & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+                    if (r >= stop || (over(q[0]) | over(q[1]) | over(q[2]) | over(q[3])) == 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) q[k] &= ~((over(q[k]) >> 15) * 0xFFFFu);
+                    *reinterpret_cast<uint4 *>(v + r * 128) = x[i];
+                    atomicOr(&bad[(tt & 1) * 4 + r / 32], 1u << (r & 31));
                 }
             }
+#pragma unroll 4
+            for (int r = stop + lane / C; r < kTile; r += ROWS) *reinterpret_cast<uint4 *>(v + r * 128) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __threadfence_block();
             warp_arrive(bar(L::bFix + (fixes & 3u)));   // the ring of V keeps this at most NV ahead
