@@ -446,8 +446,8 @@ moe_status_t moe_fit_op_times(int32_t count, const int32_t *n, const int32_t *U,
 moe_status_t moe_last_device_error(void *ws, moe_stream_t s, int32_t *code);
 
 /*
- * Sets, for the expert-operation calls issued after it by this process, how many SM clock
- * cycles one device pipeline wait (a shared-memory barrier, or another CTA's flag) may take
+ * Sets, for the expert-operation and tree-attention calls issued after it by this process, how
+ * many SM clock cycles one device pipeline wait (a shared-memory barrier, or another CTA's flag) may take
  * before the call gives up: it then records MOE_ERR_DEVICE_TIMEOUT in the workspace's error
  * word, waits (bounded) for its copies and tensor-core operations in flight, frees its
  * tensor memory and returns, leaving the CUDA context usable.  cycles = 0 restores the

@@ -217,7 +217,7 @@ def last_device_error(ws: torch.Tensor) -> int:
 
 
 def set_wait_limit(cycles: int) -> None:
-    """moe_set_wait_limit: SM cycles one device pipeline wait of later expert calls may take
+    """moe_set_wait_limit: SM cycles one device pipeline wait of later expert and tree-attention calls may take
     before the call records MOE_ERR_DEVICE_TIMEOUT and returns (0: the default; infrastructure)."""
     _check(lib().moe_set_wait_limit(int(cycles)), "moe_set_wait_limit")
 

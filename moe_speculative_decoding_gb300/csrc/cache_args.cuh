@@ -40,6 +40,7 @@ struct TreeArgs {
     void *part;                // partial results (after the workspace header)
     long long wait_limit;
     int32_t seqs, tokens, max_tokens, max_pages, group;
+    int32_t undivided;         // an item is one CTA's (short contexts)
     float scale_log2;          // scale * log2(e)
 };
 
@@ -52,7 +53,7 @@ cudaError_t launch_tree_simt(const TreeArgs &a, cudaStream_t s, bool pdl);
 // launch (cudaErrorNotSupported: strides that no tensor map describes).
 bool tree_attn_supports(const moe_kv_cache_t &c, const moe_heads_t &q, const moe_heads_t &out);
 size_t tree_attn_part_bytes(int dim);
-cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t s, bool pdl);
+cudaError_t launch_tree_attn(TreeArgs a, cudaStream_t s, bool pdl);
 long long current_wait_limit();   // moe_set_wait_limit's, or the default
 
 }  // namespace moe

@@ -74,7 +74,7 @@ struct Lay {
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
                          bCE = bCF + NC, bS = bCE + NC, bP = bS + 2, bQ = bP + 2, bO = bQ + 1, bFix = bO + 1,
                          bDrain = bFix + 4, bW = bDrain + 1, kBars = bW + kRecords;
-    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued
+    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued, tiles copied, turns
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);    // F8: float [NC], the running power of two
@@ -195,7 +195,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2, *const turn_s = v_issued + 3;
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const copied = v_issued + 1, *const turn_s = v_issued + 3;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -227,7 +227,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         mbar_init(bar(L::bDrain), 2);
         for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         *abort_flag = 0;
-        *v_issued = *k_issued = *turn_s = 0;
+        *v_issued = copied[0] = copied[1] = *turn_s = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -250,7 +250,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     Walk w;
     if (warp == kProducerWarp) {
         walk_begin(a, w, blockIdx.x == 0);
-        produce<L, F8, DP, 0, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
+        produce<L, F8, DP, 0, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
     } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
         // ---------------------------------------------------------------- products
         // One warp issues both products of one softmax warpgroup's tiles, so that neither waits in
@@ -345,7 +345,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         __syncwarp();
     } else if (warp >= L::kAux) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, v_issued, follow);
+            convert_values<L, DP>(a, w, smem, warp - L::kAux, 0, abort_flag, follow);
         else
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
     }
@@ -550,6 +550,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     }
     tc_fence_before();
     __syncthreads();
+    if (warp == kProducerWarp && *abort_flag != 0) drain_copies<L, F8>(smem, copied);
     if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_co
         *sums[k] = 0;
         for (int i = 0; i < kJoinThreads / 32; ++i) *sums[k] += red[k][i];
     }
-    const int extra = item_cost(total, ctas);
+    const int extra = item_cost(a, total, ctas);
     const long long W = total.tiles + extra * total.items;
     const int pair = row0 / (2 * kTile), mt = row0 / kTile % 2, r0 = row0 % kTile;
     const long long item0 = before.tiles + extra * before.items +
@@ -758,7 +759,7 @@ size_t tree_attn_part_bytes(int dim) {
     return static_cast<size_t>(sms) * 2 * 2 * kTile * (dim_padded(dim) * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t s, bool pdl) {
+cudaError_t launch_tree_attn(TreeArgs a, cudaStream_t s, bool pdl) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -769,20 +770,27 @@ cudaError_t launch_tree_attn(const TreeArgs &a, cudaStream_t s, bool pdl) {
     CUtensorMap tm_k, tm_v;
     if (!encode(&tm_k, a.cache, a.cache.k, rows, true) || !encode(&tm_v, a.cache, a.cache.v, rows, !f8))
         return cudaErrorNotSupported;
+    // Short contexts: an item's few tiles one after the other take less time than another end of an
+    // item and the launch that joins the parts.  8 heads of 128, 4 rows, one sequence: 7.9 us
+    // undivided against 8.8 at two tiles, 8.6 and 8.9 at three, 9.3 and 8.9 at four (and 2 us less
+    // for the host), 12.2 and 9.2 at eight; 256 rows, four sequences: 24.0 and 30.8 at eight.  With
+    // enough items for the SMs (16 sequences, e4m3): 16.7 and 24.8 at eight, 22.6 and 24.4 at twelve,
+    // 27.4 and 26.9 at sixteen.
+    const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kTile - 1) / kTile;
+    const long long items = static_cast<long long>(a.seqs) * a.cache.heads * ((a.max_tokens * a.group + 2 * kTile - 1) / (2 * kTile));
+    a.undivided = item_tiles <= (2 * items >= sms ? 12 : a.max_tokens * a.group > kNarrowRows ? 8 : 4);
     // no more CTAs than the page tables could fill with tiles
-    const long long most = static_cast<long long>(a.seqs) * a.cache.heads * ((a.max_tokens * a.group + 2 * kTile - 1) / (2 * kTile)) *
-                           ((static_cast<long long>(a.max_pages) * a.cache.page + kTile - 1) / kTile);
-    const int ctas = static_cast<int>(std::min<long long>(sms, most));
+    const int ctas = static_cast<int>(std::min<long long>(sms, items * item_tiles));
     if (a.max_tokens * a.group <= kNarrowRows) {
         e = launch_tree_narrow(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || a.undivided) return e;
         return wide_head ? launch_join<true, 128>(a, ctas, s, pdl) : launch_join<true, 64>(a, ctas, s, pdl);
     }
     if (wide_head)
         e = f8 ? launch_wide<true, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : launch_wide<false, 128>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
     else
         e = f8 ? launch_wide<true, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl) : launch_wide<false, 64>(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.undivided) return e;
     return wide_head ? launch_join<false, 128>(a, ctas, s, pdl) : launch_join<false, 64>(a, ctas, s, pdl);
 }
 

@@ -52,14 +52,15 @@ struct Lay {
     static constexpr int bKF = 0, bKE = NK, bVF = 2 * NK, bVE = bVF + NV, bSF = bVE + NV, bSE = bSF + NS, bCF = bSE + NS,
                          bCE = bCF + NC, bS = bCE + NC, bSFree = bS + 2, bP = bSFree + 2, bPV = bP + 2, bQ = bPV + 2,
                          bO = bQ + 1, bFix = bO + 1, bW = bFix + 4, bDrain = bW + kRecords, kBars = bDrain + 1;
-    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;
+    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued, tiles copied
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
     static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);   // F8: float [NC][4], the warps' largest value scales
     static constexpr uint32_t oCs = oSigma + (F8 ? NC * 16 : 0);        // F8: float [NT]: score to log2 units
-    static constexpr uint32_t oM = oCs + (F8 ? NT * 4 : 0);    // float [2][NT]: minus the maxima of a warpgroup
+    static constexpr uint32_t oM = oCs + (F8 ? NT * 4 : 0);    // float [2][NT]: minus a warpgroup's maxima, 0 where there is none
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
-    static constexpr uint32_t oRed = oAlpha + 2 * NT * 4;          // float [2][4][NT]: per warp
+    static constexpr uint32_t oDelta = oAlpha + 2 * NT * 4;        // float [2][NT]: its logarithm
+    static constexpr uint32_t oRed = oDelta + 2 * NT * 4;          // float [2][4][NT]: per warp
     static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
     static constexpr uint32_t oTo = oMask + NT * 8;                // int64 [NT]: the rows' output offsets
     static constexpr uint32_t oUnit = oTo + NT * 8;          // float [2]: a warpgroup's accumulator unit
@@ -168,7 +169,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     volatile int32_t *const abort_flag = reinterpret_cast<volatile int32_t *>(smem + L::oMisc + 4);
-    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const k_issued = v_issued + 2;   // v_issued: one word per converter group
+    volatile uint32_t *const v_issued = reinterpret_cast<volatile uint32_t *>(smem + L::oMisc + 8), *const copied = v_issued + 1;
     const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = static_cast<int>(threadIdx.x & 31);
     const long long limit = a.wait_limit;
@@ -202,7 +203,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_init(bar(L::bDrain), 2);
         for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         *abort_flag = 0;
-        v_issued[0] = v_issued[1] = *k_issued = 0;
+        *v_issued = copied[0] = copied[1] = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_k);
         tma_prefetch_map(&tm_v);
@@ -225,7 +226,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     Walk w;
     if (warp == kProducerWarp) {
         walk_begin(a, w, blockIdx.x == 0);
-        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
+        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
     } else if (warp == kScoreWarp) {
         // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
         const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
@@ -306,10 +307,10 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         mbar_wait_drain(bar(L::bDrain), 0, kDrain);
         __syncwarp();
     } else if (warp == kValueWarp) {
-        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, k_issued, v_issued, follow);
+        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
     } else if (warp >= kAuxWarp) {
         if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, v_issued, follow);
+            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, follow);
         else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
             clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
     }
@@ -322,6 +323,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         const uint32_t s_addr = tmem + lanes + g * NT, o_addr = tmem + lanes + (2 + g) * NT;
         float *const nm_s = reinterpret_cast<float *>(smem + L::oM) + g * NT;
         float *const alpha_s = reinterpret_cast<float *>(smem + L::oAlpha) + g * NT;
+        float *const delta_s = reinterpret_cast<float *>(smem + L::oDelta) + g * NT;
         float *const red_s = reinterpret_cast<float *>(smem + L::oRed) + g * 4 * NT;
         const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
         const volatile float *const sigma_s = reinterpret_cast<const volatile float *>(smem + L::oSigma);
@@ -374,7 +376,9 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 }
             }
             if (threadIdx.x < NT) mask_s[threadIdx.x] = next_mask;
-            if (p < NT) nm_s[p] = -kNone;
+            float m_own = kNone;   // of column p
+            bool all_seen = false;
+            if (p < NT) nm_s[p] = 0.0f;
             fence_proxy_async_smem();
             warp_arrive(bar(L::bQ));
             named_barrier(4, 256);
@@ -406,15 +410,20 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     warp_arrive(bar(L::bSFree + g));
                     if (F8) warp_arrive(bar(L::bCE + sb));
                 }
-                // scores in log2 units; what a row does not see is -inf
+                // scores in log2 units above the rows' maxima so far (above 0 where a row has none);
+                // what a row does not see is -inf
                 const F2 ks2 = f2(ks, ks);
 #pragma unroll
                 for (int c = 0; c < NT; c += 4) {
-                    F2 s0 = f2_mul(f2(x[c], x[c + 1]), ks2), s1 = f2_mul(f2(x[c + 2], x[c + 3]), ks2);
+                    const float4 n = *reinterpret_cast<const float4 *>(nm_s + c);
+                    F2 s0 = f2(x[c], x[c + 1]), s1 = f2(x[c + 2], x[c + 3]);
                     if (F8) {
                         const float4 k = *reinterpret_cast<const float4 *>(cs_s + c);
-                        s0 = f2_mul(s0, f2(k.x, k.y));
-                        s1 = f2_mul(s1, f2(k.z, k.w));
+                        s0 = f2_fma(f2_mul(s0, ks2), f2(k.x, k.y), f2(n.x, n.y));
+                        s1 = f2_fma(f2_mul(s1, ks2), f2(k.z, k.w), f2(n.z, n.w));
+                    } else {
+                        s0 = f2_fma(s0, ks2, f2(n.x, n.y));
+                        s1 = f2_fma(s1, ks2, f2(n.z, n.w));
                     }
                     float s[4];
                     f2_get(s0, s[0], s[1]);
@@ -430,21 +439,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             if (d >= 64 || !(mask_s[c] >> d & 1ull)) x[c] = __float_as_uint(ninf());
                     }
                 }
-                // any score far above its row's maximum so far?  (That is kNone before a row has
-                // seen anything, so that its first finite score is.)
-                bool move = t < 2 || (F8 && sigma_new != sigma);
-                if (t >= 2) {
-                    float over = ninf();
+                // any score far above its row's maximum so far, or a row that had seen nothing?
+                bool move = !all_seen || (F8 && sigma_new != sigma);
+                float over = ninf();
 #pragma unroll
-                    for (int c = 0; c < NT; c += 4) {
-                        const float4 n = *reinterpret_cast<const float4 *>(nm_s + c);
-                        float d0, d1, d2, d3;
-                        f2_get(f2_add(f2(x[c], x[c + 1]), f2(n.x, n.y)), d0, d1);
-                        f2_get(f2_add(f2(x[c + 2], x[c + 3]), f2(n.z, n.w)), d2, d3);
-                        over = fmaxf(fmaxf(over, d0), fmaxf(d1, fmaxf(d2, d3)));
-                    }
-                    move = move || over > kLazy;
-                }
+                for (int c = 0; c < NT; c += 2) over = fmaxf(over, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+                move = move || over > kLazy;
                 if (bar_any(2 + g, 128, move)) {
                     // the columns' maxima over the 128 positions (NaN left out): over the warp's lanes,
                     // then over the four warps
@@ -454,13 +454,28 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     warp_columns<NT, true>(top, lane);
                     store_columns<NT>(red_s + q4 * NT, top, lane);
                     named_barrier(2 + g, 128);
+                    bool unseen = false;
                     if (p < NT) {
-                        const float old = -nm_s[p];
-                        const float mn = fmaxf(fmaxf(old, fmaxf(red_s[p], red_s[NT + p])), fmaxf(red_s[2 * NT + p], red_s[3 * NT + p]));
-                        nm_s[p] = -mn;
-                        alpha_s[p] = ex2(old - mn);
+                        const float n = nm_s[p];
+                        const float here = fmaxf(fmaxf(red_s[p], red_s[NT + p]), fmaxf(red_s[2 * NT + p], red_s[3 * NT + p]));
+                        const float mn = fmaxf(m_own, here - n);
+                        unseen = mn == kNone;
+                        const float n_new = unseen ? 0.0f : -mn;
+                        nm_s[p] = n_new;
+                        delta_s[p] = n_new - n;
+                        alpha_s[p] = ex2(m_own - mn);
+                        m_own = mn;
                     }
-                    named_barrier(2 + g, 128);
+                    all_seen = !bar_any(2 + g, 128, unseen);
+#pragma unroll
+                    for (int c = 0; c < NT; c += 4) {
+                        const float4 n = *reinterpret_cast<const float4 *>(delta_s + c);
+                        float s[4];
+                        f2_get(f2_add(f2(x[c], x[c + 1]), f2(n.x, n.y)), s[0], s[1]);
+                        f2_get(f2_add(f2(x[c + 2], x[c + 3]), f2(n.z, n.w)), s[2], s[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[c + i] = __float_as_uint(s[i]);
+                    }
                     if (t >= 2) {
                         // O so far is complete when the previous product is
                         if (!dead) dead = !wait_for(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
@@ -493,11 +508,9 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int c = c8 * 8 + h * 4;
-                        const float4 n = *reinterpret_cast<const float4 *>(nm_s + c);
                         float w0, w1, w2, w3;
-                        f2_get(f2_add(f2(x[c], x[c + 1]), f2(n.x, n.y)), w0, w1);
-                        f2_get(f2_add(f2(x[c + 2], x[c + 3]), f2(n.z, n.w)), w2, w3);
-                        F2 a0 = f2(ex2(w0), ex2(w1)), a1 = f2(ex2(w2), ex2(w3));
+                        F2 a0 = f2(ex2(__uint_as_float(x[c])), ex2(__uint_as_float(x[c + 1])));
+                        F2 a1 = f2(ex2(__uint_as_float(x[c + 2])), ex2(__uint_as_float(x[c + 3])));
                         l2[c / 2] = f2_add(l2[c / 2], a0);
                         l2[c / 2 + 1] = f2_add(l2[c / 2 + 1], a1);
                         if (F8) {
@@ -527,6 +540,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             for (int c = 0; c < NT; c += 2) f2_get(l2[c / 2], l[c], l[c + 1]);
             warp_columns<NT, false>(l, lane);
             store_columns<NT>(red_s + q4 * NT, l, lane);
+            if (p < NT) nm_s[p] = -m_own;
             if (lane == 0 && q4 == 0) unit_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
             named_barrier(4, 256);
             const bool second = T > 1;   // the second warpgroup had a tile
@@ -619,6 +633,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    if (warp == kProducerWarp && *abort_flag != 0) drain_copies<L, F8>(smem, copied);
     if (warp == kScoreWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmem);

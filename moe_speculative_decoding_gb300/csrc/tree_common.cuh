@@ -224,7 +224,9 @@ __device__ __forceinline__ Work seq_work(const TreeArgs &a, const Seq &s) {
     w.tiles = w.items * s.tiles;
     return w;
 }
-__device__ __forceinline__ int item_cost(const Work &total, int ctas) { return total.tiles > 2ll * ctas ? kItemCost : 0; }
+__device__ __forceinline__ int item_cost(const TreeArgs &a, const Work &total, int ctas) {
+    return total.tiles > 2ll * ctas && !a.undivided ? kItemCost : 0;
+}
 // At most as many ranges as units, so that none is empty.
 __device__ __forceinline__ int used_ctas(long long W, int ctas) { return static_cast<int>(min(W, static_cast<long long>(ctas))); }
 // First unit of CTA c's range, and the CTA whose range holds unit x.
@@ -283,7 +285,7 @@ __device__ __forceinline__ void walk_begin(const TreeArgs &a, Walk &w, bool repo
         total.tiles += __shfl_sync(0xFFFFFFFFu, incl.tiles, 31);
         total.items += __shfl_sync(0xFFFFFFFFu, incl.items, 31);
     }
-    w.extra = item_cost(total, gridDim.x);
+    w.extra = item_cost(a, total, gridDim.x);
     const long long W = total.tiles + w.extra * total.items;
     const int C = used_ctas(W, gridDim.x), c = static_cast<int>(blockIdx.x);
     if (c >= C) return;
@@ -335,8 +337,13 @@ __device__ __forceinline__ bool walk_next(const TreeArgs &a, Walk &w) {
         }
         w.first = false;
         const long long tile0 = w.item0 + w.extra, past = tile0 + w.s.tiles, stop = min(w.end, past);
-        w.lo = static_cast<int>(max(w.at, tile0) - tile0);
-        w.hi = static_cast<int>(stop - tile0);
+        if (a.undivided) {   // the item is the range's that holds its first tile
+            w.lo = w.at > tile0 ? w.s.tiles : 0;
+            w.hi = w.s.tiles;
+        } else {
+            w.lo = static_cast<int>(max(w.at, tile0) - tile0);
+            w.hi = static_cast<int>(stop - tile0);
+        }
         w.whole = w.lo == 0 && w.hi == w.s.tiles;
         w.at = stop;
         if (w.hi > w.lo) {
@@ -502,7 +509,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 template <typename L, bool F8, int DP, int FIRST, int LAST>
 __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtensorMap *tm_k, const CUtensorMap *tm_v,
                                         uint8_t *smem, int box_rows, volatile int32_t *abort_flag,
-                                        volatile uint32_t *k_issued, volatile uint32_t *v_issued, Follow f) {
+                                        volatile uint32_t *copied, volatile uint32_t *v_issued, Follow f) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31);
@@ -510,7 +517,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
     const moe_kv_cache_t &kc = a.cache;
     constexpr uint32_t NV = F8 ? L::NS : L::NV;
     constexpr int kNone = -2147483647;    // a box beyond the length
-    uint32_t cnt = 0, k_cnt = 0;
+    uint32_t cnt = 0, ahead = 0;   // ahead: K of tile cnt is on its way
     bool ok = true;
     while (ok && (FIRST == 0 ? walk_lead(a, w, f) : walk_follow(a, w, f, abort_flag))) {
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
@@ -554,6 +561,7 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
                 const uint32_t dst = base + (v ? (F8 ? L::oS + slot * L::kStage : L::oV + slot * L::kVSlot)
                                                : L::oK + slot * L::kKSlot);
                 if (!wait_for(empty, (use & 1u) ^ 1u, abort_flag, a.err, a.wait_limit)) {
+                    ahead = v - FIRST;
                     ok = false;
                     break;
                 }
@@ -577,23 +585,33 @@ __device__ __forceinline__ void produce(const TreeArgs &a, Walk &w, const CUtens
                     }
                 }
                 __syncwarp();
-                // once a tile is announced, its slot's previous use is over, and the slot's parity
-                // tells this use from that one
-                if (v == 0) ++k_cnt;
-                if (lane == 0 && (v == 0 || !F8)) {
+                // for V's cleaner: once a tile is announced, its slot's previous use is over, and the
+                // slot's parity tells this use from that one
+                if (v == 1 && !F8 && lane == 0) {
                     __threadfence_block();
-                    *(v ? v_issued : k_issued) = cnt + 1;
+                    *v_issued = cnt + 1;
                 }
             }
             if (!ok) break;
         }
     }
-    if (*abort_flag != 0) {   // copies nobody waited for must land before the CTA leaves
-        for (uint32_t j = k_cnt > L::NK ? k_cnt - L::NK : 0; j < k_cnt; ++j)
-            mbar_wait_drain(bar(L::bKF + j % L::NK), (j / L::NK) & 1u, kDrain);
-        for (uint32_t j = LAST == 0 || cnt <= NV ? 0 : cnt - NV; LAST == 1 && j < cnt; ++j)
-            mbar_wait_drain(bar((F8 ? L::bSF : L::bVF) + j % NV), (j / NV) & 1u, kDrain);
+    if (lane == 0) {
+        if (FIRST == 0) copied[0] = cnt + ahead;
+        if (LAST == 1) copied[1] = cnt;
     }
+}
+
+// After an abort copies that nobody waited for must land before the CTA leaves.  One warp calls
+// this when all roles have ended: a role may give up after the producers are done.  copied: the
+// announced tiles of K and V.
+template <typename L, bool F8>
+__device__ __forceinline__ void drain_copies(uint8_t *smem, const volatile uint32_t *copied) {
+    const uint32_t base = smem_u32(smem), NV = F8 ? L::NS : L::NV, nk = copied[0], nv = copied[1];
+    auto bar = [&](int i) { return base + L::oBar + 8u * i; };
+    for (uint32_t j = nk > L::NK ? nk - L::NK : 0; j < nk; ++j)
+        mbar_wait_drain(bar(L::bKF + j % L::NK), (j / L::NK) & 1u, kDrain);
+    for (uint32_t j = nv > NV ? nv - NV : 0; j < nv; ++j)
+        mbar_wait_drain(bar((F8 ? L::bSF : L::bVF) + j % NV), (j / NV) & 1u, kDrain);
 }
 
 // bf16: V's cleaner, one warp, over the tiles that reach past the context.  Positions beyond the
@@ -683,7 +701,7 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 // group's).
 template <typename L, int DP>
 __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw, int group,
-                                               volatile int32_t *abort_flag, volatile uint32_t *v_issued, Follow f) {
+                                               volatile int32_t *abort_flag, Follow f) {
     const uint32_t base = smem_u32(smem);
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31), j = cw * 32 + lane;
@@ -755,7 +773,6 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             warp_arrive(bar(L::bCF + sb));
             if (!L::kLandScales && !(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
             if (!(ok = wait_for(bar(L::bVE + slot), ((cnt / L::NV) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
-            if (cw == 0 && lane == 0) v_issued[L::kGroups == 2 ? group : 0] = cnt + 1;   // the slot's previous use is over
             uint8_t *const src = smem + L::oS + ss * L::kStage;
             uint8_t *const dst = smem + L::oV + slot * L::kVSlot;
             // 4 (8) rows of 128 (64) codes a step: 16 codes per lane

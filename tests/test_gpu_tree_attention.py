@@ -307,3 +307,46 @@ def test_empty_call():
     z = torch.zeros(1, dtype=torch.int32, device=DEV)
     out = api.tree_attention(c, e, z, torch.empty(0, dtype=torch.int32, device=DEV), torch.empty((0, 1), dtype=torch.int32, device=DEV))
     assert out.shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_wide_page_tables(case, cache):
+    """A table with room for far longer contexts than these: the same lengths are then divided among
+    CTAs and joined, where a table of just their width leaves short ones whole."""
+    ctx, n, hq, hk, dim, page = CASES[case]
+    p = Pass(ctx, n, hq, hk, dim, page, cache, tree=True, seed=case)
+    table = torch.from_numpy(p.table)
+    wide = torch.full((table.shape[0], 40000 // page), 2 ** 30, dtype=torch.int32)   # unused places may hold anything
+    wide[:, : table.shape[1]] = table
+    _check(p, page_table=wide.to(DEV))
+    narrow = p.device(api)
+    ws = api.tree_attention_workspace(narrow["cache"], p.q.shape[0], len(ctx), hq)
+    api.tree_attention(**dict(narrow, page_table=wide.to(DEV)), ws=ws)
+    assert api.last_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("ctx,n", [([9000, 300, 4000], 4), ([9000, 300, 4000], 16), ([6000, 5000], 64), ([200, 100], 8)])
+def test_wait_that_runs_out_reports_timeout(ctx, n, cache):
+    """With a limit of half a microsecond the call gives up and says so, or, where the barriers'
+    hardware waits outlast the limit (they return when the data are there), has its ordinary results;
+    the next call on the same workspace has them in any case.  V's cleaner polls a count in shared
+    memory: over a long bf16 cache its wait for a part's last tile is always beyond the limit."""
+    p = Pass(ctx, [n] * len(ctx), 32, 8, 128, 64, cache, seed=21)
+    args = p.device(api)
+    ws = api.tree_attention_workspace(args["cache"], p.q.shape[0], len(ctx), 32)
+    base = api.tree_attention(**args, ws=ws)
+    assert api.last_device_error(ws) == 0
+    try:
+        api.set_wait_limit(1000)
+        out = api.tree_attention(**args, ws=ws)
+        code = api.last_device_error(ws)   # synchronises
+    finally:
+        api.set_wait_limit(0)
+    if cache == "bf16" and ctx[0] > 4000:
+        assert code == 6   # MOE_ERR_DEVICE_TIMEOUT
+    assert code == 6 or (code == 0 and torch.equal(out, base))
+    for _ in range(2):
+        assert torch.equal(api.tree_attention(**args, ws=ws), base)
+        assert api.last_device_error(ws) == 0
