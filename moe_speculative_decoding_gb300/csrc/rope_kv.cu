@@ -6,6 +6,12 @@
 // gradients).  A quantised row is codes of x / scale with scale = amax / 448.  All of it is
 // streaming work, a few operations per element: the bound is memory traffic, each row read once
 // and written once.
+//
+// Rows of 128 channels, against the copy bandwidth of 6.79 TB/s: 16381 tokens x 40 rows of bf16
+// rotated 56.9 us (5.98 TB/s), 16300 x 16 rows written as e4m3 codes 20.9 us (4.86), 8190 x 40
+// rows rotated and 8 of them written 30.3 us (5.68), 131000 x 16 rows of codes read back as bf16
+// 129 us (6.29); a pass of a few tokens 2.3 to 3.1 us, the latency of its chain of loads (position
+// or slot, then table row, then channels).
 #include "cache_args.cuh"
 #include "common.cuh"
 
@@ -100,12 +106,6 @@ __device__ __forceinline__ float2 unpack_e4m3x2(uint16_t codes) {
     return r;
 }
 
-// amax / 448, or 1 where that is 0 (a zero row, or one below the smallest scale)
-__device__ __forceinline__ float row_scale(float amax) {
-    const float s = amax / 448.0f;
-    return s > 0.0f ? s : 1.0f;
-}
-
 // x / s, correctly rounded, from r = 1 / s rounded to nearest: q = x r, and one step with the exact
 // remainder x - q s (Markstein's theorem, IBM J. Res. Dev. 34 (1990)): three operations where a
 // division takes a dozen.  s within 2^+-100, so that neither r nor the remainder leaves the range
@@ -114,13 +114,36 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     const float q = x * r;
     return fmaf(fmaf(-q, s, x), r, q);
 }
+// The same for two numbers at a time, in packed operations.
+__device__ __forceinline__ void quotient2(float &x0, float &x1, uint64_t s_neg, uint64_t r) {
+    uint64_t x, q, e;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(s_neg), "l"(x));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(q));
+}
+
+// amax / 448, or 1 where that is 0 (a zero row, or one below the smallest scale)
+__device__ __forceinline__ float row_scale(float amax) {
+    // (an infinite amax: the remainder would be NaN)
+    const float s = amax > 7.888609e-31f && amax < 3.4028235e38f ? quotient(amax, 448.0f, 1.0f / 448.0f) : amax / 448.0f;
+    return s > 0.0f ? s : 1.0f;
+}
 // The chunk's eight codes for scale s.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
     float q[8];
     if (s >= 7.888609e-31f && s <= 1.2676506e30f) {
         const float r = __frcp_rn(s);
+        uint64_t r2, s2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(r2) : "f"(r));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(-s));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = quotient(x[i], s, r);
+        for (int i = 0; i < 8; i += 2) {
+            q[i] = x[i];
+            q[i + 1] = x[i + 1];
+            quotient2(q[i], q[i + 1], s2, r2);
+        }
     } else {   // also infinite and NaN
 #pragma unroll
         for (int i = 0; i < 8; ++i) q[i] = x[i] / s;
@@ -199,6 +222,32 @@ __device__ __forceinline__ Row locate(const RowArgs &a, uint32_t g, uint32_t row
 // step through its heads by pointer.  A thread holds 16 channels of a row, in two chunks of 8: both
 // halves of 8 pairs of the half layout, or 16 consecutive channels; the token's 8 cosines and sines
 // stay in its registers, and the next row's loads are on their way while it works on one.
+
+// Sixteen bf16 channels in one store of 32 bytes where the address allows it: two of 16 bytes write
+// every sector in halves (8190 tokens x 40 rows rotated and written: 31.1 us against 30.4).
+__device__ __forceinline__ bool at32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+__device__ __forceinline__ void store32(void *p, const uint4 &a, const uint4 &b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+template <int TYPE>   // two chunks of eight channels, o1 apart
+__device__ __forceinline__ void store16(void *base, int64_t off, int o1, const float (&x)[8], const float (&y)[8]) {
+    if constexpr (TYPE == MOE_BF16) {
+        const uint4 a = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        const uint4 b = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        uint16_t *const p = static_cast<uint16_t *>(base) + off;
+        if (o1 == 8 && at32(p)) {
+            store32(p, a, b);
+        } else {
+            *reinterpret_cast<uint4 *>(p) = a;
+            *reinterpret_cast<uint4 *>(p + o1) = b;
+        }
+    } else {
+        store8(base, TYPE, off, x);
+        store8(base, TYPE, off + o1, y);
+    }
+}
 
 // 16 channels as they come from memory
 template <typename E>
@@ -318,8 +367,7 @@ __global__ void __launch_bounds__(kThreads, 4) rows_vec_kernel(const __grid_cons
             const bool q = CT >= 0 || r < a.q.heads;
             const moe_heads_t &h = q ? a.q_out : a.k_out;
             const int64_t off = t * h.token_stride + (q ? r : r - a.q.heads) * h.head_stride + q0;
-            store8(h.ptr, kInType, off, x);
-            store8(h.ptr, kInType, off + q1, y);
+            store16<kInType>(h.ptr, off, q1, x, y);
         }
     }
     if constexpr (CT >= 0) {
@@ -474,9 +522,10 @@ __device__ __forceinline__ Back locate_back(const ReadArgs &a, uint32_t r) {
 }
 
 // Tokens shared as by the rows above: the slot is found once, the heads are stepped through, the
-// next row's loads on their way.
+// next row's loads on their way.  Six CTAs an SM: 131000 tokens x 16 rows of e4m3 to bf16 take 128.5 us
+// (6.3 TB/s), with five (what its registers left) 135.3, with eight, which spill, 131.4.
 template <int CT, typename OUT, int T>
-__global__ void __launch_bounds__(kThreads) read_vec_kernel(const __grid_constant__ ReadArgs a, int share) {
+__global__ void __launch_bounds__(kThreads, 6) read_vec_kernel(const __grid_constant__ ReadArgs a, int share) {
     constexpr int kOutType = sizeof(OUT) == 2 ? MOE_BF16 : MOE_F32;
     pdl_wait();
     pdl_trigger();
@@ -538,8 +587,7 @@ __global__ void __launch_bounds__(kThreads) read_vec_kernel(const __grid_constan
         const bool k = r < kc.heads;
         const moe_heads_t &o = k ? a.k_out : a.v_out;
         const int64_t off = t * o.token_stride + (k ? r : r - kc.heads) * o.head_stride + ch;
-        store8(o.ptr, kOutType, off, x);
-        store8(o.ptr, kOutType, off + 8, y);
+        store16<kOutType>(o.ptr, off, 8, x, y);
     }
 }
 
@@ -595,11 +643,13 @@ cudaError_t launch_rope_table(const double *w, int half, double magnitude, int p
 namespace {
 
 // Groups of threads that share a token: one token to a CTA while that leaves SMs free, so that a
-// short call is short; else eight groups (or as many as the token has rows), whose lanes then all
-// have work and load the token's table row once for several heads.
+// short call is short; else so few that a group has eight rows to step through, since a CTA's first
+// row waits for its slot, its table row and its channels in turn.  (Eight groups whatever the rows:
+// 16300 tokens x 16 rows of 128, bf16 to e4m3, 23.1 us against 20.7; 131000 x 16 read back 150.9
+// against 136.2; 8190 x 40 rotated and written 33.0 against 30.8.)
 int share_of(int groups, int64_t tokens, int rows) {
     int share = groups;
-    while (share > 8 && tokens * share > 152ll * groups * 4) share /= 2;
+    while (share > 1 && rows < 8 * share && tokens * share > 152ll * groups * 4) share /= 2;
     while (share > 1 && share / 2 >= rows) share /= 2;
     return share;
 }
