@@ -708,6 +708,13 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
     float *const scale_s = reinterpret_cast<float *>(smem + L::oScale);
     volatile float *const sigma_s = reinterpret_cast<volatile float *>(smem + L::oSigma);
     const float kMax = 3.4028234e38f;
+    // A position's page without a division for each (they took 600 cycles a tile): with the floor of
+    // 2^32 / page the product's high word is the quotient or one less.
+    const uint32_t psize = static_cast<uint32_t>(a.cache.page), recip = static_cast<uint32_t>((1ull << 32) / psize);
+    auto page_of = [&](uint32_t pos) {
+        const uint32_t q = __umulhi(pos, recip);
+        return q + (pos - q * psize >= psize ? 1u : 0u);
+    };
     uint32_t cnt = 0;
     bool ok = true;
     while (ok && walk_follow(a, w, f, abort_flag)) {
@@ -722,12 +729,14 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
         auto page_at = [&](int tt) {
             const int64_t pos = static_cast<int64_t>(tt) * kTile + j;
-            return !L::kLandScales && tt < w.hi && pos < w.s.len ? __ldg(table + static_cast<int>(pos) / a.cache.page) : -1;
+            return !L::kLandScales && tt < w.hi && pos < w.s.len ? __ldg(table + page_of(static_cast<uint32_t>(pos))) : -1;
         };
         auto scales_at = [&](int tt, int page, float &ks, float &vs) {
             ks = vs = 0.0f;
             if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return;
-            const int64_t o = (static_cast<int64_t>(page) * a.cache.heads + w.hk) * a.cache.page + (tt * kTile + j) % a.cache.page;
+            const uint32_t pos = static_cast<uint32_t>(tt * kTile + j);
+            const int64_t o = (static_cast<int64_t>(page) * a.cache.heads + w.hk) * a.cache.page +
+                              (pos - page_of(pos) * static_cast<uint32_t>(a.cache.page));
             ks = __ldg(a.cache.k_scale + o);
             vs = __ldg(a.cache.v_scale + o);
         };
@@ -815,8 +824,7 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
                 *reinterpret_cast<uint4 *>(to + i * RS * 128 + (o0 ^ flip)) = lo;
                 *reinterpret_cast<uint4 *>(to + i * RS * 128 + (o1 ^ flip)) = hi;
             }
-            fence_proxy_async_smem();
-            __threadfence_block();
+            fence_proxy_async_smem();   // (the arrival releases the warp's stores: no other fence)
             warp_arrive(bar(L::bSE + ss));
             warp_arrive(bar(L::bVF + slot));
         }
