@@ -19,6 +19,12 @@
 // The two warpgroups take alternate tiles, each with its own maxima, sums and O^T, joined at the
 // item's end.  S^T of a warpgroup's next tile is formed while it weighs the present one.  Work list,
 // copies, value cleaning and conversion, parts and their join are those of tree_attn.cu.
+//
+// Measured, 8 cache heads of 128 channels, 60-65 thousand positions of 4 sequences: bf16 with 16 or 32
+// rows 156-161 us (6.5-6.7 TB/s of the 6.79 of a copy: the cache's bytes bound it), with 64 rows 169;
+// e4m3 with 16 rows 91-98 us (5.4-5.9 TB/s), with 32 rows 104-108, with 64 rows 154: there a tile's
+// chain of conversion, weights and products, 1,650 cycles, takes as long as its bytes or longer.
+// One token over 300 positions: 8.2 us, a chain of latencies (lengths, page table, K, scores, V).
 #include "tree_common.cuh"
 
 namespace moe {
@@ -220,100 +226,100 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
     const int G = a.group;
 
     if (warp >= 8) {
-    regs_down<L::kOther>();
-    pdl_wait();
-    pdl_trigger();
-    Walk w;
-    if (warp == kProducerWarp) {
-        walk_begin(a, w, blockIdx.x == 0);
-        produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
-    } else if (warp == kScoreWarp) {
-        // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
-        const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
-        uint32_t c = 0, sc[2] = {0, 0}, items = 0;
-        bool ok = true;
-        while (ok && walk_follow(a, w, follow, abort_flag)) {
-            ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
-            for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
-                const uint32_t slot = c % L::NK, g = t & 1, s_col = tmem + g * NT;
-                // the warpgroup has taken this buffer's previous scores
-                ok = (sc[g] == 0 || wait_for(bar(L::bSFree + g), (sc[g] - 1) & 1u, abort_flag, a.err, limit)) &&
-                     wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
-                if (!ok) break;
-                ++sc[g];
-                tc_fence_after();
-                const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
-                if (elect_one()) {
-                    if (F8) {
+        regs_down<L::kOther>();
+        pdl_wait();
+        pdl_trigger();
+        Walk w;
+        if (warp == kProducerWarp) {
+            walk_begin(a, w, blockIdx.x == 0);
+            produce<L, F8, DP, 0, 0>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
+        } else if (warp == kScoreWarp) {
+            // ---------------------------------------------------------------- S^T = K Q^T, tile by tile
+            const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
+            uint32_t c = 0, sc[2] = {0, 0}, items = 0;
+            bool ok = true;
+            while (ok && walk_follow(a, w, follow, abort_flag)) {
+                ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
+                for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
+                    const uint32_t slot = c % L::NK, g = t & 1, s_col = tmem + g * NT;
+                    // the warpgroup has taken this buffer's previous scores
+                    ok = (sc[g] == 0 || wait_for(bar(L::bSFree + g), (sc[g] - 1) & 1u, abort_flag, a.err, limit)) &&
+                         wait_for(bar(L::bKF + slot), (c / L::NK) & 1u, abort_flag, a.err, limit);
+                    if (!ok) break;
+                    ++sc[g];
+                    tc_fence_after();
+                    const uint64_t k_desc = desc_kmajor_sw128(base + L::oK + slot * L::kKSlot);
+                    if (elect_one()) {
+                        if (F8) {
 #pragma unroll
-                        for (int i = 0; i < DP / 32; ++i)
-                            tc_mma_f8(s_col, k_desc + 2 * i, q_desc + 2 * i, idesc_e4m3_f32(128, NT), i > 0);
+                            for (int i = 0; i < DP / 32; ++i)
+                                tc_mma_f8(s_col, k_desc + 2 * i, q_desc + 2 * i, idesc_e4m3_f32(128, NT), i > 0);
 #pragma unroll
-                        for (int i = 0; i < DP / 32; ++i)
-                            tc_mma_f8(s_col, k_desc + 2 * i, q_desc + NT * 8 + 2 * i, idesc_e4m3_e5m2(128, NT), 1);
-                    } else {
+                            for (int i = 0; i < DP / 32; ++i)
+                                tc_mma_f8(s_col, k_desc + 2 * i, q_desc + NT * 8 + 2 * i, idesc_e4m3_e5m2(128, NT), 1);
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < DP / 16; ++i)   // 64-channel halves
-                            tc_mma_bf16(s_col, k_desc + (i / 4) * 1024 + (i % 4) * 2, q_desc + (i / 4) * (NT * 8) + (i % 4) * 2,
-                                        idesc_bf16_f32(128, NT), i > 0);
+                            for (int i = 0; i < DP / 16; ++i)   // 64-channel halves
+                                tc_mma_bf16(s_col, k_desc + (i / 4) * 1024 + (i % 4) * 2, q_desc + (i / 4) * (NT * 8) + (i % 4) * 2,
+                                            idesc_bf16_f32(128, NT), i > 0);
+                        }
+                        tc_commit(bar(L::bKE + slot));
+                        tc_commit(bar(L::bS + g));
                     }
-                    tc_commit(bar(L::bKE + slot));
-                    tc_commit(bar(L::bS + g));
+                    __syncwarp();
                 }
-                __syncwarp();
+                ++items;
             }
-            ++items;
-        }
-        // every product is done before the CTA leaves
-        if (elect_one()) tc_commit(bar(L::bDrain));
-        __syncwarp();
-        mbar_wait_drain(bar(L::bDrain), 0, kDrain);
-        __syncwarp();
-    } else if (warp == kOutWarp) {
-        // ---------------------------------------------------------------- O^T += V^T P^T, tile by tile
-        // (A warp of its own: a tile's K may come later than the weights of the tile before.)
-        uint32_t c = 0, fixes = 0, pc[2] = {0, 0};
-        bool ok = true;
-        while (ok && walk_follow(a, w, follow, abort_flag)) {
-            const int T = w.hi - w.lo;
-            for (int t = 0; ok && t < T; ++t, ++c) {
-                const uint32_t slot = c % L::NV, g = t & 1, o_col = tmem + (2 + g) * NT;
-                ok = wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
-                if (!F8 && ok && (w.lo + t + 1) * kTile > w.s.ctx) {   // V's cleaner has been over it
-                    ok = wait_for(bar(L::bFix + (fixes & 3u)), (fixes >> 2) & 1u, abort_flag, a.err, limit);
-                    ++fixes;
-                }
-                // (the first weights of an item come after the previous item's O was read)
-                ok = ok && wait_for(bar(L::bP + g), pc[g] & 1u, abort_flag, a.err, limit);
-                if (!ok) break;
-                ++pc[g];
-                tc_fence_after();
-                const uint64_t v_desc = desc_mn_sw128(base + L::oV + slot * L::kVSlot, DP == 128 ? kTile * 128u : 0u);
-                const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
-                if (elect_one()) {
+            // every product is done before the CTA leaves
+            if (elect_one()) tc_commit(bar(L::bDrain));
+            __syncwarp();
+            mbar_wait_drain(bar(L::bDrain), 0, kDrain);
+            __syncwarp();
+        } else if (warp == kOutWarp) {
+            // ---------------------------------------------------------------- O^T += V^T P^T, tile by tile
+            // (A warp of its own: a tile's K may come later than the weights of the tile before.)
+            uint32_t c = 0, fixes = 0, pc[2] = {0, 0};
+            bool ok = true;
+            while (ok && walk_follow(a, w, follow, abort_flag)) {
+                const int T = w.hi - w.lo;
+                for (int t = 0; ok && t < T; ++t, ++c) {
+                    const uint32_t slot = c % L::NV, g = t & 1, o_col = tmem + (2 + g) * NT;
+                    ok = wait_for(bar(L::bVF + slot), (c / L::NV) & 1u, abort_flag, a.err, limit);
+                    if (!F8 && ok && (w.lo + t + 1) * kTile > w.s.ctx) {   // V's cleaner has been over it
+                        ok = wait_for(bar(L::bFix + (fixes & 3u)), (fixes >> 2) & 1u, abort_flag, a.err, limit);
+                        ++fixes;
+                    }
+                    // (the first weights of an item come after the previous item's O was read)
+                    ok = ok && wait_for(bar(L::bP + g), pc[g] & 1u, abort_flag, a.err, limit);
+                    if (!ok) break;
+                    ++pc[g];
+                    tc_fence_after();
+                    const uint64_t v_desc = desc_mn_sw128(base + L::oV + slot * L::kVSlot, DP == 128 ? kTile * 128u : 0u);
+                    const uint64_t p_desc = desc_p<NT>(base + L::oP + g * L::kP);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int i = 0; i < kTile / 16; ++i)   // 16 positions: 2 KB of V's blocks, 2 atoms of P
-                        mma_ss_f16(o_col, v_desc + 128 * i, p_desc + (16 * NT * 2 / 16) * i, idesc_vp(NT, F8 ? 0 : 1),
-                                   t >= 2 || i > 0);
-                    tc_commit(bar(L::bVE + slot));
-                    tc_commit(bar(L::bPV + g));
-                    if (t == T - 1) tc_commit(bar(L::bO));
+                        for (int i = 0; i < kTile / 16; ++i)   // 16 positions: 2 KB of V's blocks, 2 atoms of P
+                            mma_ss_f16(o_col, v_desc + 128 * i, p_desc + (16 * NT * 2 / 16) * i, idesc_vp(NT, F8 ? 0 : 1),
+                                       t >= 2 || i > 0);
+                        tc_commit(bar(L::bVE + slot));
+                        tc_commit(bar(L::bPV + g));
+                        if (t == T - 1) tc_commit(bar(L::bO));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
+            if (elect_one()) tc_commit(bar(L::bDrain));
+            __syncwarp();
+            mbar_wait_drain(bar(L::bDrain), 0, kDrain);
+            __syncwarp();
+        } else if (warp == kValueWarp) {
+            produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
+        } else if (warp >= kAuxWarp) {
+            if constexpr (F8)
+                convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, follow);
+            else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
+                clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
         }
-        if (elect_one()) tc_commit(bar(L::bDrain));
-        __syncwarp();
-        mbar_wait_drain(bar(L::bDrain), 0, kDrain);
-        __syncwarp();
-    } else if (warp == kValueWarp) {
-        produce<L, F8, DP, 1, 1>(a, w, &tm_k, &tm_v, smem, box_rows, abort_flag, copied, v_issued, follow);
-    } else if (warp >= kAuxWarp) {
-        if constexpr (F8)
-            convert_values<L, DP>(a, w, smem, (warp - kAuxWarp) & 3, (warp - kAuxWarp) >> 2, abort_flag, follow);
-        else if (warp == kAuxWarp)   // the other three of its warpgroup are idle
-            clean_values<L, DP>(a, w, smem, abort_flag, v_issued, follow);
-    }
     } else {
         // ---------------------------------------------------------------- softmax, two warpgroups
         regs_up<L::kSoft>();
