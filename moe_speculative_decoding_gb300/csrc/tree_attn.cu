@@ -788,6 +788,10 @@ cudaError_t launch_tree_attn(TreeArgs a, cudaStream_t s, bool pdl) {
     a.undivided = item_tiles <= (2 * items >= sms ? 12 : a.max_tokens * a.group > kNarrowRows ? 8 : 4);
     // no more CTAs than the page tables could fill with tiles
     const int ctas = static_cast<int>(std::min<long long>(sms, items * item_tiles));
+    // Up to 64 rows: positions as the M operand.  Few rows against many, 60-65 thousand positions of 4
+    // sequences, 8 heads of 128: e4m3 16 rows 97 us against 164, 64 rows 154 against 165; bf16 16 rows
+    // 159 against 164, 32 rows 161 against 165, 64 rows 169 against 166; 16 short contexts of e4m3 with
+    // 20 rows 37.8 against 56.
     if (a.max_tokens * a.group <= kNarrowRows) {
         e = launch_tree_narrow(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
         if (e != cudaSuccess || a.undivided) return e;
