@@ -214,6 +214,9 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
 // tile): before that, a CTA with parts of three items took 74,000 cycles where one with the same
 // number of tiles of one item took 43,000 (sixteen sequences of 800-4100 positions, 8 heads).
 // An item's extra units come first; a CTA whose range holds only such units has nothing to do.
+// Those sixteen with chains of 5 over e4m3 codes take 39.7, 37.9, 37.7, 37.6, 39.1 and 41.7 us with 3, 4,
+// 5, 6, 10 and 14; eight sequences of 4001-8201 with trees of 64 over bf16 67.2, 66.7, 65.4, 65.2, 66.0
+// and 68.1.
 constexpr int kItemCost = 6;
 struct Work {
     long long tiles, items;
