@@ -35,7 +35,7 @@
 // (2^-11; a bf16 cache needs bf16 weights, 2^-8), relative to a running power of two.
 //
 // Measured: 8 sequences of 4001-8201 positions, trees of 64 tokens, 8 query heads to each of 4 key
-// heads, 128 channels, bf16: 65 us, 740 TFLOP/s.  A tile of K and V serves 256 rows in 3,000 cycles,
+// heads, 128 channels, bf16: 64 us, 753 TFLOP/s.  A tile of K and V serves 256 rows in 3,000 cycles,
 // where its four products need 2,050 and its 32,768 exponentials as many; an item's beginning
 // (queries, 5,000-8,000 cycles) and end (4,000-5,000) come on top.  128 rows over 60-65 thousand
 // positions of e4m3 codes: 167 us.
@@ -381,6 +381,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             {
                 constexpr int C = DP / 8;
                 const int tiles = two ? 2 : 1;
+                const Divisor by_group(G);
                 const int c = static_cast<int>(threadIdx.x) % C;   // 256 / C rows a step, eight steps' loads at a time
 #pragma unroll 1
                 for (int r0 = static_cast<int>(threadIdx.x) / C; r0 < tiles * kTile; r0 += 8 * (256 / C)) {
@@ -389,10 +390,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     for (int i = 0; i < 8; ++i) {
                         const int row = row0 + r0 + i * (256 / C);
                         x[i] = make_uint4(0, 0, 0, 0);
+                        const int token = static_cast<int>(by_group.quotient(static_cast<uint32_t>(row)));
                         if (row < R && c * 8 < a.cache.dim)
                             x[i] = *reinterpret_cast<const uint4 *>(
-                                static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + row / G) * a.q.token_stride +
-                                static_cast<int64_t>(w.hk * G + row % G) * a.q.head_stride + c * 8);
+                                static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(w.s.t0 + token) * a.q.token_stride +
+                                static_cast<int64_t>(w.hk * G + row - token * G) * a.q.head_stride + c * 8);
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {

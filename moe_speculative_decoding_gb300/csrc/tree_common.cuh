@@ -412,6 +412,17 @@ __device__ __forceinline__ float2 *narrow_ml(const TreeArgs &a, int ctas, int sl
            static_cast<size_t>(slot) * kNarrowRows;
 }
 
+// Division of many numbers below 2^31 by one: with the floor of (2^32 - 1) / d the product's high
+// word is the quotient or one less.
+struct Divisor {
+    uint32_t d, recip;
+    __device__ __forceinline__ explicit Divisor(int by) : d(static_cast<uint32_t>(by)), recip(0xFFFFFFFFu / static_cast<uint32_t>(by)) {}
+    __device__ __forceinline__ uint32_t quotient(uint32_t x) const {
+        const uint32_t q = __umulhi(x, recip);
+        return q + (x - q * d >= d ? 1u : 0u);
+    }
+};
+
 // Which of the 128 positions of tile tt a row sees: bit j of word j / 32.  M: the row's tree mask.
 __device__ __forceinline__ void seen_bits(uint64_t M, const Seq &s, int tt, uint32_t (&w)[4]) {
     if (s.n < 64) M &= (1ull << s.n) - 1ull;
@@ -711,13 +722,9 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
     float *const scale_s = reinterpret_cast<float *>(smem + L::oScale);
     volatile float *const sigma_s = reinterpret_cast<volatile float *>(smem + L::oSigma);
     const float kMax = 3.4028234e38f;
-    // A position's page without a division for each (they took 600 cycles a tile): with the floor of
-    // 2^32 / page the product's high word is the quotient or one less.
-    const uint32_t psize = static_cast<uint32_t>(a.cache.page), recip = static_cast<uint32_t>((1ull << 32) / psize);
-    auto page_of = [&](uint32_t pos) {
-        const uint32_t q = __umulhi(pos, recip);
-        return q + (pos - q * psize >= psize ? 1u : 0u);
-    };
+    // (with a division for each position's page a tile took 300 cycles more)
+    const Divisor by_page(a.cache.page);
+    auto page_of = [&](uint32_t pos) { return by_page.quotient(pos); };
     uint32_t cnt = 0;
     bool ok = true;
     while (ok && walk_follow(a, w, f, abort_flag)) {
