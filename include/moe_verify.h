@@ -640,7 +640,9 @@ size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t t
  * a mask, j <= i (a chain).  Query head h reads cache head h / (q heads / cache heads).
  *     s_p = scale * <q, k_p>,  lse = ln sum_p e^(s_p),  out = sum_p e^(s_p - lse) v_p
  * over the positions seen; a token that sees none gets out = 0, lse = -inf.  What stands in a
- * position that a token does not see, infinities and NaN included, does not reach it.
+ * position that a token does not see, infinities and NaN included, does not reach it.  Over e4m3 codes
+ * on the tensor cores a weight e^(s_p) times the value's scale is held in 16 bits, to 2^-11 of it and to
+ * 2^-31 of the row's largest such product, with scales from 2^-90 to 2^100.
  *   q_start [dev] int32 [seqs + 1] (non-decreasing, 0 .. tokens), ctx [dev] int32 [seqs],
  *   page_table [dev] int32 [seqs, max_pages], mask [dev] uint64 [tokens] or NULL, scale > 0,
  *   q and out [tokens, q heads, dim] of one type; lse [dev] fp32 [tokens, q heads] or NULL.

@@ -32,7 +32,8 @@
 // of at most 8), down to 2^-14 of the row's largest; so two products give q k exactly, and the
 // key's scale is applied to the column of S in fp32.  V's codes become fp16 (exact) in shared
 // memory; the value's scale goes onto the weight in fp32 before the weight is rounded to fp16
-// (2^-11; a bf16 cache needs bf16 weights, 2^-8), relative to a running power of two.
+// (2^-11; a bf16 cache needs bf16 weights, 2^-8).  The running maximum is then that of the score plus
+// the scale's logarithm, so that it is a row's largest weight that lies near 1.
 //
 // Measured: 8 sequences of 4001-8201 positions, trees of 64 tokens, 8 query heads to each of 4 key
 // heads, 128 channels, bf16: 64 us, 753 TFLOP/s.  A tile of K and V serves 256 rows in 3,000 cycles,
@@ -83,20 +84,22 @@ struct Lay {
                          bDrain = bFix + 4, bW = bDrain + 1, kBars = bW + kRecords;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued, tiles copied, turns
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
-    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
-    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);    // F8: float [NC], the running power of two
-    static constexpr uint32_t oQs = oSigma + (F8 ? 32 : 0);         // F8: float [2][128], row factors
+    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs, log2 of vs][128]
+    static constexpr uint32_t oTop = oScale + (F8 ? NC * 1536 : 0);  // F8: float [NC], the tile's largest log2 of vs
+    static constexpr uint32_t oQs = oTop + (F8 ? NC * 4 : 0);       // F8: float [2][128], row factors
     static constexpr uint32_t oWalk = (oQs + (F8 ? 1024 : 0) + 7) & ~7u;   // records of walks
     static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
 // ------------------------------------------------------------------ softmax of a tile
-// The largest of a row's 128 scores (times their key scales), unseen ones left out.  The next 32
-// columns load while 32 are looked at.
-template <bool F8, bool EDGE>
-__device__ __forceinline__ float tile_max(uint32_t s_addr, const float *ks, const uint32_t (&see)[4]) {
+// The largest of a row's 128 scores (times their key scales), unseen ones left out.  LV: in log2 units
+// (cs to a score) plus the logarithms of the value scales.  The next 32 columns load while 32 are
+// looked at.
+template <bool F8, bool EDGE, bool LV>
+__device__ __forceinline__ float tile_max(uint32_t s_addr, const float *ks, const float *lv, float cs, const uint32_t (&see)[4]) {
     uint32_t x[2][32];
+    const F2 cs2 = f2(cs, cs);
     float m0 = ninf(), m1 = ninf();
     tmem_ld32(s_addr, x[0]);
 #pragma unroll
@@ -111,8 +114,14 @@ __device__ __forceinline__ float tile_max(uint32_t s_addr, const float *ks, cons
             for (int k = 0; k < 4; ++k) a[k] = __uint_as_float(y[i + k]);
             if (F8) {
                 const float4 q = *reinterpret_cast<const float4 *>(ks + 32 * c + i);
-                f2_get(f2_mul(f2(a[0], a[1]), f2(q.x, q.y)), a[0], a[1]);
-                f2_get(f2_mul(f2(a[2], a[3]), f2(q.z, q.w)), a[2], a[3]);
+                F2 s0 = f2_mul(f2(a[0], a[1]), f2(q.x, q.y)), s1 = f2_mul(f2(a[2], a[3]), f2(q.z, q.w));
+                if (LV) {
+                    const float4 z = *reinterpret_cast<const float4 *>(lv + 32 * c + i);
+                    s0 = f2_fma(s0, cs2, f2(z.x, z.y));
+                    s1 = f2_fma(s1, cs2, f2(z.z, z.w));
+                }
+                f2_get(s0, a[0], a[1]);
+                f2_get(s1, a[2], a[3]);
             }
             if (EDGE) {
 #pragma unroll
@@ -365,8 +374,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const uint32_t s_addr = tmem + lanes + g * kTile, o_addr = tmem + lanes + 256 + g * DP;
         float *const qs = reinterpret_cast<float *>(smem + L::oQs);
         const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
-        const volatile float *const sigma_s = reinterpret_cast<const volatile float *>(smem + L::oSigma);
-        float4 *const exch = reinterpret_cast<float4 *>(smem);   // [2][128], over Q when Q is done with
+        const volatile float *const top_s = reinterpret_cast<const volatile float *>(smem + L::oTop);
+        float2 *const exch = reinterpret_cast<float2 *>(smem);   // [2][128], over Q when Q is done with
         uint32_t sc = 0, scnt = 0;
         bool ok = true;
         pdl_wait();
@@ -415,42 +424,45 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             warp_arrive(bar(L::bQ));
             if (F8) named_barrier(3, 256);   // the row factors, before other threads' are read
             const float cs = F8 ? a.scale_log2 * qs[mt * 128 + r] : a.scale_log2;
-            float m = ninf(), l = 0.0f, sigma = 1.0f;
+            float m = ninf(), l = 0.0f;
             for (int u = g; u < U; u += 2) {
                 const int tt = w.lo + (two ? u >> 1 : u);
                 const bool edge = (tt + 1) * kTile > w.s.ctx;
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
                 if (edge) seen_bits(M, w.s, tt, see);
                 const uint32_t tile_no = scnt + (two ? u >> 1 : u), sb = tile_no % L::NC;
-                const float *const ks = scale_s + sb * 256, *const vs = ks + 128;
+                const float *const ks = scale_s + sb * 384, *const vs = ks + 128, *const lv = ks + 256;
                 if (F8 && !(ok = wait_for(bar(L::bCF + sb), (tile_no / L::NC) & 1u, abort_flag, a.err, limit))) break;
                 if (!(ok = wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit))) break;
                 ++sc;
                 tc_fence_after();
-                float mx = edge ? tile_max<F8, true>(s_addr, ks, see) : tile_max<F8, false>(s_addr, ks, see);
-                mx *= cs;   // cs > 0; -inf stays
-                float keep = 1.0f;
-                bool move = u < 2 || mx - m > kLazy;
-                const float sigma_new = F8 ? sigma_s[sb] : 1.0f;   // the tile's value scales are relative to it
-                if (F8 && sigma_new != sigma) move = true;
-                if (__any_sync(0xFFFFFFFFu, move)) {
+                float mx = 0.0f, keep = 1.0f;
+                bool look = F8 && (edge || u < 2);
+                if (!look) {
+                    mx = !F8 && edge ? tile_max<F8, true, false>(s_addr, ks, lv, cs, see) : tile_max<F8, false, false>(s_addr, ks, lv, cs, see);
+                    mx *= cs;   // cs > 0; -inf stays
+                    // e4m3: with the tile's largest value scale this is at or above what counts, a score plus its
+                    // own value's; only where that does not do is that one looked for (in every tile: 128 rows
+                    // over 60-65 thousand positions 180 us against 169)
+                    look = F8 && __any_sync(0xFFFFFFFFu, mx + top_s[sb] - m > kLazy);
+                }
+                if (F8 && look) mx = tile_max<F8, true, true>(s_addr, ks, lv, cs, see);
+                if ((!F8 || look) && __any_sync(0xFFFFFFFFu, u < 2 || mx - m > kLazy)) {
                     const float mn = fmaxf(m, mx);
                     if (u >= 2) {
                         keep = mn == ninf() ? 1.0f : ex2(m - mn);
                         l *= keep;
-                        const float f = F8 ? keep * (sigma / sigma_new) : keep;
 #pragma unroll
                         for (int c = 0; c < DP / 32; ++c) {
                             uint32_t x[32];
                             tmem_ld32(o_addr + 32 * c, x);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * keep);
                             tmem_st32(o_addr + 32 * c, x);
                         }
                     }
                     m = mn;
-                    sigma = sigma_new;
                 }
                 const float ref = m == ninf() ? 0.0f : m;   // nothing seen yet: every weight is 0
                 l += edge ? tile_weights<F8, true>(s_addr, ks, vs, cs, ref, see)
@@ -464,19 +476,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             ok = ok && wait_for(bar(L::bO), static_cast<uint32_t>(w.index) & 1u, abort_flag, a.err, limit);
             tc_fence_after();
             scnt += T;
-            const float gain = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
+            constexpr float gain = F8 ? 1.0f / kWeightUp : 1.0f;   // of the accumulator
             float wt[2] = {0.0f, 0.0f}, mm = m, ll = l;
             int c0 = 0, c1 = DP;
             if (!two) {   // both warpgroups hold a part of the same rows: half of the channels each
-                exch[g * 128 + r] = make_float4(m, l, gain, 0.0f);
+                exch[g * 128 + r] = make_float2(m, l);
                 named_barrier(3, 256);
-                const float4 e0 = exch[r], e1 = exch[128 + r];
+                const float2 e0 = exch[r], e1 = exch[128 + r];
                 mm = fmaxf(e0.x, e1.x);
                 const float ref = mm == ninf() ? 0.0f : mm;
                 const float k0 = ex2(e0.x - ref), k1 = ex2(e1.x - ref);
                 ll = e0.y * k0 + e1.y * k1;
-                wt[0] = k0 * e0.z;
-                wt[1] = k1 * e1.z;
+                wt[0] = k0 * gain;
+                wt[1] = k1 * gain;
                 c0 = g * (DP / 2);
                 c1 = c0 + DP / 2;
             } else {

@@ -60,17 +60,16 @@ struct Lay {
                          bO = bQ + 1, bFix = bO + 1, bW = bFix + 4, bDrain = bW + kRecords, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued, tiles copied
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
-    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs][128]
-    static constexpr uint32_t oSigma = oScale + (F8 ? NC * 1024 : 0);   // F8: float [NC][4], the warps' largest value scales
-    static constexpr uint32_t oCs = oSigma + (F8 ? NC * 16 : 0);        // F8: float [NT]: score to log2 units
+    static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs, log2 of vs][128]
+    static constexpr uint32_t oTop = oScale;                       // (not kept)
+    static constexpr uint32_t oCs = oScale + (F8 ? NC * 1536 : 0);      // F8: float [NT]: score to log2 units
     static constexpr uint32_t oM = oCs + (F8 ? NT * 4 : 0);    // float [2][NT]: minus a warpgroup's maxima, 0 where there is none
     static constexpr uint32_t oAlpha = oM + 2 * NT * 4;            // float [2][NT]: a rescaling
     static constexpr uint32_t oDelta = oAlpha + 2 * NT * 4;        // float [2][NT]: its logarithm
     static constexpr uint32_t oRed = oDelta + 2 * NT * 4;          // float [2][4][NT]: per warp
     static constexpr uint32_t oMask = oRed + 8 * NT * 4;           // uint64 [NT]: the rows' tree masks
     static constexpr uint32_t oTo = oMask + NT * 8;                // int64 [NT]: the rows' output offsets
-    static constexpr uint32_t oUnit = oTo + NT * 8;          // float [2]: a warpgroup's accumulator unit
-    static constexpr uint32_t oWalk = (oUnit + 16 + 7) & ~7u;   // records of walks
+    static constexpr uint32_t oWalk = oTo + NT * 8;                // records of walks
     static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
     static constexpr uint32_t kTmem = 4 * NT < 32 ? 32 : 4 * NT;
     static_assert(kSmem <= 232448, "shared memory");
@@ -135,17 +134,18 @@ __device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
 
 // Sums (or maxima of) v[c] over the warp's lanes: afterwards lane l holds in v[0 .. NT/32) those of
 // columns l * NT/32 + i (NT = 16: of column l / 2 in v[0]).  A halving exchange: about NT shuffles in
-// all, where a reduction instruction per column took 100 cycles each.  The order is fixed.
-template <int NT, bool MAX>
-__device__ __forceinline__ void warp_columns(float (&v)[NT], int lane) {
+// all, where a reduction instruction per column took 100 cycles each.  The order is fixed.  N columns
+// over lanes FIRST apart and nearer.
+template <int N, bool MAX, int FIRST = 16>
+__device__ __forceinline__ void warp_columns(float (&v)[N], int lane) {
     auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
 #pragma unroll
-    for (int o = 16, n = NT; o > 0; o >>= 1) {
+    for (int o = FIRST, n = N; o > 0; o >>= 1) {
         if (n > 1) {
             n >>= 1;
             const bool up = (lane & o) != 0;
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i) {
+            for (int i = 0; i < N / 2; ++i) {
                 if (i < n) {
                     const float send = up ? v[i] : v[i + n], kept = up ? v[i + n] : v[i];
                     v[i] = join(kept, __shfl_xor_sync(0xFFFFFFFFu, send, o));
@@ -156,8 +156,22 @@ __device__ __forceinline__ void warp_columns(float (&v)[NT], int lane) {
         }
     }
 }
-template <int NT>
-__device__ __forceinline__ void store_columns(float *to, const float (&v)[NT], int lane) {
+// The same maxima of x[c] + the lane's own shift; the first exchange goes by x itself, whose registers
+// the scores stay in.
+template <int NT, bool SHIFT>
+__device__ __forceinline__ void warp_maxima(const uint32_t (&x)[NT], float shift, float (&v)[NT / 2], int lane) {
+    const bool up = (lane & 16) != 0;
+    const float other = SHIFT ? __shfl_xor_sync(0xFFFFFFFFu, shift, 16) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) {
+        const float kept = __uint_as_float(up ? x[i + NT / 2] : x[i]);
+        const float got = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, up ? x[i] : x[i + NT / 2], 16));
+        v[i] = SHIFT ? fmaxf(kept + shift, got + other) : fmaxf(kept, got);
+    }
+    warp_columns<NT / 2, true, 8>(v, lane);
+}
+template <int NT, int N>
+__device__ __forceinline__ void store_columns(float *to, const float (&v)[N], int lane) {
     if constexpr (NT == 16) {
         if ((lane & 1) == 0) to[lane / 2] = v[0];
     } else {
@@ -332,8 +346,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
         float *const delta_s = reinterpret_cast<float *>(smem + L::oDelta) + g * NT;
         float *const red_s = reinterpret_cast<float *>(smem + L::oRed) + g * 4 * NT;
         const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
-        const volatile float *const sigma_s = reinterpret_cast<const volatile float *>(smem + L::oSigma);
-        float *const unit_s = reinterpret_cast<float *>(smem + L::oUnit);
         uint8_t *const p_buf = smem + L::oP + g * L::kP;
         uint32_t sc = 0, tiles = 0;   // this warpgroup's tiles; all tiles
         bool dead = false;            // a wait gave up: only the barriers are kept
@@ -391,22 +403,20 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             F2 l2[NT / 2];
 #pragma unroll
             for (int c = 0; c < NT / 2; ++c) l2[c] = f2(0.0f, 0.0f);
-            float sigma = kSigmaLow;
             for (int t = g; t < T; t += 2) {
                 const int tt = w.lo + t, pos = tt * kTile + p;
                 const bool edge = (tt + 1) * kTile > w.s.ctx;
                 const uint32_t no = tiles + t, sb = no % L::NC;
-                float ks = 1.0f, vs = 1.0f, sigma_new = sigma;
+                float ks = 1.0f, vs = 1.0f, lv = 0.0f;   // lv: of the value's scale, in the rows' references
                 uint32_t x[NT];
                 if (F8 && !dead) dead = !wait_for(bar(L::bCF + sb), (no / L::NC) & 1u, abort_flag, a.err, limit);
                 if (!dead) dead = !wait_for(bar(L::bS + g), sc & 1u, abort_flag, a.err, limit);
                 tc_fence_after();
                 tmem_ld_cols<NT>(s_addr, x);
                 if (F8) {
-                    ks = scale_s[sb * 256 + p];
-                    vs = scale_s[sb * 256 + 128 + p];
-                    sigma_new = sigma_above(sigma, fmaxf(fmaxf(sigma_s[sb * 4], sigma_s[sb * 4 + 1]), fmaxf(sigma_s[sb * 4 + 2], sigma_s[sb * 4 + 3])));
-                    vs *= kWeightUp / sigma_new;
+                    ks = scale_s[sb * 384 + p];
+                    vs = scale_s[sb * 384 + 128 + p];
+                    lv = scale_s[sb * 384 + 256 + p];
                 } else {
                     ks = a.scale_log2;
                 }
@@ -416,7 +426,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                     warp_arrive(bar(L::bSFree + g));
                     if (F8) warp_arrive(bar(L::bCE + sb));
                 }
-                // scores in log2 units above the rows' maxima so far (above 0 where a row has none);
+                // scores in log2 units above the rows' references so far (above 0 where a row has none);
                 // what a row does not see is -inf
                 const F2 ks2 = f2(ks, ks);
 #pragma unroll
@@ -445,19 +455,17 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             if (d >= 64 || !(mask_s[c] >> d & 1ull)) x[c] = __float_as_uint(ninf());
                     }
                 }
-                // any score far above its row's maximum so far, or a row that had seen nothing?
-                bool move = !all_seen || (F8 && sigma_new != sigma);
+                // any weight far above its row's largest so far, or a row that had seen nothing?
+                bool move = !all_seen;
                 float over = ninf();
 #pragma unroll
                 for (int c = 0; c < NT; c += 2) over = fmaxf(over, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
-                move = move || over > kLazy;
+                move = move || over + lv > kLazy;
                 if (bar_any(2 + g, 128, move)) {
                     // the columns' maxima over the 128 positions (NaN left out): over the warp's lanes,
                     // then over the four warps
-                    float top[NT];
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) top[c] = __uint_as_float(x[c]);
-                    warp_columns<NT, true>(top, lane);
+                    float top[NT / 2];
+                    warp_maxima<NT, F8>(x, lv, top, lane);
                     store_columns<NT>(red_s + q4 * NT, top, lane);
                     named_barrier(2 + g, 128);
                     bool unseen = false;
@@ -486,7 +494,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         // O so far is complete when the previous product is
                         if (!dead) dead = !wait_for(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
                         tc_fence_after();
-                        const float f = F8 ? sigma / sigma_new : 1.0f;
 #pragma unroll
                         for (int c0 = 0; c0 < NT; c0 += 16) {
                             uint32_t o[16];
@@ -496,14 +503,13 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                             for (int c = 0; c < 16; c += 2) {
                                 const float2 k = *reinterpret_cast<const float2 *>(alpha_s + c0 + c);
                                 l2[(c0 + c) / 2] = f2_mul(l2[(c0 + c) / 2], f2(k.x, k.y));
-                                o[c] = __float_as_uint(__uint_as_float(o[c]) * (k.x * f));
-                                o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * (k.y * f));
+                                o[c] = __float_as_uint(__uint_as_float(o[c]) * k.x);
+                                o[c + 1] = __float_as_uint(__uint_as_float(o[c + 1]) * k.y);
                             }
                             tmem_st16(o_addr + c0, o);
                         }
                         tmem_wait_st();
                     }
-                    sigma = sigma_new;
                 }
                 // the weights' buffer is free when the previous product has read it
                 if (t >= 2 && !dead) dead = !wait_for(bar(L::bPV + g), (sc - 1) & 1u, abort_flag, a.err, limit);
@@ -547,7 +553,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
             warp_columns<NT, false>(l, lane);
             store_columns<NT>(red_s + q4 * NT, l, lane);
             if (p < NT) nm_s[p] = -m_own;
-            if (lane == 0 && q4 == 0) unit_s[g] = F8 ? sigma / kWeightUp : 1.0f;   // of the accumulator
             named_barrier(4, 256);
             const bool second = T > 1;   // the second warpgroup had a tile
             const float *const m0_s = reinterpret_cast<const float *>(smem + L::oM), *const m1_s = m0_s + NT;
@@ -563,9 +568,9 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 float ll = (red0[c] + red0[NT + c] + red0[2 * NT + c] + red0[3 * NT + c]) * ka;
                 if (second) ll += (red1[c] + red1[NT + c] + red1[2 * NT + c] + red1[3 * NT + c]) * kb;
                 const bool none = mm == ninf() && ll == 0.0f;
-                const float inv = !w.whole ? 1.0f : (none ? 0.0f : 1.0f / ll);
-                w0_s[c] = ka * unit_s[0] * inv;
-                w1_s[c] = second ? kb * unit_s[1] * inv : 0.0f;
+                const float inv = (!w.whole ? 1.0f : (none ? 0.0f : 1.0f / ll)) * (F8 ? 1.0f / kWeightUp : 1.0f);
+                w0_s[c] = ka * inv;
+                w1_s[c] = second ? kb * inv : 0.0f;
                 to_s[c] = static_cast<int64_t>(w.s.t0 + c / G) * a.out.token_stride + static_cast<int64_t>(w.hk * G + c % G) * a.out.head_stride;
                 if (c < R) {
                     if (!w.whole)

@@ -17,6 +17,12 @@ constexpr long long kDrain = 400000000ll;       // about 0.2 s
 constexpr int kMaxCtas = 256;
 constexpr float kLazy = 8.0f;                   // log2 growth of a maximum that O is rescaled for
 constexpr float kWeightUp = 128.0f;             // fp16 weights: at most 2^8 * 2^7, flushed below 2^-31
+// e4m3: a row's weight at a position is its exponential times the value's scale, and it is that product's
+// largest among what the row sees that its weights are held against (score plus the scale's logarithm,
+// in one reference per row).  So neither a scale that a row does not see nor one that it gives no
+// weight moves its other weights.  Logarithms are cut to this range: an exponential alone is then
+// at most 2^(8 + 90) and the largest product's at least 2^-100, and fp32 sums hold them.
+constexpr float kScaleLow = -90.0f, kScaleHigh = 100.0f;   // NaN: the lowest
 
 // ------------------------------------------------------------------ tcgen05, TMA and arithmetic pieces
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
@@ -92,6 +98,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 // Registers of a warpgroup's threads from here on (all its warps call).
@@ -510,7 +521,7 @@ __device__ __forceinline__ void store_query(uint8_t *q, int rows, int row, int c
 
 // ------------------------------------------------------------------ roles
 // L gives the places in shared memory: oK, oV, oS (V codes landing), oSSc (their scales), oBad,
-// oScale, oSigma, ring sizes NK, NV, NS, barriers bKF ... at oBar.
+// oScale, oTop, ring sizes NK, NV, NS, barriers bKF ... at oBar.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
@@ -685,15 +696,12 @@ __device__ __forceinline__ void clean_values(const TreeArgs &a, Walk &w, uint8_t
     }
 }
 
+__device__ __forceinline__ float log2_scale(float s) { return fminf(fmaxf(lg2(fabsf(s)), kScaleLow), kScaleHigh); }
+
 // All ones in the bytes of four codes that are not NaN (0x7f, 0xff).
 __device__ __forceinline__ uint32_t finite_codes(uint32_t x) {
     const uint32_t nan = ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // bit 7 of such a byte
     return ~((nan >> 7) * 0xFFu);
-}
-
-constexpr float kSigmaLow = 7.888609e-31f;   // 2^-100: below any value scale that counts
-__device__ __forceinline__ float sigma_above(float sigma, float top) {   // the power of two at or above top
-    return top > sigma ? __int_as_float(min((__float_as_int(top) + 0x7fffff) & 0x7f800000, 0x7e800000)) : sigma;
 }
 
 // Four codes to fp16, exact.  (Assembling the fp16 bits with integer operations, five or more for four
@@ -705,14 +713,13 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 }
 
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
-// layout, the scales into a ring for the softmax.  With kLandScales (a softmax thread owns a row) the
-// value scales there are relative to sigma, a power of two at or above all of the item's finite ones
-// so far, times kWeightUp; without (it owns a position) they are as the cache has them, with each
-// warp's largest, and sigma is the softmax's.  What clean_values does for bf16 is done on the way.
-// With two groups of four warps each takes every other tile (of one softmax warpgroup, whose sigma
-// it is; rings are even, so that a slot is one group's).  A tile takes a group 2,000 cycles of its
-// own, 1,150 of them the codes' loop, and every second one is its: about what a tile of the cache
-// takes to arrive.
+// layout, the scales into a ring for the softmax: of a position the key's, the value's times
+// kWeightUp, and the logarithm of the value's.  The scales come from beside the codes (kLandScales:
+// a softmax thread owns a row, and has the tile's largest logarithm too) or are loaded here.  What
+// clean_values does for bf16 is done on the way.
+// With two groups of four warps each takes every other tile (of one softmax warpgroup; rings are
+// even, so that a slot is one group's).  A tile takes a group 2,000 cycles of its own, 1,150 of them
+// the codes' loop, and every second one is its: about what a tile of the cache takes to arrive.
 template <typename L, int DP>
 __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8_t *smem, int cw, int group,
                                                volatile int32_t *abort_flag, Follow f) {
@@ -720,7 +727,7 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
     auto bar = [&](int i) { return base + L::oBar + 8u * i; };
     const int lane = static_cast<int>(threadIdx.x & 31), j = cw * 32 + lane;
     float *const scale_s = reinterpret_cast<float *>(smem + L::oScale);
-    volatile float *const sigma_s = reinterpret_cast<volatile float *>(smem + L::oSigma);
+    volatile float *const top_s = reinterpret_cast<volatile float *>(smem + L::oTop);
     const float kMax = 3.4028234e38f;
     // (with a division for each position's page a tile took 300 cycles more)
     const Divisor by_page(a.cache.page);
@@ -733,7 +740,6 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
         const int odd = L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(w.lo) ^ static_cast<uint32_t>(group)) & 1u) : 0;
         if (lane < 2 && (L::kGroups == 1 || lane == odd)) bad[lane * 4 + cw] = 0;
         __syncwarp();
-        float sigma = kSigmaLow;
         // without landing scales: this thread's position of the group's tiles, the scales loaded a
         // tile ahead and the page two
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
@@ -758,36 +764,36 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             if (L::kGroups == 2 && (cnt & 1u) != static_cast<uint32_t>(group)) continue;
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
             const uint32_t ss = cnt % L::NS, slot = cnt % L::NV;
-            float top = 0.0f, ks = 0.0f, vs = 0.0f;
+            float ks = 0.0f, vs = 0.0f, top = 0.0f;
             if (L::kLandScales) {
                 if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
                 const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {   // every warp forms the tile's largest: no barrier
                     const float v = k * 32 + lane < stop ? land[128 + k * 32 + lane] : 0.0f;
-                    if (fabsf(v) <= kMax) top = fmaxf(top, fabsf(v));
+                    top = fmaxf(top, fabsf(v));
                     if (k == cw) vs = v;
                 }
                 if (j < stop) ks = land[j];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             } else {
                 ks = ks_next;
                 vs = vs_next;
-                if (fabsf(vs) <= kMax) top = fabsf(vs);
                 scales_at(tt + L::kGroups, page_next, ks_next, vs_next);   // in flight during this tile
                 page_next = page_at(tt + 2 * L::kGroups);
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            if (L::kLandScales) sigma = sigma_above(sigma, top);
             const bool odd_scale = j >= first && j < stop && !(fabsf(vs) <= kMax);
+            if (odd_scale) vs = 0.0f;
             // The scales have a ring of their own, so that a tile can be weighed before its values are
             // converted (with the V slot's, a tile waited for the product two before it: 4000 cycles
             // for two tiles instead of 2700).
             const uint32_t sb = cnt % L::NC;
             if (!(ok = wait_for(bar(L::bCE + sb), ((cnt / L::NC) & 1u) ^ 1u, abort_flag, a.err, a.wait_limit))) break;
-            scale_s[sb * 256 + j] = ks;
-            scale_s[sb * 256 + 128 + j] = odd_scale ? 0.0f : (L::kLandScales ? vs * (kWeightUp / sigma) : vs);
-            if (lane == 0) sigma_s[L::kLandScales ? sb : sb * 4 + cw] = L::kLandScales ? sigma : top;
+            scale_s[sb * 384 + j] = ks;
+            scale_s[sb * 384 + 128 + j] = vs * kWeightUp;
+            scale_s[sb * 384 + 256 + j] = log2_scale(vs);
+            if (L::kLandScales && lane == 0) top_s[sb] = log2_scale(top);   // at or above all of the tile's
             if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
             warp_arrive(bar(L::bCF + sb));
             if (!L::kLandScales && !(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
