@@ -114,12 +114,14 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
     const float q = x * r;
     return fmaf(fmaf(-q, s, x), r, q);
 }
-// The same for two numbers at a time, in packed operations.
+// The same for two numbers at a time, in packed operations.  The remainder, which is exact, is formed
+// rounding down so that a remainder of zero is -0 (rounding to nearest makes it +0): added to a
+// quotient of zero it leaves its sign, and the codes of -0 and of +0 differ.
 __device__ __forceinline__ void quotient2(float &x0, float &x1, uint64_t s_neg, uint64_t r) {
     uint64_t x, q, e;
     asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(x0), "f"(x1));
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(r));
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(s_neg), "l"(x));
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(e) : "l"(q), "l"(s_neg), "l"(x));
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(e), "l"(r), "l"(q));
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x0), "=f"(x1) : "l"(q));
 }
