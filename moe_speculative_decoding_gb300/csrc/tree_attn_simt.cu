@@ -178,13 +178,17 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
     }
 }
 
+constexpr size_t smem_bytes(int D) {
+    return (kRows * D + ((kTile * (D + 1) + 1) & ~1)) * sizeof(float) + kTile * sizeof(int64_t) + 2 * kTile * sizeof(float);
+}
+
 template <int DC>
 cudaError_t launch(const TreeArgs &a, dim3 grid, cudaStream_t s, bool pdl) {
-    const int D = a.cache.dim;
-    const size_t smem = (kRows * D + ((kTile * (D + 1) + 1) & ~1)) * sizeof(float) + kTile * sizeof(int64_t) +
-                        2 * kTile * sizeof(float);
+    const size_t smem = smem_bytes(a.cache.dim);
+    // always what the widest head needs: the limit is the function's, and a smaller one, set for this
+    // call, could come between another thread's setting and its launch
     cudaError_t e = cudaFuncSetAttribute(tree_simt_kernel<DC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         static_cast<int>(smem_bytes(32 * DC)));
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
