@@ -172,6 +172,23 @@ def _check(code: int, what: str):
         raise MoeError(code, what)
 
 
+# Kernels, and the number of SMs they are sized by, go by the current device and not by the tensors':
+# every call is made with its tensors' device current.  (torch.cuda.current_device and its checks take
+# 2 us of a call that takes 10.)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(name: str, device, *args):
+    """A call of the library with a tensor's device current."""
+    if device.index == _current_device():
+        code = getattr(_lib or lib(), name)(*args)
+    else:
+        with torch.cuda.device(device.index):
+            code = getattr(_lib or lib(), name)(*args)
+    if code:
+        raise MoeError(code, name)
+
+
 def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
@@ -203,16 +220,15 @@ def workspace(layer: Layer, n_max: int = PERSLOT_LAUNCH_TOKENS, device=None) -> 
     deduplicating call of n > 16 tokens needs n_max >= n."""
     nbytes = int(lib().moe_workspace_bytes(ctypes.byref(layer), n_max))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
-    _check(lib().moe_workspace_init(ctypes.c_void_p(ws.data_ptr()), nbytes, _stream(ws.device)),
-           "moe_workspace_init")
+    _call("moe_workspace_init", ws.device, ctypes.c_void_p(ws.data_ptr()), nbytes, _stream(ws.device))
     return ws
 
 
 def last_device_error(ws: torch.Tensor) -> int:
     """moe_last_device_error: synchronise, return and clear the workspace's device error code (infrastructure)."""
     code = ctypes.c_int32(0)
-    _check(lib().moe_last_device_error(ctypes.c_void_p(ws.data_ptr()), _stream(ws.device),
-                                       ctypes.byref(code)), "moe_last_device_error")
+    _call("moe_last_device_error", ws.device, ctypes.c_void_p(ws.data_ptr()), _stream(ws.device),
+          ctypes.byref(code))
     return int(code.value)
 
 
@@ -231,10 +247,9 @@ def route_topm(logits: torch.Tensor, m: int, renorm: bool = True, ids=None, gate
         ids = torch.empty((n, m), dtype=torch.int32, device=logits.device)
     if gates is None:
         gates = torch.empty((n, m), dtype=torch.float32, device=logits.device)
-    _check(lib().moe_route_topm(_dev(logits, "logits", torch.float32), n, N, m, int(bool(renorm)),
-                                _dev(ids, "ids", torch.int32, (n, m)),
-                                _dev(gates, "gates", torch.float32, (n, m)), _stream(logits.device)),
-           "moe_route_topm")
+    _call("moe_route_topm", logits.device, _dev(logits, "logits", torch.float32), n, N, m, int(bool(renorm)),
+          _dev(ids, "ids", torch.int32, (n, m)),
+          _dev(gates, "gates", torch.float32, (n, m)), _stream(logits.device))
     return ids, gates
 
 
@@ -256,11 +271,11 @@ def group_slots(ids: torch.Tensor, N: int, out: Grouping | None = None, ws=None)
     """moe_group_slots: the pass's slots grouped by expert, a counting sort ([Lan] §1, App. E): U, expert list, offsets, slot order."""
     n, m = ids.shape
     g = out or Grouping.empty(n, m, N, ids.device)
-    _check(lib().moe_group_slots(_dev(ids, "ids", torch.int32), n, m, N,
-                                 _dev(g.num_distinct, "num_distinct"), _dev(g.expert_list, "expert_list"),
-                                 _dev(g.offsets, "offsets"), _dev(g.slot_order, "slot_order"),
-                                 ctypes.c_void_p(ws.data_ptr()) if ws is not None else None,
-                                 _stream(ids.device)), "moe_group_slots")
+    _call("moe_group_slots", ids.device, _dev(ids, "ids", torch.int32), n, m, N,
+          _dev(g.num_distinct, "num_distinct"), _dev(g.expert_list, "expert_list"),
+          _dev(g.offsets, "offsets"), _dev(g.slot_order, "slot_order"),
+          ctypes.c_void_p(ws.data_ptr()) if ws is not None else None,
+          _stream(ids.device))
     return g
 
 
@@ -285,12 +300,12 @@ def expert_op_perslot(layer: Layer, weights, x: torch.Tensor, ids: torch.Tensor,
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _check(lib().moe_expert_op_perslot(ctypes.byref(layer), *_weights(layer, weights),
-                                       _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-                                       _dev(ids, "ids", torch.int32, (n, layer.m)),
-                                       _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                       int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                       ws.numel(), _stream(x.device)), "moe_expert_op_perslot")
+    _call("moe_expert_op_perslot", x.device, ctypes.byref(layer), *_weights(layer, weights),
+          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+          _dev(ids, "ids", torch.int32, (n, layer.m)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(x.device))
     return y
 
 
@@ -300,12 +315,12 @@ def expert_op_dedup_ids(layer: Layer, weights, x: torch.Tensor, ids: torch.Tenso
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _check(lib().moe_expert_op_dedup_ids(ctypes.byref(layer), *_weights(layer, weights),
-                                         _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-                                         _dev(ids, "ids", torch.int32, (n, layer.m)),
-                                         _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                         int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                         ws.numel(), _stream(x.device)), "moe_expert_op_dedup_ids")
+    _call("moe_expert_op_dedup_ids", x.device, ctypes.byref(layer), *_weights(layer, weights),
+          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+          _dev(ids, "ids", torch.int32, (n, layer.m)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(x.device))
     return y
 
 
@@ -315,15 +330,15 @@ def expert_op_dedup(layer: Layer, weights, x: torch.Tensor, gates: torch.Tensor,
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _check(lib().moe_expert_op_dedup(ctypes.byref(layer), *_weights(layer, weights),
-                                     _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-                                     _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                     _dev(grouping.num_distinct, "num_distinct"),
-                                     _dev(grouping.expert_list, "expert_list"),
-                                     _dev(grouping.offsets, "offsets"),
-                                     _dev(grouping.slot_order, "slot_order"),
-                                     int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                     ws.numel(), _stream(x.device)), "moe_expert_op_dedup")
+    _call("moe_expert_op_dedup", x.device, ctypes.byref(layer), *_weights(layer, weights),
+          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          _dev(grouping.num_distinct, "num_distinct"),
+          _dev(grouping.expert_list, "expert_list"),
+          _dev(grouping.offsets, "offsets"),
+          _dev(grouping.slot_order, "slot_order"),
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(x.device))
     return y
 
 
@@ -444,10 +459,9 @@ def quantize_rows_e4m3(src: torch.Tensor):
     rows = src.numel() // cols
     q = torch.empty(src.shape, dtype=torch.uint8, device=src.device)
     scale = torch.empty(src.shape[:-1], dtype=torch.float32, device=src.device)
-    _check(lib().moe_quantize_rows_e4m3(_dev(src, "src"), MOE_F32 if src.dtype == torch.float32 else MOE_BF16,
-                                        rows, cols, ctypes.c_void_p(q.data_ptr()),
-                                        ctypes.c_void_p(scale.data_ptr()), _stream(src.device)),
-           "moe_quantize_rows_e4m3")
+    _call("moe_quantize_rows_e4m3", src.device, _dev(src, "src"), MOE_F32 if src.dtype == torch.float32 else MOE_BF16,
+          rows, cols, ctypes.c_void_p(q.data_ptr()),
+          ctypes.c_void_p(scale.data_ptr()), _stream(src.device))
     return q, scale
 
 
@@ -471,13 +485,13 @@ def expert_op_perslot_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_sca
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _check(lib().moe_expert_op_perslot_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-                                           _dev(xq, "x", torch.uint8, (n, layer.d)),
-                                           _dev(x_scale, "x_scale", torch.float32, (n,)),
-                                           _dev(ids, "ids", torch.int32, (n, layer.m)),
-                                           _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                           int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                           ws.numel(), _stream(xq.device)), "moe_expert_op_perslot_fp8")
+    _call("moe_expert_op_perslot_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+          _dev(xq, "x", torch.uint8, (n, layer.d)),
+          _dev(x_scale, "x_scale", torch.float32, (n,)),
+          _dev(ids, "ids", torch.int32, (n, layer.m)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(xq.device))
     return y
 
 
@@ -488,13 +502,13 @@ def expert_op_dedup_ids_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_s
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _check(lib().moe_expert_op_dedup_ids_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-                                             _dev(xq, "x", torch.uint8, (n, layer.d)),
-                                             _dev(x_scale, "x_scale", torch.float32, (n,)),
-                                             _dev(ids, "ids", torch.int32, (n, layer.m)),
-                                             _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                             int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                             ws.numel(), _stream(xq.device)), "moe_expert_op_dedup_ids_fp8")
+    _call("moe_expert_op_dedup_ids_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+          _dev(xq, "x", torch.uint8, (n, layer.d)),
+          _dev(x_scale, "x_scale", torch.float32, (n,)),
+          _dev(ids, "ids", torch.int32, (n, layer.m)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(xq.device))
     return y
 
 
@@ -505,16 +519,16 @@ def expert_op_dedup_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_scale
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _check(lib().moe_expert_op_dedup_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-                                         _dev(xq, "x", torch.uint8, (n, layer.d)),
-                                         _dev(x_scale, "x_scale", torch.float32, (n,)),
-                                         _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-                                         _dev(grouping.num_distinct, "num_distinct"),
-                                         _dev(grouping.expert_list, "expert_list"),
-                                         _dev(grouping.offsets, "offsets"),
-                                         _dev(grouping.slot_order, "slot_order"),
-                                         int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-                                         ws.numel(), _stream(xq.device)), "moe_expert_op_dedup_fp8")
+    _call("moe_expert_op_dedup_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+          _dev(xq, "x", torch.uint8, (n, layer.d)),
+          _dev(x_scale, "x_scale", torch.float32, (n,)),
+          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+          _dev(grouping.num_distinct, "num_distinct"),
+          _dev(grouping.expert_list, "expert_list"),
+          _dev(grouping.offsets, "offsets"),
+          _dev(grouping.slot_order, "slot_order"),
+          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+          ws.numel(), _stream(xq.device))
     return y
 
 
@@ -532,10 +546,10 @@ def spec_accept(draft, q, p, r, u, greedy: bool = False, n_accepted=None, token=
     if token is None:
         token = torch.empty(B, dtype=torch.int32, device=dev)
     dptr = lambda t, name, dt: None if t is None else _dev(t, name, dt)
-    _check(lib().moe_spec_accept(dptr(draft, "draft", torch.int32) if K else None, dptr(q, "q", torch.float32),
-                                 _dev(p, "p", torch.float32), dptr(r, "r", torch.float32), dptr(u, "u", torch.float32),
-                                 B, K, V, int(bool(greedy)), _dev(n_accepted, "n_accepted", torch.int32),
-                                 _dev(token, "token", torch.int32), _stream(dev)), "moe_spec_accept")
+    _call("moe_spec_accept", dev, dptr(draft, "draft", torch.int32) if K else None, dptr(q, "q", torch.float32),
+          _dev(p, "p", torch.float32), dptr(r, "r", torch.float32), dptr(u, "u", torch.float32),
+          B, K, V, int(bool(greedy)), _dev(n_accepted, "n_accepted", torch.int32),
+          _dev(token, "token", torch.int32), _stream(dev))
     return n_accepted, token
 
 
@@ -552,22 +566,22 @@ def union_cost(bitmaps, subsets, pv, bcoef, beta: float, out=None, ws=None):
                    best=torch.empty(1, dtype=torch.int32, device=dev))
     if ws is None:
         ws = torch.empty(int(lib().moe_union_cost_workspace_bytes(S)), dtype=torch.uint8, device=dev)
-    _check(lib().moe_union_cost(_dev(bitmaps, "bitmaps", torch.int64), nodes1 - 1, L, W,
-                                _dev(subsets, "subsets", torch.int32), S,
-                                _dev(pv, "pv", torch.float64) if nodes1 > 1 else None,
-                                _dev(bcoef, "bcoef", torch.float64), float(beta),
-                                _dev(out["F"], "F", torch.int32), _dev(out["size"], "size", torch.int32),
-                                _dev(out["R"], "R", torch.float64), _dev(out["T"], "T", torch.float64),
-                                _dev(out["best"], "best", torch.int32), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-                                _stream(dev)), "moe_union_cost")
+    _call("moe_union_cost", dev, _dev(bitmaps, "bitmaps", torch.int64), nodes1 - 1, L, W,
+          _dev(subsets, "subsets", torch.int32), S,
+          _dev(pv, "pv", torch.float64) if nodes1 > 1 else None,
+          _dev(bcoef, "bcoef", torch.float64), float(beta),
+          _dev(out["F"], "F", torch.int32), _dev(out["size"], "size", torch.int32),
+          _dev(out["R"], "R", torch.float64), _dev(out["T"], "T", torch.float64),
+          _dev(out["best"], "best", torch.int32), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+          _stream(dev))
     return out
 
 
 def read_probe(buf: torch.Tensor, ws: torch.Tensor) -> int:
     """Enqueue the read-only streaming probe over buf (a CUDA tensor); returns the bytes it reads."""
     nbytes = buf.numel() * buf.element_size()
-    _check(lib().moe_read_probe(ctypes.c_void_p(buf.data_ptr()), nbytes, ctypes.c_void_p(ws.data_ptr()),
-                                _stream(buf.device)), "moe_read_probe")
+    _call("moe_read_probe", buf.device, ctypes.c_void_p(buf.data_ptr()), nbytes, ctypes.c_void_p(ws.data_ptr()),
+          _stream(buf.device))
     return nbytes // 32768 * 32768
 
 
@@ -648,8 +662,8 @@ def rope_table(positions: int, w, magnitude: float = 1.0, device=None) -> torch.
     """moe_rope_table: fp32 [positions, rot / 2, 2] of m cos(p w_i), m sin(p w_i)."""
     w = np.ascontiguousarray(np.asarray(w, dtype=np.float64))
     table = torch.empty((positions, w.size, 2), dtype=torch.float32, device=device or "cuda")
-    _check(lib().moe_rope_table(ctypes.c_void_p(w.ctypes.data), w.size, float(magnitude), int(positions),
-                                ctypes.c_void_p(table.data_ptr()), _stream(table.device)), "moe_rope_table")
+    _call("moe_rope_table", table.device, ctypes.c_void_p(w.ctypes.data), w.size, float(magnitude), int(positions),
+          ctypes.c_void_p(table.data_ptr()), _stream(table.device))
     return table
 
 
@@ -669,6 +683,9 @@ def rope(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool =
     may be its input.  ws (any workspace) records positions beyond the table."""
     ref = q if q is not None else k
     device = _device_of(ref, "q" if q is not None else "k")
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return rope(q, k, positions, table, interleaved, inverse, q_out, k_out, ws)
     tokens, _, dim = ref.shape
     dq = dqo = dk = dko = None
     if q is not None:
@@ -740,6 +757,9 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     before, and q [tokens, q heads, dim], when given, is rotated into q_out, which is returned (None
     without q).  ws (any workspace) records slots and positions out of range."""
     device, dim = cache.index, cache.dim
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return kv_write(cache, k, v, slots, q, positions, table, interleaved, q_out, ws)
     tokens = k.shape[0]
     dk = _heads(k, "k", tokens, cache.heads, dim, device)
     dv = _heads(v, "v", tokens, cache.heads, dim, device)
@@ -770,6 +790,9 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=Non
     """moe_kv_read: the cache's rows of slots int32 [tokens] as (k, v) [tokens, heads, dim], fp32 or bf16;
     zeros for a negative slot."""
     device = cache.index
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return kv_read(cache, slots, dtype, k_out, v_out, ws)
     tokens = slots.shape[0]
     shape = (tokens, cache.heads, cache.dim)
     if k_out is None:
@@ -786,9 +809,10 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=Non
 
 def tree_attention_workspace(cache: KVCache, tokens: int, seqs: int, q_heads: int) -> torch.Tensor:
     """A zeroed workspace for tree_attention calls of up to this many tokens and sequences."""
-    nbytes = int(lib().moe_tree_attention_workspace_bytes(cache.address, tokens, seqs, q_heads))
+    with torch.cuda.device(cache.index):   # the size goes by its number of SMs
+        nbytes = int(lib().moe_tree_attention_workspace_bytes(cache.address, tokens, seqs, q_heads))
     ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
-    _check(lib().moe_workspace_init(ws.data_ptr(), nbytes, _stream(cache.device)), "moe_workspace_init")
+    _call("moe_workspace_init", cache.device, ws.data_ptr(), nbytes, _stream(cache.device))
     return ws
 
 
@@ -801,6 +825,9 @@ def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: 
     where it sees drafted token j of its sequence (None: a chain); scale defaults to dim^-0.5.  Returns
     out, or (out, lse) with return_lse."""
     device, dim = cache.index, cache.dim
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return tree_attention(cache, q, q_start, ctx, page_table, mask, scale, max_tokens, out, lse, return_lse, ws)
     tokens, heads = q.shape[0], q.shape[1]
     seqs, max_pages = page_table.shape
     dq = _heads(q, "q", tokens, heads, dim, device)
