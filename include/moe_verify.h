@@ -647,8 +647,8 @@ size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t t
  *   page_table [dev] int32 [seqs, max_pages], mask [dev] uint64 [tokens] or NULL, scale > 0,
  *   q and out [tokens, q heads, dim] of one type; lse [dev] fp32 [tokens, q heads] or NULL.
  * A page outside the cache is recorded and reads as zeros.  A sequence whose lengths do not fit
- * (ctx < 0, n_b outside [0, max_tokens], ctx + n_b > max_pages * page, tokens beyond q) is recorded
- * and its rows are not written.
+ * (ctx < 0, n_b outside [0, max_tokens], ctx + n_b > max_pages * page or > 2^31 - 128, tokens beyond
+ * q) is recorded and its rows are not written.
  * bf16 q over a bf16 or e4m3 cache with dim <= 128 runs on the tensor cores when q is 16-byte
  * aligned with strides that are multiples of 8 elements, as out, page is a multiple of 8 and the
  * scales are 16-byte aligned; all else on

@@ -30,6 +30,9 @@ struct ReadArgs {
     int32_t tokens;
 };
 
+// Most positions of a sequence: whole tiles of 128 that 31 bits number.
+constexpr long long kMaxPositions = (1ll << 31) - 128;
+
 struct TreeArgs {
     moe_kv_cache_t cache;
     moe_heads_t q, out;

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_simt_kernel(const __grid_con
     const int t0 = a.q_start[b], n = a.q_start[b + 1] - t0, ctx = a.ctx[b];
     const int64_t len = static_cast<int64_t>(ctx) + n;
     if (ctx < 0 || n < 0 || n > a.max_tokens || t0 < 0 || t0 > a.tokens - n ||
-        len > static_cast<int64_t>(a.max_pages) * c.page) {
+        len > static_cast<int64_t>(a.max_pages) * c.page || len > kMaxPositions) {
         if (threadIdx.x == 0) record_error(a.err, MOE_ERR_BAD_ID);
         return;
     }

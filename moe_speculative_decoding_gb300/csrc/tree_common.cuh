@@ -213,7 +213,7 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs &a, int b) {
     s.ctx = a.ctx[b];
     const long long len = s.ctx + n;
     s.bad = s.ctx < 0 || n < 0 || n > a.max_tokens || s.t0 < 0 || s.t0 > a.tokens - n ||
-            len > static_cast<long long>(a.max_pages) * a.cache.page;
+            len > static_cast<long long>(a.max_pages) * a.cache.page || len > kMaxPositions;
     s.n = s.bad ? 0 : static_cast<int>(n);
     s.len = s.bad ? 0 : static_cast<int>(len);
     s.tiles = (s.len + kTile - 1) / kTile;
