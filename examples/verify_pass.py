@@ -80,9 +80,16 @@ class Model:
             api.kv_write(cache, k, v, new)
 
 
+def check_room(tokens):
+    """Places beyond a sequence's pages have no slot (and an index on the device is not checked on the host)."""
+    if tokens > PAGES_EACH * PAGE:
+        raise ValueError(f"a sequence would need {tokens} places of the cache and has {PAGES_EACH * PAGE}")
+
+
 def prefill(model, prompts):
     """The prompts [seqs, n] as chains, a pass of up to 64 tokens at a time; the last token's logits."""
     seqs, n = prompts.shape
+    check_room(n)
     step = max(1, 64 // seqs)
     for i in range(0, n, step):
         m = min(step, n - i)
@@ -111,6 +118,7 @@ def decode(model, prompts, rounds, seed=0):
     last, length = logits.argmax(-1).tolist(), [n] * seqs
     out, final = [[t] for t in last], [logits[b] for b in range(seqs)]
     for _ in range(rounds):
+        check_room(max(length) + T)
         # a drafter would propose likely tokens; these are random
         trees = torch.randint(VOCAB, (seqs, T), generator=g)
         trees[:, 0] = torch.tensor(last)
