@@ -178,6 +178,12 @@ def _check(code: int, what: str):
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+def _there(t: torch.Tensor, fn, *args):
+    """fn with t's device current (a call tests for it in line: another function's call would cost it a microsecond)."""
+    with torch.cuda.device(t.get_device()):
+        return fn(*args)
+
+
 def _call(name: str, device, *args):
     """A call of the library with a tensor's device current."""
     if device.index == _current_device():
@@ -242,14 +248,17 @@ def set_wait_limit(cycles: int) -> None:
 
 def route_topm(logits: torch.Tensor, m: int, renorm: bool = True, ids=None, gates=None):
     """Top-m routing of fp32 logits [n, N] -> (ids int32 [n, m], gates fp32 [n, m])."""
+    if (index := logits.get_device()) >= 0 and index != _current_device():
+        return _there(logits, route_topm, logits, m, renorm, ids, gates)
     n, N = logits.shape
     if ids is None:
         ids = torch.empty((n, m), dtype=torch.int32, device=logits.device)
     if gates is None:
         gates = torch.empty((n, m), dtype=torch.float32, device=logits.device)
-    _call("moe_route_topm", logits.device, _dev(logits, "logits", torch.float32), n, N, m, int(bool(renorm)),
-          _dev(ids, "ids", torch.int32, (n, m)),
-          _dev(gates, "gates", torch.float32, (n, m)), _stream(logits.device))
+    _check(lib().moe_route_topm(_dev(logits, "logits", torch.float32), n, N, m, int(bool(renorm)),
+                                _dev(ids, "ids", torch.int32, (n, m)),
+                                _dev(gates, "gates", torch.float32, (n, m)), _stream(logits.device)),
+           "moe_route_topm")
     return ids, gates
 
 
@@ -269,13 +278,15 @@ class Grouping:
 
 def group_slots(ids: torch.Tensor, N: int, out: Grouping | None = None, ws=None) -> Grouping:
     """moe_group_slots: the pass's slots grouped by expert, a counting sort ([Lan] §1, App. E): U, expert list, offsets, slot order."""
+    if (index := ids.get_device()) >= 0 and index != _current_device():
+        return _there(ids, group_slots, ids, N, out, ws)
     n, m = ids.shape
     g = out or Grouping.empty(n, m, N, ids.device)
-    _call("moe_group_slots", ids.device, _dev(ids, "ids", torch.int32), n, m, N,
-          _dev(g.num_distinct, "num_distinct"), _dev(g.expert_list, "expert_list"),
-          _dev(g.offsets, "offsets"), _dev(g.slot_order, "slot_order"),
-          ctypes.c_void_p(ws.data_ptr()) if ws is not None else None,
-          _stream(ids.device))
+    _check(lib().moe_group_slots(_dev(ids, "ids", torch.int32), n, m, N,
+                                 _dev(g.num_distinct, "num_distinct"), _dev(g.expert_list, "expert_list"),
+                                 _dev(g.offsets, "offsets"), _dev(g.slot_order, "slot_order"),
+                                 ctypes.c_void_p(ws.data_ptr()) if ws is not None else None,
+                                 _stream(ids.device)), "moe_group_slots")
     return g
 
 
@@ -297,48 +308,54 @@ def _y(layer, x, y):
 def expert_op_perslot(layer: Layer, weights, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor,
                       y=None, accumulate: bool = False, ws=None):
     """moe_expert_op_perslot: the per-slot form of the expert operation, one expert read per slot ([Lan] §1)."""
+    if (index := x.get_device()) >= 0 and index != _current_device():
+        return _there(x, expert_op_perslot, layer, weights, x, ids, gates, y, accumulate, ws)
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _call("moe_expert_op_perslot", x.device, ctypes.byref(layer), *_weights(layer, weights),
-          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-          _dev(ids, "ids", torch.int32, (n, layer.m)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(x.device))
+    _check(lib().moe_expert_op_perslot(ctypes.byref(layer), *_weights(layer, weights),
+                                       _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+                                       _dev(ids, "ids", torch.int32, (n, layer.m)),
+                                       _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                       int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                       ws.numel(), _stream(x.device)), "moe_expert_op_perslot")
     return y
 
 
 def expert_op_dedup_ids(layer: Layer, weights, x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor,
                         y=None, accumulate: bool = False, ws=None):
     """The deduplicating form from ids in one launch (the grouping built inside the kernel)."""
+    if (index := x.get_device()) >= 0 and index != _current_device():
+        return _there(x, expert_op_dedup_ids, layer, weights, x, ids, gates, y, accumulate, ws)
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _call("moe_expert_op_dedup_ids", x.device, ctypes.byref(layer), *_weights(layer, weights),
-          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-          _dev(ids, "ids", torch.int32, (n, layer.m)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(x.device))
+    _check(lib().moe_expert_op_dedup_ids(ctypes.byref(layer), *_weights(layer, weights),
+                                         _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+                                         _dev(ids, "ids", torch.int32, (n, layer.m)),
+                                         _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                         int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                         ws.numel(), _stream(x.device)), "moe_expert_op_dedup_ids")
     return y
 
 
 def expert_op_dedup(layer: Layer, weights, x: torch.Tensor, gates: torch.Tensor, grouping: Grouping,
                     y=None, accumulate: bool = False, ws=None):
     """moe_expert_op_dedup: the deduplicating form on a precomputed grouping, each distinct expert read once ([Lan] §1)."""
+    if (index := x.get_device()) >= 0 and index != _current_device():
+        return _there(x, expert_op_dedup, layer, weights, x, gates, grouping, y, accumulate, ws)
     n = x.shape[0]
     ws = ws if ws is not None else workspace(layer, n, x.device)
     y, yp = _y(layer, x, y)
-    _call("moe_expert_op_dedup", x.device, ctypes.byref(layer), *_weights(layer, weights),
-          _dev(x, "x", layer.torch_dtype, (n, layer.d)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          _dev(grouping.num_distinct, "num_distinct"),
-          _dev(grouping.expert_list, "expert_list"),
-          _dev(grouping.offsets, "offsets"),
-          _dev(grouping.slot_order, "slot_order"),
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(x.device))
+    _check(lib().moe_expert_op_dedup(ctypes.byref(layer), *_weights(layer, weights),
+                                     _dev(x, "x", layer.torch_dtype, (n, layer.d)),
+                                     _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                     _dev(grouping.num_distinct, "num_distinct"),
+                                     _dev(grouping.expert_list, "expert_list"),
+                                     _dev(grouping.offsets, "offsets"),
+                                     _dev(grouping.slot_order, "slot_order"),
+                                     int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                     ws.numel(), _stream(x.device)), "moe_expert_op_dedup")
     return y
 
 
@@ -453,15 +470,18 @@ def fit_op_times(n, U, t, m: int, b: float, form: str) -> tuple:
 def quantize_rows_e4m3(src: torch.Tensor):
     """Row-wise e4m3 codes (uint8, same shape) and fp32 row scales of a 2-D or 3-D fp32/bf16
     CUDA tensor (rows = all leading dimensions)."""
+    if (index := src.get_device()) >= 0 and index != _current_device():
+        return _there(src, quantize_rows_e4m3, src)
     if src.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("quantize_rows_e4m3 takes fp32 or bf16")
     cols = src.shape[-1]
     rows = src.numel() // cols
     q = torch.empty(src.shape, dtype=torch.uint8, device=src.device)
     scale = torch.empty(src.shape[:-1], dtype=torch.float32, device=src.device)
-    _call("moe_quantize_rows_e4m3", src.device, _dev(src, "src"), MOE_F32 if src.dtype == torch.float32 else MOE_BF16,
-          rows, cols, ctypes.c_void_p(q.data_ptr()),
-          ctypes.c_void_p(scale.data_ptr()), _stream(src.device))
+    _check(lib().moe_quantize_rows_e4m3(_dev(src, "src"), MOE_F32 if src.dtype == torch.float32 else MOE_BF16,
+                                        rows, cols, ctypes.c_void_p(q.data_ptr()),
+                                        ctypes.c_void_p(scale.data_ptr()), _stream(src.device)),
+           "moe_quantize_rows_e4m3")
     return q, scale
 
 
@@ -481,54 +501,60 @@ def _scales(layer: Layer, scales) -> WeightScales:
 def expert_op_perslot_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_scale: torch.Tensor, ids: torch.Tensor,
                           gates: torch.Tensor, y=None, accumulate: bool = False, ws=None):
     """moe_expert_op_perslot_fp8: the per-slot form on e4m3 experts with row scales (the quantized experts of [Lan] App. E Table 6)."""
+    if (index := xq.get_device()) >= 0 and index != _current_device():
+        return _there(xq, expert_op_perslot_fp8, layer, weights, scales, xq, x_scale, ids, gates, y, accumulate, ws)
     n = xq.shape[0]
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _call("moe_expert_op_perslot_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-          _dev(xq, "x", torch.uint8, (n, layer.d)),
-          _dev(x_scale, "x_scale", torch.float32, (n,)),
-          _dev(ids, "ids", torch.int32, (n, layer.m)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(xq.device))
+    _check(lib().moe_expert_op_perslot_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+                                           _dev(xq, "x", torch.uint8, (n, layer.d)),
+                                           _dev(x_scale, "x_scale", torch.float32, (n,)),
+                                           _dev(ids, "ids", torch.int32, (n, layer.m)),
+                                           _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                           int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                           ws.numel(), _stream(xq.device)), "moe_expert_op_perslot_fp8")
     return y
 
 
 def expert_op_dedup_ids_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_scale: torch.Tensor, ids: torch.Tensor,
                             gates: torch.Tensor, y=None, accumulate: bool = False, ws=None):
     """moe_expert_op_dedup_ids_fp8: the deduplicating form from ids on e4m3 experts, the grouping built in the kernel ([Lan] §1; App. E Table 6)."""
+    if (index := xq.get_device()) >= 0 and index != _current_device():
+        return _there(xq, expert_op_dedup_ids_fp8, layer, weights, scales, xq, x_scale, ids, gates, y, accumulate, ws)
     n = xq.shape[0]
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _call("moe_expert_op_dedup_ids_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-          _dev(xq, "x", torch.uint8, (n, layer.d)),
-          _dev(x_scale, "x_scale", torch.float32, (n,)),
-          _dev(ids, "ids", torch.int32, (n, layer.m)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(xq.device))
+    _check(lib().moe_expert_op_dedup_ids_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+                                             _dev(xq, "x", torch.uint8, (n, layer.d)),
+                                             _dev(x_scale, "x_scale", torch.float32, (n,)),
+                                             _dev(ids, "ids", torch.int32, (n, layer.m)),
+                                             _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                             int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                             ws.numel(), _stream(xq.device)), "moe_expert_op_dedup_ids_fp8")
     return y
 
 
 def expert_op_dedup_fp8(layer: Layer, weights, scales, xq: torch.Tensor, x_scale: torch.Tensor, gates: torch.Tensor,
                         grouping: Grouping, y=None, accumulate: bool = False, ws=None):
     """moe_expert_op_dedup_fp8: the deduplicating form on e4m3 experts and a precomputed grouping ([Lan] §1; App. E Table 6)."""
+    if (index := xq.get_device()) >= 0 and index != _current_device():
+        return _there(xq, expert_op_dedup_fp8, layer, weights, scales, xq, x_scale, gates, grouping, y, accumulate, ws)
     n = xq.shape[0]
     ws = ws if ws is not None else workspace(layer, n, xq.device)
     y, yp = _y(layer, xq, y)
     sc = _scales(layer, scales)
-    _call("moe_expert_op_dedup_fp8", xq.device, ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
-          _dev(xq, "x", torch.uint8, (n, layer.d)),
-          _dev(x_scale, "x_scale", torch.float32, (n,)),
-          _dev(gates, "gates", torch.float32, (n, layer.m)), n,
-          _dev(grouping.num_distinct, "num_distinct"),
-          _dev(grouping.expert_list, "expert_list"),
-          _dev(grouping.offsets, "offsets"),
-          _dev(grouping.slot_order, "slot_order"),
-          int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
-          ws.numel(), _stream(xq.device))
+    _check(lib().moe_expert_op_dedup_fp8(ctypes.byref(layer), *_weights(layer, weights), ctypes.byref(sc),
+                                         _dev(xq, "x", torch.uint8, (n, layer.d)),
+                                         _dev(x_scale, "x_scale", torch.float32, (n,)),
+                                         _dev(gates, "gates", torch.float32, (n, layer.m)), n,
+                                         _dev(grouping.num_distinct, "num_distinct"),
+                                         _dev(grouping.expert_list, "expert_list"),
+                                         _dev(grouping.offsets, "offsets"),
+                                         _dev(grouping.slot_order, "slot_order"),
+                                         int(bool(accumulate)), yp, ctypes.c_void_p(ws.data_ptr()),
+                                         ws.numel(), _stream(xq.device)), "moe_expert_op_dedup_fp8")
     return y
 
 
@@ -538,6 +564,8 @@ def spec_accept(draft, q, p, r, u, greedy: bool = False, n_accepted=None, token=
     Algorithm 1) on the device.  draft int32 [B, K], q fp32 [B, K, V], p fp32 [B, K+1, V],
     r fp32 [B, K], u fp32 [B] (q, r, u may be None when greedy).  Returns (n_accepted, token),
     int32 [B] each."""
+    if (index := p.get_device()) >= 0 and index != _current_device():
+        return _there(p, spec_accept, draft, q, p, r, u, greedy, n_accepted, token)
     B, K1, V = p.shape
     K = K1 - 1
     dev = p.device
@@ -546,10 +574,10 @@ def spec_accept(draft, q, p, r, u, greedy: bool = False, n_accepted=None, token=
     if token is None:
         token = torch.empty(B, dtype=torch.int32, device=dev)
     dptr = lambda t, name, dt: None if t is None else _dev(t, name, dt)
-    _call("moe_spec_accept", dev, dptr(draft, "draft", torch.int32) if K else None, dptr(q, "q", torch.float32),
-          _dev(p, "p", torch.float32), dptr(r, "r", torch.float32), dptr(u, "u", torch.float32),
-          B, K, V, int(bool(greedy)), _dev(n_accepted, "n_accepted", torch.int32),
-          _dev(token, "token", torch.int32), _stream(dev))
+    _check(lib().moe_spec_accept(dptr(draft, "draft", torch.int32) if K else None, dptr(q, "q", torch.float32),
+                                 _dev(p, "p", torch.float32), dptr(r, "r", torch.float32), dptr(u, "u", torch.float32),
+                                 B, K, V, int(bool(greedy)), _dev(n_accepted, "n_accepted", torch.int32),
+                                 _dev(token, "token", torch.int32), _stream(dev)), "moe_spec_accept")
     return n_accepted, token
 
 
@@ -557,6 +585,8 @@ def union_cost(bitmaps, subsets, pv, bcoef, beta: float, out=None, ws=None):
     """SpecFit §3.2 eqs (3)-(5) on the device: bitmaps uint64-as-int64 [nodes+1, L, W], subsets
     int32/uint32 bits [S], pv float64 [nodes], bcoef float64 [nodes+1].  Returns dict(F, size,
     R, T, best) of device tensors."""
+    if (index := bitmaps.get_device()) >= 0 and index != _current_device():
+        return _there(bitmaps, union_cost, bitmaps, subsets, pv, bcoef, beta, out, ws)
     nodes1, L, W = bitmaps.shape
     S = subsets.numel()
     dev = bitmaps.device
@@ -566,14 +596,14 @@ def union_cost(bitmaps, subsets, pv, bcoef, beta: float, out=None, ws=None):
                    best=torch.empty(1, dtype=torch.int32, device=dev))
     if ws is None:
         ws = torch.empty(int(lib().moe_union_cost_workspace_bytes(S)), dtype=torch.uint8, device=dev)
-    _call("moe_union_cost", dev, _dev(bitmaps, "bitmaps", torch.int64), nodes1 - 1, L, W,
-          _dev(subsets, "subsets", torch.int32), S,
-          _dev(pv, "pv", torch.float64) if nodes1 > 1 else None,
-          _dev(bcoef, "bcoef", torch.float64), float(beta),
-          _dev(out["F"], "F", torch.int32), _dev(out["size"], "size", torch.int32),
-          _dev(out["R"], "R", torch.float64), _dev(out["T"], "T", torch.float64),
-          _dev(out["best"], "best", torch.int32), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-          _stream(dev))
+    _check(lib().moe_union_cost(_dev(bitmaps, "bitmaps", torch.int64), nodes1 - 1, L, W,
+                                _dev(subsets, "subsets", torch.int32), S,
+                                _dev(pv, "pv", torch.float64) if nodes1 > 1 else None,
+                                _dev(bcoef, "bcoef", torch.float64), float(beta),
+                                _dev(out["F"], "F", torch.int32), _dev(out["size"], "size", torch.int32),
+                                _dev(out["R"], "R", torch.float64), _dev(out["T"], "T", torch.float64),
+                                _dev(out["best"], "best", torch.int32), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+                                _stream(dev)), "moe_union_cost")
     return out
 
 
@@ -684,8 +714,7 @@ def rope(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool =
     ref = q if q is not None else k
     device = _device_of(ref, "q" if q is not None else "k")
     if device != _current_device():
-        with torch.cuda.device(device):
-            return rope(q, k, positions, table, interleaved, inverse, q_out, k_out, ws)
+        return _there(ref, rope, q, k, positions, table, interleaved, inverse, q_out, k_out, ws)
     tokens, _, dim = ref.shape
     dq = dqo = dk = dko = None
     if q is not None:
@@ -758,8 +787,7 @@ def kv_write(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tens
     without q).  ws (any workspace) records slots and positions out of range."""
     device, dim = cache.index, cache.dim
     if device != _current_device():
-        with torch.cuda.device(device):
-            return kv_write(cache, k, v, slots, q, positions, table, interleaved, q_out, ws)
+        return _there(cache.k, kv_write, cache, k, v, slots, q, positions, table, interleaved, q_out, ws)
     tokens = k.shape[0]
     dk = _heads(k, "k", tokens, cache.heads, dim, device)
     dv = _heads(v, "v", tokens, cache.heads, dim, device)
@@ -791,8 +819,7 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype=torch.bfloat16, k_out=Non
     zeros for a negative slot."""
     device = cache.index
     if device != _current_device():
-        with torch.cuda.device(device):
-            return kv_read(cache, slots, dtype, k_out, v_out, ws)
+        return _there(cache.k, kv_read, cache, slots, dtype, k_out, v_out, ws)
     tokens = slots.shape[0]
     shape = (tokens, cache.heads, cache.dim)
     if k_out is None:
@@ -826,8 +853,7 @@ def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: 
     out, or (out, lse) with return_lse."""
     device, dim = cache.index, cache.dim
     if device != _current_device():
-        with torch.cuda.device(device):
-            return tree_attention(cache, q, q_start, ctx, page_table, mask, scale, max_tokens, out, lse, return_lse, ws)
+        return _there(cache.k, tree_attention, cache, q, q_start, ctx, page_table, mask, scale, max_tokens, out, lse, return_lse, ws)
     tokens, heads = q.shape[0], q.shape[1]
     seqs, max_pages = page_table.shape
     dq = _heads(q, "q", tokens, heads, dim, device)

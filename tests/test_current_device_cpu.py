@@ -91,3 +91,15 @@ def test_expert_side(entered):
     api.last_device_error(ws)
     launching = {k: v for k, v in entered.items() if not k.endswith("_bytes")}
     assert len(launching) == 14 and set(launching.values()) == {1}, entered
+
+
+def test_host_tensors_are_still_refused():
+    layer, w = api.make_layer(16, 8, 4, 2, "f32"), torch.zeros
+    with pytest.raises(TypeError):
+        api.route_topm(w(3, 4), 2)
+    with pytest.raises(TypeError):
+        api.quantize_rows_e4m3(w(3, 16))
+    with pytest.raises(TypeError):
+        api.expert_op_dedup_ids(layer, (w(4, 8, 16), w(4, 8, 16), w(4, 16, 8)), w(3, 16), w(3, 2), w(3, 2), ws=w(9))
+    with pytest.raises(TypeError):
+        api.rope(w(3, 2, 4), None, w(3), w(4, 2, 2))
