@@ -295,25 +295,25 @@ __device__ __forceinline__ void from_raw(const Raw<E> &r, float (&x)[8], float (
     }
 }
 
+// One pair, with its two roundings spelled out: the kernels for any layout and for aligned ones give
+// the same numbers.
+__device__ __forceinline__ void turn_pair(float &a, float &b, float c, float s) {
+    const float x = fmaf(a, c, -__fmul_rn(b, s)), y = fmaf(a, s, __fmul_rn(b, c));
+    a = x;
+    b = y;
+}
 // One rotation of the thread's pairs.  cs: 8 (cos, sin); a thread with unrotated channels holds
 // (1, 0) there and skips nothing: x * 1 - y * 0 would turn an infinity into NaN, so `turn` decides.
 __device__ __forceinline__ void turn16(float (&x)[8], float (&y)[8], const float (&cs)[16], bool adjacent) {
     if (adjacent) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1], c = y[2 * i], d = y[2 * i + 1];
-            x[2 * i] = a * cs[2 * i] - b * cs[2 * i + 1];
-            x[2 * i + 1] = b * cs[2 * i] + a * cs[2 * i + 1];
-            y[2 * i] = c * cs[8 + 2 * i] - d * cs[8 + 2 * i + 1];
-            y[2 * i + 1] = d * cs[8 + 2 * i] + c * cs[8 + 2 * i + 1];
+            turn_pair(x[2 * i], x[2 * i + 1], cs[2 * i], cs[2 * i + 1]);
+            turn_pair(y[2 * i], y[2 * i + 1], cs[8 + 2 * i], cs[8 + 2 * i + 1]);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = x[i], b = y[i];
-            x[i] = a * cs[2 * i] - b * cs[2 * i + 1];
-            y[i] = b * cs[2 * i] + a * cs[2 * i + 1];
-        }
+        for (int i = 0; i < 8; ++i) turn_pair(x[i], y[i], cs[2 * i], cs[2 * i + 1]);
     }
 }
 
@@ -451,15 +451,11 @@ __global__ void __launch_bounds__(kThreads) rows_any_kernel(const __grid_constan
             o0 = 2 * i;
             o1 = 2 * i + 1;
         }
-        const float u = load1(w.src, w.src_type, w.src_off + o0);
-        const float v = o1 < a.dim ? load1(w.src, w.src_type, w.src_off + o1) : 0.0f;
-        p = u;
-        q = v;
+        p = load1(w.src, w.src_type, w.src_off + o0);
+        q = o1 < a.dim ? load1(w.src, w.src_type, w.src_off + o1) : 0.0f;
         if (i < half) {
             const float2 cs = __ldg(w.cs + i);
-            const float s = a.rot.inverse ? -cs.y : cs.y;
-            p = u * cs.x - v * s;
-            q = v * cs.x + u * s;
+            turn_pair(p, q, cs.x, a.rot.inverse ? -cs.y : cs.y);
         }
     };
     float sc = 1.0f;
