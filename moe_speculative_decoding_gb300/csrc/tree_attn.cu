@@ -85,8 +85,8 @@ struct Lay {
     static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, V tiles issued, tiles copied, turns
     static constexpr uint32_t oBad = (oMisc + 32 + 15) & ~15u;     // uint32 [8 items][2 tiles][4]
     static constexpr uint32_t oScale = oBad + 256;                 // F8: float [NC][ks, vs, log2 of vs][128]
-    static constexpr uint32_t oTop = oScale + (F8 ? NC * 1536 : 0);  // F8: float [NC], the tile's largest log2 of vs
-    static constexpr uint32_t oQs = oTop + (F8 ? NC * 4 : 0);       // F8: float [2][128], row factors
+    static constexpr uint32_t oTop = oScale + (F8 ? NC * 1536 : 0);  // F8: float [NC][4], the warps' largest log2 of vs so far
+    static constexpr uint32_t oQs = oTop + (F8 ? NC * 16 : 0);      // F8: float [2][128], row factors
     static constexpr uint32_t oWalk = (oQs + (F8 ? 1024 : 0) + 7) & ~7u;   // records of walks
     static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
     static_assert(kSmem <= 232448, "shared memory");
@@ -374,7 +374,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const uint32_t s_addr = tmem + lanes + g * kTile, o_addr = tmem + lanes + 256 + g * DP;
         float *const qs = reinterpret_cast<float *>(smem + L::oQs);
         const float *const scale_s = reinterpret_cast<const float *>(smem + L::oScale);
-        const volatile float *const top_s = reinterpret_cast<const volatile float *>(smem + L::oTop);
+        const float4 *const top_s = reinterpret_cast<const float4 *>(smem + L::oTop);
         float2 *const exch = reinterpret_cast<float2 *>(smem);   // [2][128], over Q when Q is done with
         uint32_t sc = 0, scnt = 0;
         bool ok = true;
@@ -441,10 +441,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 if (!look) {
                     mx = !F8 && edge ? tile_max<F8, true, false>(s_addr, ks, lv, cs, see) : tile_max<F8, false, false>(s_addr, ks, lv, cs, see);
                     mx *= cs;   // cs > 0; -inf stays
-                    // e4m3: with the tile's largest value scale this is at or above what counts, a score plus its
+                    // e4m3: with the largest value scale so far this is at or above what counts, a score plus its
                     // own value's; only where that does not do is that one looked for (in every tile: 128 rows
-                    // over 60-65 thousand positions 180 us against 169)
-                    look = F8 && __any_sync(0xFFFFFFFFu, mx + top_s[sb] - m > kLazy);
+                    // over 60-65 thousand positions 180 us against 170)
+                    if (F8) {
+                        const float4 t = top_s[sb];
+                        look = __any_sync(0xFFFFFFFFu, mx + fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)) - m > kLazy);
+                    }
                 }
                 if (F8 && look) mx = tile_max<F8, true, true>(s_addr, ks, lv, cs, see);
                 if ((!F8 || look) && __any_sync(0xFFFFFFFFu, u < 2 || mx - m > kLazy)) {

@@ -715,8 +715,8 @@ __device__ __forceinline__ void codes_to_f16(uint32_t x, uint32_t &lo, uint32_t 
 // e4m3: V's converters, four warps of 32 positions each: codes to fp16 (exact) in the products'
 // layout, the scales into a ring for the softmax: of a position the key's, the value's times
 // kWeightUp, and the logarithm of the value's.  The scales come from beside the codes (kLandScales:
-// a softmax thread owns a row, and has the tile's largest logarithm too) or are loaded here.  What
-// clean_values does for bf16 is done on the way.
+// a softmax thread owns a row, and has a bound on the tile's logarithms too, a warp's largest so far
+// from each) or are loaded here.  What clean_values does for bf16 is done on the way.
 // With two groups of four warps each takes every other tile (of one softmax warpgroup; rings are
 // even, so that a slot is one group's).  A tile takes a group 2,000 cycles of its own, 1,150 of them
 // the codes' loop, and every second one is its: about what a tile of the cache takes to arrive.
@@ -740,6 +740,9 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
         const int odd = L::kGroups == 2 ? static_cast<int>((cnt ^ static_cast<uint32_t>(w.lo) ^ static_cast<uint32_t>(group)) & 1u) : 0;
         if (lane < 2 && (L::kGroups == 1 || lane == odd)) bad[lane * 4 + cw] = 0;
         __syncwarp();
+        // the largest value scale of the warp's positions so far (formed for each tile anew it cost 4% of
+        // 128 rows' time)
+        float top = 0.0f, top_log = kScaleLow;
         // without landing scales: this thread's position of the group's tiles, the scales loaded a
         // tile ahead and the page two
         const int32_t *const table = a.page_table + static_cast<int64_t>(w.b) * a.max_pages;
@@ -764,19 +767,14 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             if (L::kGroups == 2 && (cnt & 1u) != static_cast<uint32_t>(group)) continue;
             const int first = max(0, w.s.ctx - tt * kTile), stop = min(kTile, w.s.len - tt * kTile);
             const uint32_t ss = cnt % L::NS, slot = cnt % L::NV;
-            float ks = 0.0f, vs = 0.0f, top = 0.0f;
+            float ks = 0.0f, vs = 0.0f;
             if (L::kLandScales) {
                 if (!(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
                 const float *const land = reinterpret_cast<const float *>(smem + L::oSSc + ss * 1024);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {   // every warp forms the tile's largest: no barrier
-                    const float v = k * 32 + lane < stop ? land[128 + k * 32 + lane] : 0.0f;
-                    top = fmaxf(top, fabsf(v));
-                    if (k == cw) vs = v;
+                if (j < stop) {
+                    ks = land[j];
+                    vs = land[128 + j];
                 }
-                if (j < stop) ks = land[j];
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             } else {
                 ks = ks_next;
                 vs = vs_next;
@@ -793,7 +791,15 @@ __device__ __forceinline__ void convert_values(const TreeArgs &a, Walk &w, uint8
             scale_s[sb * 384 + j] = ks;
             scale_s[sb * 384 + 128 + j] = vs * kWeightUp;
             scale_s[sb * 384 + 256 + j] = log2_scale(vs);
-            if (L::kLandScales && lane == 0) top_s[sb] = log2_scale(top);   // at or above all of the tile's
+            if (L::kLandScales) {
+                if (__any_sync(0xFFFFFFFFu, fabsf(vs) > top)) {
+                    top = fmaxf(top, fabsf(vs));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    top_log = log2_scale(top);
+                }
+                if (lane == 0) top_s[sb * 4 + cw] = top_log;
+            }
             if (odd_scale) atomicOr(&bad[(tt & 1) * 4 + cw], 1u << lane);
             warp_arrive(bar(L::bCF + sb));
             if (!L::kLandScales && !(ok = wait_for(bar(L::bSF + ss), (cnt / L::NS) & 1u, abort_flag, a.err, a.wait_limit))) break;
