@@ -610,7 +610,8 @@ moe_status_t moe_rope(const moe_heads_t *q, const moe_heads_t *q_out, const moe_
  * (for every token, whatever its slot); a token whose position is outside the table is recorded
  * and nothing of it is written.  e4m3: scale = amax / 448 over the row (1 where that is 0; NaN
  * elements do not count), codes of the fp32 quotient x / scale, rounded to nearest, ties to even.
- * tokens >= 0; k and v [tokens, cache heads, cache dim].  ws may be NULL.  Asynchronous on s.
+ * tokens >= 0; k and v [tokens, cache heads, cache dim]; the rows that are read do not overlap what is
+ * written (q_out may be q itself).  ws may be NULL.  Asynchronous on s.
  */
 moe_status_t moe_kv_write(const moe_kv_cache_t *cache, const moe_heads_t *k, const moe_heads_t *v,
                           const int32_t *slots, int32_t tokens, const moe_rotary_t *rotary, const moe_heads_t *q,
@@ -627,8 +628,9 @@ moe_status_t moe_kv_read(const moe_kv_cache_t *cache, const int32_t *slots, int3
 /* Largest number of drafted tokens of one sequence (the bits of a tree mask). */
 #define MOE_MAX_TREE_TOKENS 64
 
-/* Bytes of device workspace moe_tree_attention needs (zero it once with moe_workspace_init):
- * 256 bytes with the error word, and the partial results of sequences that several CTAs share. */
+/* Bytes of device workspace moe_tree_attention needs on the current device (zero it once with
+ * moe_workspace_init): 256 bytes with the error word, and the partial results of sequences that
+ * several CTAs share, by the device's number of SMs. */
 size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t tokens, int32_t seqs, int32_t q_heads);
 
 /*
@@ -652,8 +654,11 @@ size_t moe_tree_attention_workspace_bytes(const moe_kv_cache_t *cache, int32_t t
  * bf16 q over a bf16 or e4m3 cache with dim <= 128 runs on the tensor cores when q is 16-byte
  * aligned with strides that are multiples of 8 elements, as out, page is a multiple of 8 and the
  * scales are 16-byte aligned; all else on
- * the CUDA cores in fp32.  tokens >= 0; 1 <= max_tokens <= 64; q heads a multiple of the cache's,
- * at most 64 times as many.  Asynchronous on s.
+ * the CUDA cores in fp32, where a long context is not divided among CTAs and takes long.  The bound
+ * max_tokens decides, with max_pages, how the tensor cores are used: a call with max_tokens times
+ * (q heads / cache heads) of at most 64 runs a kernel for few rows, and a page table of little more than
+ * the contexts' width lets short ones go undivided; a loose bound is right and slower.  tokens >= 0;
+ * 1 <= max_tokens <= 64; q heads a multiple of the cache's, at most 64 times as many.  Asynchronous on s.
  */
 moe_status_t moe_tree_attention(const moe_kv_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,
                                 const int32_t *q_start, const int32_t *ctx, const int32_t *page_table,

@@ -850,7 +850,11 @@ def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: 
     tokens of all sequences, q_start int32 [seqs + 1] their bounds, ctx int32 [seqs] the cached positions
     before them, page_table int32 [seqs, max pages]; mask int64 [tokens], bit j of a token's word set
     where it sees drafted token j of its sequence (None: a chain); scale defaults to dim^-0.5.  Returns
-    out, or (out, lse) with return_lse."""
+    out, or (out, lse) with return_lse.
+
+    max_tokens bounds a sequence's tokens and chooses the kernel: with max_tokens times the query heads of
+    a key head at most 64, that for few rows, which is faster for them.  Without ws (tree_attention_workspace)
+    each call allocates and clears one of tens of megabytes."""
     device, dim = cache.index, cache.dim
     if device != _current_device():
         return _there(cache.k, tree_attention, cache, q, q_start, ctx, page_table, mask, scale, max_tokens, out, lse, return_lse, ws)

@@ -8,10 +8,12 @@
 // and written once.
 //
 // Rows of 128 channels, against the copy bandwidth of 6.79 TB/s: 16381 tokens x 40 rows of bf16
-// rotated 56.9 us (5.98 TB/s), 16300 x 16 rows written as e4m3 codes 20.9 us (4.86), 8190 x 40
-// rows rotated and 8 of them written 30.3 us (5.68), 131000 x 16 rows of codes read back as bf16
+// rotated 56.4 us (6.02 TB/s), 16300 x 16 rows written as e4m3 codes 20.7 us (4.89), 8190 x 40
+// rows rotated and 8 of them written 30.1 us (5.72), 131000 x 16 rows of codes read back as bf16
 // 129 us (6.29); a pass of a few tokens 2.3 to 3.1 us, the latency of its chain of loads (position
-// or slot, then table row, then channels).
+// or slot, then table row, then channels).  fp32 rows, whose kernels spill 60-150 bytes a thread under
+// launch bounds chosen for narrower ones: 16381 x 40 rotated 110 us (6.12), 131000 x 8 rows of 128
+// written to an fp32 cache 176 us (6.11) and read back 204 us (5.27).
 #include "cache_args.cuh"
 #include "common.cuh"
 

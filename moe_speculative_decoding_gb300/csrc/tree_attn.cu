@@ -37,9 +37,11 @@
 //
 // Measured: 8 sequences of 4001-8201 positions, trees of 64 tokens, 8 query heads to each of 4 key
 // heads, 128 channels, bf16: 64 us, 753 TFLOP/s.  A tile of K and V serves 256 rows in 3,000 cycles,
-// where its four products need 2,050 and its 32,768 exponentials as many; an item's beginning
-// (queries, 5,000-8,000 cycles) and end (4,000-5,000) come on top.  128 rows over 60-65 thousand
-// positions of e4m3 codes: 167 us.
+// where its four products need 2,050 and its 32,768 exponentials 1,020 (a loop of them alone issues 32 a
+// cycle and SM); the rest is the turns and what else a weight takes.  An item's beginning (queries,
+// 5,000-8,000 cycles) and end (4,000-5,000) come on top, and the joining kernel: 53-54 and 17-20 us
+// one after the other under the profiler.  128 rows over 60-65 thousand positions of e4m3 codes: 167 us,
+// twice the floor of their bytes.
 //
 // Every wait is bounded (an abort flag, MOE_ERR_DEVICE_TIMEOUT, then copies and products are
 // drained and TMEM is freed).
@@ -771,8 +773,9 @@ bool tree_attn_supports(const moe_kv_cache_t &c, const moe_heads_t &q, const moe
            (c.dtype == MOE_BF16 || ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15u) == 0);
 }
 
-// A workspace serves whichever kernel a call runs on, on any device: room for kMaxCtas CTAs' parts
-// is more than most calls touch, so it goes by this device's SMs.
+// A workspace serves whichever kernel a call runs on, on the device that is current when its size is
+// asked for (room for kMaxCtas CTAs' parts would be more than any call there touches): a larger
+// device refuses it.
 size_t tree_attn_part_bytes(int dim) {
     int dev = 0;
     int sms = 152;
@@ -806,9 +809,9 @@ cudaError_t launch_tree_attn(TreeArgs a, cudaStream_t s, bool pdl) {
     // no more CTAs than the page tables could fill with tiles
     const int ctas = static_cast<int>(std::min<long long>(sms, items * item_tiles));
     // Up to 64 rows: positions as the M operand.  Few rows against many, 60-65 thousand positions of 4
-    // sequences, 8 heads of 128: e4m3 16 rows 97 us against 164, 64 rows 154 against 165; bf16 16 rows
-    // 159 against 164, 32 rows 161 against 165, 64 rows 169 against 166; 16 short contexts of e4m3 with
-    // 20 rows 37.8 against 56.
+    // sequences, 8 heads of 128: e4m3 16 rows 90 us against 159, 32 rows 100 against 160, 64 rows 155 against
+    // 162; bf16 16 rows 155 against 160, 32 rows 156 against 161, 64 rows 165 against 163; 16 short contexts
+    // of e4m3 with 20 rows 36.8 against 57.5.
     if (a.max_tokens * a.group <= kNarrowRows) {
         e = launch_tree_narrow(a, dev, ctas, rows, tm_k, tm_v, s, pdl);
         if (e != cudaSuccess || a.undivided) return e;

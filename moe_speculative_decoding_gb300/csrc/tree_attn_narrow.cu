@@ -1,5 +1,6 @@
 // tree_attn_narrow.cu -- tree attention on the tensor cores for up to 64 rows (token, query head of
-// the group) of a cache head: the ordinary verification pass, and single tokens.
+// the group) of a cache head, by the caller's bound on a sequence's tokens: short chains, small trees
+// and single tokens.
 //
 // Bound: the cache's bytes; 4 * dim flops per position, row and head leave the tensor cores far from
 // their limit, so what counts is that nothing else of a tile costs its rows twice: padding 8 or 20
@@ -22,7 +23,7 @@
 //
 // Measured, 8 cache heads of 128 channels, 60-65 thousand positions of 4 sequences: bf16 with 16 or 32
 // rows 156-161 us (6.5-6.7 TB/s of the 6.79 of a copy: the cache's bytes bound it), with 64 rows 169;
-// e4m3 with 16 rows 91-98 us (5.4-5.9 TB/s), with 32 rows 104-108, with 64 rows 154: there a tile's
+// e4m3 with 16 rows 90-97 us (5.5-6.0 TB/s), with 32 rows 100-105, with 64 rows 155: there a tile's
 // chain of conversion, weights and products, 1,650 cycles, takes as long as its bytes or longer.
 // One token over 300 positions: 8.2 us, a chain of latencies (lengths, page table, K, scores, V).
 #include "tree_common.cuh"

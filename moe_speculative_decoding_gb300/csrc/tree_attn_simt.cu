@@ -4,6 +4,11 @@
 // maximum and sum.  Serves fp32 queries, heads wider than 128 channels and layouts the
 // tensor-core kernel does not take.
 //
+// For short contexts: the positions are not divided among CTAs, so a long one is one CTA's work for every
+// 16 rows.  16 tokens of two sequences, 32 and 4 heads of 128, pages of 4: 3.1 ms over 4,000 positions;
+// over 115,000 144 ms (fp32 queries the same; heads of 256 291 ms), where the same computation in
+// elementary tensor operations takes 7 and the tensor-core kernel, where it serves, 0.09.
+//
 // A CTA takes 16 rows (token, query head of the group) of one (sequence, cache head) and walks
 // the positions in tiles of 32: the tile's keys are staged in shared memory as fp32, a lane owns
 // one key and forms its dot products with the warp's 4 rows, the softmax statistics go over the
