@@ -607,12 +607,12 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                 if (second) o = fmaf(__uint_as_float(ob[i]), w1_s[c], o);
                 oa[i] = __float_as_uint(o);
             }
-            if (any_bad != 0 && p < a.cache.dim) {   // non-finite values of drafted tokens, for the rows that see them
+            if (any_bad != 0) {   // non-finite values of drafted tokens, for the rows that see them
 #pragma unroll 1
                 for (int tt = max(w.lo, w.s.ctx / kTile); tt < w.hi; ++tt)
 #pragma unroll 1
                     for (int j = 0; j < kTile; ++j) {
-                        if (!(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u)) continue;
+                        if (p >= a.cache.dim || !(bad[(tt & 1) * 4 + j / 32] >> (j & 31) & 1u)) continue;
                         const float v = value_at<F8>(a, w.b, w.hk, tt * kTile + j, p);
                         if (fabsf(v) <= 3.4028234e38f) continue;
                         const int d = tt * kTile + j - w.s.ctx;   // only drafted tokens are marked
@@ -620,8 +620,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_consta
                         for (int i = 0; i < H; ++i)
                             if (mask_s[g * H + i] >> d & 1ull) oa[i] = __float_as_uint(__uint_as_float(oa[i]) + v);
                     }
-                __syncwarp();
             }
+            __syncwarp();   // every lane comes here, also those beyond the head's channels
             if (w.whole) {
                 // two rows at a time: neighbouring lanes trade, and each stores two channels of one row
                 const int odd = lane & 1;
