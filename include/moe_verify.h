@@ -446,7 +446,7 @@ moe_status_t moe_fit_op_times(int32_t count, const int32_t *n, const int32_t *U,
 moe_status_t moe_last_device_error(void *ws, moe_stream_t s, int32_t *code);
 
 /*
- * Sets, for the expert-operation and tree-attention calls issued after it by this process, how
+ * Sets, for the expert-operation, tree-attention and latent-attention calls issued after it by this process, how
  * many SM clock cycles one device pipeline wait (a shared-memory barrier, or another CTA's flag) may take
  * before the call gives up: it then records MOE_ERR_DEVICE_TIMEOUT in the workspace's error
  * word, waits (bounded) for its copies and tensor-core operations in flight, frees its
@@ -664,6 +664,157 @@ moe_status_t moe_tree_attention(const moe_kv_cache_t *cache, const moe_heads_t *
                                 const int32_t *q_start, const int32_t *ctx, const int32_t *page_table,
                                 const uint64_t *mask, int32_t seqs, int32_t tokens, int32_t max_tokens,
                                 int32_t max_pages, float scale, void *ws, size_t ws_bytes, moe_stream_t s);
+
+/* ---------------------------------------------------------------- latent attention
+ *
+ * Attention whose keys and values come from one compressed vector a token, in the absorbed form: the
+ * cache holds for each position a latent of `rank` channels and `rope` rotary channels, read by all
+ * heads alike.  With K_h = W_h c and V_h = U_h c, a query q_h = [n_h | r_h] scores
+ * <W_h^T n_h, c> + <r_h, k_r>, and sum_p w_p U_h c_p = U_h sum_p w_p c_p: the queries come here
+ * multiplied by W_h^T, and the outputs leave before U_h.
+ */
+
+/* A paged cache of latent rows: position `r` of page `b` starts at element b * page_stride +
+ * r * token_stride of rows, rank latent channels and then rope rotary ones, contiguous.  dtype
+ * MOE_F32 or MOE_BF16; rows 16-byte aligned, strides, rank and rope multiples of 16 bytes;
+ * 1 <= rank <= 512, 1 <= rope <= 128, page >= 1, pages * page < 2^31. */
+typedef struct {
+    void *rows;                       /* [dev] */
+    int64_t page_stride, token_stride;
+    int32_t dtype, rank, rope, page, pages;
+    int32_t reserved;                 /* 0 */
+} moe_latent_cache_t;
+
+/*
+ * Writes the rows of `tokens` tokens into cache slots[t] (int32 [dev]; slot s is row s % page of page
+ * s / page): the latent channels, normalised when norm is not NULL,
+ *     y_i = c_i norm_i / sqrt(mean_j(c_j^2) + eps),
+ * and the rotary channels, turned by the token's position when rotary is not NULL (rotary->rot
+ * <= rope; channels from rot on are copied), in fp32, rounded once to the cache's type.  When q is not
+ * NULL (with rotary), its rows of rope channels are rotated into q_out in the same launch, for every
+ * token, whatever its slot.  A negative slot takes nothing; one beyond the cache is recorded and takes
+ * nothing; slots that are not negative must differ.  A token whose position is outside the table is
+ * recorded and nothing of it is written.
+ *   latent [tokens, 1, rank] and k_rope [tokens, 1, rope] (heads = 1); norm [dev] fp32 [rank] or NULL;
+ *   eps >= 0, finite; q and q_out [tokens, heads, rope].  The rows that are read do not overlap what
+ *   is written (q_out may be q itself).  tokens >= 0; ws may be NULL.  Asynchronous on s.
+ */
+moe_status_t moe_latent_write(const moe_latent_cache_t *cache, const moe_heads_t *latent, const moe_heads_t *k_rope,
+                              const int32_t *slots, int32_t tokens, const float *norm, float eps,
+                              const moe_rotary_t *rotary, const moe_heads_t *q, const moe_heads_t *q_out, void *ws,
+                              moe_stream_t s);
+
+/* Bytes of device workspace moe_latent_attention needs on the current device (zero it once with
+ * moe_workspace_init): 256 bytes with the error word, and the partial results of what several CTAs
+ * share, by the device's number of SMs. */
+size_t moe_latent_attention_workspace_bytes(const moe_latent_cache_t *cache, int32_t tokens, int32_t seqs, int32_t heads);
+
+/*
+ * Attention of the drafted tokens of `seqs` sequences over a latent cache: sequences, page table, masks
+ * and what a token sees are those of moe_tree_attention, and so is what a call does with lengths
+ * that do not fit and pages outside the cache.
+ *     s_p = scale * <q, row_p>,  lse = ln sum_p e^(s_p),  out = sum_p e^(s_p - lse) latent_p
+ * over the positions seen; a token that sees none gets out = 0, lse = -inf.  What stands in a position
+ * that a token does not see, infinities and NaN included, does not reach it; a non-finite latent
+ * that it sees makes those channels of its output, or all of them, NaN.
+ *   q [tokens, heads, rank + rope], out [tokens, heads, rank] of one type; lse [dev] fp32
+ *   [tokens, heads] or NULL; q_start, ctx, page_table, mask as for moe_tree_attention; scale > 0.
+ * bf16 q over a bf16 cache with rope <= 64 runs on the tensor cores when q and out are 16-byte aligned with
+ * strides that are multiples of 8 elements and page is a multiple of 8; the weights e^(s_p - m) are
+ * rounded to bf16 there for the product with the latents.  All else runs on the CUDA cores in fp32,
+ * where a long context is not divided among CTAs and takes long.  The bound max_tokens chooses, with heads,
+ * how many rows a tile of the cache serves at a time (16, 32 or 64); a loose bound is right and slower.
+ * tokens >= 0; 1 <= max_tokens <= 64; 1 <= heads <= 1024.  Asynchronous on s.
+ */
+moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,
+                                  const int32_t *q_start, const int32_t *ctx, const int32_t *page_table,
+                                  const uint64_t *mask, int32_t seqs, int32_t tokens, int32_t max_tokens,
+                                  int32_t max_pages, float scale, void *ws, size_t ws_bytes, moe_stream_t s);
+
+/* ---------------------------------------------------------------- pages of a cache
+ *
+ * Sequences that share pages: a pool counts each page's holders, and the calls below fork, extend,
+ * compact and free sequences on the device, without a word to the host, for all layers' caches at once.
+ * The page table of a pool is the page_table of the attention calls.
+ *
+ * Sequence b holds held[b] pages, table[b][0 .. held[b]), and has its tokens in the first positions of
+ * them; entries beyond are left as they were.  Pages behind the one with its last token are its own
+ * (the calls see to that).  Device-only problems (ids, lengths, pages or paths out of range) are
+ * recorded as MOE_ERR_BAD_ID in the error word of ws, and the sequence concerned is left as it was.
+ */
+
+/* The pool, in memory the caller owns; refs and held all zero: every page free, nothing held. */
+typedef struct {
+    int32_t *refs;                    /* [dev] [pages]: holders of a page, 0: free */
+    int32_t *table;                   /* [dev] [seqs, max_pages] */
+    int32_t *held;                    /* [dev] [seqs] */
+    int32_t pages, page, seqs, max_pages;
+} moe_page_pool_t;
+
+/* The caches whose rows live in the pool's pages, one of each layer, every one with the pool's pages
+ * and page; either list may be empty (NULL, 0). */
+typedef struct {
+    const moe_kv_cache_t *kv;          /* [host] [kv_count] */
+    const moe_latent_cache_t *latent;  /* [host] [latent_count] */
+    int32_t kv_count, latent_count;
+} moe_page_caches_t;
+
+/* Most sequences of moe_pages_reserve and pairs of moe_pages_fork. */
+#define MOE_MAX_POOL_SEQS 1024
+
+/* Bytes of device workspace of the calls below (zero it once with moe_workspace_init): 256 bytes with
+ * the error word, and lists of pages and sequences. */
+size_t moe_pages_workspace_bytes(const moe_page_pool_t *pool);
+
+/*
+ * Makes room for need[b] more tokens of every sequence after its length[b]: it then holds
+ * ceil((length[b] + need[b]) / page) pages (those it had, if they are more).  New pages are the lowest
+ * free ones, sequences in order.  If position length[b] lies inside a page that others hold too, and
+ * need[b] > 0, that page is replaced by a new one and its rows below the length are copied, in every
+ * cache; of several sequences that share it in one call, each in order takes a copy as long as
+ * others still hold it.  From the first sequence on that the free pages do not suffice for, none that
+ * needs a page gets any: got[b] = 0 and it is left as it was, otherwise 1 (0 also for one that is
+ * recorded).
+ *   length, need [dev] int32 [seqs]: need[b] >= 0, 0 <= length[b] <= held[b] * page; got [dev] int32
+ *   [seqs] or NULL.  seqs <= MOE_MAX_POOL_SEQS.  ws of moe_pages_workspace_bytes.  Asynchronous on s.
+ */
+moe_status_t moe_pages_reserve(const moe_page_pool_t *pool, const int32_t *length, const int32_t *need, int32_t *got,
+                               const moe_page_caches_t *caches, void *ws, size_t ws_bytes, moe_stream_t s);
+
+/*
+ * Gives sequence dst[i] the pages of the first length[src[i]] tokens of sequence src[i], which it shares
+ * from then on, and that length; dst[i] must hold nothing, and of equal dst the first counts and the
+ * others are recorded.  All
+ * sequences are read as the call finds them.  Nothing is copied: moe_pages_reserve does that where a
+ * shared page is to be written.
+ *   src, dst [dev] int32 [count], length [dev] int32 [seqs], read and written.  0 <= count <=
+ *   MOE_MAX_POOL_SEQS.  Asynchronous on s.
+ */
+moe_status_t moe_pages_fork(const moe_page_pool_t *pool, const int32_t *src, const int32_t *dst, int32_t count,
+                            int32_t *length, void *ws, size_t ws_bytes, moe_stream_t s);
+
+/*
+ * After a verification pass: of the tokens drafted behind ctx[b] cached ones, those path[b][0 ..
+ * count[b]) are kept, and become the positions ctx[b], ctx[b] + 1, ...: row ctx[b] + path[b][i] moves to
+ * ctx[b] + i in every cache, bit by bit.  after[b] = ctx[b] + count[b], and pages beyond
+ * ceil(after[b] / page) are given up.  A negative count leaves the sequence alone (after[b] = ctx[b]).
+ *   path [dev] int32 [seqs, max_path], 0 <= path[b][0] < path[b][1] < ..., or NULL for the first count[b]
+ *   tokens (nothing moves); count [dev] int32 [seqs], at most max_path; after [dev] int32 [seqs] or
+ *   NULL, may be ctx itself.  ctx[b] + path[b][i] must lie in the pages held; the pages written must be
+ *   the sequence's own, as moe_pages_reserve leaves them.  1 <= max_path <= MOE_MAX_TREE_TOKENS.
+ *   Asynchronous on s.
+ */
+moe_status_t moe_pages_accept(const moe_page_pool_t *pool, const int32_t *ctx, const int32_t *path, const int32_t *count,
+                              int32_t max_path, int32_t *after, const moe_page_caches_t *caches, void *ws,
+                              size_t ws_bytes, moe_stream_t s);
+
+/*
+ * Sequences ids[i] (int32 [dev] [count]; a negative one names none, one may be named twice) give up all
+ * their pages; with length [dev] int32 [seqs], which may be NULL, their length becomes 0.  Asynchronous
+ * on s.
+ */
+moe_status_t moe_pages_free(const moe_page_pool_t *pool, const int32_t *ids, int32_t count, int32_t *length, void *ws,
+                            size_t ws_bytes, moe_stream_t s);
 
 #ifdef __cplusplus
 }

@@ -75,6 +75,24 @@ class Rotary(ctypes.Structure):
                [(f, ctypes.c_int32) for f in ("table_positions", "rot", "interleaved", "inverse")]
 
 
+class LatentDesc(ctypes.Structure):
+    """moe_latent_cache_t."""
+    _fields_ = [("rows", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)] + \
+               [(f, ctypes.c_int32) for f in ("dtype", "rank", "rope", "page", "pages", "reserved")]
+
+
+class PoolDesc(ctypes.Structure):
+    """moe_page_pool_t."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("refs", "table", "held")] + \
+               [(f, ctypes.c_int32) for f in ("pages", "page", "seqs", "max_pages")]
+
+
+class CachesDesc(ctypes.Structure):
+    """moe_page_caches_t."""
+    _fields_ = [("kv", ctypes.c_void_p), ("latent", ctypes.c_void_p), ("kv_count", ctypes.c_int32),
+                ("latent_count", ctypes.c_int32)]
+
+
 class ThresholdIn(ctypes.Structure):
     _fields_ = [(f, ctypes.c_double) for f in ("mW", "B_k", "beta_1", "tau_1", "dD_over_betaD", "dphi")]
 
@@ -94,7 +112,8 @@ EXPORTED = ("moe_abi_version", "moe_status_str", "moe_workspace_bytes", "moe_wor
             "moe_union_cost_workspace_bytes", "moe_union_cost", "moe_expert_op_dedup_ids",
             "moe_expert_op_dedup_ids_fp8", "moe_read_probe", "moe_set_wait_limit", "moe_rope_frequencies",
             "moe_rope_table", "moe_rope", "moe_kv_write", "moe_kv_read", "moe_tree_attention_workspace_bytes",
-            "moe_tree_attention")
+            "moe_tree_attention", "moe_latent_write", "moe_latent_attention_workspace_bytes", "moe_latent_attention",
+            "moe_pages_workspace_bytes", "moe_pages_reserve", "moe_pages_fork", "moe_pages_accept", "moe_pages_free")
 
 _lib = None
 
@@ -158,6 +177,14 @@ def lib():
         "moe_kv_read": ([P, P, I32, P, P, P, P], I32),
         "moe_tree_attention_workspace_bytes": ([P, I32, I32, I32], SZ),
         "moe_tree_attention": ([P, P, P, P, P, P, P, P, I32, I32, I32, I32, ctypes.c_float, P, SZ, P], I32),
+        "moe_latent_write": ([P, P, P, P, I32, P, ctypes.c_float, P, P, P, P, P], I32),
+        "moe_latent_attention_workspace_bytes": ([P, I32, I32, I32], SZ),
+        "moe_latent_attention": ([P, P, P, P, P, P, P, P, I32, I32, I32, I32, ctypes.c_float, P, SZ, P], I32),
+        "moe_pages_workspace_bytes": ([P], SZ),
+        "moe_pages_reserve": ([P, P, P, P, P, P, SZ, P], I32),
+        "moe_pages_fork": ([P, P, P, I32, P, P, SZ, P], I32),
+        "moe_pages_accept": ([P, P, P, P, I32, P, P, P, SZ, P], I32),
+        "moe_pages_free": ([P, P, I32, P, P, SZ, P], I32),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -239,7 +266,7 @@ def last_device_error(ws: torch.Tensor) -> int:
 
 
 def set_wait_limit(cycles: int) -> None:
-    """moe_set_wait_limit: SM cycles one device pipeline wait of later expert and tree-attention calls may take
+    """moe_set_wait_limit: SM cycles one device pipeline wait of later expert and attention calls may take
     before the call records MOE_ERR_DEVICE_TIMEOUT and returns (0: the default; infrastructure)."""
     _check(lib().moe_set_wait_limit(int(cycles)), "moe_set_wait_limit")
 
@@ -880,3 +907,247 @@ def tree_attention(cache: KVCache, q: torch.Tensor, q_start: torch.Tensor, ctx: 
     if code:
         raise MoeError(code, "moe_tree_attention")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- latent attention
+class LatentCache:
+    """A paged cache of latent rows (moe_latent_cache_t) over a tensor the caller owns: rows [pages, page,
+    rank + rope] (fp32 or bf16, dense channels), the latent of a token in its first rank channels and its
+    rotary key in the others."""
+
+    def __init__(self, rows: torch.Tensor, rank: int):
+        if not rows.is_cuda:
+            raise TypeError("rows must be a CUDA tensor")
+        code = _HEAD_TYPES.get(rows.dtype)
+        if code is None:
+            raise TypeError(f"rows must be float32 or bfloat16, got {rows.dtype}")
+        if rows.dim() != 3 or rows.stride(2) != 1:
+            raise ValueError("rows must have shape (pages, page, rank + rope) and dense channels")
+        if not 0 < rank < rows.shape[2]:
+            raise ValueError(f"rank must leave rotary channels of {rows.shape[2]}, got {rank}")
+        self.rows, self.rank, self.rope = rows, rank, rows.shape[2] - rank
+        self.pages, self.page = rows.shape[:2]
+        self.desc = LatentDesc(rows.data_ptr(), *rows.stride()[:2], code, rank, self.rope, self.page, self.pages, 0)
+        self.device, self.index = rows.device, rows.get_device()
+        self.address = ctypes.addressof(self.desc)
+
+
+def latent_cache(pages: int, page: int, rank: int, rope: int, dtype: str = "bf16", device=None) -> LatentCache:
+    """A zeroed latent cache of `pages` pages of `page` tokens: dtype "bf16" or "f32"."""
+    t = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    return LatentCache(torch.zeros((pages, page, rank + rope), dtype=t, device=device or "cuda"), rank)
+
+
+def _rows(t: torch.Tensor, name: str, tokens: int, dim: int, device: int) -> bytes:
+    """The descriptor of a [tokens, dim] tensor on `device`: any token stride, dense channels."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError(f"{name} must be a CUDA tensor on device {device}")
+    code = _HEAD_TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.shape != (tokens, dim):
+        raise ValueError(f"{name} must have shape {(tokens, dim)}, got {tuple(t.shape)}")
+    st, sd = t.stride()
+    if sd != 1 and dim > 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return _pack_heads(t.data_ptr(), st, 0, 1, code)
+
+
+def latent_write(cache: LatentCache, latent: torch.Tensor, k_rope: torch.Tensor, slots: torch.Tensor, norm=None,
+                 eps: float = 1e-6, q=None, positions=None, table=None, interleaved: bool = False, q_out=None, ws=None):
+    """moe_latent_write: latents [tokens, rank] and rotary keys [tokens, rope] into the cache's slots int32
+    [tokens] (a negative slot takes nothing).  With norm (fp32 [rank]) the latents are RMS-normalised and
+    multiplied by it; with positions and table the rotary keys are rotated, and q [tokens, heads, rope], the
+    queries' rotary channels, when given, into q_out, which is returned (None without q).  ws (any
+    workspace) records slots and positions out of range."""
+    device = cache.index
+    if device != _current_device():
+        return _there(cache.rows, latent_write, cache, latent, k_rope, slots, norm, eps, q, positions, table, interleaved, q_out, ws)
+    tokens, rope = latent.shape[0], cache.rope
+    dl = _rows(latent, "latent", tokens, cache.rank, device)
+    dk = _rows(k_rope, "k_rope", tokens, rope, device)
+    rot = dq = dqo = None
+    if (table is None) != (positions is None):
+        raise ValueError("rotation takes both positions and table")
+    if table is not None:
+        rot = _rotary(table, positions, tokens, interleaved, False, device)
+    if q is not None:
+        if table is None:
+            raise ValueError("q is only rotated: it takes positions and table")
+        heads = q.shape[1]
+        dq = _heads(q, "q", tokens, heads, rope, device)
+        if q_out is None:
+            q_out, dqo = _new_heads(q, tokens, heads, rope)
+        else:
+            dqo = _heads(q_out, "q_out", tokens, heads, rope, device)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    code = (_lib or lib()).moe_latent_write(cache.address, dl, dk, _flat(slots, "slots", torch.int32, (tokens,), device), tokens,
+                                            None if norm is None else _flat(norm, "norm", torch.float32, (cache.rank,), device),
+                                            eps, rot, dq, dqo, _ws_ptr(ws, device), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_latent_write")
+    return q_out
+
+
+def latent_attention_workspace(cache: LatentCache, tokens: int, seqs: int, heads: int) -> torch.Tensor:
+    """A zeroed workspace for latent_attention calls of up to this many tokens and sequences."""
+    with torch.cuda.device(cache.index):   # the size goes by its number of SMs
+        nbytes = int(lib().moe_latent_attention_workspace_bytes(cache.address, tokens, seqs, heads))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=cache.device)
+    _call("moe_workspace_init", cache.device, ws.data_ptr(), nbytes, _stream(cache.device))
+    return ws
+
+
+def latent_attention(cache: LatentCache, q: torch.Tensor, q_start: torch.Tensor, ctx: torch.Tensor, page_table: torch.Tensor,
+                     scale: float, mask=None, max_tokens: int = MAX_TREE_TOKENS, out=None, lse=None,
+                     return_lse: bool = False, ws=None):
+    """moe_latent_attention: attention of drafted tokens over a latent cache in the absorbed form.  q [tokens,
+    heads, rank + rope] holds each head's query multiplied by its key matrix, and its rotary channels;
+    q_start, ctx, page_table and mask are tree_attention's.  scale has no default: it goes by the width
+    of the queries before they were multiplied.  Returns out [tokens, heads, rank], to be multiplied
+    by each head's value matrix, or (out, lse) with return_lse.
+
+    max_tokens bounds a sequence's tokens and chooses, with heads, how many rows a tile of the cache serves.
+    Without ws (latent_attention_workspace) each call allocates and clears one of tens of megabytes."""
+    device = cache.index
+    if device != _current_device():
+        return _there(cache.rows, latent_attention, cache, q, q_start, ctx, page_table, scale, mask, max_tokens, out, lse,
+                      return_lse, ws)
+    tokens, heads = q.shape[0], q.shape[1]
+    seqs, max_pages = page_table.shape
+    dq = _heads(q, "q", tokens, heads, cache.rank + cache.rope, device)
+    if out is None:
+        out, do = _new_heads(q, tokens, heads, cache.rank)
+    else:
+        do = _heads(out, "out", tokens, heads, cache.rank, device)
+    if return_lse and lse is None:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=cache.device)
+    if ws is None:
+        ws = latent_attention_workspace(cache, tokens, seqs, heads)
+    code = (_lib or lib()).moe_latent_attention(
+        cache.address, dq, do,
+        None if lse is None else _flat(lse, "lse", torch.float32, (tokens, heads), device),
+        _flat(q_start, "q_start", torch.int32, (seqs + 1,), device), _flat(ctx, "ctx", torch.int32, (seqs,), device),
+        _flat(page_table, "page_table", torch.int32, (seqs, max_pages), device),
+        None if mask is None else _flat(mask, "mask", torch.int64, (tokens,), device),
+        seqs, tokens, max_tokens, max_pages, scale, _ws_ptr(ws, device), ws.numel(), _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_latent_attention")
+    return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------- pages of a cache
+class PagePool:
+    """The pages of some layers' caches (KVCache or LatentCache, equal numbers of pages and tokens a page) and
+    who holds them (moe_page_pool_t), over tensors the caller owns: refs int32 [pages] (holders of a page),
+    table int32 [seqs, max pages] (the page_table of the attention calls), held int32 [seqs] (pages a
+    sequence holds).  All zero: every page is free.  ws is the calls' workspace; its error word records
+    ids, lengths and paths out of range."""
+
+    def __init__(self, caches, refs: torch.Tensor, table: torch.Tensor, held: torch.Tensor):
+        self.caches, self.refs, self.table, self.held = list(caches), refs, table, held
+        if not self.caches:
+            raise ValueError("a pool needs a cache")
+        for c in self.caches:
+            if not isinstance(c, (KVCache, LatentCache)):
+                raise TypeError("caches must be KVCache or LatentCache")
+        first = self.caches[0]
+        self.pages, self.page, self.device, self.index = first.pages, first.page, first.device, first.index
+        for c in self.caches:
+            if (c.pages, c.page, c.index) != (self.pages, self.page, self.index):
+                raise ValueError("caches must have equal pages and lie on one device")
+        index = self.index
+        _flat(refs, "refs", torch.int32, (self.pages,), index)
+        if table.dim() != 2:
+            raise ValueError("table must have shape (seqs, max pages)")
+        self.seqs, self.max_pages = table.shape
+        self.desc = PoolDesc(refs.data_ptr(), _flat(table, "table", torch.int32, table.shape, index),
+                             _flat(held, "held", torch.int32, (self.seqs,), index), self.pages, self.page, self.seqs, self.max_pages)
+        kv = [c.desc for c in self.caches if isinstance(c, KVCache)]
+        latent = [c.desc for c in self.caches if isinstance(c, LatentCache)]
+        self._kv, self._latent = (CacheDesc * max(len(kv), 1))(*kv), (LatentDesc * max(len(latent), 1))(*latent)
+        self._caches = CachesDesc(ctypes.addressof(self._kv), ctypes.addressof(self._latent), len(kv), len(latent))
+        self.address, self.caches_address = ctypes.addressof(self.desc), ctypes.addressof(self._caches)
+        self.ws_bytes = int(lib().moe_pages_workspace_bytes(self.address))
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        _call("moe_workspace_init", self.device, self.ws.data_ptr(), self.ws_bytes, _stream(self.device))
+
+
+def page_pool(caches, seqs: int, max_pages: int) -> PagePool:
+    """A pool over these caches with every page free."""
+    caches = list(caches)
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=caches[0].device)
+    return PagePool(caches, z(caches[0].pages), z(seqs, max_pages), z(seqs))
+
+
+def pages_reserve(pool: PagePool, length: torch.Tensor, need: torch.Tensor, got=None) -> torch.Tensor:
+    """moe_pages_reserve: pages for need int32 [seqs] more tokens of every sequence after its length int32 [seqs],
+    the lowest free ones, sequences in order; a shared page that would be written is copied in every
+    cache.  Returns got int32 [seqs]: 1 where the sequence has its pages, 0 where they ran out."""
+    device = pool.index
+    if device != _current_device():
+        return _there(pool.refs, pages_reserve, pool, length, need, got)
+    shape = (pool.seqs,)
+    if got is None:
+        got = torch.empty(shape, dtype=torch.int32, device=pool.device)
+    code = (_lib or lib()).moe_pages_reserve(pool.address, _flat(length, "length", torch.int32, shape, device),
+                                             _flat(need, "need", torch.int32, shape, device),
+                                             _flat(got, "got", torch.int32, shape, device), pool.caches_address,
+                                             pool.ws.data_ptr(), pool.ws_bytes, _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_pages_reserve")
+    return got
+
+
+def pages_fork(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, length: torch.Tensor) -> None:
+    """moe_pages_fork: sequences dst int32 [n], which hold nothing, share the pages of sequences src int32 [n] and
+    take their length (length int32 [seqs] is read and written)."""
+    device = pool.index
+    if device != _current_device():
+        return _there(pool.refs, pages_fork, pool, src, dst, length)
+    n = src.shape[0]
+    code = (_lib or lib()).moe_pages_fork(pool.address, _flat(src, "src", torch.int32, (n,), device),
+                                          _flat(dst, "dst", torch.int32, (n,), device), n,
+                                          _flat(length, "length", torch.int32, (pool.seqs,), device),
+                                          pool.ws.data_ptr(), pool.ws_bytes, _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_pages_fork")
+
+
+def pages_accept(pool: PagePool, ctx: torch.Tensor, path, count: torch.Tensor, after=None) -> torch.Tensor:
+    """moe_pages_accept: of the tokens drafted behind ctx int32 [seqs] those path int32 [seqs, max path] names (ascending,
+    the first count int32 [seqs] of a row; None: the first ones) are kept: their rows become consecutive
+    in every cache, pages behind them are given up.  A negative count leaves a sequence alone.  Returns
+    after int32 [seqs], the new lengths (may be ctx itself)."""
+    device = pool.index
+    if device != _current_device():
+        return _there(pool.refs, pages_accept, pool, ctx, path, count, after)
+    shape = (pool.seqs,)
+    if after is None:
+        after = torch.empty(shape, dtype=torch.int32, device=pool.device)
+    if path is not None and path.dim() != 2:
+        raise ValueError("path must have shape (seqs, max path)")
+    most = MAX_TREE_TOKENS if path is None else path.shape[1]
+    code = (_lib or lib()).moe_pages_accept(pool.address, _flat(ctx, "ctx", torch.int32, shape, device),
+                                            None if path is None else _flat(path, "path", torch.int32, (pool.seqs, most), device),
+                                            _flat(count, "count", torch.int32, shape, device), most,
+                                            _flat(after, "after", torch.int32, shape, device), pool.caches_address,
+                                            pool.ws.data_ptr(), pool.ws_bytes, _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_pages_accept")
+    return after
+
+
+def pages_free(pool: PagePool, ids: torch.Tensor, length=None) -> None:
+    """moe_pages_free: sequences ids int32 [n] (negative: none) give up their pages; length int32 [seqs], when given,
+    becomes 0 for them."""
+    device = pool.index
+    if device != _current_device():
+        return _there(pool.refs, pages_free, pool, ids, length)
+    n = ids.shape[0]
+    code = (_lib or lib()).moe_pages_free(pool.address, _flat(ids, "ids", torch.int32, (n,), device), n,
+                                          None if length is None else _flat(length, "length", torch.int32, (pool.seqs,), device),
+                                          pool.ws.data_ptr(), pool.ws_bytes, _raw_stream(device))
+    if code:
+        raise MoeError(code, "moe_pages_free")

@@ -1,0 +1,447 @@
+// pages.cu -- sequences that share the pages of a cache: fork, reserve with copy on write, acceptance of a
+// drafted path with its compaction, free.
+//
+// A page's holders are counted (refs; 0: free).  Which pages a call hands out goes by their numbers and the
+// sequences' order alone, not by the order in which threads run: free pages are found in ascending order and
+// requests are met by a prefix sum, so one CTA does the bookkeeping of reserve and fork (counts are 4 bytes
+// a page: 128 KB for 32,768 pages a step).  The rows move in a second kernel, in all layers at once, as
+// the bits they are: its bound is memory traffic, each row read once and written once.
+#include <algorithm>
+
+#include "common.cuh"
+#include "latent_args.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBook = 1024;          // threads of the bookkeeping CTA
+constexpr int kStep = kBook * 32;    // pages it looks at in a step
+
+// Lists in the workspace: [4] (copies to make), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
+// rows to move), [pages] free pages in order.
+__device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
+__device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
+__device__ __forceinline__ int32_t *table_of(const PageArgs &a, int b) { return a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages; }
+__device__ __forceinline__ bool in_pool(const PageArgs &a, int page) {
+    const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.pages);
+    if (!ok) record_error(a.err, MOE_ERR_BAD_ID);
+    return ok;
+}
+
+// Sum of v over the threads before this one (32-bit sums hold: requests are at most seqs * max_pages),
+// and over all.
+__device__ __forceinline__ int before_me(int v, int *tmp, int &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();   // tmp's last use
+    if (lane == 31) tmp[warp] = x;
+    __syncthreads();
+    int w = tmp[lane];   // 32 warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xFFFFFFFFu, w, 31);
+    return __shfl_sync(0xFFFFFFFFu, w, warp) - tmp[warp] + x - v;
+}
+
+// ------------------------------------------------------------------ reserve
+__global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_constant__ PageArgs a) {
+    __shared__ int shared_s[kBook], tmp[32], copies_s, fail_s;
+    pdl_wait();
+    pdl_trigger();
+    const int b = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const moe_page_pool_t &pool = a.pool;
+    const bool in = b < pool.seqs;
+    int length = 0, need = 0, held = 0, want = 0, first = 0, rows = 0, at = -1, holders = 0;
+    bool bad = false;
+    if (in) {
+        length = a.length[b];
+        need = a.need[b];
+        held = pool.held[b];
+        const long long end = static_cast<long long>(length) + need;
+        bad = need < 0 || length < 0 || held < 0 || held > pool.max_pages || length > static_cast<long long>(held) * pool.page ||
+              end > static_cast<long long>(pool.max_pages) * pool.page;
+        want = held;
+        if (!bad && need > 0) {
+            want = max(held, static_cast<int>((end + pool.page - 1) / pool.page));
+            first = length / pool.page;
+            rows = length - first * pool.page;
+            if (rows > 0) {
+                at = table_of(a, b)[first];
+                bad = static_cast<uint32_t>(at) >= static_cast<uint32_t>(pool.pages);
+                if (!bad) holders = pool.refs[at];
+            }
+        }
+        if (bad) {
+            record_error(a.err, MOE_ERR_BAD_ID);
+            want = held;
+        }
+    }
+    const bool shared = !bad && holders > 1;
+    shared_s[b] = shared ? at : -1;
+    if (b == 0) {
+        copies_s = 0;
+        fail_s = kBook;
+    }
+    __syncthreads();
+    // holders before this sequence that take a copy: its own is needed while others are left
+    auto sharers = [&](int stop) {
+        int n = 0;
+        for (int i = 0; i < stop; ++i) n += shared_s[i] == at;
+        return n;
+    };
+    bool copy = shared && holders - sharers(b) > 1;
+    const int extra = want - held + (copy ? 1 : 0);
+    int total;
+    const int mine = before_me(extra, tmp, total);
+    // the lowest free pages, as many as are asked for
+    int found = 0;
+    int32_t *const order = order_of(a);
+    for (int64_t base = 0; found < total && base < pool.pages; base += kStep) {
+        // a warp looks at 1024 pages, a lane keeps the 32 from lane * 32 on
+        uint32_t free = 0;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+            const int64_t p = base + warp * 1024 + k * 32 + lane;
+            const uint32_t set = __ballot_sync(0xFFFFFFFFu, p < pool.pages && pool.refs[p] == 0);
+            if (lane == k) free = set;
+        }
+        int here;
+        int rank = found + before_me(__popc(free), tmp, here);
+        for (uint32_t left = free; left != 0 && rank < total; left &= left - 1)
+            order[rank++] = static_cast<int32_t>(base + warp * 1024 + lane * 32 + __ffs(left) - 1);
+        found += here;
+    }
+    bool ok = in && !bad && (extra == 0 || mine + extra <= found);
+    if (in && !bad && !ok) atomicMin(&fail_s, b);
+    __syncthreads();   // the order is written, the first that goes without is known
+    // behind that one a page is the sequence's own only if those before it have given it up
+    if (ok && shared && !copy && b > fail_s && holders - sharers(fail_s) > 1) ok = false;
+    copy = copy && ok;
+    const int grown = ok ? want - held : 0;
+    if (in) {
+        if (a.got != nullptr) a.got[b] = ok ? 1 : 0;
+        if (ok) pool.held[b] = want;
+        if (copy) {
+            const int page = order[mine];
+            table_of(a, b)[first] = page;
+            pool.refs[page] = 1;
+            atomicSub(pool.refs + at, 1);
+            int32_t *const e = list_of(a, atomicAdd(&copies_s, 1));   // (in any order: the copies are independent)
+            e[0] = at;
+            e[1] = page;
+            e[2] = rows;
+        }
+    }
+    // the pages behind those held, a warp's sequences one after the other
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, grown > 0); left != 0; left &= left - 1) {
+        const int l = __ffs(left) - 1, n = __shfl_sync(0xFFFFFFFFu, grown, l), from = __shfl_sync(0xFFFFFFFFu, held, l);
+        const int rank = __shfl_sync(0xFFFFFFFFu, mine + (copy ? 1 : 0), l);
+        int32_t *const row = table_of(a, warp * 32 + l) + from;
+        for (int j = lane; j < n; j += 32) {
+            const int page = order[rank + j];
+            row[j] = page;
+            pool.refs[page] = 1;
+        }
+    }
+    __syncthreads();
+    if (b == 0) a.lists[0] = copies_s;
+}
+
+// ------------------------------------------------------------------ rows
+struct Divide {   // of numbers below 2^31, as a product
+    uint32_t d, recip;
+    __device__ __forceinline__ explicit Divide(int by) : d(static_cast<uint32_t>(by)), recip(0xFFFFFFFFu / static_cast<uint32_t>(by)) {}
+    __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
+        const uint32_t q = __umulhi(x, recip);
+        return q + (x - q * d >= d ? 1u : 0u);
+    }
+};
+__device__ __forceinline__ void copy_unit(const uint8_t *from, uint8_t *to, bool wide) {
+    if (wide)
+        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+    else
+        *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+}
+
+// The first rows of listed pages to others.  An item is up to kUnits units of 16 bytes (4 for scales) of
+// one plane of one layer; the CTAs step over the items, whose number the bookkeeping found.
+constexpr int kCopy = 256, kUnits = 4 * kCopy;
+
+__global__ void __launch_bounds__(kCopy) pages_copy_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int slices) {
+    pdl_wait();
+    pdl_trigger();
+    const int64_t items = static_cast<int64_t>(a.lists[0]) * p.layers * p.planes * slices;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        uint32_t i = static_cast<uint32_t>(item / slices);
+        const int slice = static_cast<int>(item - static_cast<int64_t>(i) * slices);
+        const int which = static_cast<int>(i % p.planes);
+        i /= p.planes;
+        const int layer = static_cast<int>(i % p.layers);
+        const int4 e = *reinterpret_cast<const int4 *>(list_of(a, static_cast<int>(i / p.layers)));
+        const Plane &pl = p.plane[which];
+        const bool wide = pl.bytes % 16 == 0;
+        const int unit = wide ? 16 : 4, per_seg = pl.bytes / unit, per_row = per_seg * pl.segs, total = per_row * e.z;
+        const uint8_t *const from = static_cast<const uint8_t *>(p.base[layer][which]) + e.x * pl.page_stride;
+        uint8_t *const to = static_cast<uint8_t *>(p.base[layer][which]) + e.y * pl.page_stride;
+        const Divide by_row(per_row), by_seg(per_seg);
+        const int u0 = slice * kUnits + static_cast<int>(threadIdx.x);
+        auto place = [&](int u) {
+            const int r = static_cast<int>(by_row(u)), w = u - r * per_row, sg = static_cast<int>(by_seg(w));
+            return r * pl.row_stride + sg * pl.seg_stride + static_cast<int64_t>(w - sg * per_seg) * unit;
+        };
+        if (wide) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (u0 + k * kCopy < total) x[k] = *reinterpret_cast<const uint4 *>(from + place(u0 + k * kCopy));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (u0 + k * kCopy < total) *reinterpret_cast<uint4 *>(to + place(u0 + k * kCopy)) = x[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (u0 + k * kCopy < total) copy_unit(from + place(u0 + k * kCopy), to + place(u0 + k * kCopy), false);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ accept
+// A warp per sequence: checks its path, gives up the pages behind what it keeps, and leaves ctx and the
+// number of rows to move for the rows' kernel (0 where nothing moves; ctx may be overwritten here).
+__global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant__ PageArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int b = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const moe_page_pool_t &pool = a.pool;
+    if (b >= pool.seqs) return;
+    const int ctx = a.ctx[b], count = a.count[b], held = pool.held[b];
+    const long long room = static_cast<long long>(held) * pool.page;
+    bool bad = held < 0 || held > pool.max_pages || ctx < 0 || ctx > room || count > a.max_path;
+    int moves = 0;
+    if (!bad && count > 0) {
+        const int32_t *const path = a.path != nullptr ? a.path + static_cast<int64_t>(b) * a.max_path : nullptr;
+        int last = -1;   // of the 32 before
+        for (int i0 = 0; i0 < count; i0 += 32) {
+            const int i = i0 + lane, p = i < count ? (path != nullptr ? path[i] : i) : 0;
+            int prev = __shfl_up_sync(0xFFFFFFFFu, p, 1);
+            if (lane == 0) prev = last;
+            bad |= __any_sync(0xFFFFFFFFu, i < count && (p <= prev || static_cast<long long>(ctx) + p >= room));
+            if (__any_sync(0xFFFFFFFFu, i < count && p != i)) moves = count;
+            last = __shfl_sync(0xFFFFFFFFu, p, 31);
+        }
+    }
+    if (bad && lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
+    const bool act = !bad && count >= 0;
+    const int after = act ? ctx + count : ctx;
+    if (lane == 0) {
+        int32_t *const e = list_of(a, b);
+        e[0] = ctx;
+        e[1] = act ? moves : 0;
+        if (a.after != nullptr) a.after[b] = after;
+    }
+    if (!act) return;
+    const int left = (after + pool.page - 1) / pool.page;   // at most held
+    const int32_t *const table = table_of(a, b);
+    for (int j = left + lane; j < held; j += 32)
+        if (in_pool(a, table[j])) atomicSub(pool.refs + table[j], 1);
+    if (lane == 0) pool.held[b] = left;
+}
+
+// A thread takes one column of a row (16 bytes, 4 of scales) through all of a sequence's moves in order: the
+// path ascends, so target i is at or before source i and before every later one, and no row is written
+// before it was read.  Eight rows' loads are in flight together.
+constexpr int kMove = 128;
+
+__global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int columns, int slices) {
+    __shared__ int source_s[MOE_MAX_TREE_TOKENS][2], target_s[MOE_MAX_TREE_TOKENS][2];   // page, row
+    pdl_wait();
+    pdl_trigger();
+    const int64_t items = static_cast<int64_t>(a.pool.seqs) * p.layers * slices;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int b = static_cast<int>(item / (p.layers * slices)), rest = static_cast<int>(item - static_cast<int64_t>(b) * p.layers * slices);
+        const int layer = rest / slices;
+        int column = (rest - layer * slices) * kMove + static_cast<int>(threadIdx.x);
+        const int32_t *const e = list_of(a, b);
+        const int ctx = e[0], count = e[1];
+        if (count == 0) continue;
+        const int32_t *const path = a.path + static_cast<int64_t>(b) * a.max_path;
+        __syncthreads();   // the previous item's places
+        {
+            const int i = static_cast<int>(threadIdx.x) & 63;
+            if (i < count) {
+                const int pos = ctx + (threadIdx.x < 64 ? path[i] : i), k = pos / a.pool.page;
+                int page = table_of(a, b)[k];
+                if (!in_pool(a, page)) page = -1;
+                int(&to)[2] = threadIdx.x < 64 ? source_s[i] : target_s[i];
+                to[0] = page;
+                to[1] = pos - k * a.pool.page;
+            }
+        }
+        __syncthreads();
+        if (column >= columns) continue;
+        int which = 0, unit = 16, per_row = 0;
+        for (;; ++which) {
+            const Plane &pl = p.plane[which];
+            unit = pl.bytes % 16 == 0 ? 16 : 4;
+            per_row = pl.bytes / unit * pl.segs;
+            if (column < per_row) break;
+            column -= per_row;
+        }
+        const Plane &pl = p.plane[which];
+        const int per_seg = pl.bytes / unit, seg = column / per_seg;
+        uint8_t *const base = static_cast<uint8_t *>(p.base[layer][which]) + seg * pl.seg_stride + static_cast<int64_t>(column - seg * per_seg) * unit;
+        auto at = [&](const int (&x)[2]) { return base + x[0] * pl.page_stride + x[1] * pl.row_stride; };
+        constexpr int AHEAD = 8;
+        for (int i0 = 0; i0 < count; i0 += AHEAD) {
+            uint4 x[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int i = i0 + k;
+                if (i >= count || source_s[i][0] < 0) continue;
+                if (unit == 16)
+                    x[k] = *reinterpret_cast<const uint4 *>(at(source_s[i]));
+                else
+                    x[k].x = *reinterpret_cast<const uint32_t *>(at(source_s[i]));
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int i = i0 + k;
+                if (i >= count || source_s[i][0] < 0 || target_s[i][0] < 0) continue;
+                if (unit == 16)
+                    *reinterpret_cast<uint4 *>(at(target_s[i])) = x[k];
+                else
+                    *reinterpret_cast<uint32_t *>(at(target_s[i])) = x[k].x;
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ fork, free
+__global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant__ PageArgs a) {
+    __shared__ int dst_s[kBook];
+    pdl_wait();
+    pdl_trigger();
+    const int i = threadIdx.x, lane = threadIdx.x & 31;
+    const moe_page_pool_t &pool = a.pool;
+    const bool in = i < a.items;
+    int src = 0, dst = -1, length = 0, pages = 0;
+    bool ok = in;
+    if (in) {
+        src = a.src[i];
+        dst = a.ids[i];
+        ok = static_cast<uint32_t>(src) < static_cast<uint32_t>(pool.seqs) && static_cast<uint32_t>(dst) < static_cast<uint32_t>(pool.seqs) && src != dst;
+        if (ok) {
+            length = a.length_out[src];
+            const int held = pool.held[src];
+            ok = pool.held[dst] == 0 && held >= 0 && held <= pool.max_pages && length >= 0 && length <= static_cast<long long>(held) * pool.page;
+        }
+    }
+    dst_s[i] = dst;
+    __syncthreads();   // all is read that the call may write
+    for (int k = 0; ok && k < i; ++k) ok = dst_s[k] != dst;
+    if (in && !ok) record_error(a.err, MOE_ERR_BAD_ID);
+    if (ok) {
+        pages = (length + pool.page - 1) / pool.page;
+        pool.held[dst] = pages;
+        a.length_out[dst] = length;
+    }
+    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, ok && pages > 0); left != 0; left &= left - 1) {
+        const int l = __ffs(left) - 1, n = __shfl_sync(0xFFFFFFFFu, pages, l);
+        const int32_t *const from = table_of(a, __shfl_sync(0xFFFFFFFFu, src, l));
+        int32_t *const to = table_of(a, __shfl_sync(0xFFFFFFFFu, dst, l));
+        for (int j = lane; j < n; j += 32) {
+            const int page = from[j];
+            to[j] = page;
+            if (in_pool(a, page)) atomicAdd(pool.refs + page, 1);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__ PageArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const int i = static_cast<int>(blockIdx.x * 8 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    if (i >= a.items) return;
+    const int b = a.ids[i];
+    if (b < 0) return;
+    int held = 0;
+    if (lane == 0) {
+        if (b >= a.pool.seqs) {
+            record_error(a.err, MOE_ERR_BAD_ID);
+        } else {
+            held = atomicExch(a.pool.held + b, 0);   // of two that name it one finds its pages
+            if (held < 0 || held > a.pool.max_pages) {
+                record_error(a.err, MOE_ERR_BAD_ID);
+                held = 0;
+            }
+            if (a.length_out != nullptr) a.length_out[b] = 0;
+        }
+    }
+    held = __shfl_sync(0xFFFFFFFFu, held, 0);
+    if (held == 0) return;
+    const int32_t *const table = table_of(a, b);
+    for (int j = lane; j < held; j += 32)
+        if (in_pool(a, table[j])) atomicSub(a.pool.refs + table[j], 1);
+}
+
+template <typename K, typename... Args>
+cudaError_t launch(K kernel, unsigned grid, unsigned threads, cudaStream_t s, bool pdl, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+int units_of_row(const Plane &p) { return p.bytes / (p.bytes % 16 == 0 ? 16 : 4) * p.segs; }
+constexpr int64_t kSms = 152;
+
+}  // namespace
+
+size_t pages_list_bytes(const moe_page_pool_t &pool) { return 16 + 16 * static_cast<size_t>(pool.seqs) + 4 * static_cast<size_t>(pool.pages); }
+
+cudaError_t launch_pages_reserve(const PageArgs &a, const PageRows *rows, int launches, cudaStream_t s, bool pdl) {
+    cudaError_t e = launch(pages_reserve_kernel, 1, kBook, s, pdl, a);
+    for (int i = 0; i < launches && e == cudaSuccess; ++i) {
+        int64_t most = 1;   // units of a page in a plane
+        for (int k = 0; k < rows[i].planes; ++k) most = std::max<int64_t>(most, static_cast<int64_t>(units_of_row(rows[i].plane[k])) * a.pool.page);
+        const int slices = static_cast<int>((most + kUnits - 1) / kUnits);
+        const int64_t items = static_cast<int64_t>(a.pool.seqs) * rows[i].layers * rows[i].planes * slices;
+        e = launch(pages_copy_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 8)), kCopy, s, pdl, a, rows[i], slices);
+    }
+    return e;
+}
+
+cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int launches, cudaStream_t s, bool pdl) {
+    cudaError_t e = launch(pages_accept_kernel, static_cast<unsigned>((a.pool.seqs + 7) / 8), 256, s, pdl, a);
+    if (a.path == nullptr) return e;   // nothing moves
+    for (int i = 0; i < launches && e == cudaSuccess; ++i) {
+        int columns = 0;
+        for (int k = 0; k < rows[i].planes; ++k) columns += units_of_row(rows[i].plane[k]);
+        const int slices = (columns + kMove - 1) / kMove;
+        const int64_t items = static_cast<int64_t>(a.pool.seqs) * rows[i].layers * slices;
+        e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, rows[i], columns, slices);
+    }
+    return e;
+}
+
+cudaError_t launch_pages_fork(const PageArgs &a, cudaStream_t s, bool pdl) { return launch(pages_fork_kernel, 1, kBook, s, pdl, a); }
+
+cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t s, bool pdl) {
+    return launch(pages_free_kernel, static_cast<unsigned>((a.items + 7) / 8), 256, s, pdl, a);
+}
+
+}  // namespace moe

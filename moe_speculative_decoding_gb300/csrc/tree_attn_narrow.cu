@@ -76,24 +76,6 @@ struct Lay {
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// The weights' operand [128 positions][NT], MN-major, rows of NT * 2 = 32, 64 or 128 bytes with the
-// swizzle of that width: 16-byte chunk ^= the row's index within an atom of 8, at that granularity.
-constexpr float kNone = -3.0e38f;   // the maximum of a row that has seen nothing: below every score, finite
-
-template <int NT>
-__device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
-    constexpr uint64_t mode = NT == 64 ? 2 : (NT == 32 ? 4 : 6);
-    constexpr uint32_t atom = 8 * NT * 2;   // 8 positions
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
-           static_cast<uint64_t>(atom >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | mode << 61;
-}
-template <int NT>
-__device__ __forceinline__ uint32_t p_chunk(int row, int chunk) {   // byte offset of a 16-byte chunk
-    const int x = NT == 64 ? row & 7 : (NT == 32 ? row >> 1 & 3 : row >> 2 & 1);
-    return static_cast<uint32_t>(row * NT * 2 + ((chunk ^ x) << 4));
-}
-// kind::f16, A (V^T) and B (P^T) MN-major; fmt 0: fp16, 1: bf16
-__host__ __device__ constexpr uint32_t idesc_vp(int N, uint32_t fmt) { return idesc_pv(N, fmt) | (1u << 15); }
 // kind::f8f6f4, A e4m3, B e5m2
 __host__ __device__ constexpr uint32_t idesc_e4m3_e5m2(int M, int N) { return idesc_e4m3_f32(M, N) | (1u << 10); }
 
@@ -118,19 +100,6 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t addr, const uint32_t (&x)[
 #pragma unroll
         for (int c = 0; c < NT / 32; ++c) tmem_st32(addr + 32 * c, reinterpret_cast<const uint32_t(&)[32]>(x[32 * c]));
     }
-}
-
-__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %1, 0;\n\t"
-        "barrier.red.or.pred q, %2, %3, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}\n"
-        : "=r"(r)
-        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
-        : "memory");
-    return r != 0;
 }
 
 // Sums (or maxima of) v[c] over the warp's lanes: afterwards lane l holds in v[0 .. NT/32) those of

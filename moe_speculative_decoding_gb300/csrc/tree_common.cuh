@@ -86,6 +86,25 @@ __host__ __device__ constexpr uint32_t idesc_pv(int N, uint32_t fmt) {
 // kind::f8f6f4, A e5m2 (format 1), B e4m3 (0), both K-major
 __host__ __device__ constexpr uint32_t idesc_e5m2_e4m3(int M, int N) { return idesc_e4m3_f32(M, N) | (1u << 7); }
 
+// A weights' operand [positions][NT], MN-major, rows of NT * 2 = 32, 64 or 128 bytes with the
+// swizzle of that width: 16-byte chunk ^= the row's index within an atom of 8, at that granularity.
+constexpr float kNone = -3.0e38f;   // the maximum of a row that has seen nothing: below every score, finite
+
+template <int NT>
+__device__ __forceinline__ uint64_t desc_p(uint32_t saddr) {
+    constexpr uint64_t mode = NT == 64 ? 2 : (NT == 32 ? 4 : 6);
+    constexpr uint32_t atom = 8 * NT * 2;   // 8 positions
+    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | static_cast<uint64_t>(1u) << 16 |
+           static_cast<uint64_t>(atom >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | mode << 61;
+}
+template <int NT>
+__device__ __forceinline__ uint32_t p_chunk(int row, int chunk) {   // byte offset of a 16-byte chunk
+    const int x = NT == 64 ? row & 7 : (NT == 32 ? row >> 1 & 3 : row >> 2 & 1);
+    return static_cast<uint32_t>(row * NT * 2 + ((chunk ^ x) << 4));
+}
+// kind::f16, A (V^T) and B (P^T) MN-major; fmt 0: fp16, 1: bf16
+__host__ __device__ constexpr uint32_t idesc_vp(int N, uint32_t fmt) { return idesc_pv(N, fmt) | (1u << 15); }
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3) {
     asm volatile(
@@ -161,6 +180,20 @@ __device__ __forceinline__ bool softmax_any(bool v) {
         "selp.u32 %0, 1, 0, q;\n\t}\n"
         : "=r"(r)
         : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
+// Barrier over some warps that also ORs a predicate.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(v)), "r"(id), "r"(threads)
         : "memory");
     return r != 0;
 }
