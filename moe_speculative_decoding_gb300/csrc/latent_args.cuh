@@ -41,7 +41,7 @@ cudaError_t launch_latent_simt(const LatentArgs &a, cudaStream_t s, bool pdl);
 // The tensor-core kernel: whether it takes these operands, its workspace after the header, the
 // launch (cudaErrorNotSupported: strides that no tensor map describes).
 bool latent_attn_supports(const moe_latent_cache_t &c, const moe_heads_t &q, const moe_heads_t &out);
-size_t latent_attn_part_bytes(int rank);
+size_t latent_attn_part_bytes();
 cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl);
 
 // Rows of one layer's cache that move from page to page: up to four planes (keys, values, and their

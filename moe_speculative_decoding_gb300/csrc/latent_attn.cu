@@ -16,8 +16,8 @@
 //
 // because an accumulator of 128 rows by 512 channels would be all of TMEM, and its queries, 147 KB, most
 // of the shared memory.  With 64 rows O^T takes 256 of the 512 columns and Q 74 KB, which leaves
-// a ring of seven 16 KB units (64 positions by 128 channels, TMA, 128-byte swizzle) beside two places
-// for the tiles' rotary channels.  A tile is 64 positions, not 128, so that the ring holds nearly two:
+// a ring of eight 16 KB units (64 positions by 128 channels, TMA, 128-byte swizzle) beside three places
+// for tiles' rotary channels and then their weights.  A tile is 64 positions, not 128, so that the ring holds two:
 // the units of one are held from the scores' product to the output's, and meanwhile the next arrive.
 //
 // Two softmax warpgroups share a tile, each with half of the rows, its own maxima, sums and vote: the
@@ -38,28 +38,36 @@ namespace moe {
 namespace {
 
 constexpr int kPos = 64;                        // positions of a tile
-constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 10, kThreads = 352;
+// How many tiles ahead of its copy a tile is fetched into L2.
+constexpr int kAhead = 2;
+constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 11, kThreads = 384;   // two score warps
 constexpr uint32_t kUnit = 16384, kRopeTile = 8192;
-constexpr int kRope = 2;                        // places for tiles' rotary channels
+
+// What the others need to know of a part of an item: a record of the producer's walk.
+struct Item {
+    int t0, n, ctx, len;   // the sequence: first token, tokens, cached positions, all positions
+    int b, blk, lo, hi;    // its number, the block of rows, the part of its tiles
+    int index, whole;      // items before in this CTA; the item lies in this CTA alone
+};
 
 template <int NT>
 struct Lay {
-    static constexpr int NU = NT == 64 ? 7 : (NT == 32 ? 10 : 11);   // units of the ring: what fits
-    static constexpr uint32_t kP = kPos * NT * 2;                    // weights of a tile
+    // The ring's units and the places for tiles' rotary channels: what fits.  A tile's weights take the
+    // place of its rotary channels, which are done with when its scores are formed.
+    static constexpr int NU = NT == 64 ? 8 : (NT == 32 ? 10 : 11), NR = 3;
+    static_assert(kPos * NT * 2 <= kRopeTile, "the weights of a tile");
     static constexpr uint32_t kQBlock = NT * 128;                    // 64 channels of the queries
-    static constexpr uint32_t oU = 0, oR = oU + NU * kUnit, oP = oR + kRope * kRopeTile, oQ = oP + 2 * kP, oBar = oQ + 9 * kQBlock;
-    static constexpr int bUF = 0, bUE = NU, bRF = 2 * NU, bRE = bRF + kRope, bS = bRE + kRope, bSFree = bS + 2, bP = bSFree + 2,
-                         bPV = bP + 2, bQ = bPV + 2, bO = bQ + 1, bW = bO + 1, bDrain = bW + kRecords, kBars = bDrain + 1;
-    static constexpr uint32_t oMisc = oBar + 8 * kBars + 8;        // TMEM address, abort flag, units and rotary tiles copied
-    static constexpr uint32_t oBad = (oMisc + 16 + 15) & ~15u;     // uint32 [2 items][2]: drafted tokens with non-finite latents
+    static constexpr uint32_t oU = 0, oR = oU + NU * kUnit, oQ = oR + NR * kRopeTile, oBar = oQ + 9 * kQBlock;
+    static constexpr int bUF = 0, bUE = NU, bRF = 2 * NU, bRE = bRF + NR, bS = bRE + NR, bSFree = bS + 2, bP = bSFree + 2,
+                         bQ = bP + NR, bO = bQ + 1, bW = bO + 1, bDrain = bW + kRecords, kBars = bDrain + 1;
+    static constexpr uint32_t oMisc = oBar + 8 * kBars;            // TMEM address, abort flag, units, rotary tiles and queries copied
+    static constexpr uint32_t oBad = (oMisc + 20 + 15) & ~15u;     // uint32 [2 items][2]: drafted tokens with non-finite latents
     static constexpr uint32_t oM = oBad + 16;                      // float [NT]: minus the rows' maxima, 0 where there is none
     static constexpr uint32_t oAlpha = oM + NT * 4;                // float [NT]: a rescaling; an item's last factors
-    static constexpr uint32_t oDelta = oAlpha + NT * 4;            // float [NT]: its logarithm
-    static constexpr uint32_t oRed = oDelta + NT * 4;              // float [2][4][NT / 2]: per warp
-    static constexpr uint32_t oMask = oRed + 4 * NT * 4;           // uint64 [2 items][NT]: the rows' tree masks
-    static constexpr uint32_t oTo = oMask + 2 * NT * 8;            // int64 [2 items][NT]: the rows' output offsets
-    static constexpr uint32_t oWalk = oTo + 2 * NT * 8;            // records of walks
-    static constexpr uint32_t kSmem = oWalk + kRecords * kRecordBytes;
+    static constexpr uint32_t oRed = oAlpha + NT * 4;              // float [2][4][NT / 2]: per warp
+    static constexpr uint32_t oMask = oRed + 4 * NT * 4;           // uint64 [NT]: the rows' tree masks
+    static constexpr uint32_t oWalk = oMask + NT * 8;              // records of parts
+    static constexpr uint32_t kSmem = oWalk + kRecords * sizeof(Item);
     static constexpr uint32_t kTmem = NT == 64 ? 512 : 8 * NT;     // 2 NT of S^T, up to 4 NT of O^T
     static_assert(kSmem <= 232448, "shared memory");
 };
@@ -70,6 +78,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
+}
+// The box on its way into L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
+                 "r"(c1), "r"(c2)
+                 : "memory");
 }
 // 16 lanes (the quarter's first: an accumulator with M = 64 has 16 rows in each quarter) by 8 N columns:
 // of columns 8 i .. 8 i + 7 a thread gets lane / 4's (2 (lane % 4), + 1) in r[4 i], r[4 i + 1], and those of
@@ -148,7 +162,6 @@ struct Part {
     int index;                  // items walked before
     bool whole, first;          // the item lies in this CTA alone; the range's first item has not been looked at
 };
-static_assert(sizeof(Part) <= kRecordBytes, "a record holds a part");
 
 // The whole warp calls these; the outcome is uniform.
 template <int NT>
@@ -249,32 +262,35 @@ __device__ __forceinline__ bool part_next(const LatentArgs &a, Part &w) {
     }
     return false;
 }
-// The producer walks, the others follow it through a ring of records: it is at most the ring of units
-// ahead of the products, fewer tiles than there are records, and an item has at least one.
+// The producer walks, the others follow it through a ring of records.  It is at most four items ahead of the
+// last: it waits for the rotary tile before its last to be scored, scores for the queries, those for the
+// scores of the item before, and these for the output's product two tiles before.
 template <int NT>
 __device__ __forceinline__ bool part_lead(const LatentArgs &a, Part &w, Follow &f) {
     const bool more = part_next<NT>(a, w);
     if ((threadIdx.x & 31) == 0) {
-        Part *const r = reinterpret_cast<Part *>(f.ring + (f.n % kRecords) * kRecordBytes);
-        *r = w;
-        if (!more) r->lo = -1;   // the end
+        Item *const r = reinterpret_cast<Item *>(f.ring) + f.n % kRecords;
+        const Item x = {w.s.t0, w.s.n, w.s.ctx, w.s.len, w.b, w.blk, more ? w.lo : -1, w.hi, w.index, w.whole ? 1 : 0};
+        *r = x;
     }
     warp_arrive(f.bars + 8u * (f.n % kRecords));
     ++f.n;
     return more;
 }
-__device__ __forceinline__ bool part_follow(const LatentArgs &a, Part &w, Follow &f, volatile int32_t *abort_flag) {
+__device__ __forceinline__ bool part_follow(const LatentArgs &a, Item &w, Follow &f, volatile int32_t *abort_flag) {
     if (!wait_for(f.bars + 8u * (f.n % kRecords), (f.n / kRecords) & 1u, abort_flag, a.err, a.wait_limit)) return false;
-    w = *reinterpret_cast<const Part *>(f.ring + (f.n % kRecords) * kRecordBytes);
+    w = reinterpret_cast<const Item *>(f.ring)[f.n % kRecords];
     ++f.n;
-    return w.lo >= 0;
+    return w.lo >= 0;   // negative: the end
 }
 
-// Partial results: per CTA two slots (its first item, its last), each [NT rows][units * 128] fp32 of unnormalised
-// output, then, after all slots, [slot][NT] (maximum, sum).
+// Partial results: per CTA two slots (its first item, its last), each [NT rows][kPitch] fp32 of unnormalised
+// output (a constant step: with the rank's own the stores took three times as long), then, after all
+// slots, [slot][NT] (maximum, sum).
+constexpr int kPitch = 512;
 __host__ __device__ constexpr int units_of(int rank) { return (rank + 127) / 128; }
 __device__ __forceinline__ float *part_o(const LatentArgs &a, int nt, int slot) {
-    return static_cast<float *>(a.part) + static_cast<size_t>(slot) * nt * (units_of(a.cache.rank) * 128);
+    return static_cast<float *>(a.part) + static_cast<size_t>(slot) * nt * kPitch;
 }
 __device__ __forceinline__ float2 *part_s(const LatentArgs &a, int nt, int ctas, int slot) {
     return reinterpret_cast<float2 *>(part_o(a, nt, 2 * ctas)) + static_cast<size_t>(slot) * nt;
@@ -284,7 +300,7 @@ __device__ __forceinline__ float2 *part_s(const LatentArgs &a, int nt, int ctas,
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_r,
-                   const __grid_constant__ LatentArgs a, int box_rows) {
+                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ LatentArgs a, int box_rows, int q_map) {
     using L = Lay<NT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
@@ -301,22 +317,21 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             mbar_init(bar(L::bUF + i), 1);
             mbar_init(bar(L::bUE + i), 1);
         }
-        for (int i = 0; i < kRope; ++i) {
+        for (int i = 0; i < L::NR; ++i) {
             mbar_init(bar(L::bRF + i), 1);
             mbar_init(bar(L::bRE + i), 1);
+            mbar_init(bar(L::bP + i), 8);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(L::bS + i), 1);
             mbar_init(bar(L::bSFree + i), 8);
-            mbar_init(bar(L::bP + i), 8);
-            mbar_init(bar(L::bPV + i), 1);
         }
-        mbar_init(bar(L::bQ), 8);
+        mbar_init(bar(L::bQ), q_map ? 1 : 8);
         mbar_init(bar(L::bO), 1);
         for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
-        mbar_init(bar(L::bDrain), 2);
+        mbar_init(bar(L::bDrain), 3);
         *abort_flag = 0;
-        copied[0] = copied[1] = 0;
+        copied[0] = copied[1] = copied[2] = 0;
         fence_mbar_init();
         tma_prefetch_map(&tm_c);
         tma_prefetch_map(&tm_r);
@@ -328,7 +343,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc);
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t *>(smem + L::oMisc), 0);
     Follow follow = {smem + L::oWalk, bar(L::bW), 0};
     pdl_wait();
     pdl_trigger();
@@ -373,71 +388,121 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     record_error(a.err, MOE_ERR_BAD_ID);
                     page = kc.pages;   // beyond the tensor: the copy writes zeros
                 }
-                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, mine && half == 0)), bytes = n * box_rows * 128u;
-                const uint32_t rs = rc % kRope;
-                if (!(ok = wait_for(bar(L::bRE + rs), ((rc / kRope) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(L::bRF + rs), bytes);
-                __syncwarp();
-                if (mine && half == 0) tma_load_3d(base + L::oR + rs * kRopeTile + box * box_rows * 128u, &tm_r, bar(L::bRF + rs), 0, row, page);
-                __syncwarp();
-                for (int u = 0; u < U; ++u, ++uc) {
-                    const uint32_t slot = uc % L::NU;
-                    if (!(ok = wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit))) {
-                        ++rc;   // its copies are on their way
-                        break;
+                const uint32_t rs = rc % L::NR;
+                if (!(ok = wait_for(bar(L::bRE + rs), ((rc / L::NR) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
+                const uint32_t r_dst = base + L::oR + rs * kRopeTile, r_bar = bar(L::bRF + rs);
+                // the tile kAhead further, to L2
+                if (NT == 64 && w.s.blocks == 1 && tt + kAhead < w.hi) {
+                    const int at = (k + kAhead) * boxes + box;
+                    const int page_a = __shfl_sync(0xFFFFFFFFu, at < 32 ? page_now : page_next, at & 31);
+                    const int row_a = __shfl_sync(0xFFFFFFFFu, at < 32 ? row_now : row_next, at & 31);
+                    if (half < 2 && static_cast<uint32_t>(page_a) < static_cast<uint32_t>(kc.pages)) {
+                        for (int u = 0; u < U; ++u) tma_prefetch_3d(&tm_c, u * 128 + half * 64, row_a, page_a);
+                        if (half == 0) tma_prefetch_3d(&tm_r, 0, row_a, page_a);
                     }
-                    if (lane == 0) mbar_arrive_expect_tx(bar(L::bUF + slot), 2 * bytes);
-                    __syncwarp();
-                    if (mine)
-                        tma_load_3d(base + L::oU + slot * kUnit + half * 8192u + box * box_rows * 128u, &tm_c, bar(L::bUF + slot),
-                                    u * 128 + half * 64, row, page);
                     __syncwarp();
                 }
-                if (!ok) break;
+                if (boxes == 1) {
+                    // one box: issued by an elected lane from uniform registers (by one lane of a condition
+                    // on the lane a unit took 450 cycles)
+                    const int page1 = __shfl_sync(0xFFFFFFFFu, page, 0), row1 = __shfl_sync(0xFFFFFFFFu, row, 0);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(r_bar, kRopeTile);
+                        tma_load_3d(r_dst, &tm_r, r_bar, 0, row1, page1);
+                    }
+                    __syncwarp();
+                    for (int u = 0; u < U; ++u, ++uc) {
+                        const uint32_t slot = uc % L::NU, u_dst = base + L::oU + slot * kUnit, u_bar = bar(L::bUF + slot);
+                        if (!(ok = wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
+                        if (elect_one()) {
+                            mbar_arrive_expect_tx(u_bar, kUnit);
+                            tma_load_3d(u_dst, &tm_c, u_bar, u * 128, row1, page1);
+                            tma_load_3d(u_dst + 8192u, &tm_c, u_bar, u * 128 + 64, row1, page1);
+                        }
+                        __syncwarp();
+                    }
+                } else {
+                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, mine && half == 0)), bytes = n * box_rows * 128u;
+                    const uint32_t off = half * 8192u + box * box_rows * 128u;
+                    if (lane == 0) mbar_arrive_expect_tx(r_bar, bytes);
+                    __syncwarp();
+                    if (mine && half == 0) tma_load_3d(r_dst + off, &tm_r, r_bar, 0, row, page);
+                    __syncwarp();
+                    for (int u = 0; u < U; ++u, ++uc) {
+                        const uint32_t slot = uc % L::NU, u_bar = bar(L::bUF + slot);
+                        if (!(ok = wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
+                        if (lane == 0) mbar_arrive_expect_tx(u_bar, 2 * bytes);
+                        __syncwarp();
+                        if (mine) tma_load_3d(base + L::oU + slot * kUnit + off, &tm_c, u_bar, u * 128 + half * 64, row, page);
+                        __syncwarp();
+                    }
+                }
+                if (!ok) {
+                    ++rc;   // the rotary tile's copies are on their way
+                    break;
+                }
             }
         }
         if (lane == 0) {
             copied[0] = uc;
             copied[1] = rc;
         }
-    } else if (warp == kScoreWarp) {
-        // -------------------------------------------------------------------- S^T = C Q^T, tile by tile
-        Part w;
+    } else if (warp == kScoreWarp || warp == kScoreWarp + 1) {
+        // -------------------------------------------------------------------- S^T = C Q^T
+        // Two warps take alternate tiles: the turn of one's loop (waits, fences, the first product's issue) takes
+        // as long as ten products, and the other's products go on meanwhile.
+        const uint32_t side = static_cast<uint32_t>(warp - kScoreWarp), s_col = tmem + side * NT;
+        Item w;
         const uint64_t q_desc = desc_kmajor_sw128(base + L::oQ);
         const int rope_steps = (a.cache.rope + 15) / 16;
         uint32_t c = 0, uc = 0, items = 0;
         bool ok = true;
         while (ok && part_follow(a, w, follow, abort_flag)) {
             ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
-            for (int t = 0; ok && t < w.hi - w.lo; ++t, ++c) {
-                const uint32_t buf = c & 1u, s_col = tmem + buf * NT, rs = c % kRope;
-                // the softmax has taken this buffer's previous scores
-                ok = (c < 2 || wait_for(bar(L::bSFree + buf), ((c >> 1) - 1) & 1u, abort_flag, a.err, limit)) &&
-                     wait_for(bar(L::bRF + rs), (c / kRope) & 1u, abort_flag, a.err, limit);
+            const int T = __shfl_sync(0xFFFFFFFFu, w.hi - w.lo, 0);
+            for (int t = 0; ok && t < T; ++t, ++c) {
+                if ((c & 1u) != side) {
+                    uc += U;
+                    continue;
+                }
+                const uint32_t rs = c % L::NR;
+                // The softmax has taken this buffer's previous scores, tile c - 2's.  So that tile and all before it
+                // have landed, the ring's previous uses of this one's places among them, and the parities
+                // below tell this use from those.
+                ok = (c < 2 || wait_for(bar(L::bSFree + side), ((c >> 1) - 1) & 1u, abort_flag, a.err, limit)) &&
+                     wait_for(bar(L::bRF + rs), (c / L::NR) & 1u, abort_flag, a.err, limit);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t r_desc = desc_kmajor_sw128(base + L::oR + rs * kRopeTile);
                 if (elect_one()) {
                     for (int i = 0; i < rope_steps; ++i)
                         tc_mma_bf16(s_col, r_desc + 2 * i, q_desc + 2 * U * (L::kQBlock / 16) + 2 * i, idesc_bf16_f32(64, NT), i > 0);
-                    tc_commit(bar(L::bRE + rs));
                 }
                 __syncwarp();
-                for (int u = 0; u < U; ++u, ++uc) {
-                    const uint32_t slot = uc % L::NU;
+                for (int u = 0; u < U;) {
+                    // a unit, and those behind it that have landed too
+                    uint32_t slot = uc % L::NU;
                     if (!(ok = wait_for(bar(L::bUF + slot), (uc / L::NU) & 1u, abort_flag, a.err, limit))) break;
+                    int n = 1;
+                    while (u + n < U && __all_sync(0xFFFFFFFFu, mbar_test_wait(bar(L::bUF + (uc + n) % L::NU), ((uc + n) / L::NU) & 1u))) ++n;
                     tc_fence_after();
-                    const uint64_t c_desc = desc_kmajor_sw128(base + L::oU + slot * kUnit);
                     if (elect_one()) {
+                        uint64_t qd = q_desc + 2 * u * (L::kQBlock / 16);
+                        for (int k = 0; k < n; ++k) {
+                            const uint64_t c_desc = desc_kmajor_sw128(base + L::oU + slot * kUnit);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)   // two blocks of 64 channels
-                            tc_mma_bf16(s_col, c_desc + (i / 4) * 512 + (i % 4) * 2,
-                                        q_desc + (2 * u + i / 4) * (L::kQBlock / 16) + (i % 4) * 2, idesc_bf16_f32(64, NT), 1);
-                        if (u == U - 1) tc_commit(bar(L::bS + buf));
+                            for (int i = 0; i < 8; ++i)   // two blocks of 64 channels
+                                tc_mma_bf16(s_col, c_desc + (i / 4) * 512 + (i % 4) * 2, qd + (i / 4) * (L::kQBlock / 16) + (i % 4) * 2,
+                                            idesc_bf16_f32(64, NT), 1);
+                            qd += 2 * (L::kQBlock / 16);
+                            if (++slot == L::NU) slot = 0;
+                        }
+                        if (u + n == U) tc_commit(bar(L::bS + side));
                     }
                     __syncwarp();
+                    u += n;
+                    uc += n;
                 }
-                if (!ok) break;
             }
             ++items;
         }
@@ -448,37 +513,37 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         __syncwarp();
     } else if (warp == kOutWarp) {
         // -------------------------------------------------------------------- O^T += C^T P^T, tile by tile
-        // (A warp of its own: a tile's copies may come later than the weights of the tile before.)
-        Part w;
+        Item w;
         uint32_t c = 0, uc = 0;
         bool ok = true;
         while (ok && part_follow(a, w, follow, abort_flag)) {
-            const int T = w.hi - w.lo;
+            const int T = __shfl_sync(0xFFFFFFFFu, w.hi - w.lo, 0);
             for (int t = 0; ok && t < T; ++t, ++c) {
-                const uint32_t buf = c & 1u;
+                const uint32_t rs = c % L::NR;
+                // the units that the product reads: complete before the scores were
+                for (int u = 0; ok && u < U; ++u)
+                    ok = wait_for(bar(L::bUF + (uc + u) % L::NU), ((uc + u) / L::NU) & 1u, abort_flag, a.err, limit);
                 // (the first weights of an item come after the previous item's O was read)
-                if (!(ok = wait_for(bar(L::bP + buf), (c >> 1) & 1u, abort_flag, a.err, limit))) break;
-                const uint64_t p_desc = desc_p<NT>(base + L::oP + buf * L::kP);
-                for (int u = 0; u < U; ++u, ++uc) {
-                    const uint32_t slot = uc % L::NU;
-                    // (complete before the scores were; waited for as what the product reads)
-                    if (!(ok = wait_for(bar(L::bUF + slot), (uc / L::NU) & 1u, abort_flag, a.err, limit))) break;
-                    tc_fence_after();
-                    const uint64_t c_desc = desc_mn_sw128(base + L::oU + slot * kUnit, 8192u);
-                    if (elect_one()) {
+                ok = ok && wait_for(bar(L::bP + rs), (c / L::NR) & 1u, abort_flag, a.err, limit);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t p_desc = desc_p<NT>(base + L::oR + rs * kRopeTile);
+                uint32_t slot = uc % L::NU;
+                if (elect_one()) {
+                    for (int u = 0; u < U; ++u) {
+                        const uint64_t c_desc = desc_mn_sw128(base + L::oU + slot * kUnit, 8192u);
 #pragma unroll
                         for (int i = 0; i < kPos / 16; ++i)   // 16 positions: 2 KB of a block, 2 atoms of P
                             tc_mma_bf16(tmem + (2 + u) * NT, c_desc + 128 * i, p_desc + (16 * NT * 2 / 16) * i, idesc_vp(NT, 1),
                                         t > 0 || i > 0);
                         tc_commit(bar(L::bUE + slot));
-                        if (u == U - 1) {
-                            tc_commit(bar(L::bPV + buf));
-                            if (t == T - 1) tc_commit(bar(L::bO));
-                        }
+                        if (++slot == L::NU) slot = 0;
                     }
-                    __syncwarp();
+                    tc_commit(bar(L::bRE + rs));
+                    if (t == T - 1) tc_commit(bar(L::bO));
                 }
-                if (!ok) break;
+                __syncwarp();
+                uc += U;
             }
         }
         if (elect_one()) tc_commit(bar(L::bDrain));
@@ -493,32 +558,58 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         const uint32_t lanes = static_cast<uint32_t>(q4 * 32) << 16;
         float *const nm_s = reinterpret_cast<float *>(smem + L::oM) + g * H;
         float *const alpha_s = reinterpret_cast<float *>(smem + L::oAlpha) + g * H;
-        float *const delta_s = reinterpret_cast<float *>(smem + L::oDelta) + g * H;
+        uint64_t *const mask_s = reinterpret_cast<uint64_t *>(smem + L::oMask) + g * H;
         float *const red_s = reinterpret_cast<float *>(smem + L::oRed) + g * 4 * H;
         uint32_t *const bad_s = reinterpret_cast<uint32_t *>(smem + L::oBad);
         const Divisor by_heads(a.heads);
+        const bool even_out = a.out.token_stride == static_cast<int64_t>(a.heads) * a.out.head_stride;
         bool dead = false;   // a wait gave up: only the barriers are kept
         uint32_t c = 0;      // tiles
-        Part w, next;
-        // An item's queries into shared memory, 16 bytes a piece: blocks of 64 channels, [NT rows][128
-        // bytes], the rotary channels' block last; zeros beyond the rows and channels.  The rows' masks and
-        // output offsets beside them, for the item after the present one.
-        auto load_queries = [&](const Part &v) {
-            const int R = v.s.n * a.heads - v.blk * NT, pieces = (2 * U + 1) * NT * 8;
-            constexpr int BATCH = 6;
+        Item w, next;
+        // An item's queries into shared memory: blocks of 64 channels, [NT rows][128 bytes], the rotary channels'
+        // block last.  Rows that are one step apart are copied (q_map): loaded by these threads, 64 rows took
+        // 8,000 cycles behind the first tiles' copies.
+        uint64_t next_mask = 0;   // of row g * H + p
+        auto load_queries = [&](const Item &v) {
+            const int R = v.n * a.heads - v.blk * NT;
+            // the row's mask goes to shared memory when the present item's are done with
+            next_mask = 0;
+            if (p < H && g * H + p < R) {
+                const uint32_t token = by_heads.quotient(static_cast<uint32_t>(v.blk * NT + g * H + p));
+                next_mask = a.mask != nullptr ? a.mask[v.t0 + static_cast<int>(token)] : (2ull << token) - 1ull;
+                if (v.n < 64) next_mask &= (1ull << v.n) - 1ull;
+            }
+            if (q_map) {   // (rows beyond the block's are another's, or zeros: their columns go nowhere)
+                if (warp == 0) {
+                    if (elect_one()) {
+                        const int row = v.t0 * a.heads + v.blk * NT;
+                        mbar_arrive_expect_tx(bar(L::bQ), static_cast<uint32_t>(2 * U + 1) * L::kQBlock);
+                        for (int b = 0; b < 2 * U; ++b) tma_load_2d(base + L::oQ + b * L::kQBlock, &tm_q, bar(L::bQ), b * 64, row);
+                        tma_load_2d(base + L::oQ + 2 * U * L::kQBlock, &tm_q, bar(L::bQ), a.cache.rank, row);
+                        copied[2] = static_cast<uint32_t>(v.index) + 1;
+                    }
+                    __syncwarp();
+                }
+                return;
+            }
+            const int pieces = (2 * U + 1) * NT * 8;
+            constexpr int BATCH = 9;
+            // 16 bytes a piece; rows beyond the block's repeat its last one, channels beyond are zeros
+            const int row0 = v.blk * NT, last = min(R, NT) - 1;
+            const uint16_t *const q = static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(v.t0) * a.q.token_stride;
 #pragma unroll 1
             for (int i0 = static_cast<int>(threadIdx.x); i0 < pieces; i0 += BATCH * 256) {
                 uint4 x[BATCH];
 #pragma unroll
                 for (int i = 0; i < BATCH; ++i) {
-                    const int at = i0 + i * 256, block = at / (NT * 8), row = at / 8 % NT, ch = at % 8 * 8;
+                    const int at = i0 + i * 256, block = at / (NT * 8), ch = at % 8 * 8;
                     const bool rope = block == 2 * U;
                     x[i] = make_uint4(0, 0, 0, 0);
-                    if (at < pieces && row < R && (rope ? ch < a.cache.rope : block * 64 + ch < a.cache.rank)) {
-                        const uint32_t r = static_cast<uint32_t>(v.blk * NT + row), token = by_heads.quotient(r);
-                        x[i] = *reinterpret_cast<const uint4 *>(
-                            static_cast<const uint16_t *>(a.q.ptr) + static_cast<int64_t>(v.s.t0 + static_cast<int>(token)) * a.q.token_stride +
-                            static_cast<int64_t>(r - token * a.heads) * a.q.head_stride + (rope ? a.cache.rank : block * 64) + ch);
+                    if (at < pieces && (rope ? ch < a.cache.rope : block * 64 + ch < a.cache.rank)) {
+                        const uint32_t r = static_cast<uint32_t>(row0 + min(at / 8 % NT, last)), token = by_heads.quotient(r);
+                        x[i] = *reinterpret_cast<const uint4 *>(q + static_cast<int64_t>(token) * a.q.token_stride +
+                                                                static_cast<int64_t>(r - token * a.heads) * a.q.head_stride +
+                                                                (rope ? a.cache.rank : block * 64) + ch);
                     }
                 }
 #pragma unroll
@@ -528,22 +619,45 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         *reinterpret_cast<uint4 *>(smem + L::oQ + block * L::kQBlock + row * 128 + ((chunk ^ (row & 7)) * 16)) = x[i];
                 }
             }
-            if (threadIdx.x < NT) {
-                const int row = static_cast<int>(threadIdx.x), even = v.index & 1;
-                uint64_t mask = 0;
-                int64_t to = 0;
-                if (row < R) {
-                    const uint32_t r = static_cast<uint32_t>(v.blk * NT + row), token = by_heads.quotient(r);
-                    mask = a.mask != nullptr ? a.mask[v.s.t0 + static_cast<int>(token)] : (2ull << token) - 1ull;
-                    if (v.s.n < 64) mask &= (1ull << v.s.n) - 1ull;
-                    to = static_cast<int64_t>(v.s.t0 + static_cast<int>(token)) * a.out.token_stride +
-                         static_cast<int64_t>(r - token * a.heads) * a.out.head_stride;
-                }
-                reinterpret_cast<uint64_t *>(smem + L::oMask)[even * NT + row] = mask;
-                reinterpret_cast<int64_t *>(smem + L::oTo)[even * NT + row] = to;
-            }
             fence_proxy_async_smem();
             warp_arrive(bar(L::bQ));
+        };
+        // The latents as the output's product may have them: positions beyond the length become zeros (their
+        // weights are 0, what the ring holds there may be anything), and so do non-finite elements of
+        // drafted tokens, which a row that does not see them must not meet.  The scores of the tile are
+        // complete, so this changes nothing of them; and where all of them are finite, so are the latents,
+        // and are not looked at.  (odd: a warpgroup whose scores are not looks at the whole tile.)
+        auto clean = [&](int tt, bool odd) {
+            const int first = max(0, w.ctx - tt * kPos), stop = min(kPos, w.len - tt * kPos);
+            if (stop < kPos) {
+                const int chunk = static_cast<int>(threadIdx.x) & 15, r0 = static_cast<int>(threadIdx.x) >> 4;
+                for (int u = 0; u < U; ++u) {
+                    uint8_t *const v = smem + L::oU + ((c * U + u) % L::NU) * kUnit + (chunk >> 3) * 8192 + (chunk & 7) * 16;
+                    for (int r = stop + r0; r < kPos; r += 16) *reinterpret_cast<uint4 *>(v + r * 128) = make_uint4(0, 0, 0, 0);
+                }
+            }
+            if (!bar_any(2 + g, 128, odd)) return;
+            const int chunk = p & 15;
+            uint32_t *const bad = bad_s + (w.index & 1) * 2;
+#pragma unroll 1
+            for (int u = 0; u < U; ++u) {
+                uint8_t *const v = smem + L::oU + ((c * U + u) % L::NU) * kUnit + (chunk >> 3) * 8192;
+#pragma unroll 1
+                for (int r = first + (p >> 4); r < stop; r += 8) {
+                    uint4 *const q = reinterpret_cast<uint4 *>(v + r * 128 + (((chunk & 7) ^ (r & 7)) * 16));
+                    uint4 y = *q;
+                    // bit 15 of a half whose exponent is all ones
+                    auto over = [](uint32_t z) { return ((z & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
+                    if ((over(y.x) | over(y.y) | over(y.z) | over(y.w)) == 0) continue;
+                    y.x &= ~((over(y.x) >> 15) * 0xFFFFu);
+                    y.y &= ~((over(y.y) >> 15) * 0xFFFFu);
+                    y.z &= ~((over(y.z) >> 15) * 0xFFFFu);
+                    y.w &= ~((over(y.w) >> 15) * 0xFFFFu);
+                    *q = y;
+                    const int d = tt * kPos + r - w.ctx;
+                    atomicOr(&bad[d >> 5], 1u << (d & 31));
+                }
+            }
         };
         bool more = part_follow(a, next, follow, abort_flag);
         if (more) load_queries(next);
@@ -553,20 +667,21 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             if (bar_any(1, 256, dead || *abort_flag != 0) || !more) break;
             w = next;
             const int T = w.hi - w.lo;
-            const uint64_t *const mask_s = reinterpret_cast<const uint64_t *>(smem + L::oMask) + (w.index & 1) * NT;
-            const int64_t *const to_s = reinterpret_cast<const int64_t *>(smem + L::oTo) + (w.index & 1) * NT;
-            uint32_t *const bad = bad_s + (w.index & 1) * 2;
+            const uint32_t *const bad = bad_s + (w.index & 1) * 2;
             float m_own = kNone;   // of row g * H + p
             bool all_seen = false;
-            if (p < H) nm_s[p] = 0.0f;
+            if (p < H) {
+                nm_s[p] = 0.0f;
+                mask_s[p] = next_mask;
+            }
             F2 l2[G8];
 #pragma unroll
             for (int i = 0; i < G8; ++i) l2[i] = f2(0.0f, 0.0f);
             named_barrier(2 + g, 128);
             for (int t = 0; t < T; ++t, ++c) {
                 const int tt = w.lo + t;
-                const uint32_t buf = c & 1u;
-                const bool edge = (tt + 1) * kPos > w.s.ctx;
+                const uint32_t buf = c & 1u, rs = c % L::NR;
+                const bool edge = (tt + 1) * kPos > w.ctx;
                 uint32_t x[4 * G8];
                 if (!dead) dead = !wait_for(bar(L::bS + buf), (c >> 1) & 1u, abort_flag, a.err, limit);
                 tc_fence_after();
@@ -574,12 +689,19 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 tmem_wait_ld();
                 tc_fence_before();
                 if (!dead) warp_arrive(bar(L::bSFree + buf));
+                bool odd_scores = false;   // of drafted tokens
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 4 * G8; ++i)
+                        odd_scores |= tt * kPos + pos0 + (i & 2) * 4 >= w.ctx && !(fabsf(__uint_as_float(x[i])) <= 3.4028234e38f);
+                }
                 // scores in log2 units above the rows' maxima so far (above 0 where a row has none); what a
                 // row does not see is -inf
                 const F2 scale2 = f2(a.scale_log2, a.scale_log2);
+                float2 ref[G8];
 #pragma unroll
                 for (int i = 0; i < G8; ++i) {
-                    const float2 n = *reinterpret_cast<const float2 *>(nm_s + 8 * i + col);
+                    const float2 n = ref[i] = *reinterpret_cast<const float2 *>(nm_s + 8 * i + col);
                     float s[4];
                     f2_get(f2_fma(f2(x[4 * i], x[4 * i + 1]), scale2, f2(n.x, n.y)), s[0], s[1]);
                     f2_get(f2_fma(f2(x[4 * i + 2], x[4 * i + 3]), scale2, f2(n.x, n.y)), s[2], s[3]);
@@ -589,13 +711,13 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 if (edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int d = tt * kPos + pos0 + 8 * h - w.s.ctx;   // drafted token; masks have no bits beyond n
+                        const int d = tt * kPos + pos0 + 8 * h - w.ctx;   // drafted token; masks have no bits beyond n
                         if (d < 0) continue;
 #pragma unroll
                         for (int i = 0; i < G8; ++i)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                if (d >= 64 || !(mask_s[g * H + 8 * i + col + k] >> d & 1ull)) x[4 * i + 2 * h + k] = __float_as_uint(ninf());
+                                if (d >= 64 || !(mask_s[8 * i + col + k] >> d & 1ull)) x[4 * i + 2 * h + k] = __float_as_uint(ninf());
                     }
                 }
                 float over = ninf();
@@ -625,14 +747,15 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         unseen = mn == kNone;
                         const float n_new = unseen ? 0.0f : -mn;
                         nm_s[p] = n_new;
-                        delta_s[p] = n_new - n;
                         alpha_s[p] = ex2(m_own - mn);
                         m_own = mn;
                     }
                     all_seen = !bar_any(2 + g, 128, unseen);
 #pragma unroll
                     for (int i = 0; i < G8; ++i) {
-                        const float2 n = *reinterpret_cast<const float2 *>(delta_s + 8 * i + col);
+                        float2 n = *reinterpret_cast<const float2 *>(nm_s + 8 * i + col);
+                        n.x -= ref[i].x;
+                        n.y -= ref[i].y;
                         const float2 k = *reinterpret_cast<const float2 *>(alpha_s + 8 * i + col);
                         float s[4];
                         f2_get(f2_add(f2(x[4 * i], x[4 * i + 1]), f2(n.x, n.y)), s[0], s[1]);
@@ -643,7 +766,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     }
                     if (t > 0) {
                         // O so far is complete when the previous product is
-                        if (!dead) dead = !wait_for(bar(L::bPV + ((c - 1) & 1u)), ((c - 1) >> 1) & 1u, abort_flag, a.err, limit);
+                        if (!dead) dead = !wait_for(bar(L::bRE + (c - 1) % L::NR), ((c - 1) / L::NR) & 1u, abort_flag, a.err, limit);
                         tc_fence_after();
                         for (int u = 0; u < U; ++u) {
                             uint32_t o[H];
@@ -662,9 +785,8 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         tmem_wait_st();
                     }
                 }
-                // the weights' buffer is free when the product before the last has read it
-                if (c >= 2 && !dead) dead = !wait_for(bar(L::bPV + buf), ((c >> 1) - 1) & 1u, abort_flag, a.err, limit);
-                uint8_t *const p_buf = smem + L::oP + buf * L::kP + col * 2;
+                // (in the place of the rotary channels: the scores are complete)
+                uint8_t *const p_buf = smem + L::oR + rs * kRopeTile + col * 2;
 #pragma unroll
                 for (int i = 0; i < G8; ++i) {
                     float w0 = ex2(__uint_as_float(x[4 * i])), w1 = ex2(__uint_as_float(x[4 * i + 1]));
@@ -673,38 +795,10 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0, g * G8 + i)) = pack2(w0, w1, false);
                     *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0 + 8, g * G8 + i)) = pack2(w2, w3, false);
                 }
-                if (edge) {
-                    // The latents as the output's product may have them: positions beyond the length become zeros
-                    // (their weights are 0, what the ring holds there may be anything), and so do non-finite
-                    // elements of drafted tokens, which a row that does not see them must not meet.  The scores
-                    // of the tile are complete, so this changes nothing of them.
-                    const int first = max(0, w.s.ctx - tt * kPos), stop = min(kPos, w.s.len - tt * kPos);
-                    const int chunk = static_cast<int>(threadIdx.x) & 15, r0 = static_cast<int>(threadIdx.x) >> 4;
-                    for (int u = 0; u < U; ++u) {
-                        uint8_t *const v = smem + L::oU + ((c * U + u) % L::NU) * kUnit + (chunk >> 3) * 8192;
-                        for (int r = first + r0; r < kPos; r += 16) {
-                            uint4 *const q = reinterpret_cast<uint4 *>(v + r * 128 + (((chunk & 7) ^ (r & 7)) * 16));
-                            if (r >= stop) {
-                                *q = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            uint4 y = *q;
-                            // bit 15 of a half whose exponent is all ones
-                            auto odd = [](uint32_t z) { return ((z & 0x7F807F80u) + 0x00800080u) & 0x80008000u; };
-                            if ((odd(y.x) | odd(y.y) | odd(y.z) | odd(y.w)) == 0) continue;
-                            y.x &= ~((odd(y.x) >> 15) * 0xFFFFu);
-                            y.y &= ~((odd(y.y) >> 15) * 0xFFFFu);
-                            y.z &= ~((odd(y.z) >> 15) * 0xFFFFu);
-                            y.w &= ~((odd(y.w) >> 15) * 0xFFFFu);
-                            *q = y;
-                            const int d = tt * kPos + r - w.s.ctx;
-                            atomicOr(&bad[d >> 5], 1u << (d & 31));
-                        }
-                    }
-                }
+                if (edge) clean(tt, odd_scores);
                 fence_proxy_async_smem();
                 tc_fence_before();
-                if (!dead) warp_arrive(bar(L::bP + buf));
+                if (!dead) warp_arrive(bar(L::bP + rs));
             }
             // ------------------------------------------------------------ the item's end
             // every score of the item is formed: the next one's queries may take the place of these
@@ -723,7 +817,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 for (int i = 0; i < 2 * G8; ++i) red_s[q4 * H + 8 * (i / 2) + col + i % 2] = l[i];
             }
             named_barrier(2 + g, 128);
-            const int R = w.s.n * a.heads - w.blk * NT;   // the block's rows (more, where others follow)
+            const int R = w.n * a.heads - w.blk * NT;   // the block's rows (more, where others follow)
             const int slot = 2 * static_cast<int>(blockIdx.x) + (w.index == 0 ? 0 : 1);
             if (p < H) {
                 const int r = g * H + p;
@@ -736,7 +830,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         part_s(a, NT, gridDim.x, slot)[r] = make_float2(mm, ll);
                     } else if (a.lse != nullptr) {
                         const uint32_t row = static_cast<uint32_t>(w.blk * NT + r), token = by_heads.quotient(row);
-                        a.lse[static_cast<int64_t>(w.s.t0 + static_cast<int>(token)) * a.heads + (row - token * a.heads)] =
+                        a.lse[static_cast<int64_t>(w.t0 + static_cast<int>(token)) * a.heads + (row - token * a.heads)] =
                             none ? ninf() : (mm + log2f(ll)) * 0.69314718055994531f;
                     }
                 }
@@ -746,7 +840,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             tc_fence_after();
             // non-finite latents of drafted tokens (of parts that reach past the context: the products waited
             // for the words there)
-            const uint64_t odd_tokens = w.hi * kPos > w.s.ctx ? *reinterpret_cast<const uint64_t *>(bad) : 0ull;
+            const uint64_t odd_tokens = w.hi * kPos > w.ctx ? *reinterpret_cast<const uint64_t *>(bad) : 0ull;
             for (int u = 0; u < U; ++u) {
                 uint32_t o[H];
                 tmem_ld_rows<H>(tmem + lanes + (2 + u) * NT + g * H, o);
@@ -757,7 +851,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 if (odd_tokens != 0 && ch < a.cache.rank) {
 #pragma unroll 1
                     for (uint64_t left = odd_tokens; left != 0; left &= left - 1) {
-                        const int d = __ffsll(static_cast<long long>(left)) - 1, pos = w.s.ctx + d;
+                        const int d = __ffsll(static_cast<long long>(left)) - 1, pos = w.ctx + d;
                         const int page = a.page_table[static_cast<int64_t>(w.b) * a.max_pages + pos / a.cache.page];
                         if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) continue;
                         const uint32_t v = static_cast<const uint16_t *>(
@@ -765,27 +859,40 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                         if ((v & 0x7F80u) != 0x7F80u) continue;
 #pragma unroll
                         for (int i = 0; i < H; ++i)
-                            if (mask_s[g * H + i] >> d & 1ull) o[i] = 0x7FFFFFFFu;
+                            if (mask_s[i] >> d & 1ull) o[i] = 0x7FFFFFFFu;
                     }
                 }
                 __syncwarp();
-                if (w.whole) {
-                    // two rows at a time: neighbouring lanes trade, and each stores two channels of one row
-                    const int odd = lane & 1;
-                    uint16_t *const out = static_cast<uint16_t *>(a.out.ptr) + (ch & ~1);
+                if (!w.whole) {   // (rows beyond the block's too: they are read by nobody)
+                    float *const po = part_o(a, NT, slot) + g * H * kPitch + ch;
+#pragma unroll
+                    for (int i = 0; i < H; ++i) po[i * kPitch] = __uint_as_float(o[i]);
+                    continue;
+                }
+                // two rows at a time: neighbouring lanes trade, and each stores two channels of one row
+                const int odd = lane & 1;
+                uint32_t two[H / 2];
+#pragma unroll
+                for (int i = 0; i < H; i += 2) {
+                    const float mine = __uint_as_float(odd ? o[i + 1] : o[i]);
+                    const float other = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, odd ? o[i] : o[i + 1], 1));
+                    two[i / 2] = odd ? pack2(other, mine, false) : pack2(mine, other, false);
+                }
+                if (ch >= a.cache.rank) continue;
+                uint16_t *const to = static_cast<uint16_t *>(a.out.ptr) + static_cast<int64_t>(w.t0) * a.out.token_stride + (ch & ~1);
+                const int row0 = w.blk * NT + g * H + odd;
+                if (even_out && g * H + H <= R) {   // rows one step apart, none beyond
+                    uint16_t *at = to + row0 * a.out.head_stride;
+#pragma unroll
+                    for (int i = 0; i < H; i += 2, at += 2 * a.out.head_stride) *reinterpret_cast<uint32_t *>(at) = two[i / 2];
+                } else {
 #pragma unroll
                     for (int i = 0; i < H; i += 2) {
-                        const float mine = __uint_as_float(odd ? o[i + 1] : o[i]);
-                        const float other = __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, odd ? o[i] : o[i + 1], 1));
-                        const int r = g * H + i + odd;
-                        if (r < R && ch < a.cache.rank)
-                            *reinterpret_cast<uint32_t *>(out + to_s[r]) = odd ? pack2(other, mine, false) : pack2(mine, other, false);
+                        const uint32_t r = static_cast<uint32_t>(row0 + i), token = by_heads.quotient(r);
+                        if (g * H + i + odd < R)
+                            *reinterpret_cast<uint32_t *>(to + static_cast<int64_t>(token) * a.out.token_stride +
+                                                          static_cast<int64_t>(r - token * a.heads) * a.out.head_stride) = two[i / 2];
                     }
-                } else {
-                    float *const po = part_o(a, NT, slot) + ch;
-#pragma unroll
-                    for (int i = 0; i < H; ++i)
-                        if (g * H + i < R) po[(g * H + i) * (U * 128)] = __uint_as_float(o[i]);
                 }
             }
             tc_fence_before();   // the next item's first product follows this warp's arrival on bP
@@ -798,7 +905,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         // copies that nobody waited for must land before the CTA leaves
         const uint32_t uc = copied[0], rc = copied[1];
         for (uint32_t j = uc > L::NU ? uc - L::NU : 0; j < uc; ++j) mbar_wait_drain(bar(L::bUF + j % L::NU), (j / L::NU) & 1u, kDrain);
-        for (uint32_t j = rc > kRope ? rc - kRope : 0; j < rc; ++j) mbar_wait_drain(bar(L::bRF + j % kRope), (j / kRope) & 1u, kDrain);
+        const uint32_t qc = copied[2];   // (of one item at a time)
+        if (qc > 0) mbar_wait_drain(bar(L::bQ), (qc - 1) & 1u, kDrain);
+        for (uint32_t j = rc > L::NR ? rc - L::NR : 0; j < rc; ++j) mbar_wait_drain(bar(L::bRF + j % L::NR), (j / L::NR) & 1u, kDrain);
     }
     if (warp == kScoreWarp) {
         tc_fence_after();
@@ -808,26 +917,27 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 
 // ------------------------------------------------------------------ joining the parts
 // For an item that several CTAs shared: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over its parts
-// in order.  A thread takes four channels of one row, its first parts on their way while a warp per row
-// forms the weights, a lane per part.
-constexpr int kJoinThreads = 256;
+// in order.  The parts lie in L2, so what counts is the chain of latencies and how many loads are in
+// flight: a warp works by itself, its first parts on their way while it forms the weights, a lane per
+// part.  MANY: the CTA's eight warps take every eighth part of 128 channels of a row and add up their
+// sums in order; else a warp takes a row.
+constexpr int kJoinWarps = 8;
 
-template <int Q>   // threads of a row, four channels each
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_constant__ LatentArgs a, int nt, int ctas) {
-    constexpr int ROWS = kJoinThreads / Q, AHEAD = 8;
-    __shared__ long long red[4][kJoinThreads / 32];
-    __shared__ float wt[kMaxCtas][ROWS], inv_s[ROWS];
-    const int b = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <bool MANY, int UNITS>   // UNITS: of 128 channels that a warp takes
+__global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const __grid_constant__ LatentArgs a, int nt, int ctas) {
+    constexpr int STEP = MANY ? kJoinWarps : 1, AHEAD = MANY ? 8 : 12 / UNITS;
+    __shared__ float wt_s[kJoinWarps][kMaxCtas];
+    __shared__ float4 sum_s[MANY ? kJoinWarps : 1][32];
+    const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // the lengths are no product of the first kernel, which waited for what came before it
     const Rows s = load_rows(a, nt, b);
-    const int row0 = blockIdx.x * ROWS, R = s.n * a.heads;
-    if (row0 >= R) {
+    const int row = MANY ? blockIdx.x : blockIdx.x * kJoinWarps + warp, R = s.n * a.heads;
+    if (row >= R) {   // (MANY: the whole CTA)
         pdl_wait();
         return;
     }
     long long sums[4] = {0, 0, 0, 0};   // tiles and items before, in all
-    for (int i = threadIdx.x; i < a.seqs; i += kJoinThreads) {
+    for (int i = lane; i < a.seqs; i += 32) {
         const Rows x = load_rows(a, nt, i);
         const long long items = x.tiles > 0 ? x.blocks : 0, tiles = items * x.tiles;
         sums[2] += tiles;
@@ -841,17 +951,10 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sums[k] += __shfl_xor_sync(0xFFFFFFFFu, sums[k], o);
-        if (lane == 0) red[k][warp] = sums[k];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        sums[k] = 0;
-        for (int i = 0; i < kJoinThreads / 32; ++i) sums[k] += red[k][i];
     }
     const int extra = end_cost(a, sums[2], ctas);
     const long long W = sums[2] + extra * sums[3];
-    const int blk = row0 / nt, r0 = row0 % nt;
+    const int blk = row / nt, r = row % nt;
     const long long item0 = sums[0] + extra * sums[1] + static_cast<long long>(blk) * (s.tiles + extra);
     const long long first = item0 + extra;   // the unit of the item's first tile
     const int C = used_ctas(W, ctas);
@@ -863,62 +966,79 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const __grid_
     // the last tile of the one before)
     const bool head_slot = range_lo(W, ca, C) >= item0;
     auto slot = [&](int i) { return 2 * (ca + i) + (i == 0 && !head_slot ? 1 : 0); };
-    const int parts = cb - ca + 1, rr = threadIdx.x / Q, quad = threadIdx.x % Q, pitch = units_of(a.cache.rank) * 128;
-    const bool live = row0 + rr < R && quad * 4 < a.cache.rank;
-    auto part = [&](int i) { return *reinterpret_cast<const float4 *>(part_o(a, nt, slot(i)) + (r0 + rr) * pitch + quad * 4); };
-    float4 x[AHEAD];
+    const int parts = cb - ca + 1, i0 = MANY ? warp : 0, ch = (MANY ? blockIdx.z * 128 : 0) + lane * 4;
+    auto part = [&](int i, int u) { return *reinterpret_cast<const float4 *>(part_o(a, nt, slot(i)) + r * kPitch + u * 128 + ch); };
+    float4 x[AHEAD][UNITS];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
-        if (live && i < parts) x[i] = part(i);
-    for (int r = warp; r < ROWS; r += kJoinThreads / 32) {
-        if (row0 + r >= R) continue;
-        auto ml = [&](int i) { return part_s(a, nt, ctas, slot(i))[r0 + r]; };
-        float m = ninf(), l = 0.0f;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml(i).x);
+        if (i0 + i * STEP < parts) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float ref = m == ninf() ? 0.0f : m;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 y = ml(i);
-            const float k = ex2(y.x - ref);
-            l += y.y * k;
-            wt[i][r] = k;
+            for (int u = 0; u < UNITS; ++u) x[i][u] = part(i0 + i * STEP, u);
         }
+    float m = ninf(), l = 0.0f;
+    float *const wt = wt_s[warp];
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, part_s(a, nt, ctas, slot(i))[r].x);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-        if (lane == 0) {
-            const bool none = m == ninf() && l == 0.0f;
-            inv_s[r] = none ? 0.0f : 1.0f / l;
-            const int row = row0 + r;
-            if (a.lse != nullptr)
-                a.lse[static_cast<int64_t>(s.t0 + row / a.heads) * a.heads + row % a.heads] =
-                    none ? ninf() : (m + log2f(l)) * 0.69314718055994531f;
-        }
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float ref = m == ninf() ? 0.0f : m;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 y = part_s(a, nt, ctas, slot(i))[r];
+        const float k = ex2(y.x - ref);
+        l += y.y * k;
+        wt[i] = k;
     }
-    __syncthreads();
-    if (!live) return;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < parts; i0 += AHEAD) {
-        if (i0 > 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    const bool none = m == ninf() && l == 0.0f;
+    const float inv = none ? 0.0f : 1.0f / l;
+    if (a.lse != nullptr && lane == 0 && blockIdx.z == 0 && i0 == 0)
+        a.lse[static_cast<int64_t>(s.t0 + row / a.heads) * a.heads + row % a.heads] = none ? ninf() : (m + log2f(l)) * 0.69314718055994531f;
+    __syncwarp();
+    float4 o[UNITS];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = i0; p0 < parts; p0 += AHEAD * STEP) {
+        if (p0 > i0) {
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i)
-                if (i0 + i < parts) x[i] = part(i0 + i);
+                if (p0 + i * STEP < parts) {
+#pragma unroll
+                    for (int u = 0; u < UNITS; ++u) x[i][u] = part(p0 + i * STEP, u);
+                }
         }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) {
-            if (i0 + i >= parts) continue;
-            const float k = wt[i0 + i][rr];
-            o.x = fmaf(x[i].x, k, o.x);
-            o.y = fmaf(x[i].y, k, o.y);
-            o.z = fmaf(x[i].z, k, o.z);
-            o.w = fmaf(x[i].w, k, o.w);
+            if (p0 + i * STEP >= parts) continue;
+            const float k = wt[p0 + i * STEP];
+#pragma unroll
+            for (int u = 0; u < UNITS; ++u) {
+                o[u].x = fmaf(x[i][u].x, k, o[u].x);
+                o[u].y = fmaf(x[i][u].y, k, o[u].y);
+                o[u].z = fmaf(x[i][u].z, k, o[u].z);
+                o[u].w = fmaf(x[i][u].w, k, o[u].w);
+            }
         }
     }
-    const float inv = inv_s[rr];
-    const int row = row0 + rr;
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out.ptr) + static_cast<int64_t>(s.t0 + row / a.heads) * a.out.token_stride +
-                               static_cast<int64_t>(row % a.heads) * a.out.head_stride + quad * 4) =
-        make_uint2(pack2(o.x * inv, o.y * inv, false), pack2(o.z * inv, o.w * inv, false));
+    if constexpr (MANY) {
+        sum_s[warp][lane] = o[0];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int i = 1; i < kJoinWarps; ++i) {
+            const float4 y = sum_s[i][lane];
+            o[0].x += y.x;
+            o[0].y += y.y;
+            o[0].z += y.z;
+            o[0].w += y.w;
+        }
+    }
+    uint16_t *const to = static_cast<uint16_t *>(a.out.ptr) + static_cast<int64_t>(s.t0 + row / a.heads) * a.out.token_stride +
+                         static_cast<int64_t>(row % a.heads) * a.out.head_stride + ch;
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+        if (ch + u * 128 < a.cache.rank)
+            *reinterpret_cast<uint2 *>(to + u * 128) =
+                make_uint2(pack2(o[u].x * inv, o[u].y * inv, false), pack2(o[u].z * inv, o[u].w * inv, false));
 }
 
 // ------------------------------------------------------------------ host side
@@ -951,9 +1071,26 @@ bool encode_rows(CUtensorMap *map, const moe_latent_cache_t &c, int first, int c
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as rows (token, head) one step apart, boxes of 64 channels by nt rows; false where they are not.
+bool encode_queries(CUtensorMap *map, const LatentArgs &a, int nt) {
+    EncodeTiledFn fn = encode_fn();
+    const int64_t step = a.heads == 1 ? a.q.token_stride : a.q.head_stride;
+    if (fn == nullptr || a.q.token_stride != a.heads * step || step < a.cache.rank + a.cache.rope) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(a.cache.rank + a.cache.rope), static_cast<cuuint64_t>(a.tokens) * a.heads};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(step) * 2};
+    cuuint32_t box[2] = {64, static_cast<cuuint32_t>(nt)};
+    cuuint32_t estr[2] = {1, 1};
+    return static_cast<int64_t>(a.tokens) * a.heads < (1ll << 31) &&
+           fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.q.ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int NT>
 cudaError_t launch(const LatentArgs &a, int dev, int ctas, int rows, const CUtensorMap &tm_c, const CUtensorMap &tm_r,
                    cudaStream_t s, bool pdl) {
+    CUtensorMap tm_q;
+    const int q_map = encode_queries(&tm_q, a, NT) ? 1 : 0;
+    if (!q_map) tm_q = tm_c;   // not used
     using L = Lay<NT>;
     {
         std::lock_guard<std::mutex> lock(g_mu);
@@ -974,22 +1111,22 @@ cudaError_t launch(const LatentArgs &a, int dev, int ctas, int rows, const CUten
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<NT>, tm_c, tm_r, a, rows);
+    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<NT>, tm_c, tm_r, tm_q, a, rows, q_map);
 }
 
-template <int Q>
+template <bool MANY, int UNITS>
 cudaError_t launch_join(const LatentArgs &a, int nt, int ctas, cudaStream_t s, bool pdl) {
-    constexpr int ROWS = kJoinThreads / Q;
+    const int rows = a.max_tokens * a.heads;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.max_tokens * a.heads + ROWS - 1) / ROWS, a.seqs);
-    cfg.blockDim = dim3(kJoinThreads);
+    cfg.gridDim = MANY ? dim3(rows, a.seqs, units_of(a.cache.rank)) : dim3((rows + kJoinWarps - 1) / kJoinWarps, a.seqs);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_join_kernel<Q>, a, nt, ctas);
+    return cudaLaunchKernelEx(&cfg, latent_join_kernel<MANY, UNITS>, a, nt, ctas);
 }
 
 bool wide16(const moe_heads_t &h) {
@@ -1003,13 +1140,13 @@ bool latent_attn_supports(const moe_latent_cache_t &c, const moe_heads_t &q, con
 }
 
 // For the device that is current when it is asked for: a larger one refuses such a workspace.
-size_t latent_attn_part_bytes(int rank) {
+size_t latent_attn_part_bytes() {
     int dev = 0, sms = 152;
     if (cudaGetDevice(&dev) == cudaSuccess) {
         const int n = sm_count(dev);
         if (n > 0) sms = n;
     }
-    return static_cast<size_t>(sms) * 2 * 64 * (units_of(rank) * 128 * sizeof(float) + sizeof(float2));
+    return static_cast<size_t>(sms) * 2 * 64 * (kPitch * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
@@ -1034,9 +1171,11 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     else
         e = nt == 32 ? launch<32>(a, dev, ctas, box, tm_c, tm_r, s, pdl) : launch<64>(a, dev, ctas, box, tm_c, tm_r, s, pdl);
     if (e != cudaSuccess || a.undivided) return e;
+    // a CTA for every row's 128 channels, when there are many parts and all those CTAs are resident at once
     const int units = units_of(a.cache.rank);
-    if (units == 1) return launch_join<32>(a, nt, ctas, s, pdl);
-    return units == 2 ? launch_join<64>(a, nt, ctas, s, pdl) : launch_join<128>(a, nt, ctas, s, pdl);
+    if (ctas >= 8 * items && static_cast<int64_t>(a.seqs) * rows * units <= 8ll * sms) return launch_join<true, 1>(a, nt, ctas, s, pdl);
+    if (units == 1) return launch_join<false, 1>(a, nt, ctas, s, pdl);
+    return units == 2 ? launch_join<false, 2>(a, nt, ctas, s, pdl) : launch_join<false, 4>(a, nt, ctas, s, pdl);
 }
 
 }  // namespace moe

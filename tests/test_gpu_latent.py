@@ -193,20 +193,26 @@ def test_graph_and_stream():
     assert api.last_device_error(ws) == 0
 
 
-def test_wait_limit():
-    """A limit shorter than any wait: the call gives up, records it, and the next one is right."""
-    p = LatentPass([4000], [4], 16, 512, 64, 64, seed=12)
+@pytest.mark.parametrize("heads", [4, 8, 16])
+def test_wait_that_runs_out(heads):
+    """With a limit of half a microsecond the call gives up and says so, or, where the barriers' hardware waits
+    outlast the limit (they return when the data are there), has its ordinary results; the next call on
+    the same workspace has them in any case."""
+    p = LatentPass([9000, 300], [4, 4], heads, 512, 64, 64, seed=12)
     d = p.device(api)
-    ws = api.latent_attention_workspace(d["cache"], 4, 1, 16)
-    api.set_wait_limit(1)
-    try:
-        api.latent_attention(**d, ws=ws, max_tokens=4)
-        assert api.last_device_error(ws) == 6
-    finally:
-        api.set_wait_limit(0)
-    out, lse = api.latent_attention(**d, ws=ws, return_lse=True, max_tokens=4)
+    ws = api.latent_attention_workspace(d["cache"], 8, 2, heads)
+    base = api.latent_attention(**d, ws=ws, max_tokens=4)
     assert api.last_device_error(ws) == 0
-    p.check(api, out, lse)
+    for limit in (1, 1000):
+        api.set_wait_limit(limit)
+        try:
+            out = api.latent_attention(**d, ws=ws, max_tokens=4)
+            code = api.last_device_error(ws)   # synchronises
+        finally:
+            api.set_wait_limit(0)
+        assert code == 6 or (code == 0 and torch.equal(out, base))
+        assert torch.equal(api.latent_attention(**d, ws=ws, max_tokens=4), base)
+        assert api.last_device_error(ws) == 0
 
 
 # ---------------------------------------------------------------- rows
