@@ -752,7 +752,8 @@ typedef struct {
 } moe_page_pool_t;
 
 /* The caches whose rows live in the pool's pages, one of each layer, every one with the pool's pages
- * and page; either list may be empty (NULL, 0). */
+ * and page; either list may be empty (NULL, 0).  At most 1024 of equal shape one after the other, and
+ * seqs * ceil(bytes of a page's keys / 16384) < 2^23. */
 typedef struct {
     const moe_kv_cache_t *kv;          /* [host] [kv_count] */
     const moe_latent_cache_t *latent;  /* [host] [latent_count] */

@@ -66,16 +66,34 @@ PageArgs page_args(const moe_page_pool_t *pool, void *ws) {
 
 // A plane whose rows are one piece where they lie together.
 Plane plane_of(int64_t page, int64_t row, int64_t seg, int segs, int bytes) {
-    Plane p = {page, row, seg, segs, bytes};
+    Plane p;
+    std::memset(&p, 0, sizeof p);
+    p.page_stride = page;
+    p.row_stride = row;
+    p.seg_stride = seg;
+    p.segs = segs;
+    p.bytes = bytes;
     if (segs == 1 || seg == bytes) {
         p.bytes = bytes * segs;
         p.segs = 1;
         p.seg_stride = p.bytes;
     }
+    p.unit = p.bytes % 16 == 0 ? 16 : 4;
+    p.per_seg = p.bytes / p.unit;
+    p.per_row = p.per_seg * p.segs;
+    p.dense = p.segs == 1 && row == p.bytes;
+    p.by_seg = 0xFFFFFFFFu / static_cast<uint32_t>(p.per_seg);
+    p.by_row = 0xFFFFFFFFu / static_cast<uint32_t>(p.per_row);
     return p;
 }
 bool same(const PageRows &a, const PageRows &b) {
     return a.planes == b.planes && std::memcmp(a.plane, b.plane, sizeof a.plane) == 0;
+}
+
+// The rows' kernels number their work, sequences by layers, planes and pieces of up to 1024 units, in 31 bits.
+bool too_much(const moe_page_pool_t *pool, const Plane &p) {
+    const int64_t pieces = (static_cast<int64_t>(p.per_row) * pool->page + 1023) / 1024;
+    return pieces >= (1ll << 21) || pool->seqs * pieces >= (1ll << 31) / (kLayersLaunch * kPlanes);
 }
 
 constexpr int kMaxLaunches = 16;   // of the rows' kernel in one call: 1024 caches of equal shape
@@ -114,10 +132,11 @@ moe_status_t collect(const moe_page_pool_t *pool, const moe_page_caches_t *cache
         std::memset(&shape, 0, sizeof shape);
         shape.planes = c.dtype == MOE_E4M3 ? 4 : 2;
         shape.plane[0] = shape.plane[1] = plane_of(c.page_stride * es, c.token_stride * es, c.head_stride * es, c.heads, c.dim * es);
-        if (c.dtype == MOE_E4M3) {
-            Plane p = {static_cast<int64_t>(c.heads) * c.page * 4, 4, static_cast<int64_t>(c.page) * 4, c.heads, 4};
-            shape.plane[2] = shape.plane[3] = p;
-        }
+        if (c.dtype == MOE_E4M3)
+            shape.plane[2] = shape.plane[3] =
+                plane_of(static_cast<int64_t>(c.heads) * c.page * 4, 4, static_cast<int64_t>(c.page) * 4, c.heads, 4);
+        for (int k = 0; k < shape.planes; ++k)
+            if (too_much(pool, shape.plane[k])) return MOE_ERR_UNSUPPORTED;
         void *const base[kPlanes] = {c.k, c.v, c.k_scale, c.v_scale};
         const moe_status_t full = out.add(shape, base);
         if (full != MOE_OK) return full;
@@ -131,6 +150,7 @@ moe_status_t collect(const moe_page_pool_t *pool, const moe_page_caches_t *cache
         std::memset(&shape, 0, sizeof shape);
         shape.planes = 1;
         shape.plane[0] = plane_of(c.page_stride * es, c.token_stride * es, 0, 1, (c.rank + c.rope) * es);
+        if (too_much(pool, shape.plane[0])) return MOE_ERR_UNSUPPORTED;
         void *const base[kPlanes] = {c.rows, nullptr, nullptr, nullptr};
         const moe_status_t full = out.add(shape, base);
         if (full != MOE_OK) return full;

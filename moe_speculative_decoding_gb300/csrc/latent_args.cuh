@@ -49,6 +49,9 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl);
 struct Plane {
     int64_t page_stride, row_stride, seg_stride;
     int32_t segs, bytes;
+    int32_t unit, per_seg, per_row;   // bytes moved at a time (16, 4 for scales), units of a piece and of a row
+    int32_t dense;                    // a page's rows are one piece
+    uint32_t by_seg, by_row;          // floor((2^32 - 1) / per_seg), of per_row
 };
 constexpr int kPlanes = 4, kLayersLaunch = 64;   // caches of equal shape in one launch
 struct PageRows {

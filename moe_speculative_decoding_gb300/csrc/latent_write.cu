@@ -94,11 +94,10 @@ __global__ void __launch_bounds__(kRowThreads) latent_any_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ 16 bytes at a time
-// A warp takes a token's cache row, or kPasses * 32 / T of its query rows: T threads (a power of two,
-// T * 16 >= rope) hold a row of rotary channels, 16 each, both halves of 8 pairs of the half layout or
-// 16 consecutive ones, and the token's 8 cosines and sines stay in registers.
-constexpr int kPasses = 2;
-
+// `share` warps to a token.  A token's groups are its cache row (group 0) and its query heads, 32 / T at a time:
+// T threads (a power of two, T * 16 >= rope) hold a row of rotary channels, 16 each, both halves of 8 pairs
+// of the half layout or 16 consecutive ones.  A warp takes every share-th group; the token's slot, position
+// and table row are found once, and the next group's loads are on their way while it works on one.
 template <typename IN>
 struct Eight {
     uint4 v[sizeof(IN) / 2];   // 8 channels as they come from memory
@@ -123,25 +122,57 @@ __device__ __forceinline__ void widen(const Eight<IN> &r, float (&x)[8]) {
     }
 }
 
+
+// Two chunks of eight channels at o0 and o1: one access of 32 bytes where they are one piece.
+template <typename IN>
+__device__ __forceinline__ void fetch_pair(const IN *p, int o0, int o1, Eight<IN> (&r)[2]) {
+    if constexpr (sizeof(IN) == 2) {
+        if (o1 == o0 + 8 && (reinterpret_cast<uintptr_t>(p + o0) & 31u) == 0) {
+            uint4 &x = r[0].v[0], &y = r[1].v[0];
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w), "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                         : "l"(p + o0)
+                         : "memory");
+            return;
+        }
+    }
+    fetch8(p + o0, r[0]);
+    fetch8(p + o1, r[1]);
+}
+template <int TYPE>
+__device__ __forceinline__ void store_pair(void *base, int64_t at, int o0, int o1, const float (&x)[8], const float (&y)[8]) {
+    if constexpr (TYPE == MOE_BF16) {
+        uint16_t *const p = static_cast<uint16_t *>(base) + at + o0;
+        if (o1 == o0 + 8 && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(pack_bf16(x[0], x[1])),
+                         "r"(pack_bf16(x[2], x[3])), "r"(pack_bf16(x[4], x[5])), "r"(pack_bf16(x[6], x[7])), "r"(pack_bf16(y[0], y[1])),
+                         "r"(pack_bf16(y[2], y[3])), "r"(pack_bf16(y[4], y[5])), "r"(pack_bf16(y[6], y[7]))
+                         : "memory");
+            return;
+        }
+    }
+    store8(base, TYPE, at + o0, x);
+    store8(base, TYPE, at + o1, y);
+}
+
 template <typename IN, typename OUT, int T>
-__global__ void __launch_bounds__(kRowThreads) latent_vec_kernel(const __grid_constant__ LatentWriteArgs a, uint32_t tasks, uint32_t total) {
+__global__ void __launch_bounds__(kRowThreads, 4) latent_vec_kernel(const __grid_constant__ LatentWriteArgs a, uint32_t share, uint32_t total) {
     constexpr int kOut = sizeof(OUT) == 2 ? MOE_BF16 : MOE_F32, kIn = sizeof(IN) == 2 ? MOE_BF16 : MOE_F32;
     constexpr int kRows = 32 / T;
     pdl_wait();
     pdl_trigger();
     const uint32_t g = blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
     if (g >= total) return;
-    const int64_t t = g / tasks;
-    const int task = static_cast<int>(g - static_cast<uint32_t>(t) * tasks), lane = static_cast<int>(threadIdx.x & 31);
+    const int64_t t = g / share;
+    const int mine = static_cast<int>(g - static_cast<uint32_t>(t) * share), lane = static_cast<int>(threadIdx.x & 31);
     const int c = lane % T, sub = lane / T;
-    const int slot = task == 0 ? __ldg(a.slots + t) : 0;
+    const int slot = mine == 0 ? __ldg(a.slots + t) : 0;
     const int p = a.rot.rot > 0 ? __ldg(a.rot.positions + t) : 0;
     // what needs no place is on its way beside the slot and the position
     const bool turn = 16 * c < a.rot.rot, split = turn && !a.rot.interleaved, on = 16 * c < a.cache.rope;
     const int o0 = split ? 8 * c : 16 * c, o1 = split ? (a.rot.rot >> 1) + 8 * c : 16 * c + 8;
-    Eight<IN> raw[kPasses][2], lat[2];
-    const int h0 = (task - 1) * kPasses * kRows + sub;
-    if (task == 0) {
+    Eight<IN> lat[2], key[2], next[2];
+    if (mine == 0) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int ch = (j * 32 + lane) * 8;
@@ -149,26 +180,21 @@ __global__ void __launch_bounds__(kRowThreads) latent_vec_kernel(const __grid_co
         }
         if (on && sub == 0) {
             const IN *const k = static_cast<const IN *>(a.k.ptr) + t * a.k.token_stride;
-            fetch8(k + o0, raw[0][0]);
-            fetch8(k + o1, raw[0][1]);
+            fetch_pair(k, o0, o1, key);
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kPasses; ++j) {
-            const int h = h0 + j * kRows;
-            if (on && h < a.q.heads) {
-                const IN *const q = static_cast<const IN *>(a.q.ptr) + t * a.q.token_stride + h * a.q.head_stride;
-                fetch8(q + o0, raw[j][0]);
-                fetch8(q + o1, raw[j][1]);
-            }
-        }
+    }
+    const int step = static_cast<int>(share) * kRows;   // heads
+    int h = (mine == 0 ? static_cast<int>(share) - 1 : mine - 1) * kRows + sub;
+    const IN *q = static_cast<const IN *>(a.q.ptr) + t * a.q.token_stride + h * a.q.head_stride;
+    if (on && h < a.q.heads) {
+        fetch_pair(q, o0, o1, next);
     }
     if (a.rot.rot > 0 && static_cast<uint32_t>(p) >= static_cast<uint32_t>(a.rot.table_positions)) {
         record_error(a.err, MOE_ERR_BAD_ID);
         return;
     }
     float cs[16];
-    if (turn && (task > 0 || sub == 0)) {
+    if (turn) {
         const float4 *const k = reinterpret_cast<const float4 *>(a.rot.table + static_cast<int64_t>(p) * a.rot.rot) + 4 * c;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -194,9 +220,9 @@ __global__ void __launch_bounds__(kRowThreads) latent_vec_kernel(const __grid_co
             for (int i = 0; i < 8; ++i) turn_pair(x[i], y[i], cs[2 * i], cs[2 * i + 1]);
         }
     };
-    if (task == 0) {
-        float v[2][8];
-        float sum = 0.0f;
+    const int64_t at = mine == 0 ? row_at(a, slot) : -1;
+    if (at >= 0) {   // (the whole warp)
+        float v[2][8], sum = 0.0f, scale = 1.0f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             if ((j * 32 + lane) * 8 >= a.cache.rank) continue;
@@ -204,10 +230,7 @@ __global__ void __launch_bounds__(kRowThreads) latent_vec_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum = fmaf(v[j][i], v[j][i], sum);
         }
-        float scale = 1.0f;
         if (a.norm != nullptr) scale = 1.0f / sqrtf(warp_sum(sum) / static_cast<float>(a.cache.rank) + a.eps);
-        const int64_t at = row_at(a, slot);
-        if (at < 0) return;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int ch = (j * 32 + lane) * 8;
@@ -226,29 +249,33 @@ __global__ void __launch_bounds__(kRowThreads) latent_vec_kernel(const __grid_co
         }
         if (on && sub == 0) {
             float x[8], y[8];
-            rotated(raw[0], x, y);
-            store8(a.cache.rows, kOut, at + a.cache.rank + o0, x);
-            store8(a.cache.rows, kOut, at + a.cache.rank + o1, y);
+            rotated(key, x, y);
+            store_pair<kOut>(a.cache.rows, at + a.cache.rank, o0, o1, x, y);
         }
-        return;
     }
-#pragma unroll
-    for (int j = 0; j < kPasses; ++j) {
-        const int h = h0 + j * kRows;
-        if (!on || h >= a.q.heads) continue;
+    if (!on) return;
+    const int64_t q_step = step * a.q.head_stride, out_step = step * a.q_out.head_stride;
+    int64_t to = t * a.q_out.token_stride + h * a.q_out.head_stride;
+    for (; h < a.q.heads; h += step, to += out_step) {
         float x[8], y[8];
-        rotated(raw[j], x, y);
-        const int64_t to = t * a.q_out.token_stride + h * a.q_out.head_stride;
-        store8(a.q_out.ptr, kIn, to + o0, x);
-        store8(a.q_out.ptr, kIn, to + o1, y);
+        rotated(next, x, y);
+        q += q_step;
+        if (h + step < a.q.heads) {
+            fetch_pair(q, o0, o1, next);
+        }
+        store_pair<kIn>(a.q_out.ptr, to, o0, o1, x, y);
     }
 }
 
+// A warp for every group while all of them are resident at once, so that a short call is short; else one to a
+// token.
 template <typename IN, typename OUT, int T>
 cudaError_t launch(const LatentWriteArgs &a, cudaStream_t s, bool pdl) {
-    constexpr int rows = kPasses * 32 / T;
-    const uint32_t tasks = 1 + (a.q.heads + rows - 1) / rows, total = tasks * static_cast<uint32_t>(a.tokens);
-    return launch_flat(latent_vec_kernel<IN, OUT, T>, (total + kRowThreads / 32 - 1) / (kRowThreads / 32), s, pdl, a, tasks, total);
+    constexpr int rows = 32 / T;
+    uint32_t share = 1 + (a.q.heads + rows - 1) / rows;
+    if (static_cast<int64_t>(share) * a.tokens > 152ll * 32) share = 1;
+    const uint32_t total = share * static_cast<uint32_t>(a.tokens);
+    return launch_flat(latent_vec_kernel<IN, OUT, T>, (total + kRowThreads / 32 - 1) / (kRowThreads / 32), s, pdl, a, share, total);
 }
 template <typename IN, typename OUT>
 cudaError_t by_rope(const LatentWriteArgs &a, cudaStream_t s, bool pdl) {

@@ -3,9 +3,9 @@
 //
 // A page's holders are counted (refs; 0: free).  Which pages a call hands out goes by their numbers and the
 // sequences' order alone, not by the order in which threads run: free pages are found in ascending order and
-// requests are met by a prefix sum, so one CTA does the bookkeeping of reserve and fork (counts are 4 bytes
-// a page: 128 KB for 32,768 pages a step).  The rows move in a second kernel, in all layers at once, as
-// the bits they are: its bound is memory traffic, each row read once and written once.
+// requests are met by a prefix sum, so one CTA does the bookkeeping of reserve (counts are 4 bytes a page,
+// 32 KB for 8,192 pages a step).  The rows move in a second kernel, in all layers at once, as the bits
+// they are: its bound is memory traffic, each row read once and written once.
 #include <algorithm>
 
 #include "common.cuh"
@@ -15,9 +15,10 @@ namespace moe {
 namespace {
 
 constexpr int kBook = 1024;          // threads of the bookkeeping CTA
-constexpr int kStep = kBook * 32;    // pages it looks at in a step
+constexpr int kMine = 8;             // pages a thread looks at in a step
+constexpr int kStep = kBook * kMine;
 
-// Lists in the workspace: [4] (copies to make), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
+// Lists in the workspace: [4] (copies to make, CTAs of a fork that are done, most rows of a copy), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
 // rows to move), [pages] free pages in order.
 __device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
 __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
@@ -53,7 +54,8 @@ __device__ __forceinline__ int before_me(int v, int *tmp, int &total) {
 
 // ------------------------------------------------------------------ reserve
 __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_constant__ PageArgs a) {
-    __shared__ int shared_s[kBook], tmp[32], copies_s, fail_s;
+    __shared__ __align__(16) int shared_s[kBook];
+    __shared__ int tmp[32], copies_s, rows_s, fail_s;
     pdl_wait();
     pdl_trigger();
     const int b = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -87,36 +89,53 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
     const bool shared = !bad && holders > 1;
     shared_s[b] = shared ? at : -1;
     if (b == 0) {
-        copies_s = 0;
+        copies_s = rows_s = 0;
         fail_s = kBook;
     }
     __syncthreads();
     // holders before this sequence that take a copy: its own is needed while others are left
     auto sharers = [&](int stop) {
-        int n = 0;
-        for (int i = 0; i < stop; ++i) n += shared_s[i] == at;
+        int n = 0, i = 0;
+        for (; i + 4 <= stop; i += 4) {
+            const int4 x = *reinterpret_cast<const int4 *>(shared_s + i);
+            n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
+        }
+        for (; i < stop; ++i) n += shared_s[i] == at;
         return n;
     };
     bool copy = shared && holders - sharers(b) > 1;
     const int extra = want - held + (copy ? 1 : 0);
     int total;
     const int mine = before_me(extra, tmp, total);
-    // the lowest free pages, as many as are asked for
+    // the lowest free pages, as many as are asked for: the next step's counts are on their way while this
+    // one's free pages are numbered
     int found = 0;
     int32_t *const order = order_of(a);
-    for (int64_t base = 0; found < total && base < pool.pages; base += kStep) {
-        // a warp looks at 1024 pages, a lane keeps the 32 from lane * 32 on
-        uint32_t free = 0;
+    const bool wide = (reinterpret_cast<uintptr_t>(pool.refs) & 15u) == 0;
+    auto counts = [&](int64_t base, int (&x)[kMine]) {
+        const int64_t p = base + static_cast<int64_t>(b) * kMine;
+        if (wide && p + kMine <= pool.pages) {
+            *reinterpret_cast<int4 *>(x) = *reinterpret_cast<const int4 *>(pool.refs + p);
+            *reinterpret_cast<int4 *>(x + 4) = *reinterpret_cast<const int4 *>(pool.refs + p + 4);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-            const int64_t p = base + warp * 1024 + k * 32 + lane;
-            const uint32_t set = __ballot_sync(0xFFFFFFFFu, p < pool.pages && pool.refs[p] == 0);
-            if (lane == k) free = set;
+            for (int k = 0; k < kMine; ++k) x[k] = p + k < pool.pages ? pool.refs[p + k] : 1;
         }
-        int here;
-        int rank = found + before_me(__popc(free), tmp, here);
-        for (uint32_t left = free; left != 0 && rank < total; left &= left - 1)
-            order[rank++] = static_cast<int32_t>(base + warp * 1024 + lane * 32 + __ffs(left) - 1);
+    };
+    alignas(16) int now[kMine], next[kMine];
+    if (total > 0) counts(0, now);
+    for (int64_t base = 0; found < total && base < pool.pages; base += kStep) {
+        counts(base + kStep, next);
+        int n = 0, here;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) n += now[k] == 0;
+        int rank = found + before_me(n, tmp, here);
+        const int p = static_cast<int>(base) + b * kMine;
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+            if (now[k] == 0 && rank < total) order[rank++] = p + k;
+            now[k] = next[k];
+        }
         found += here;
     }
     bool ok = in && !bad && (extra == 0 || mine + extra <= found);
@@ -138,6 +157,7 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
             e[0] = at;
             e[1] = page;
             e[2] = rows;
+            atomicMax(&rows_s, rows);
         }
     }
     // the pages behind those held, a warp's sequences one after the other
@@ -152,63 +172,72 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
         }
     }
     __syncthreads();
-    if (b == 0) a.lists[0] = copies_s;
+    if (b == 0) {
+        a.lists[0] = copies_s;
+        a.lists[2] = rows_s;
+    }
 }
 
 // ------------------------------------------------------------------ rows
 struct Divide {   // of numbers below 2^31, as a product
     uint32_t d, recip;
-    __device__ __forceinline__ explicit Divide(int by) : d(static_cast<uint32_t>(by)), recip(0xFFFFFFFFu / static_cast<uint32_t>(by)) {}
+    __device__ __forceinline__ explicit Divide(uint32_t by) : d(by), recip(0xFFFFFFFFu / by) {}
     __device__ __forceinline__ uint32_t operator()(uint32_t x) const {
         const uint32_t q = __umulhi(x, recip);
         return q + (x - q * d >= d ? 1u : 0u);
     }
 };
-__device__ __forceinline__ void copy_unit(const uint8_t *from, uint8_t *to, bool wide) {
-    if (wide)
-        *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
-    else
-        *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(from);
+__device__ __forceinline__ uint32_t quotient(uint32_t x, uint32_t d, uint32_t recip) {
+    const uint32_t q = __umulhi(x, recip);
+    return q + (x - q * d >= d ? 1u : 0u);
 }
 
 // The first rows of listed pages to others.  An item is up to kUnits units of 16 bytes (4 for scales) of
 // one plane of one layer; the CTAs step over the items, whose number the bookkeeping found.
 constexpr int kCopy = 256, kUnits = 4 * kCopy;
 
-__global__ void __launch_bounds__(kCopy) pages_copy_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int slices) {
+__global__ void __launch_bounds__(kCopy) pages_copy_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int row_units) {
     pdl_wait();
     pdl_trigger();
-    const int64_t items = static_cast<int64_t>(a.lists[0]) * p.layers * p.planes * slices;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        uint32_t i = static_cast<uint32_t>(item / slices);
-        const int slice = static_cast<int>(item - static_cast<int64_t>(i) * slices);
-        const int which = static_cast<int>(i % p.planes);
-        i /= p.planes;
-        const int layer = static_cast<int>(i % p.layers);
-        const int4 e = *reinterpret_cast<const int4 *>(list_of(a, static_cast<int>(i / p.layers)));
+    const int copies = a.lists[0], slices = (a.lists[2] * row_units + kUnits - 1) / kUnits;   // of the copy with most rows
+    if (copies == 0) return;
+    // (the launch keeps the items below 2^31; with divisions for every item and unit the integer pipe was
+    // the bound, 28 us for 66 MB)
+    const uint32_t whole = static_cast<uint32_t>(copies * p.layers * p.planes), items = whole * static_cast<uint32_t>(slices);
+    const Divide by_whole(whole), by_copies(static_cast<uint32_t>(copies));
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        // (all pages' first slices before their second ones, which copies of few rows do not have)
+        const uint32_t slice = by_whole(item), i = item - slice * whole, at = by_copies(i);
+        const int layer = static_cast<int>(p.planes == 1 ? at : (p.planes == 2 ? at >> 1 : at >> 2)), which = static_cast<int>(at & (p.planes - 1));
+        const int4 e = *reinterpret_cast<const int4 *>(list_of(a, static_cast<int>(i - at * copies)));
         const Plane &pl = p.plane[which];
-        const bool wide = pl.bytes % 16 == 0;
-        const int unit = wide ? 16 : 4, per_seg = pl.bytes / unit, per_row = per_seg * pl.segs, total = per_row * e.z;
+        const int total = pl.per_row * e.z, u0 = static_cast<int>(slice) * kUnits + static_cast<int>(threadIdx.x);
+        if (u0 >= total) continue;
         const uint8_t *const from = static_cast<const uint8_t *>(p.base[layer][which]) + e.x * pl.page_stride;
         uint8_t *const to = static_cast<uint8_t *>(p.base[layer][which]) + e.y * pl.page_stride;
-        const Divide by_row(per_row), by_seg(per_seg);
-        const int u0 = slice * kUnits + static_cast<int>(threadIdx.x);
-        auto place = [&](int u) {
-            const int r = static_cast<int>(by_row(u)), w = u - r * per_row, sg = static_cast<int>(by_seg(w));
-            return r * pl.row_stride + sg * pl.seg_stride + static_cast<int64_t>(w - sg * per_seg) * unit;
-        };
-        if (wide) {
+        if (pl.dense && pl.unit == 16) {
+            const uint4 *const src = reinterpret_cast<const uint4 *>(from) + u0;
+            uint4 *const dst = reinterpret_cast<uint4 *>(to) + u0;
             uint4 x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (u0 + k * kCopy < total) x[k] = *reinterpret_cast<const uint4 *>(from + place(u0 + k * kCopy));
+                if (u0 + k * kCopy < total) x[k] = src[k * kCopy];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (u0 + k * kCopy < total) *reinterpret_cast<uint4 *>(to + place(u0 + k * kCopy)) = x[k];
-        } else {
+                if (u0 + k * kCopy < total) dst[k * kCopy] = x[k];
+            continue;
+        }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (u0 + k * kCopy < total) copy_unit(from + place(u0 + k * kCopy), to + place(u0 + k * kCopy), false);
+        for (int k = 0; k < 4; ++k) {
+            const int u = u0 + k * kCopy;
+            if (u >= total) continue;
+            const int r = static_cast<int>(quotient(u, pl.per_row, pl.by_row)), w = u - r * pl.per_row;
+            const int sg = static_cast<int>(quotient(w, pl.per_seg, pl.by_seg));
+            const int64_t off = r * pl.row_stride + sg * pl.seg_stride + static_cast<int64_t>(w - sg * pl.per_seg) * pl.unit;
+            if (pl.unit == 16)
+                *reinterpret_cast<uint4 *>(to + off) = *reinterpret_cast<const uint4 *>(from + off);
+            else
+                *reinterpret_cast<uint32_t *>(to + off) = *reinterpret_cast<const uint32_t *>(from + off);
         }
     }
 }
@@ -264,11 +293,13 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
     __shared__ int source_s[MOE_MAX_TREE_TOKENS][2], target_s[MOE_MAX_TREE_TOKENS][2];   // page, row
     pdl_wait();
     pdl_trigger();
-    const int64_t items = static_cast<int64_t>(a.pool.seqs) * p.layers * slices;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int b = static_cast<int>(item / (p.layers * slices)), rest = static_cast<int>(item - static_cast<int64_t>(b) * p.layers * slices);
-        const int layer = rest / slices;
-        int column = (rest - layer * slices) * kMove + static_cast<int>(threadIdx.x);
+    const uint32_t seqs = static_cast<uint32_t>(a.pool.seqs), whole = seqs * static_cast<uint32_t>(p.layers);
+    const uint32_t items = whole * static_cast<uint32_t>(slices);   // (the launch keeps them below 2^31)
+    const Divide by_whole(whole), by_seqs(seqs);
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const uint32_t slice = by_whole(item), i = item - slice * whole, layer = by_seqs(i);
+        const int b = static_cast<int>(i - layer * seqs);
+        int column = static_cast<int>(slice) * kMove + static_cast<int>(threadIdx.x);
         const int32_t *const e = list_of(a, b);
         const int ctx = e[0], count = e[1];
         if (count == 0) continue;
@@ -287,17 +318,11 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
         }
         __syncthreads();
         if (column >= columns) continue;
-        int which = 0, unit = 16, per_row = 0;
-        for (;; ++which) {
-            const Plane &pl = p.plane[which];
-            unit = pl.bytes % 16 == 0 ? 16 : 4;
-            per_row = pl.bytes / unit * pl.segs;
-            if (column < per_row) break;
-            column -= per_row;
-        }
+        int which = 0;
+        while (column >= p.plane[which].per_row) column -= p.plane[which++].per_row;
         const Plane &pl = p.plane[which];
-        const int per_seg = pl.bytes / unit, seg = column / per_seg;
-        uint8_t *const base = static_cast<uint8_t *>(p.base[layer][which]) + seg * pl.seg_stride + static_cast<int64_t>(column - seg * per_seg) * unit;
+        const int unit = pl.unit, seg = static_cast<int>(quotient(column, pl.per_seg, pl.by_seg));
+        uint8_t *const base = static_cast<uint8_t *>(p.base[layer][which]) + seg * pl.seg_stride + static_cast<int64_t>(column - seg * pl.per_seg) * unit;
         auto at = [&](const int (&x)[2]) { return base + x[0] * pl.page_stride + x[1] * pl.row_stride; };
         constexpr int AHEAD = 8;
         for (int i0 = 0; i0 < count; i0 += AHEAD) {
@@ -325,14 +350,17 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ fork, free
+// Every CTA checks all pairs (a thread each) and copies the page numbers of some, a warp to a pair; the last
+// to be done writes what the checks read, the lengths and the numbers of pages held.
 __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant__ PageArgs a) {
-    __shared__ int dst_s[kBook];
+    __shared__ __align__(16) int dst_s[kBook];
+    __shared__ int src_s[kBook], pages_s[kBook], last_s;
     pdl_wait();
     pdl_trigger();
-    const int i = threadIdx.x, lane = threadIdx.x & 31;
+    const int i = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const moe_page_pool_t &pool = a.pool;
     const bool in = i < a.items;
-    int src = 0, dst = -1, length = 0, pages = 0;
+    int src = 0, dst = -1, length = 0;
     bool ok = in;
     if (in) {
         src = a.src[i];
@@ -345,23 +373,41 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant
         }
     }
     dst_s[i] = dst;
-    __syncthreads();   // all is read that the call may write
-    for (int k = 0; ok && k < i; ++k) ok = dst_s[k] != dst;
-    if (in && !ok) record_error(a.err, MOE_ERR_BAD_ID);
-    if (ok) {
-        pages = (length + pool.page - 1) / pool.page;
-        pool.held[dst] = pages;
-        a.length_out[dst] = length;
+    src_s[i] = src;
+    __syncthreads();
+    int same = 0, k = 0;   // pairs before this one with its target
+    for (; k + 4 <= i && ok; k += 4) {
+        const int4 x = *reinterpret_cast<const int4 *>(dst_s + k);
+        same += (x.x == dst) + (x.y == dst) + (x.z == dst) + (x.w == dst);
     }
-    for (uint32_t left = __ballot_sync(0xFFFFFFFFu, ok && pages > 0); left != 0; left &= left - 1) {
-        const int l = __ffs(left) - 1, n = __shfl_sync(0xFFFFFFFFu, pages, l);
-        const int32_t *const from = table_of(a, __shfl_sync(0xFFFFFFFFu, src, l));
-        int32_t *const to = table_of(a, __shfl_sync(0xFFFFFFFFu, dst, l));
+    for (; k < i && ok; ++k) same += dst_s[k] == dst;
+    ok = ok && same == 0;
+    if (in && !ok) record_error(a.err, MOE_ERR_BAD_ID);
+    const int pages = ok ? (length + pool.page - 1) / pool.page : 0;
+    pages_s[i] = pages;
+    __syncthreads();
+    for (int p = blockIdx.x * 32 + warp; p < a.items; p += gridDim.x * 32) {
+        const int n = pages_s[p];
+        if (n == 0) continue;
+        const int32_t *const from = table_of(a, src_s[p]);
+        int32_t *const to = table_of(a, dst_s[p]);
+#pragma unroll 4
         for (int j = lane; j < n; j += 32) {
             const int page = from[j];
             to[j] = page;
             if (in_pool(a, page)) atomicAdd(pool.refs + page, 1);
         }
+    }
+    if (gridDim.x > 1) {
+        __syncthreads();
+        if (i == 0) last_s = atom_add_acq_rel_gpu(reinterpret_cast<uint32_t *>(a.lists + 1), 1u) == gridDim.x - 1;
+        __syncthreads();
+        if (!last_s) return;
+        if (i == 0) a.lists[1] = 0;   // for the next call
+    }
+    if (ok) {
+        pool.held[dst] = pages;
+        a.length_out[dst] = length;
     }
 }
 
@@ -388,8 +434,11 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__
     held = __shfl_sync(0xFFFFFFFFu, held, 0);
     if (held == 0) return;
     const int32_t *const table = table_of(a, b);
-    for (int j = lane; j < held; j += 32)
-        if (in_pool(a, table[j])) atomicSub(a.pool.refs + table[j], 1);
+#pragma unroll 4
+    for (int j = lane; j < held; j += 32) {
+        const int page = table[j];
+        if (in_pool(a, page)) atomicSub(a.pool.refs + page, 1);
+    }
 }
 
 template <typename K, typename... Args>
@@ -406,7 +455,6 @@ cudaError_t launch(K kernel, unsigned grid, unsigned threads, cudaStream_t s, bo
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-int units_of_row(const Plane &p) { return p.bytes / (p.bytes % 16 == 0 ? 16 : 4) * p.segs; }
 constexpr int64_t kSms = 152;
 
 }  // namespace
@@ -416,11 +464,11 @@ size_t pages_list_bytes(const moe_page_pool_t &pool) { return 16 + 16 * static_c
 cudaError_t launch_pages_reserve(const PageArgs &a, const PageRows *rows, int launches, cudaStream_t s, bool pdl) {
     cudaError_t e = launch(pages_reserve_kernel, 1, kBook, s, pdl, a);
     for (int i = 0; i < launches && e == cudaSuccess; ++i) {
-        int64_t most = 1;   // units of a page in a plane
-        for (int k = 0; k < rows[i].planes; ++k) most = std::max<int64_t>(most, static_cast<int64_t>(units_of_row(rows[i].plane[k])) * a.pool.page);
-        const int slices = static_cast<int>((most + kUnits - 1) / kUnits);
+        int most = 1;   // units of a row in a plane
+        for (int k = 0; k < rows[i].planes; ++k) most = std::max(most, rows[i].plane[k].per_row);
+        const int64_t slices = (static_cast<int64_t>(most) * a.pool.page + kUnits - 1) / kUnits;
         const int64_t items = static_cast<int64_t>(a.pool.seqs) * rows[i].layers * rows[i].planes * slices;
-        e = launch(pages_copy_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 8)), kCopy, s, pdl, a, rows[i], slices);
+        e = launch(pages_copy_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 8)), kCopy, s, pdl, a, rows[i], most);
     }
     return e;
 }
@@ -430,7 +478,7 @@ cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int lau
     if (a.path == nullptr) return e;   // nothing moves
     for (int i = 0; i < launches && e == cudaSuccess; ++i) {
         int columns = 0;
-        for (int k = 0; k < rows[i].planes; ++k) columns += units_of_row(rows[i].plane[k]);
+        for (int k = 0; k < rows[i].planes; ++k) columns += rows[i].plane[k].per_row;
         const int slices = (columns + kMove - 1) / kMove;
         const int64_t items = static_cast<int64_t>(a.pool.seqs) * rows[i].layers * slices;
         e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, rows[i], columns, slices);
@@ -438,7 +486,9 @@ cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int lau
     return e;
 }
 
-cudaError_t launch_pages_fork(const PageArgs &a, cudaStream_t s, bool pdl) { return launch(pages_fork_kernel, 1, kBook, s, pdl, a); }
+cudaError_t launch_pages_fork(const PageArgs &a, cudaStream_t s, bool pdl) {
+    return launch(pages_fork_kernel, static_cast<unsigned>(std::min((a.items + 31) / 32, 32)), kBook, s, pdl, a);
+}
 
 cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t s, bool pdl) {
     return launch(pages_free_kernel, static_cast<unsigned>((a.items + 7) / 8), 256, s, pdl, a);
