@@ -741,6 +741,8 @@ moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_hea
  * them; entries beyond are left as they were.  Pages behind the one with its last token are its own
  * (the calls see to that).  Device-only problems (ids, lengths, pages or paths out of range) are
  * recorded as MOE_ERR_BAD_ID in the error word of ws, and the sequence concerned is left as it was.
+ * Calls on one pool, and calls that share a workspace, run one after the other (on one stream, or ordered by
+ * events).
  */
 
 /* The pool, in memory the caller owns; refs and held all zero: every page free, nothing held. */
@@ -801,8 +803,8 @@ moe_status_t moe_pages_fork(const moe_page_pool_t *pool, const int32_t *src, con
  * ceil(after[b] / page) are given up.  A negative count leaves the sequence alone (after[b] = ctx[b]).
  *   path [dev] int32 [seqs, max_path], 0 <= path[b][0] < path[b][1] < ..., or NULL for the first count[b]
  *   tokens (nothing moves); count [dev] int32 [seqs], at most max_path; after [dev] int32 [seqs] or
- *   NULL, may be ctx itself.  ctx[b] + path[b][i] must lie in the pages held; the pages written must be
- *   the sequence's own, as moe_pages_reserve leaves them.  1 <= max_path <= MOE_MAX_TREE_TOKENS.
+ *   NULL, may be ctx itself.  ctx[b] + path[b][i] must lie in the pages held, and pages that rows move to
+ *   must be the sequence's own, as moe_pages_reserve leaves them.  1 <= max_path <= MOE_MAX_TREE_TOKENS.
  *   Asynchronous on s.
  */
 moe_status_t moe_pages_accept(const moe_page_pool_t *pool, const int32_t *ctx, const int32_t *path, const int32_t *count,

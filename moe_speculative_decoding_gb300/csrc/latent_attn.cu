@@ -38,8 +38,6 @@ namespace moe {
 namespace {
 
 constexpr int kPos = 64;                        // positions of a tile
-// How many tiles ahead of its copy a tile is fetched into L2.
-constexpr int kAhead = 2;
 constexpr int kProducerWarp = 8, kScoreWarp = 9, kOutWarp = 11, kThreads = 384;   // two score warps
 constexpr uint32_t kUnit = 16384, kRopeTile = 8192;
 
@@ -78,12 +76,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
         : "memory");
-}
-// The box on its way into L2.
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(c0),
-                 "r"(c1), "r"(c2)
-                 : "memory");
 }
 // 16 lanes (the quarter's first: an accumulator with M = 64 has 16 rows in each quarter) by 8 N columns:
 // of columns 8 i .. 8 i + 7 a thread gets lane / 4's (2 (lane % 4), + 1) in r[4 i], r[4 i + 1], and those of
@@ -263,8 +255,8 @@ __device__ __forceinline__ bool part_next(const LatentArgs &a, Part &w) {
     return false;
 }
 // The producer walks, the others follow it through a ring of records.  It is at most four items ahead of the
-// last: it waits for the rotary tile before its last to be scored, scores for the queries, those for the
-// scores of the item before, and these for the output's product two tiles before.
+// last: before its next item it waits for a place that the output's product of the tile three before
+// frees, and that product's weights came from scores of all tiles up to it.
 template <int NT>
 __device__ __forceinline__ bool part_lead(const LatentArgs &a, Part &w, Follow &f) {
     const bool more = part_next<NT>(a, w);
@@ -391,17 +383,6 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 const uint32_t rs = rc % L::NR;
                 if (!(ok = wait_for(bar(L::bRE + rs), ((rc / L::NR) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
                 const uint32_t r_dst = base + L::oR + rs * kRopeTile, r_bar = bar(L::bRF + rs);
-                // the tile kAhead further, to L2
-                if (NT == 64 && w.s.blocks == 1 && tt + kAhead < w.hi) {
-                    const int at = (k + kAhead) * boxes + box;
-                    const int page_a = __shfl_sync(0xFFFFFFFFu, at < 32 ? page_now : page_next, at & 31);
-                    const int row_a = __shfl_sync(0xFFFFFFFFu, at < 32 ? row_now : row_next, at & 31);
-                    if (half < 2 && static_cast<uint32_t>(page_a) < static_cast<uint32_t>(kc.pages)) {
-                        for (int u = 0; u < U; ++u) tma_prefetch_3d(&tm_c, u * 128 + half * 64, row_a, page_a);
-                        if (half == 0) tma_prefetch_3d(&tm_r, 0, row_a, page_a);
-                    }
-                    __syncwarp();
-                }
                 if (boxes == 1) {
                     // one box: issued by an elected lane from uniform registers (by one lane of a condition
                     // on the lane a unit took 450 cycles)
@@ -678,17 +659,21 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
 #pragma unroll
             for (int i = 0; i < G8; ++i) l2[i] = f2(0.0f, 0.0f);
             named_barrier(2 + g, 128);
-            for (int t = 0; t < T; ++t, ++c) {
+            // The first item begins with a pass over nothing, which brings the loop's code into the instruction
+            // caches while the first tiles are on their way: after them, behind all CTAs' copies, the first tile's
+            // weights took 4,500 cycles, not 600, and the ring stood still meanwhile.
+            for (int t = w.index == 0 ? -1 : 0; t < T; ++t) {
+                const bool dry = t < 0;
                 const int tt = w.lo + t;
                 const uint32_t buf = c & 1u, rs = c % L::NR;
-                const bool edge = (tt + 1) * kPos > w.ctx;
+                const bool edge = !dry && (tt + 1) * kPos > w.ctx;
                 uint32_t x[4 * G8];
-                if (!dead) dead = !wait_for(bar(L::bS + buf), (c >> 1) & 1u, abort_flag, a.err, limit);
+                if (!dead && !dry) dead = !wait_for(bar(L::bS + buf), (c >> 1) & 1u, abort_flag, a.err, limit);
                 tc_fence_after();
                 tmem_ld_16x256<G8>(tmem + lanes + buf * NT + g * H, x);
                 tmem_wait_ld();
                 tc_fence_before();
-                if (!dead) warp_arrive(bar(L::bSFree + buf));
+                if (!dead && !dry) warp_arrive(bar(L::bSFree + buf));
                 bool odd_scores = false;   // of drafted tokens
                 if (edge) {
 #pragma unroll
@@ -792,13 +777,25 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     float w0 = ex2(__uint_as_float(x[4 * i])), w1 = ex2(__uint_as_float(x[4 * i + 1]));
                     float w2 = ex2(__uint_as_float(x[4 * i + 2])), w3 = ex2(__uint_as_float(x[4 * i + 3]));
                     l2[i] = f2_add(l2[i], f2_add(f2(w0, w1), f2(w2, w3)));
-                    *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0, g * G8 + i)) = pack2(w0, w1, false);
-                    *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0 + 8, g * G8 + i)) = pack2(w2, w3, false);
+                    if (!dry) {
+                        *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0, g * G8 + i)) = pack2(w0, w1, false);
+                        *reinterpret_cast<uint32_t *>(p_buf + p_chunk<NT>(pos0 + 8, g * G8 + i)) = pack2(w2, w3, false);
+                    }
                 }
                 if (edge) clean(tt, odd_scores);
                 fence_proxy_async_smem();
                 tc_fence_before();
+                if (dry) {   // as before it
+                    m_own = kNone;
+                    all_seen = false;
+                    if (p < H) nm_s[p] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < G8; ++i) l2[i] = f2(0.0f, 0.0f);
+                    named_barrier(2 + g, 128);
+                    continue;
+                }
                 if (!dead) warp_arrive(bar(L::bP + rs));
+                ++c;
             }
             // ------------------------------------------------------------ the item's end
             // every score of the item is formed: the next one's queries may take the place of these
@@ -1163,7 +1160,10 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     const int rows = a.max_tokens * a.heads, nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kPos - 1) / kPos;
     const long long items = static_cast<long long>(a.seqs) * ((rows + nt - 1) / nt);
-    a.undivided = item_tiles <= 4 || (2 * items >= sms && item_tiles <= 12);
+    // Short contexts: an item's few tiles one after the other take less time than another end of an item and the
+    // launch that joins the parts.  16 heads of one token: one sequence of five tiles 10.8 us undivided against
+    // 9.7, of sixteen 20.9 against 9.0; 64 sequences of five 13.8 against 15.8, 16 of fifteen 20.0 against 17.3.
+    a.undivided = item_tiles <= 4 || (4 * items >= sms && item_tiles <= 8) || (2 * items >= sms && item_tiles <= 12);
     // no more CTAs than the page tables could fill with tiles
     const int ctas = static_cast<int>(std::min<long long>(sms, items * item_tiles));
     if (nt == 16)

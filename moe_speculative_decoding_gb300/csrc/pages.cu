@@ -266,6 +266,15 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
             if (__any_sync(0xFFFFFFFFu, i < count && p != i)) moves = count;
             last = __shfl_sync(0xFFFFFFFFu, p, 31);
         }
+        // rows that move go to pages that nobody else holds
+        if (!bad && moves > 0) {
+            bool other = false;
+            for (int j = ctx / pool.page + lane; j <= (ctx + count - 1) / pool.page; j += 32) {
+                const int page = table_of(a, b)[j];
+                other |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(pool.pages) || pool.refs[page] > 1;
+            }
+            bad = __any_sync(0xFFFFFFFFu, other);
+        }
     }
     if (bad && lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
     const bool act = !bad && count >= 0;

@@ -206,6 +206,35 @@ def test_bad_indices_are_recorded_and_leave_their_sequence():
     assert sum(b.ref.refs) == 0
 
 
+def test_rows_do_not_move_into_shared_pages():
+    b = Both([kv(20, 4), latent(20, 4)], 3, 6)
+    b.reserve([12, 0, 0])
+    b.accept(None, [6, 0, 0])
+    b.fork([0], [1])
+    # sequence 0 drafts without reserving: its part-filled page is the other's too
+    before = b.expect([])
+    after = api.pages_accept(b.pool, i32(b.length), i32([[1], [0], [0]]), i32([1, -1, -1]))
+    assert after.tolist() == b.length
+    b.check(before, 5)
+    b.reserve([4, 0, 0])
+    b.accept([[1], [0], [0]], [1, -1, -1])
+
+
+def test_many_forks_at_once():
+    """More pairs than a CTA copies, equal targets among them, on one workspace."""
+    pages = 600
+    b = Both([latent(pages, 4, 8, 8)], 400, 8)
+    rng = random.Random(2)
+    b.reserve([rng.randint(0, 24) if i < 100 else 0 for i in range(400)])
+    b.length = [h * 4 - rng.randint(0, 3) if h else 0 for h in b.ref.held]
+    for _ in range(3):
+        free = [i for i in range(400) if b.ref.held[i] == 0]
+        dst = rng.sample(free, 150) + rng.sample(range(400), 50)
+        src = [rng.randrange(100) for _ in dst]
+        b.fork(src, dst, 5)
+        b.free([d for d in dst if d >= 100])
+
+
 def test_lengths_in_place_and_graphs():
     caches = [kv(40, 8) for _ in range(2)]
     pool = api.page_pool(caches, 3, 10)
