@@ -721,9 +721,9 @@ size_t moe_latent_attention_workspace_bytes(const moe_latent_cache_t *cache, int
  *   [tokens, heads] or NULL; q_start, ctx, page_table, mask as for moe_tree_attention; scale > 0.
  * bf16 q over a bf16 cache with rope <= 64 runs on the tensor cores when q and out are 16-byte aligned with
  * strides that are multiples of 8 elements and page is a multiple of 8; the weights e^(s_p - m) are
- * rounded to bf16 there for the product with the latents.  All else runs on the CUDA cores in fp32,
- * where a long context is not divided among CTAs and takes long.  The bound max_tokens chooses, with heads,
- * how many rows a tile of the cache serves at a time (16, 32 or 64); a loose bound is right and slower.
+ * rounded to bf16 there for the product with the latents.  All else runs on the CUDA cores in fp32.
+ * The bound max_tokens chooses, with heads, how many rows a tile of the cache serves at a time (16, 32 or 64),
+ * and with max_pages how the work is divided; a loose bound is right and slower.
  * tokens >= 0; 1 <= max_tokens <= 64; 1 <= heads <= 1024.  Asynchronous on s.
  */
 moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,

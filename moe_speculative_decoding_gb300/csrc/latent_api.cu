@@ -202,8 +202,9 @@ moe_status_t moe_latent_write(const moe_latent_cache_t *cache, const moe_heads_t
 
 size_t moe_latent_attention_workspace_bytes(const moe_latent_cache_t *cache, int32_t tokens, int32_t seqs, int32_t heads) {
     if (cache == nullptr || tokens < 0 || seqs < 0 || heads < 1) return 0;
-    const bool parts = cache->dtype == MOE_BF16 && cache->rank >= 1 && cache->rank <= 512;
-    return kWorkspaceBytes + (parts ? latent_attn_part_bytes() : 0);
+    if (cache->rank < 1 || cache->rank > 512) return kWorkspaceBytes;
+    const size_t simt = latent_simt_part_bytes(cache->rank);
+    return kWorkspaceBytes + (cache->dtype == MOE_BF16 ? std::max(latent_attn_part_bytes(), simt) : simt);
 }
 
 moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,

@@ -32,12 +32,15 @@ struct LatentArgs {
     void *part;                // partial results (after the workspace header)
     long long wait_limit;
     int32_t seqs, tokens, max_tokens, max_pages, heads;
-    int32_t undivided;         // an item is one CTA's (short contexts)
+    int32_t undivided;         // tensor cores: an item is one CTA's (short contexts)
+    int32_t divisions;         // CUDA cores: parts of the positions
     float scale_log2;          // scale * log2(e)
 };
 
 cudaError_t launch_latent_write(const LatentWriteArgs &a, cudaStream_t s, bool pdl);
+// The kernel on the CUDA cores and its workspace after the header.
 cudaError_t launch_latent_simt(const LatentArgs &a, cudaStream_t s, bool pdl);
+size_t latent_simt_part_bytes(int rank);
 // The tensor-core kernel: whether it takes these operands, its workspace after the header, the
 // launch (cudaErrorNotSupported: strides that no tensor map describes).
 bool latent_attn_supports(const moe_latent_cache_t &c, const moe_heads_t &q, const moe_heads_t &out);

@@ -29,6 +29,18 @@
 // leaves its unnormalised output, maximum and sum in the workspace, and a second kernel joins the
 // parts in order (no atomics: repeats give the same bits).
 //
+// Measured, rank 512 and 64 rotary channels, 16 heads: 64 sequences of 801-8209 positions, one token each, 66-68 us
+// (5.3-5.4 TB/s); two of 100-131 thousand with one token 56, with 4 tokens (64 rows) 65-67 us (4.3 TB/s):
+// there the ring, 128 KB, holds a tile's units for its copy's latency under load (3,000 cycles and more) and for the
+// tile's scores, weights and product, 6,500 cycles in all, which is what limits the bytes in flight.  Few rows
+// take a tile in 3,100 cycles (7.0 TB/s) between a beginning of 10,000 and an end of 6,000 and the join.
+// Many rows are bound by shared memory: the products read 4 KB for each of a tile's 36 steps of S^T (32 cycles at
+// 128 bytes a cycle) and 6 KB for each of the 16 of O^T, and its copies write 72 KB, together 2,500 cycles;
+// a tile of 64 rows takes 2,530.  Four sequences of 4001-8201 with trees of 64 tokens 81-84 us (730 TFLOP/s),
+// eight of 4001-16411 with two tokens of 128 heads 70-71 (625).  An item's end costs a CTA 11,000 cycles (its last
+// product, sums, and 128 KB of parts at 31 bytes a cycle), the join 6-8 us.  One token over 300 positions: 9.7 us,
+// a chain of latencies.
+//
 // Every wait is bounded (an abort flag, MOE_ERR_DEVICE_TIMEOUT, then copies and products are
 // drained and TMEM is freed).
 #include "latent_args.cuh"
@@ -140,7 +152,9 @@ __device__ __forceinline__ Rows load_rows(const LatentArgs &a, int nt, int b) {
     s.tiles = s.blocks > 0 ? (s.len + kPos - 1) / kPos : 0;
     return s;
 }
-// What an item's beginning and end cost, in tiles, when there are several tiles for every CTA.
+// What an item's beginning and end cost, in tiles, when there are several tiles for every CTA.  Sixteen sequences of
+// 4001-8201 positions with 64 rows take 47.7, 45.1, 42.8, 41.7 and 41.5 us with 0, 2, 4, 6 and 8; four with 1024
+// rows 84.5, 83.1, 81.2, 81.8 and 82.8; 64 of 801-8209 with 16 rows 69.1, 67.1, 67.2, 67.6 and 68.1.
 constexpr int kEndCost = 4;
 __device__ __forceinline__ int end_cost(const LatentArgs &a, long long tiles, int ctas) {
     return tiles > 2ll * ctas && !a.undivided ? kEndCost : 0;
@@ -1157,11 +1171,13 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     CUtensorMap tm_c, tm_r;
     if (!encode_rows(&tm_c, a.cache, 0, a.cache.rank, box) || !encode_rows(&tm_r, a.cache, a.cache.rank, a.cache.rope, box))
         return cudaErrorNotSupported;
+    // Columns by the rows there can be: two sequences of 100-131 thousand positions take 56 us with 16 rows, 59 with
+    // 32 and 66 with 64, whose weights and parts cost four times as much.
     const int rows = a.max_tokens * a.heads, nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kPos - 1) / kPos;
     const long long items = static_cast<long long>(a.seqs) * ((rows + nt - 1) / nt);
     // Short contexts: an item's few tiles one after the other take less time than another end of an item and the
-    // launch that joins the parts.  16 heads of one token: one sequence of five tiles 10.8 us undivided against
+    // launch that joins the parts (and 2 us less of the host).  16 heads of one token: one sequence of five tiles 10.8 us undivided against
     // 9.7, of sixteen 20.9 against 9.0; 64 sequences of five 13.8 against 15.8, 16 of fifteen 20.0 against 17.3.
     a.undivided = item_tiles <= 4 || (4 * items >= sms && item_tiles <= 8) || (2 * items >= sms && item_tiles <= 12);
     // no more CTAs than the page tables could fill with tiles

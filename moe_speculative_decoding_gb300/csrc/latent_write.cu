@@ -4,7 +4,9 @@
 //     y_i = c_i w_i / sqrt(mean(c^2) + eps),   (a, b) -> (a cos - b sin, b cos + a sin)
 //
 // Streaming work, a few operations an element: the bound is memory traffic, each row read once and
-// written once.
+// written once.  16301 tokens with 32 heads of 64 rotary channels, bf16: 35.5 us, 4.94 TB/s (a copy of the queries'
+// bytes alone, 128 of every 384, reaches 5.5); a pass of 16 tokens with 16 heads 2.8 us, the latency of its
+// chain of loads (slot and position, table row).
 #include "latent_args.cuh"
 #include "row_common.cuh"
 
@@ -268,7 +270,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) latent_vec_kernel(const __grid
 }
 
 // A warp for every group while all of them are resident at once, so that a short call is short; else one to a
-// token.
+// token (16301 tokens with 32 heads: 35.5 us, with two warps to a token 37, with three 41; four CTAs an SM: with
+// three, whose threads have 80 registers, 38, with five 42).
 template <typename IN, typename OUT, int T>
 cudaError_t launch(const LatentWriteArgs &a, cudaStream_t s, bool pdl) {
     constexpr int rows = 32 / T;

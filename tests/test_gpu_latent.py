@@ -52,6 +52,35 @@ def test_cuda_cores(kind, q_kind, page, rope, rank):
     p.check(api, *run(p))
 
 
+@pytest.mark.parametrize("ctx,n", [([2000, 5, 0], [3, 2, 1]), ([4000], [1]), ([700] * 9, [8] * 9), ([300] * 40, [20] * 40)])
+@pytest.mark.parametrize("kind", [F32, BF16])
+def test_cuda_cores_divide_the_positions(ctx, n, kind):
+    """Parts of many CTAs, parts that are empty, and rows enough for none."""
+    p = LatentPass(ctx, n, 5, 72, 8, 6, kind, F32, seed=len(ctx))
+    out, lse = run(p)
+    p.check(api, out, lse)
+    again = run(p)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_cuda_cores_do_not_touch_what_is_not_seen(value):
+    p = LatentPass([300, 64], [4, 2], 4, 256, 32, 6, F32, F32, seed=4)
+    p.mask[:4] = [1, 2, 5, 0]
+    p.mask[4:] = [1, 3]
+    page, row = p.at(0, 301)
+    p.rows[page, row, 7] = value
+    for b in range(2):
+        page, row = p.at(b, p.ctx[b] + p.n[b] - 1)
+        p.rows[page, row + 1:] = value
+    out, lse = run(p)
+    assert not torch.isfinite(out[1, :, 7]).any()
+    keep = [0, 2, 3, 4, 5]
+    ref, ref_lse, bound, lse_bound = p.reference(0.0, False)
+    within("out", out[keep], ref[keep], bound[keep])
+    within("lse", lse[keep], ref_lse[keep], lse_bound[keep])
+
+
 @pytest.mark.parametrize("heads", [4, 8, 16])   # blocks of 16, 32 and 64 rows
 def test_rows_that_see_nothing(heads):
     p = LatentPass([0, 150], [4, 3], heads, 512, 64, 64, seed=3)

@@ -79,7 +79,7 @@ def test_attention(lib, change, code):
 
 def test_workspaces(lib):
     need = lib.moe_latent_attention_workspace_bytes
-    assert need(ctypes.byref(latent()), 64, 4, 16) > need(ctypes.byref(latent(dtype=0)), 64, 4, 16) == 256
+    assert need(ctypes.byref(latent()), 64, 4, 16) > need(ctypes.byref(latent(dtype=0)), 64, 4, 16) > 256
     assert need(None, 64, 4, 16) == need(ctypes.byref(latent()), -1, 4, 16) == 0
     assert lib.moe_pages_workspace_bytes(ctypes.byref(pool())) >= 256 + 4 * 100 + 16 * 8
     assert lib.moe_pages_workspace_bytes(None) == lib.moe_pages_workspace_bytes(ctypes.byref(pool(seqs=0))) == 0
