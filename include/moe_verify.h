@@ -724,7 +724,8 @@ size_t moe_latent_attention_workspace_bytes(const moe_latent_cache_t *cache, int
  * rounded to bf16 there for the product with the latents.  All else runs on the CUDA cores in fp32.
  * The bound max_tokens chooses, with heads, how many rows a tile of the cache serves at a time (16, 32 or 64),
  * and with max_pages how the work is divided; a loose bound is right and slower.
- * tokens >= 0; 1 <= max_tokens <= 64; 1 <= heads <= 1024.  Asynchronous on s.
+ * tokens >= 0; 1 <= max_tokens <= 64; 1 <= heads <= 1024; out overlaps nothing that is read.  Calls that
+ * share a workspace run one after the other.  Asynchronous on s.
  */
 moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_heads_t *q, const moe_heads_t *out, float *lse,
                                   const int32_t *q_start, const int32_t *ctx, const int32_t *page_table,
@@ -754,8 +755,8 @@ typedef struct {
 } moe_page_pool_t;
 
 /* The caches whose rows live in the pool's pages, one of each layer, every one with the pool's pages
- * and page; either list may be empty (NULL, 0).  At most 1024 of equal shape one after the other, and
- * seqs * ceil(bytes of a page's keys / 16384) < 2^23. */
+ * and page; either list may be empty (NULL, 0).  At most 1024 of equal shape, 16 times 64 in all where shapes
+ * differ, and seqs * ceil(bytes of a page's keys / 16384) < 2^23. */
 typedef struct {
     const moe_kv_cache_t *kv;          /* [host] [kv_count] */
     const moe_latent_cache_t *latent;  /* [host] [latent_count] */

@@ -96,7 +96,7 @@ bool too_much(const moe_page_pool_t *pool, const Plane &p) {
     return pieces >= (1ll << 21) || pool->seqs * pieces >= (1ll << 31) / (kLayersLaunch * kPlanes);
 }
 
-constexpr int kMaxLaunches = 16;   // of the rows' kernel in one call: 1024 caches of equal shape
+constexpr int kMaxLaunches = 16;   // of the rows' kernel in one call: 1024 caches of equal shape, or 16 shapes
 
 // The caches as launches of up to kLayersLaunch of equal shape.
 struct Layers {
@@ -104,11 +104,14 @@ struct Layers {
     int launches = 0;
 
     moe_status_t add(const PageRows &shape, void *const (&base)[kPlanes]) {
-        if (launches == 0 || !same(rows[launches - 1], shape) || rows[launches - 1].layers == kLayersLaunch) {
+        int at = launches - 1;   // the last launch of this shape
+        while (at >= 0 && !same(rows[at], shape)) --at;
+        if (at < 0 || rows[at].layers == kLayersLaunch) {
             if (launches == kMaxLaunches) return MOE_ERR_UNSUPPORTED;
-            rows[launches++] = shape;
+            at = launches++;
+            rows[at] = shape;
         }
-        PageRows &r = rows[launches - 1];
+        PageRows &r = rows[at];
         for (int i = 0; i < kPlanes; ++i) r.base[r.layers][i] = base[i];
         ++r.layers;
         return MOE_OK;

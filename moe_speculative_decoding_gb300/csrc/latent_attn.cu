@@ -371,7 +371,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 page = kOutside;
                 row = 0;
                 if (pos < w.s.len) {
-                    page = __ldg(table + static_cast<int>(pos) / kc.page);
+                    page = max(__ldg(table + static_cast<int>(pos) / kc.page), -1);
                     row = static_cast<int>(pos) % kc.page;
                 }
             };
@@ -1171,8 +1171,9 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     CUtensorMap tm_c, tm_r;
     if (!encode_rows(&tm_c, a.cache, 0, a.cache.rank, box) || !encode_rows(&tm_r, a.cache, a.cache.rank, a.cache.rope, box))
         return cudaErrorNotSupported;
-    // Columns by the rows there can be: two sequences of 100-131 thousand positions take 56 us with 16 rows, 59 with
-    // 32 and 66 with 64, whose weights and parts cost four times as much.
+    // Columns by the rows there can be: two sequences of 100-131 thousand positions with 16 rows each take 56.8 us with
+    // 16 columns, 59.4 with 32 and 66.1 with 64; with 32 rows 59.8 and 66.1; 64 of 801-8209 with 16 rows 67.6, 70.6
+    // and 79.0.
     const int rows = a.max_tokens * a.heads, nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
     const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kPos - 1) / kPos;
     const long long items = static_cast<long long>(a.seqs) * ((rows + nt - 1) / nt);

@@ -188,6 +188,55 @@ def test_bad_lengths_and_pages_are_recorded():
     p.check(api, out, lse)
 
 
+def test_page_numbers_of_any_kind():
+    """Negative ones and large ones read as zeros, the smallest integers among them."""
+    for odd in (-1, -2 ** 31, -2 ** 31 + 1, 2 ** 31 - 1):
+        p = LatentPass([200], [2], 16, 512, 64, 16, seed=13)
+        d = p.device(api)
+        ws = api.latent_attention_workspace(d["cache"], 2, 1, 16)
+        api.latent_attention(**p.device(api), ws=ws, max_tokens=2)   # the ring holds other rows
+        assert api.last_device_error(ws) == 0
+        d["page_table"][0, 5] = odd
+        p.rows = torch.cat([p.rows, torch.zeros_like(p.rows[:1])])
+        p.table[0, 5] = p.rows.shape[0] - 1
+        out, lse = api.latent_attention(**d, return_lse=True, ws=ws, max_tokens=2)
+        assert api.last_device_error(ws) == 5
+        p.check(api, out, lse)
+
+
+def test_rows_behind_the_last_sequence_and_other_orders():
+    p = LatentPass([300, 70], [3, 2], 16, 512, 64, 32, seed=14)
+    d = p.device(api)
+    ref = api.latent_attention(**d, return_lse=True, max_tokens=3)
+    # tokens that no sequence has
+    more = torch.cat([d["q"], torch.full((3, 16, 576), float("nan"), dtype=BF16, device="cuda")])
+    out, lse = torch.full((8, 16, 512), 5.0, dtype=BF16, device="cuda"), torch.full((8, 16), 5.0, device="cuda")
+    api.latent_attention(**{**d, "q": more, "mask": torch.cat([d["mask"], d["mask"][:3]])}, out=out, lse=lse, max_tokens=3)
+    assert torch.equal(out[:5], ref[0]) and torch.equal(lse[:5], ref[1]) and out[5:].eq(5.0).all() and lse[5:].eq(5.0).all()
+    # heads outside tokens, in what is read and what is written
+    q = d["q"].transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.empty((16, 5, 512), dtype=BF16, device="cuda").transpose(0, 1)
+    api.latent_attention(**{**d, "q": q}, out=out, lse=lse[:5], max_tokens=3)
+    assert torch.equal(out, ref[0]) and torch.equal(lse[:5], ref[1])
+
+
+def test_two_streams_at_once():
+    a, b = LatentPass([5000, 100], [4, 2], 16, 512, 64, 64, seed=15), LatentPass([4000] * 3, [1] * 3, 16, 512, 64, 64, seed=16)
+    da, db = a.device(api), b.device(api)
+    wa, wb = api.latent_attention_workspace(da["cache"], 6, 2, 16), api.latent_attention_workspace(db["cache"], 3, 3, 16)
+    ra, rb = (api.latent_attention(**x, ws=w, max_tokens=4) for x, w in ((da, wa), (db, wb)))
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(8):
+        for s, x, w in ((sa, da, wa), (sb, db, wb)):
+            with torch.cuda.stream(s):
+                got.append(api.latent_attention(**x, ws=w, max_tokens=4))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ra) for x in got[::2]) and all(torch.equal(x, rb) for x in got[1::2])
+    assert api.last_device_error(wa) == 0 and api.last_device_error(wb) == 0
+
+
 def test_empty_sequences():
     p = LatentPass([50, 70, 20], [2, 0, 1], 16, 512, 64, 64, seed=10)
     p.check(api, *run(p))

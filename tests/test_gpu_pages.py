@@ -67,7 +67,7 @@ class Both:
         for b, n in enumerate(self.ref.held):
             assert self.pool.table[b, :n].tolist() == self.ref.table[b][:n]
         for x, y in zip(parts(self.pool), want):
-            assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+            assert torch.equal(x.contiguous().reshape(-1).view(torch.uint8), y.contiguous().reshape(-1).view(torch.uint8))
 
     def reserve(self, need, error=0):
         got, copies, recorded = self.ref.reserve(self.length, need)
@@ -110,6 +110,7 @@ class Both:
     (64, lambda n, p: [latent(n, p, 512, 64) for _ in range(3)]),
     (8, lambda n, p: [kv(n, p, 2, 16, "bf16", pad=3), latent(n, p, pad=1), kv(n, p, 2, 32, "e4m3", pad=1)]),
     (3, lambda n, p: [kv(n, p, 2, 8) for _ in range(70)]),   # more layers than one launch takes
+    (8, lambda n, p: [f(n, p) for _ in range(10) for f in (kv, latent, lambda n, p: kv(n, p, 1, 64, "e4m3"))]),   # shapes in turn
 ])
 def test_a_run_of_all_steps(page, make):
     """Rounds of drafting, acceptance, branching and giving up, with random paths."""
