@@ -46,6 +46,8 @@
 #include "latent_args.cuh"
 #include "tree_common.cuh"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -385,11 +387,9 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                     row_now = row_next;
                     places(tt + per, page_next, row_next);
                 }
-                // lanes 0 .. boxes - 1: the first 64 channels of a unit; the next `boxes` lanes: the others
-                const int box = lane % boxes, half = lane / boxes;
-                int page = __shfl_sync(0xFFFFFFFFu, page_now, k * boxes + box);
-                const int row = __shfl_sync(0xFFFFFFFFu, row_now, k * boxes + box);
-                const bool mine = half < 2 && page != kOutside;
+                int page = __shfl_sync(0xFFFFFFFFu, page_now, k * boxes + lane % boxes);
+                const int row = __shfl_sync(0xFFFFFFFFu, row_now, k * boxes + lane % boxes);
+                const bool mine = lane < boxes && page != kOutside;
                 if (mine && static_cast<uint32_t>(page) >= static_cast<uint32_t>(kc.pages)) {
                     record_error(a.err, MOE_ERR_BAD_ID);
                     page = kc.pages;   // beyond the tensor: the copy writes zeros
@@ -397,41 +397,43 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 const uint32_t rs = rc % L::NR;
                 if (!(ok = wait_for(bar(L::bRE + rs), ((rc / L::NR) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
                 const uint32_t r_dst = base + L::oR + rs * kRopeTile, r_bar = bar(L::bRF + rs);
-                if (boxes == 1) {
-                    // one box: issued by an elected lane from uniform registers (by one lane of a condition
-                    // on the lane a unit took 450 cycles)
-                    const int page1 = __shfl_sync(0xFFFFFFFFu, page, 0), row1 = __shfl_sync(0xFFFFFFFFu, row, 0);
+                const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));   // the first n boxes
+                const uint32_t bytes = static_cast<uint32_t>(n * box_rows) * 128u;
+                // Issued by an elected lane from uniform registers, up to E boxes one after the other: by a lane for
+                // each box a unit took 450 cycles (64 sequences of 801-8209 positions, pages of 8, 16 and 32: 106.8,
+                // 71.9 and 68.3 us against 84, 69.8 and 68.1; unrolled for eight boxes, pages of 16 take 71.5).
+                auto issue = [&](auto most) {
+                    constexpr int E = decltype(most)::value;
+                    int page_e[E], row_e[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        page_e[e] = __shfl_sync(0xFFFFFFFFu, page, e % boxes);
+                        row_e[e] = __shfl_sync(0xFFFFFFFFu, row, e % boxes);
+                    }
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(r_bar, kRopeTile);
-                        tma_load_3d(r_dst, &tm_r, r_bar, 0, row1, page1);
+                        mbar_arrive_expect_tx(r_bar, bytes);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (e < n) tma_load_3d(r_dst + e * box_rows * 128u, &tm_r, r_bar, 0, row_e[e], page_e[e]);
                     }
                     __syncwarp();
                     for (int u = 0; u < U; ++u, ++uc) {
                         const uint32_t slot = uc % L::NU, u_dst = base + L::oU + slot * kUnit, u_bar = bar(L::bUF + slot);
-                        if (!(ok = wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
+                        if (!wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit)) return false;
                         if (elect_one()) {
-                            mbar_arrive_expect_tx(u_bar, kUnit);
-                            tma_load_3d(u_dst, &tm_c, u_bar, u * 128, row1, page1);
-                            tma_load_3d(u_dst + 8192u, &tm_c, u_bar, u * 128 + 64, row1, page1);
+                            mbar_arrive_expect_tx(u_bar, 2 * bytes);
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                if (e >= n) continue;
+                                tma_load_3d(u_dst + e * box_rows * 128u, &tm_c, u_bar, u * 128, row_e[e], page_e[e]);
+                                tma_load_3d(u_dst + 8192u + e * box_rows * 128u, &tm_c, u_bar, u * 128 + 64, row_e[e], page_e[e]);
+                            }
                         }
                         __syncwarp();
                     }
-                } else {
-                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, mine && half == 0)), bytes = n * box_rows * 128u;
-                    const uint32_t off = half * 8192u + box * box_rows * 128u;
-                    if (lane == 0) mbar_arrive_expect_tx(r_bar, bytes);
-                    __syncwarp();
-                    if (mine && half == 0) tma_load_3d(r_dst + off, &tm_r, r_bar, 0, row, page);
-                    __syncwarp();
-                    for (int u = 0; u < U; ++u, ++uc) {
-                        const uint32_t slot = uc % L::NU, u_bar = bar(L::bUF + slot);
-                        if (!(ok = wait_for(bar(L::bUE + slot), ((uc / L::NU) & 1u) ^ 1u, abort_flag, a.err, limit))) break;
-                        if (lane == 0) mbar_arrive_expect_tx(u_bar, 2 * bytes);
-                        __syncwarp();
-                        if (mine) tma_load_3d(base + L::oU + slot * kUnit + off, &tm_c, u_bar, u * 128 + half * 64, row, page);
-                        __syncwarp();
-                    }
-                }
+                    return true;
+                };
+                ok = boxes <= 4 ? issue(std::integral_constant<int, 4>()) : issue(std::integral_constant<int, 8>());
                 if (!ok) {
                     ++rc;   // the rotary tile's copies are on their way
                     break;
