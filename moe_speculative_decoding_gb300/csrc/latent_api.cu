@@ -64,8 +64,10 @@ PageArgs page_args(const moe_page_pool_t *pool, void *ws) {
     return a;
 }
 
-// A plane whose rows are one piece where they lie together.
-Plane plane_of(int64_t page, int64_t row, int64_t seg, int segs, int bytes) {
+// A plane whose rows are one piece where they lie together, moved `unit` bytes at a time: 16 where addresses and
+// strides are multiples of that, 4 for scales, whose address need not be one (with pages of one position all heads'
+// scales are one piece, of any multiple of 4 bytes).
+Plane plane_of(int64_t page, int64_t row, int64_t seg, int segs, int bytes, int unit) {
     Plane p;
     std::memset(&p, 0, sizeof p);
     p.page_stride = page;
@@ -78,7 +80,7 @@ Plane plane_of(int64_t page, int64_t row, int64_t seg, int segs, int bytes) {
         p.segs = 1;
         p.seg_stride = p.bytes;
     }
-    p.unit = p.bytes % 16 == 0 ? 16 : 4;
+    p.unit = unit;
     p.per_seg = p.bytes / p.unit;
     p.per_row = p.per_seg * p.segs;
     p.dense = p.segs == 1 && row == p.bytes;
@@ -134,10 +136,10 @@ moe_status_t collect(const moe_page_pool_t *pool, const moe_page_caches_t *cache
         const int es = c.dtype == MOE_F32 ? 4 : (c.dtype == MOE_BF16 ? 2 : 1);
         std::memset(&shape, 0, sizeof shape);
         shape.planes = c.dtype == MOE_E4M3 ? 4 : 2;
-        shape.plane[0] = shape.plane[1] = plane_of(c.page_stride * es, c.token_stride * es, c.head_stride * es, c.heads, c.dim * es);
+        shape.plane[0] = shape.plane[1] = plane_of(c.page_stride * es, c.token_stride * es, c.head_stride * es, c.heads, c.dim * es, 16);
         if (c.dtype == MOE_E4M3)
             shape.plane[2] = shape.plane[3] =
-                plane_of(static_cast<int64_t>(c.heads) * c.page * 4, 4, static_cast<int64_t>(c.page) * 4, c.heads, 4);
+                plane_of(static_cast<int64_t>(c.heads) * c.page * 4, 4, static_cast<int64_t>(c.page) * 4, c.heads, 4, 4);
         for (int k = 0; k < shape.planes; ++k)
             if (too_much(pool, shape.plane[k])) return MOE_ERR_UNSUPPORTED;
         void *const base[kPlanes] = {c.k, c.v, c.k_scale, c.v_scale};
@@ -152,7 +154,7 @@ moe_status_t collect(const moe_page_pool_t *pool, const moe_page_caches_t *cache
         const int es = c.dtype == MOE_F32 ? 4 : 2;
         std::memset(&shape, 0, sizeof shape);
         shape.planes = 1;
-        shape.plane[0] = plane_of(c.page_stride * es, c.token_stride * es, 0, 1, (c.rank + c.rope) * es);
+        shape.plane[0] = plane_of(c.page_stride * es, c.token_stride * es, 0, 1, (c.rank + c.rope) * es, 16);
         if (too_much(pool, shape.plane[0])) return MOE_ERR_UNSUPPORTED;
         void *const base[kPlanes] = {c.rows, nullptr, nullptr, nullptr};
         const moe_status_t full = out.add(shape, base);
