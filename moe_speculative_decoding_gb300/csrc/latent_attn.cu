@@ -71,7 +71,7 @@ struct Lay {
     static constexpr uint32_t kQBlock = NT * 128;                    // 64 channels of the queries
     static constexpr uint32_t oU = 0, oR = oU + NU * kUnit, oQ = oR + NR * kRopeTile, oBar = oQ + 9 * kQBlock;
     static constexpr int bUF = 0, bUE = NU, bRF = 2 * NU, bRE = bRF + NR, bS = bRE + NR, bSFree = bS + 2, bP = bSFree + 2,
-                         bQ = bP + NR, bO = bQ + 1, bW = bO + 1, bDrain = bW + kRecords, kBars = bDrain + 1;
+                         bQ = bP + NR, bSeen = bQ + 1, bO = bSeen + 1, bW = bO + 1, bDrain = bW + kRecords, kBars = bDrain + 1;
     static constexpr uint32_t oMisc = oBar + 8 * kBars;            // TMEM address, abort flag, units, rotary tiles and queries copied
     static constexpr uint32_t oBad = (oMisc + 20 + 15) & ~15u;     // uint32 [2 items][2]: drafted tokens with non-finite latents
     static constexpr uint32_t oM = oBad + 16;                      // float [NT]: minus the rows' maxima, 0 where there is none
@@ -335,6 +335,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
             mbar_init(bar(L::bSFree + i), 8);
         }
         mbar_init(bar(L::bQ), q_map ? 1 : 8);
+        mbar_init(bar(L::bSeen), 2);
         mbar_init(bar(L::bO), 1);
         for (int i = 0; i < kRecords; ++i) mbar_init(bar(L::bW + i), 1);
         mbar_init(bar(L::bDrain), 3);
@@ -456,6 +457,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         bool ok = true;
         while (ok && part_follow(a, w, follow, abort_flag)) {
             ok = wait_for(bar(L::bQ), items & 1u, abort_flag, a.err, limit);
+            if (ok) warp_arrive(bar(L::bSeen));
             const int T = __shfl_sync(0xFFFFFFFFu, w.hi - w.lo, 0);
             for (int t = 0; ok && t < T; ++t, ++c) {
                 if ((c & 1u) != side) {
@@ -576,6 +578,11 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
                 next_mask = a.mask != nullptr ? a.mask[v.t0 + static_cast<int>(token)] : (2ull << token) - 1ull;
                 if (v.n < 64) next_mask &= (1ull << v.n) - 1ull;
             }
+            // Both score warps have found the previous item's: with one tile to an item only one of them has formed
+            // its scores, and the other's wait by parity would miss a phase that the next one's completion hides.
+            if (v.index > 0 && !dead && (!q_map || warp == 0))
+                dead = !wait_for(bar(L::bSeen), static_cast<uint32_t>(v.index - 1) & 1u, abort_flag, a.err, limit);
+            if (dead) return;
             if (q_map) {   // (rows beyond the block's are another's, or zeros: their columns go nowhere)
                 if (warp == 0) {
                     if (elect_one()) {
