@@ -564,7 +564,7 @@ latent_attn_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_consta
         const bool even_out = a.out.token_stride == static_cast<int64_t>(a.heads) * a.out.head_stride;
         bool dead = false;   // a wait gave up: only the barriers are kept
         uint32_t c = 0;      // tiles
-        Item w, next;
+        Item w = {}, next;
         // An item's queries into shared memory: blocks of 64 channels, [NT rows][128 bytes], the rotary channels'
         // block last.  Rows that are one step apart are copied (q_map): loaded by these threads, 64 rows took
         // 8,000 cycles behind the first tiles' copies.
