@@ -18,7 +18,8 @@ namespace moe {
 struct DeviceWorkspace {
     int32_t error;
     uint32_t sync[2];   // tensor-core path: the epoch of its flags, and a CTA exit count
-    int32_t reserved[61];
+    uint32_t forked;    // moe_pages_fork: CTAs that are done, 0 between calls
+    int32_t reserved[60];
 };
 constexpr size_t kWorkspaceBytes = sizeof(DeviceWorkspace);   // 256
 

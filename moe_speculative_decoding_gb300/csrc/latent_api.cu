@@ -60,6 +60,7 @@ PageArgs page_args(const moe_page_pool_t *pool, void *ws) {
     std::memset(&a, 0, sizeof a);
     a.pool = *pool;
     a.err = error_word(ws);
+    a.forked = &static_cast<DeviceWorkspace *>(ws)->forked;
     a.lists = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(ws) + kWorkspaceBytes);
     return a;
 }

@@ -66,7 +66,8 @@ struct PageRows {
 struct PageArgs {
     moe_page_pool_t pool;
     int32_t *err;
-    int32_t *lists;            // workspace after the header
+    uint32_t *forked;          // the header's count of a fork's CTAs
+    int32_t *lists;            // workspace after the header: nothing in it outlives a call
     const int32_t *length, *need, *ctx, *path, *count, *src, *ids;
     int32_t *got, *after, *length_out;
     int32_t items, max_path;

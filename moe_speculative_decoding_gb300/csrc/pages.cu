@@ -22,7 +22,7 @@ constexpr int kBook = 1024;          // threads of the bookkeeping CTA
 constexpr int kMine = 8;             // pages a thread looks at in a step
 constexpr int kStep = kBook * kMine;
 
-// Lists in the workspace: [4] (copies to make, CTAs of a fork that are done, most rows of a copy), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
+// Lists in the workspace: [4] (copies to make, -, most rows of a copy, -), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
 // rows to move), [pages] free pages in order.
 __device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
 __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
@@ -413,10 +413,10 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant
     }
     if (gridDim.x > 1) {
         __syncthreads();
-        if (i == 0) last_s = atom_add_acq_rel_gpu(reinterpret_cast<uint32_t *>(a.lists + 1), 1u) == gridDim.x - 1;
+        if (i == 0) last_s = atom_add_acq_rel_gpu(a.forked, 1u) == gridDim.x - 1;
         __syncthreads();
         if (!last_s) return;
-        if (i == 0) a.lists[1] = 0;   // for the next call
+        if (i == 0) *a.forked = 0;   // for the next call
     }
     if (ok) {
         pool.held[dst] = pages;
