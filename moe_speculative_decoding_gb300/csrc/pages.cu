@@ -270,15 +270,16 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
             if (__any_sync(0xFFFFFFFFu, i < count && p != i)) moves = count;
             last = __shfl_sync(0xFFFFFFFFu, p, 31);
         }
-        // rows that move go to pages that nobody else holds
-        if (!bad && moves > 0) {
-            bool other = false;
-            for (int j = ctx / pool.page + lane; j <= (ctx + count - 1) / pool.page; j += 32) {
-                const int page = table_of(a, b)[j];
-                other |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(pool.pages) || pool.refs[page] > 1;
-            }
-            bad = __any_sync(0xFFFFFFFFu, other);
+    }
+    // The pages that rows leave or go to and those that are given up are pages, and what rows go to nobody else holds.
+    if (!bad && count >= 0) {
+        const int first = moves > 0 ? ctx / pool.page : (ctx + count + pool.page - 1) / pool.page, last = moves > 0 ? (ctx + count - 1) / pool.page : -1;
+        bool other = false;
+        for (int j = first + lane; j < held; j += 32) {
+            const int page = table_of(a, b)[j];
+            other |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(pool.pages) || (j <= last && pool.refs[page] > 1);
         }
+        bad = __any_sync(0xFFFFFFFFu, other);
     }
     if (bad && lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
     const bool act = !bad && count >= 0;
@@ -292,8 +293,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     if (!act) return;
     const int left = (after + pool.page - 1) / pool.page;   // at most held
     const int32_t *const table = table_of(a, b);
-    for (int j = left + lane; j < held; j += 32)
-        if (in_pool(a, table[j])) atomicSub(pool.refs + table[j], 1);
+    for (int j = left + lane; j < held; j += 32) atomicSub(pool.refs + table[j], 1);
     if (lane == 0) pool.held[b] = left;
 }
 
@@ -322,8 +322,7 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
             const int i = static_cast<int>(threadIdx.x) & 63;
             if (i < count) {
                 const int pos = ctx + (threadIdx.x < 64 ? path[i] : i), k = pos / a.pool.page;
-                int page = table_of(a, b)[k];
-                if (!in_pool(a, page)) page = -1;
+                const int page = table_of(a, b)[k];
                 int(&to)[2] = threadIdx.x < 64 ? source_s[i] : target_s[i];
                 to[0] = page;
                 to[1] = pos - k * a.pool.page;
@@ -343,7 +342,7 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 const int i = i0 + k;
-                if (i >= count || source_s[i][0] < 0) continue;
+                if (i >= count) continue;
                 if (unit == 16)
                     x[k] = *reinterpret_cast<const uint4 *>(at(source_s[i]));
                 else
@@ -352,7 +351,7 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 const int i = i0 + k;
-                if (i >= count || source_s[i][0] < 0 || target_s[i][0] < 0) continue;
+                if (i >= count) continue;
                 if (unit == 16)
                     *reinterpret_cast<uint4 *>(at(target_s[i])) = x[k];
                 else
