@@ -805,8 +805,8 @@ moe_status_t moe_pages_fork(const moe_page_pool_t *pool, const int32_t *src, con
  *   path [dev] int32 [seqs, max_path], 0 <= path[b][0] < path[b][1] < ..., or NULL for the first count[b]
  *   tokens (nothing moves); count [dev] int32 [seqs], at most max_path; after [dev] int32 [seqs] or
  *   NULL, may be ctx itself.  ctx[b] + path[b][i] must lie in the pages held, and pages that rows move to
- *   must be the sequence's own, as moe_pages_reserve leaves them (a page that another sequence gives up in the
- *   same call may count either way; the sequence is served whole or left as it was).  1 <= max_path <= MOE_MAX_TREE_TOKENS.
+ *   must be the sequence's own, as moe_pages_reserve leaves them (holders count as the call finds them: a page
+ *   that another sequence gives up in the same call is still shared).  1 <= max_path <= MOE_MAX_TREE_TOKENS.
  *   Asynchronous on s.
  */
 moe_status_t moe_pages_accept(const moe_page_pool_t *pool, const int32_t *ctx, const int32_t *path, const int32_t *count,

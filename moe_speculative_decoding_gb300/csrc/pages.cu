@@ -22,8 +22,8 @@ constexpr int kBook = 1024;          // threads of the bookkeeping CTA
 constexpr int kMine = 8;             // pages a thread looks at in a step
 constexpr int kStep = kBook * kMine;
 
-// Lists in the workspace: [4] (copies to make, -, most rows of a copy, -), [seqs][4] (source page, target page, rows, 0; of accept: ctx,
-// rows to move), [pages] free pages in order.
+// Lists in the workspace: [4] (copies to make, -, most rows of a copy, -), [seqs][4] (source page, target page, rows, -; of accept: ctx,
+// rows to move, pages kept, pages held before), [pages] free pages in order.
 __device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
 __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
 __device__ __forceinline__ int32_t *table_of(const PageArgs &a, int b) { return a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages; }
@@ -247,8 +247,10 @@ __global__ void __launch_bounds__(kCopy) pages_copy_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ accept
-// A warp per sequence: checks its path, gives up the pages behind what it keeps, and leaves ctx and the
-// number of rows to move for the rows' kernel (0 where nothing moves; ctx may be overwritten here).
+// A warp per sequence: checks its path and leaves ctx, the number of rows to move (0 where nothing moves; ctx may be
+// overwritten here) and the pages to give up for the rows' kernel.  The counts of holders, which all
+// sequences' checks read, go down there: so a page that one sequence gives up is shared for all of this call, and
+// nobody moves rows within it while they are read.  Without paths nothing is checked against the counts.
 __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant__ PageArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -284,17 +286,19 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     if (bad && lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
     const bool act = !bad && count >= 0;
     const int after = act ? ctx + count : ctx;
+    const int left = (after + pool.page - 1) / pool.page;   // at most held
     if (lane == 0) {
         int32_t *const e = list_of(a, b);
         e[0] = ctx;
         e[1] = act ? moves : 0;
+        e[2] = left;
+        e[3] = act ? held : left;
         if (a.after != nullptr) a.after[b] = after;
+        if (act) pool.held[b] = left;
     }
-    if (!act) return;
-    const int left = (after + pool.page - 1) / pool.page;   // at most held
+    if (!act || a.path != nullptr) return;
     const int32_t *const table = table_of(a, b);
     for (int j = left + lane; j < held; j += 32) atomicSub(pool.refs + table[j], 1);
-    if (lane == 0) pool.held[b] = left;
 }
 
 // A thread takes one column of a row (16 bytes, 4 of scales) through all of a sequence's moves in order: the
@@ -302,12 +306,20 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
 // before it was read.  Eight rows' loads are in flight together.
 constexpr int kMove = 128;
 
-__global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int columns, int slices) {
+__global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int columns, int slices, int settle) {
     __shared__ int source_s[MOE_MAX_TREE_TOKENS][2], target_s[MOE_MAX_TREE_TOKENS][2];   // page, row
     pdl_wait();
     pdl_trigger();
     const uint32_t seqs = static_cast<uint32_t>(a.pool.seqs), whole = seqs * static_cast<uint32_t>(p.layers);
     const uint32_t items = whole * static_cast<uint32_t>(slices);   // (the launch keeps them below 2^31)
+    if (settle) {
+        for (int b = static_cast<int>(blockIdx.x); b < a.pool.seqs; b += static_cast<int>(gridDim.x)) {
+            const int4 e = *reinterpret_cast<const int4 *>(list_of(a, b));
+            const int32_t *const table = table_of(a, b);
+            for (int j = e.z + static_cast<int>(threadIdx.x); j < e.w; j += kMove) atomicSub(a.pool.refs + table[j], 1);
+        }
+        if (items == 0) return;
+    }
     const Divide by_whole(whole), by_seqs(seqs);
     for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
         const uint32_t slice = by_whole(item), i = item - slice * whole, layer = by_seqs(i);
@@ -488,12 +500,15 @@ cudaError_t launch_pages_reserve(const PageArgs &a, const PageRows *rows, int la
 cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int launches, cudaStream_t s, bool pdl) {
     cudaError_t e = launch(pages_accept_kernel, static_cast<unsigned>((a.pool.seqs + 7) / 8), 256, s, pdl, a);
     if (a.path == nullptr) return e;   // nothing moves
-    for (int i = 0; i < launches && e == cudaSuccess; ++i) {
+    // the first launch gives the pages up; without caches it does nothing else
+    static const PageRows none = {};
+    for (int i = 0; i < std::max(launches, 1) && e == cudaSuccess; ++i) {
+        const PageRows &r = launches > 0 ? rows[i] : none;
         int columns = 0;
-        for (int k = 0; k < rows[i].planes; ++k) columns += rows[i].plane[k].per_row;
+        for (int k = 0; k < r.planes; ++k) columns += r.plane[k].per_row;
         const int slices = (columns + kMove - 1) / kMove;
-        const int64_t items = static_cast<int64_t>(a.pool.seqs) * rows[i].layers * slices;
-        e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, rows[i], columns, slices);
+        const int64_t items = std::max<int64_t>(static_cast<int64_t>(a.pool.seqs) * r.layers * slices, a.pool.seqs);
+        e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, r, columns, slices, i == 0 ? 1 : 0);
     }
     return e;
 }
