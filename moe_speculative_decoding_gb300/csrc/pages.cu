@@ -23,7 +23,7 @@ constexpr int kMine = 8;             // pages a thread looks at in a step
 constexpr int kStep = kBook * kMine;
 
 // Lists in the workspace: [4] (copies to make, -, most rows of a copy, -), [seqs][4] (source page, target page, rows, -; of accept: ctx,
-// rows to move, pages kept, pages held before), [pages] free pages in order.
+// rows to move, pages kept, pages held before; of fork, by target: 1 where its source has no such pages), [pages] free pages in order.
 __device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
 __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
 __device__ __forceinline__ int32_t *table_of(const PageArgs &a, int b) { return a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages; }
@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------ fork, free
-// Every CTA checks all pairs (a thread each) and copies the page numbers of some, a warp to a pair; the last
+// Every CTA checks all pairs (a thread each) and copies the page numbers of some, a warp to a pair, once it has
+// looked at all of them (with several CTAs the target's list entry says whether they were pages); the last CTA
 // to be done writes what the checks read, the lengths and the numbers of pages held.
 __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant__ PageArgs a) {
     __shared__ __align__(16) int dst_s[kBook];
@@ -415,21 +416,42 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant
         if (n == 0) continue;
         const int32_t *const from = table_of(a, src_s[p]);
         int32_t *const to = table_of(a, dst_s[p]);
-#pragma unroll 4
-        for (int j = lane; j < n; j += 32) {
-            const int page = from[j];
-            to[j] = page;
-            if (in_pool(a, page)) atomicAdd(pool.refs + page, 1);
+        constexpr int MINE = 4;   // a lane's first page numbers stay in registers
+        int first[MINE];
+        bool out = false;
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            first[k] = lane + 32 * k < n ? from[lane + 32 * k] : 0;
+            out |= static_cast<uint32_t>(first[k]) >= static_cast<uint32_t>(pool.pages);
         }
+        for (int j = lane + 32 * MINE; j < n; j += 32) out |= static_cast<uint32_t>(from[j]) >= static_cast<uint32_t>(pool.pages);
+        out = __any_sync(0xFFFFFFFFu, out);
+        if (lane == 0) {
+            if (gridDim.x > 1) list_of(a, dst_s[p])[0] = out ? 1 : 0;
+            if (out) {
+                pages_s[p] = -1;
+                record_error(a.err, MOE_ERR_BAD_ID);
+            }
+        }
+        if (out) continue;
+        auto take = [&](int j, int page) {
+            to[j] = page;
+            atomicAdd(pool.refs + page, 1);
+        };
+#pragma unroll
+        for (int k = 0; k < MINE; ++k)
+            if (lane + 32 * k < n) take(lane + 32 * k, first[k]);
+        for (int j = lane + 32 * MINE; j < n; j += 32) take(j, from[j]);
     }
+    __syncthreads();
     if (gridDim.x > 1) {
-        __syncthreads();
         if (i == 0) last_s = atom_add_acq_rel_gpu(a.forked, 1u) == gridDim.x - 1;
         __syncthreads();
         if (!last_s) return;
         if (i == 0) *a.forked = 0;   // for the next call
     }
-    if (ok) {
+    const bool bad = gridDim.x > 1 ? ok && pages > 0 && list_of(a, dst)[0] != 0 : pages_s[i] < 0;
+    if (ok && !bad) {
         pool.held[dst] = pages;
         a.length_out[dst] = length;
     }

@@ -70,3 +70,32 @@ def test_accept_that_moves_nothing(number):
         after = api.pages_accept(b.pool, i32([6, 6]), path, i32([2, -1]))
         assert api.last_device_error(b.pool.ws) == BAD_ID
         assert after.tolist() == [6, 6] and state.unchanged()
+
+
+@pytest.mark.parametrize("number", NUMBERS)
+@pytest.mark.parametrize("pairs", [1, 60])   # one CTA, several
+def test_fork(number, pairs):
+    seqs = 2 + 2 * pairs
+    b = pool_of(seqs, [16, 16] + [0] * 2 * pairs, [14, 9] + [0] * 2 * pairs)
+    good = int(b.pool.table[0, 2])
+    src, dst = [0] * pairs + [1] * pairs, list(range(2, seqs))
+    length = i32(b.length)
+    b.pool.table[0, 2] = number
+    state = State(b.pool, length)
+    api.pages_fork(b.pool, i32(src[:pairs]), i32(dst[:pairs]), length)
+    assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
+    # those of the other sequence are served beside them
+    refused = b.pool.table[2:2 + pairs].clone()
+    b.ref.fork(src[pairs:], dst[pairs:], b.length)
+    api.pages_fork(b.pool, i32(src), i32(dst), length)
+    assert length.tolist() == b.length and torch.equal(b.pool.table[2:2 + pairs], refused)
+    b.pool.table[0, 2] = good
+    b.check(b.expect([]), BAD_ID)
+    # a shorter source, whose bad number lies behind it
+    length[0] = b.length[0] = 8
+    b.pool.table[0, 2] = number
+    b.ref.fork([0], [2], b.length)
+    api.pages_fork(b.pool, i32([0]), i32([2]), length)
+    b.pool.table[0, 2] = good
+    assert length.tolist() == b.length
+    b.check(b.expect([]))
