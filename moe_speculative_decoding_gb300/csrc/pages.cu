@@ -27,11 +27,7 @@ constexpr int kStep = kBook * kMine;
 __device__ __forceinline__ int32_t *list_of(const PageArgs &a, int b) { return a.lists + 4 + 4ll * b; }
 __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists + 4 + 4ll * a.pool.seqs; }
 __device__ __forceinline__ int32_t *table_of(const PageArgs &a, int b) { return a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages; }
-__device__ __forceinline__ bool in_pool(const PageArgs &a, int page) {
-    const bool ok = static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.pages);
-    if (!ok) record_error(a.err, MOE_ERR_BAD_ID);
-    return ok;
-}
+__device__ __forceinline__ bool in_pool(const PageArgs &a, int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.pages); }
 
 // Sum of v over the threads before this one (32-bit sums hold: requests are at most seqs * max_pages),
 // and over all.
@@ -81,7 +77,7 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
             rows = length - first * pool.page;
             if (rows > 0) {
                 at = table_of(a, b)[first];
-                bad = static_cast<uint32_t>(at) >= static_cast<uint32_t>(pool.pages);
+                bad = !in_pool(a, at);
                 if (!bad) holders = pool.refs[at];
             }
         }
@@ -279,7 +275,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
         bool other = false;
         for (int j = first + lane; j < held; j += 32) {
             const int page = table_of(a, b)[j];
-            other |= static_cast<uint32_t>(page) >= static_cast<uint32_t>(pool.pages) || (j <= last && pool.refs[page] > 1);
+            other |= !in_pool(a, page) || (j <= last && pool.refs[page] > 1);
         }
         bad = __any_sync(0xFFFFFFFFu, other);
     }
@@ -422,9 +418,9 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < MINE; ++k) {
             first[k] = lane + 32 * k < n ? from[lane + 32 * k] : 0;
-            out |= static_cast<uint32_t>(first[k]) >= static_cast<uint32_t>(pool.pages);
+            out |= !in_pool(a, first[k]);
         }
-        for (int j = lane + 32 * MINE; j < n; j += 32) out |= static_cast<uint32_t>(from[j]) >= static_cast<uint32_t>(pool.pages);
+        for (int j = lane + 32 * MINE; j < n; j += 32) out |= !in_pool(a, from[j]);
         out = __any_sync(0xFFFFFFFFu, out);
         if (lane == 0) {
             if (gridDim.x > 1) list_of(a, dst_s[p])[0] = out ? 1 : 0;
@@ -464,27 +460,38 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const __grid_constant__
     if (i >= a.items) return;
     const int b = a.ids[i];
     if (b < 0) return;
-    int held = 0;
-    if (lane == 0) {
-        if (b >= a.pool.seqs) {
-            record_error(a.err, MOE_ERR_BAD_ID);
-        } else {
-            held = atomicExch(a.pool.held + b, 0);   // of two that name it one finds its pages
-            if (held < 0 || held > a.pool.max_pages) {
-                record_error(a.err, MOE_ERR_BAD_ID);
-                held = 0;
-            }
-            if (a.length_out != nullptr) a.length_out[b] = 0;
+    if (b >= a.pool.seqs) {
+        if (lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
+        return;
+    }
+    // Of several warps that name the sequence one finds its pages below; here any may find them or none left.
+    int held = *const_cast<volatile int32_t *>(a.pool.held + b);
+    held = __shfl_sync(0xFFFFFFFFu, held, 0);
+    const int32_t *const table = table_of(a, b);
+    constexpr int MINE = 4;   // a lane's first page numbers stay in registers
+    int first[MINE];
+    bool bad = held < 0 || held > a.pool.max_pages;
+    if (!bad) {
+#pragma unroll
+        for (int k = 0; k < MINE; ++k) {
+            first[k] = lane + 32 * k < held ? table[lane + 32 * k] : 0;
+            bad |= !in_pool(a, first[k]);
         }
+        for (int j = lane + 32 * MINE; j < held; j += 32) bad |= !in_pool(a, table[j]);
+    }
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+        if (lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
+        return;
+    }
+    if (lane == 0) {
+        if (held > 0) held = atomicExch(a.pool.held + b, 0);
+        if (a.length_out != nullptr) a.length_out[b] = 0;
     }
     held = __shfl_sync(0xFFFFFFFFu, held, 0);
-    if (held == 0) return;
-    const int32_t *const table = table_of(a, b);
-#pragma unroll 4
-    for (int j = lane; j < held; j += 32) {
-        const int page = table[j];
-        if (in_pool(a, page)) atomicSub(a.pool.refs + page, 1);
-    }
+#pragma unroll
+    for (int k = 0; k < MINE; ++k)
+        if (lane + 32 * k < held) atomicSub(a.pool.refs + first[k], 1);
+    for (int j = lane + 32 * MINE; j < held; j += 32) atomicSub(a.pool.refs + table[j], 1);
 }
 
 template <typename K, typename... Args>

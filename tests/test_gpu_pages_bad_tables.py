@@ -99,3 +99,36 @@ def test_fork(number, pairs):
     b.pool.table[0, 2] = good
     assert length.tolist() == b.length
     b.check(b.expect([]))
+
+
+@pytest.mark.parametrize("number", NUMBERS)
+def test_free(number):
+    b = pool_of(3, [16, 16, 3], [14, 9, 3])
+    good = int(b.pool.table[0, 1])
+    b.pool.table[0, 1] = number
+    length = i32(b.length)
+    state = State(b.pool, length)
+    for ids in ([0], [0, 0, 0]):
+        api.pages_free(b.pool, i32(ids), length)
+        assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
+    b.ref.free([1, 2])
+    api.pages_free(b.pool, i32([0, 1, 0, 2, 1]), length)
+    assert length.tolist() == [14, 0, 0]
+    b.pool.table[0, 1] = good
+    b.check(b.expect([]), BAD_ID)
+
+
+@pytest.mark.parametrize("held", [-1, 7, 2 ** 31 - 1, -2 ** 31])
+def test_held_out_of_range(held):
+    b = pool_of(3, [16, 16, 0], [14, 9, 0])
+    b.pool.held[0] = held
+    length = i32(b.length)
+    state = State(b.pool, length)
+    api.pages_free(b.pool, i32([0, 0]), length)
+    assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
+    api.pages_fork(b.pool, i32([0]), i32([2]), length)
+    assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
+    assert api.pages_accept(b.pool, length, i32([[1], [0], [0]]), i32([1, -1, -1])).tolist() == b.length
+    assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
+    assert api.pages_reserve(b.pool, length, i32([4, 0, 0])).tolist() == [0, 1, 1]
+    assert api.last_device_error(b.pool.ws) == BAD_ID and state.unchanged()
