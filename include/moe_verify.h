@@ -739,8 +739,8 @@ moe_status_t moe_latent_attention(const moe_latent_cache_t *cache, const moe_hea
  * The page table of a pool is the page_table of the attention calls.
  *
  * Sequence b holds held[b] pages, table[b][0 .. held[b]), and has its tokens in the first positions of
- * them; entries beyond are left as they were.  Pages behind the one with its last token are its own
- * (the calls see to that).  Device-only problems (ids, lengths, pages or paths out of range) are
+ * them; entries beyond are left as they were.  Positions that moe_pages_reserve makes room for lie in
+ * pages that nobody else holds.  Device-only problems (ids, lengths, pages or paths out of range) are
  * recorded as MOE_ERR_BAD_ID in the error word of ws, and the sequence concerned is left as it was.
  * Calls on one pool, and calls that share a workspace, run one after the other (on one stream, or ordered by
  * events).
@@ -776,7 +776,8 @@ size_t moe_pages_workspace_bytes(const moe_page_pool_t *pool);
  * free ones, sequences in order.  If position length[b] lies inside a page that others hold too, and
  * need[b] > 0, that page is replaced by a new one and its rows below the length are copied, in every
  * cache; of several sequences that share it in one call, each in order takes a copy as long as
- * others still hold it.  From the first sequence on that the free pages do not suffice for, none that
+ * others still hold it.  Pages held behind it (of a sequence whose length was lowered) that the need[b] tokens
+ * reach and others hold too, as the call finds them, are replaced and nothing is copied.  From the first sequence on that the free pages do not suffice for, none that
  * needs a page gets any: got[b] = 0 and it is left as it was, otherwise 1 (0 also for one that is
  * recorded).
  *   length, need [dev] int32 [seqs]: need[b] >= 0, 0 <= length[b] <= held[b] * page; got [dev] int32

@@ -1084,7 +1084,7 @@ def page_pool(caches, seqs: int, max_pages: int) -> PagePool:
 def pages_reserve(pool: PagePool, length: torch.Tensor, need: torch.Tensor, got=None) -> torch.Tensor:
     """moe_pages_reserve: pages for need int32 [seqs] more tokens of every sequence after its length int32 [seqs],
     the lowest free ones, sequences in order; a shared page that would be written is copied in every
-    cache.  Returns got int32 [seqs]: 1 where the sequence has its pages, 0 where they ran out."""
+    cache, or replaced where it lies behind the length.  Returns got int32 [seqs]: 1 where the sequence has its pages, 0 where they ran out."""
     device = pool.index
     if device != _current_device():
         return _there(pool.refs, pages_reserve, pool, length, need, got)

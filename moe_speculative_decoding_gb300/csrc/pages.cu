@@ -53,6 +53,10 @@ __device__ __forceinline__ int before_me(int v, int *tmp, int &total) {
 }
 
 // ------------------------------------------------------------------ reserve
+// Of a sequence's pages that will be written, one that others hold too is replaced.  The page with rows to keep is
+// copied, by each of its holders that asks as long as others are left.  A page behind it (held beyond the length: a
+// branch whose length was lowered) has nothing to keep and is replaced whoever else holds it; its
+// count, with the copied pages', goes down when all counts have been read.
 __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_constant__ PageArgs a) {
     __shared__ __align__(16) int shared_s[kBook];
     __shared__ int tmp[32], copies_s, rows_s, fail_s;
@@ -61,7 +65,7 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
     const int b = threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const moe_page_pool_t &pool = a.pool;
     const bool in = b < pool.seqs;
-    int length = 0, need = 0, held = 0, want = 0, first = 0, rows = 0, at = -1, holders = 0;
+    int length = 0, need = 0, held = 0, want = 0, first = 0, rows = 0, at = -1, holders = 0, stop = 0, behind = 0;
     bool bad = false;
     if (in) {
         length = a.length[b];
@@ -72,13 +76,33 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
               end > static_cast<long long>(pool.max_pages) * pool.page;
         want = held;
         if (!bad && need > 0) {
-            want = max(held, static_cast<int>((end + pool.page - 1) / pool.page));
+            const int pages = static_cast<int>((end + pool.page - 1) / pool.page);
+            want = max(held, pages);
             first = length / pool.page;
             rows = length - first * pool.page;
+            // the pages that are there and will be written: the one with rows to keep, and those behind
+            stop = min(held, pages);
+            const int32_t *const row = table_of(a, b);
+            int page[2], count[2];   // of the first two at once: mostly there are no more
+#pragma unroll
+            for (int k = 0; k < 2; ++k) page[k] = first + k < stop ? row[first + k] : 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                bad |= !in_pool(a, page[k]);
+                count[k] = first + k < stop && in_pool(a, page[k]) ? pool.refs[page[k]] : 0;
+            }
             if (rows > 0) {
-                at = table_of(a, b)[first];
-                bad = !in_pool(a, at);
-                if (!bad) holders = pool.refs[at];
+                at = page[0];
+                holders = count[0];
+            } else {
+                behind += count[0] > 1;
+            }
+            behind += count[1] > 1;
+#pragma unroll 1
+            for (int j = first + 2; j < stop; ++j) {
+                const int other = row[j];
+                bad |= !in_pool(a, other);
+                if (!bad) behind += pool.refs[other] > 1;
             }
         }
         if (bad) {
@@ -87,6 +111,7 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
         }
     }
     const bool shared = !bad && holders > 1;
+    if (bad) behind = 0;
     shared_s[b] = shared ? at : -1;
     if (b == 0) {
         copies_s = rows_s = 0;
@@ -94,17 +119,17 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
     }
     __syncthreads();
     // holders before this sequence that take a copy: its own is needed while others are left
-    auto sharers = [&](int stop) {
+    auto sharers = [&](int upto) {
         int n = 0, i = 0;
-        for (; i + 4 <= stop; i += 4) {
+        for (; i + 4 <= upto; i += 4) {
             const int4 x = *reinterpret_cast<const int4 *>(shared_s + i);
             n += (x.x == at) + (x.y == at) + (x.z == at) + (x.w == at);
         }
-        for (; i < stop; ++i) n += shared_s[i] == at;
+        for (; i < upto; ++i) n += shared_s[i] == at;
         return n;
     };
     bool copy = shared && holders - sharers(b) > 1;
-    const int extra = want - held + (copy ? 1 : 0);
+    const int extra = want - held + behind + (copy ? 1 : 0);
     int total;
     const int mine = before_me(extra, tmp, total);
     // the lowest free pages, as many as are asked for: the next step's counts are on their way while this
@@ -152,18 +177,28 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
             const int page = order[mine];
             table_of(a, b)[first] = page;
             pool.refs[page] = 1;
-            atomicSub(pool.refs + at, 1);
             int32_t *const e = list_of(a, atomicAdd(&copies_s, 1));   // (in any order: the copies are independent)
             e[0] = at;
             e[1] = page;
             e[2] = rows;
             atomicMax(&rows_s, rows);
         }
+        if (ok && behind > 0) {
+            int k = mine + (copy ? 1 : 0);
+#pragma unroll 1
+            for (int j = first + (rows > 0 ? 1 : 0); j < stop; ++j) {
+                const int page = table_of(a, b)[j];
+                if (pool.refs[page] < 2) continue;
+                table_of(a, b)[j] = order[k];
+                pool.refs[order[k]] = 1;
+                order[k++] = page;
+            }
+        }
     }
     // the pages behind those held, a warp's sequences one after the other
     for (uint32_t left = __ballot_sync(0xFFFFFFFFu, grown > 0); left != 0; left &= left - 1) {
         const int l = __ffs(left) - 1, n = __shfl_sync(0xFFFFFFFFu, grown, l), from = __shfl_sync(0xFFFFFFFFu, held, l);
-        const int rank = __shfl_sync(0xFFFFFFFFu, mine + (copy ? 1 : 0), l);
+        const int rank = __shfl_sync(0xFFFFFFFFu, mine + extra - (want - held), l);
         int32_t *const row = table_of(a, warp * 32 + l) + from;
         for (int j = lane; j < n; j += 32) {
             const int page = order[rank + j];
@@ -171,7 +206,11 @@ __global__ void __launch_bounds__(kBook) pages_reserve_kernel(const __grid_const
             pool.refs[page] = 1;
         }
     }
-    __syncthreads();
+    __syncthreads();   // the counts have been read
+    if (copy) atomicSub(pool.refs + at, 1);
+    if (ok)
+#pragma unroll 1
+        for (int k = mine + (copy ? 1 : 0); behind > 0; --behind, ++k) atomicSub(pool.refs + order[k], 1);
     if (b == 0) {
         a.lists[0] = copies_s;
         a.lists[2] = rows_s;
