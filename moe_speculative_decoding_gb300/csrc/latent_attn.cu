@@ -1184,7 +1184,8 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     // 16 columns, 59.4 with 32 and 66.1 with 64; with 32 rows 59.8 and 66.1; 64 of 801-8209 with 16 rows 67.6, 70.6
     // and 79.0.
     const int rows = a.max_tokens * a.heads, nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : 64);
-    const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kPos - 1) / kPos;
+    // (a table may be wider than any sequence is long, by more than 64-bit products hold)
+    const long long item_tiles = (std::min(static_cast<long long>(a.max_pages) * a.cache.page, kMaxPositions) + kPos - 1) / kPos;
     const long long items = static_cast<long long>(a.seqs) * ((rows + nt - 1) / nt);
     // Short contexts: an item's few tiles one after the other take less time than another end of an item and the
     // launch that joins the parts (and 2 us less of the host).  16 heads of one token: one sequence of five tiles 10.8 us undivided against

@@ -803,7 +803,8 @@ cudaError_t launch_tree_attn(TreeArgs a, cudaStream_t s, bool pdl) {
     // for the host), 12.2 and 9.2 at eight; 256 rows, four sequences: 24.0 and 30.8 at eight.  With
     // enough items for the SMs (16 sequences, e4m3): 16.7 and 24.8 at eight, 22.6 and 24.4 at twelve,
     // 27.4 and 26.9 at sixteen.
-    const long long item_tiles = (static_cast<long long>(a.max_pages) * a.cache.page + kTile - 1) / kTile;
+    // (a table may be wider than any sequence is long, by more than 64-bit products hold)
+    const long long item_tiles = (std::min(static_cast<long long>(a.max_pages) * a.cache.page, kMaxPositions) + kTile - 1) / kTile;
     const long long items = static_cast<long long>(a.seqs) * a.cache.heads * ((a.max_tokens * a.group + 2 * kTile - 1) / (2 * kTile));
     a.undivided = item_tiles <= (2 * items >= sms ? 12 : a.max_tokens * a.group > kNarrowRows ? 8 : 4);
     // no more CTAs than the page tables could fill with tiles
