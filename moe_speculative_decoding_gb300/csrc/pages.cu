@@ -29,6 +29,9 @@ __device__ __forceinline__ int32_t *order_of(const PageArgs &a) { return a.lists
 __device__ __forceinline__ int32_t *table_of(const PageArgs &a, int b) { return a.pool.table + static_cast<int64_t>(b) * a.pool.max_pages; }
 __device__ __forceinline__ bool in_pool(const PageArgs &a, int page) { return static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.pages); }
 
+// Pages of n positions (n + page may be more than 31 bits hold).
+__device__ __forceinline__ int pages_of(int n, int page) { return n > 0 ? (n - 1) / page + 1 : 0; }
+
 // Sum of v over the threads before this one (32-bit sums hold: requests are at most seqs * max_pages),
 // and over all.
 __device__ __forceinline__ int before_me(int v, int *tmp, int &total) {
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     }
     // The pages that rows leave or go to and those that are given up are pages, and what rows go to nobody else holds.
     if (!bad && count >= 0) {
-        const int first = moves > 0 ? ctx / pool.page : (ctx + count + pool.page - 1) / pool.page, last = moves > 0 ? (ctx + count - 1) / pool.page : -1;
+        const int first = moves > 0 ? ctx / pool.page : pages_of(ctx + count, pool.page), last = moves > 0 ? (ctx + count - 1) / pool.page : -1;
         bool other = false;
         for (int j = first + lane; j < held; j += 32) {
             const int page = table_of(a, b)[j];
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
     if (bad && lane == 0) record_error(a.err, MOE_ERR_BAD_ID);
     const bool act = !bad && count >= 0;
     const int after = act ? ctx + count : ctx;
-    const int left = (after + pool.page - 1) / pool.page;   // at most held
+    const int left = pages_of(after, pool.page);   // at most held
     if (lane == 0) {
         int32_t *const e = list_of(a, b);
         e[0] = ctx;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kBook) pages_fork_kernel(const __grid_constant
     for (; k < i && ok; ++k) same += dst_s[k] == dst;
     ok = ok && same == 0;
     if (in && !ok) record_error(a.err, MOE_ERR_BAD_ID);
-    const int pages = ok ? (length + pool.page - 1) / pool.page : 0;
+    const int pages = ok ? pages_of(length, pool.page) : 0;
     pages_s[i] = pages;
     __syncthreads();
     for (int p = blockIdx.x * 32 + warp; p < a.items; p += gridDim.x * 32) {
