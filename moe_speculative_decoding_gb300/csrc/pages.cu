@@ -569,7 +569,7 @@ cudaError_t launch_pages_reserve(const PageArgs &a, const PageRows *rows, int la
 }
 
 cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int launches, cudaStream_t s, bool pdl) {
-    cudaError_t e = launch(pages_accept_kernel, static_cast<unsigned>((a.pool.seqs + 7) / 8), 256, s, pdl, a);
+    cudaError_t e = launch(pages_accept_kernel, (static_cast<unsigned>(a.pool.seqs) + 7) / 8, 256, s, pdl, a);
     if (a.path == nullptr) return e;   // nothing moves
     // the first launch gives the pages up; without caches it does nothing else
     static const PageRows none = {};
@@ -589,7 +589,7 @@ cudaError_t launch_pages_fork(const PageArgs &a, cudaStream_t s, bool pdl) {
 }
 
 cudaError_t launch_pages_free(const PageArgs &a, cudaStream_t s, bool pdl) {
-    return launch(pages_free_kernel, static_cast<unsigned>((a.items + 7) / 8), 256, s, pdl, a);
+    return launch(pages_free_kernel, (static_cast<unsigned>(a.items) + 7) / 8, 256, s, pdl, a);
 }
 
 }  // namespace moe

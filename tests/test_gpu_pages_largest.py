@@ -31,3 +31,15 @@ def test_pages_of_nearly_2_31_positions():
     assert L.moe_pages_free(at, ids.data_ptr(), 1, length.data_ptr(), ws.data_ptr(), 4096, s) == 0
     assert length.tolist() == [page - 1, 0, 0] and held.tolist() == [1, 0, 0] and refs.tolist() == [1]
     assert api.last_device_error(ws) == 0
+
+
+def test_free_of_nearly_2_31_ids():
+    cache = api.latent_cache(20, 4, 8, 8)
+    pool = api.page_pool([cache], 2, 6)
+    length = torch.tensor([9, 5], dtype=torch.int32, device="cuda")
+    api.pages_reserve(pool, torch.zeros_like(length), length)
+    ids = torch.full((2 ** 31 - 1,), -1, dtype=torch.int32, device="cuda")
+    ids[-1] = 1
+    api.pages_free(pool, ids, length)
+    assert length.tolist() == [9, 0] and pool.held.tolist() == [3, 0] and int(pool.refs.sum()) == 3
+    assert api.last_device_error(pool.ws) == 0
