@@ -93,7 +93,7 @@ bool same(const PageRows &a, const PageRows &b) {
     return a.planes == b.planes && std::memcmp(a.plane, b.plane, sizeof a.plane) == 0;
 }
 
-// The rows' kernels number their work, sequences by layers, planes and pieces of up to 1024 units, in 31 bits.
+// The copying kernel numbers its work, sequences by layers, planes and pieces of up to 1024 units, in 31 bits.
 bool too_much(const moe_page_pool_t *pool, const Plane &p) {
     const int64_t pieces = (static_cast<int64_t>(p.per_row) * pool->page + 1023) / 1024;
     return pieces >= (1ll << 21) || pool->seqs * pieces >= (1ll << 31) / (kLayersLaunch * kPlanes);
@@ -305,6 +305,8 @@ moe_status_t moe_pages_accept(const moe_page_pool_t *pool, const int32_t *ctx, c
         return MOE_ERR_ARG;
     Layers layers;
     if ((st = collect(pool, caches, layers)) != MOE_OK || (st = check_ws(pool, ws, ws_bytes)) != MOE_OK) return st;
+    for (int i = 0; i < layers.launches; ++i)   // the moving kernel numbers sequences by layers and slices in 31 bits
+        if (static_cast<int64_t>(pool->seqs) * move_slices(layers.rows[i]) >= (1ll << 31) / kLayersLaunch) return MOE_ERR_UNSUPPORTED;
     PageArgs a = page_args(pool, ws);
     a.ctx = ctx;
     a.path = path;

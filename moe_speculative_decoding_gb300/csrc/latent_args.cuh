@@ -62,6 +62,14 @@ struct PageRows {
     int32_t planes, layers;
     void *base[kLayersLaunch][kPlanes];
 };
+// Pieces of a row (of up to 128 units, all its planes in line) that a CTA of the moving kernel takes.
+constexpr int kMove = 128;
+inline int move_columns(const PageRows &r) {
+    int columns = 0;
+    for (int k = 0; k < r.planes; ++k) columns += r.plane[k].per_row;
+    return columns;
+}
+inline int move_slices(const PageRows &r) { return (move_columns(r) + kMove - 1) / kMove; }
 
 struct PageArgs {
     moe_page_pool_t pool;

@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kCopy) pages_copy_kernel(const __grid_constant
     pdl_trigger();
     const int copies = a.lists[0], slices = (a.lists[2] * row_units + kUnits - 1) / kUnits;   // of the copy with most rows
     if (copies == 0) return;
-    // (the launch keeps the items below 2^31; with divisions for every item and unit the integer pipe was
+    // (the caller keeps the items below 2^31; with divisions for every item and unit the integer pipe was
     // the bound, 28 us for 66 MB)
     const uint32_t whole = static_cast<uint32_t>(copies * p.layers * p.planes), items = whole * static_cast<uint32_t>(slices);
     const Divide by_whole(whole), by_copies(static_cast<uint32_t>(copies));
@@ -342,14 +342,13 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
 // A thread takes one column of a row (16 bytes, 4 of scales) through all of a sequence's moves in order: the
 // path ascends, so target i is at or before source i and before every later one, and no row is written
 // before it was read.  Eight rows' loads are in flight together.
-constexpr int kMove = 128;
 
 __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int columns, int slices, int settle) {
     __shared__ int source_s[MOE_MAX_TREE_TOKENS][2], target_s[MOE_MAX_TREE_TOKENS][2];   // page, row
     pdl_wait();
     pdl_trigger();
     const uint32_t seqs = static_cast<uint32_t>(a.pool.seqs), whole = seqs * static_cast<uint32_t>(p.layers);
-    const uint32_t items = whole * static_cast<uint32_t>(slices);   // (the launch keeps them below 2^31)
+    const uint32_t items = whole * static_cast<uint32_t>(slices);   // (the caller keeps them below 2^31)
     if (settle) {
         for (int b = static_cast<int>(blockIdx.x); b < a.pool.seqs; b += static_cast<int>(gridDim.x)) {
             const int4 e = *reinterpret_cast<const int4 *>(list_of(a, b));
@@ -575,11 +574,9 @@ cudaError_t launch_pages_accept(const PageArgs &a, const PageRows *rows, int lau
     static const PageRows none = {};
     for (int i = 0; i < std::max(launches, 1) && e == cudaSuccess; ++i) {
         const PageRows &r = launches > 0 ? rows[i] : none;
-        int columns = 0;
-        for (int k = 0; k < r.planes; ++k) columns += r.plane[k].per_row;
-        const int slices = (columns + kMove - 1) / kMove;
+        const int slices = move_slices(r);
         const int64_t items = std::max<int64_t>(static_cast<int64_t>(a.pool.seqs) * r.layers * slices, a.pool.seqs);
-        e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, r, columns, slices, i == 0 ? 1 : 0);
+        e = launch(pages_move_kernel, static_cast<unsigned>(std::min<int64_t>(items, kSms * 16)), kMove, s, pdl, a, r, move_columns(r), slices, i == 0 ? 1 : 0);
     }
     return e;
 }
