@@ -755,7 +755,8 @@ typedef struct {
 } moe_page_pool_t;
 
 /* The caches whose rows live in the pool's pages, one of each layer, every one with the pool's pages
- * and page; either list may be empty (NULL, 0).  At most 1024 of equal shape, 16 times 64 in all where shapes
+ * and page and memory of its own (rows of one that is listed twice would move twice); either list may be empty
+ * (NULL, 0).  At most 1024 of equal shape, 16 times 64 in all where shapes
  * differ, and seqs * ceil(bytes of a page's keys / 16384) < 2^23; for moe_pages_accept
  * also seqs * ceil(u / 128) < 2^25 with u units of a row, 16 bytes of keys, values or latent rows and scales of 4. */
 typedef struct {

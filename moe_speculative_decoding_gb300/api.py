@@ -1039,8 +1039,8 @@ def latent_attention(cache: LatentCache, q: torch.Tensor, q_start: torch.Tensor,
 
 # ---------------------------------------------------------------- pages of a cache
 class PagePool:
-    """The pages of some layers' caches (KVCache or LatentCache, equal numbers of pages and tokens a page) and
-    who holds them (moe_page_pool_t), over tensors the caller owns: refs int32 [pages] (holders of a page),
+    """The pages of some layers' caches (KVCache or LatentCache, equal numbers of pages and tokens a page, none
+    twice) and who holds them (moe_page_pool_t), over tensors the caller owns: refs int32 [pages] (holders of a page),
     table int32 [seqs, max pages] (the page_table of the attention calls), held int32 [seqs] (pages a
     sequence holds).  All zero: every page is free.  ws is the calls' workspace; its error word records
     ids, lengths and paths out of range."""
@@ -1057,6 +1057,9 @@ class PagePool:
         for c in self.caches:
             if (c.pages, c.page, c.index) != (self.pages, self.page, self.index):
                 raise ValueError("caches must have equal pages and lie on one device")
+        parts = [t.data_ptr() for c in self.caches for t in ((c.k, c.v) if isinstance(c, KVCache) else (c.rows,))]
+        if len(set(parts)) < len(parts):
+            raise ValueError("caches must not share memory: rows would move twice")
         index = self.index
         _flat(refs, "refs", torch.int32, (self.pages,), index)
         if table.dim() != 2:

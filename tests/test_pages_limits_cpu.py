@@ -1,10 +1,13 @@
-"""Limits of the pages' calls that the host checks, before any launch."""
+"""Limits and refusals of the pages' calls that the host checks, before any launch."""
 import ctypes
 
 import pytest
+import torch
 
 from moe_speculative_decoding_gb300 import api
 from moe_speculative_decoding_gb300 import build as mbuild
+
+from test_latent_cpu import _i32, _t, entered  # noqa: F401 (a fixture: tensors of another device over no library)
 
 UNSUPPORTED = 2
 
@@ -29,3 +32,14 @@ def test_accept_numbers_its_rows_in_31_bits(lib, seqs, heads, dtype):
     """Rows of 4,096 units of 16 bytes, or of 2,048 and 256 scales: 32 and 18 slices, of 64 layers each, for every
     sequence."""
     assert accept(lib, seqs, heads, dtype) == UNSUPPORTED
+
+
+def test_a_cache_is_listed_once(entered):  # noqa: F811
+    """Rows of one that is listed twice would move twice, those of keys that are the values too."""
+    k, v, rows = _t(4, 8, 2, 4), _t(4, 8, 2, 4), _t(4, 8, 40)
+    kv, latent = api.KVCache(k, v), api.LatentCache(rows, 32)
+    api.page_pool([kv, latent], 2, 3)
+    for caches in ([kv, kv], [latent, kv, latent], [kv, api.KVCache(k, _t(4, 8, 2, 4))], [api.KVCache(k, k)],
+                   [latent, api.LatentCache(rows, 24)]):
+        with pytest.raises(ValueError):
+            api.page_pool(caches, 2, 3)
