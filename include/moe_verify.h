@@ -27,6 +27,10 @@
  *    dereferenced.  Nothing throws across the ABI.
  *  * Threading: calls are re-entrant; calls that share a workspace must be ordered on
  *    one stream.
+ *  * Kinds of workspace: behind its first 256 bytes an expert operation's workspace keeps words that
+ *    later expert operations go by (moe_workspace_bytes), so it is not given to attention's or the pages'
+ *    calls, unless moe_workspace_init zeroes it before the next expert operation.  These keep nothing
+ *    there from one call to the next.  moe_union_cost's scratch begins at its first byte and is its own.
  */
 #ifndef MOE_VERIFY_H
 #define MOE_VERIFY_H
