@@ -694,7 +694,7 @@ typedef struct {
  * s / page): the latent channels, normalised when norm is not NULL,
  *     y_i = c_i norm_i / sqrt(mean_j(c_j^2) + eps),
  * and the rotary channels, turned by the token's position when rotary is not NULL (rotary->rot
- * <= rope; channels from rot on are copied), in fp32, rounded once to the cache's type.  When q is not
+ * <= rope; channels from rot on are copied), in fp32, the sum of squares too, rounded once to the cache's type.  When q is not
  * NULL (with rotary), its rows of rope channels are rotated into q_out in the same launch, for every
  * token, whatever its slot.  A negative slot takes nothing; one beyond the cache is recorded and takes
  * nothing; slots that are not negative must differ.  A token whose position is outside the table is

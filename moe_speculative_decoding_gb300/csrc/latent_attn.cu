@@ -36,7 +36,8 @@
 // take a tile in 3,100 cycles (7.0 TB/s) between a beginning of 10,000 and an end of 6,000 and the join.
 // Many rows are bound by shared memory: the products read 4 KB for each of a tile's 36 steps of S^T (32 cycles at
 // 128 bytes a cycle) and 6 KB for each of the 16 of O^T, and its copies write 72 KB, together 2,500 cycles;
-// a tile of 64 rows takes 2,530.  Four sequences of 4001-8201 with trees of 64 tokens 81-84 us (730 TFLOP/s),
+// a tile of 64 rows takes 2,530 (with 168 registers to a thread a few words spill: 116 bytes stored, 64 loaded by
+// the compiler's count).  Four sequences of 4001-8201 with trees of 64 tokens 81-84 us (730 TFLOP/s),
 // eight of 4001-16411 with two tokens of 128 heads 70-71 (625).  An item's end costs a CTA 11,000 cycles (its last
 // product, sums, and 128 KB of parts at 31 bytes a cycle), the join 6-8 us.  One token over 300 positions: 9.7 us,
 // a chain of latencies.
@@ -1188,8 +1189,12 @@ cudaError_t launch_latent_attn(LatentArgs a, cudaStream_t s, bool pdl) {
     const long long item_tiles = (std::min(static_cast<long long>(a.max_pages) * a.cache.page, kMaxPositions) + kPos - 1) / kPos;
     const long long items = static_cast<long long>(a.seqs) * ((rows + nt - 1) / nt);
     // Short contexts: an item's few tiles one after the other take less time than another end of an item and the
-    // launch that joins the parts (and 2 us less of the host).  16 heads of one token: one sequence of five tiles 10.8 us undivided against
-    // 9.7, of sixteen 20.9 against 9.0; 64 sequences of five 13.8 against 15.8, 16 of fifteen 20.0 against 17.3.
+    // launch that joins the parts, and 2 us less of the host.  Undivided and divided, one token of 16 heads, contexts
+    // that fill the table, in us: 4 tiles, 1, 16 and 30 sequences 10.7 and 9.1, 11.0 and 9.5, 11.1 and 11.2 (the host's
+    // time decides), 5 tiles 11.8 and 9.3, 12.1 and 9.6, 12.2 and 11.6; 8 tiles, 38, 64 and 75 sequences 16.8 and 14.0,
+    // 17.6 and 19.5, 18.4 and 20.9, 9 tiles 18.1 and 16.0, 18.8 and 19.5, 19.6 and 22.0; 12 tiles, 76 and 128 sequences 23.0 and
+    // 24.3, 27.7 and 32.1, 16 tiles 28.1 and 27.8, 33.6 and 38.5.  The rule knows the table's width, not the lengths: in a
+    // table as wide as one long sequence needs, short ones are divided too.
     a.undivided = item_tiles <= 4 || (4 * items >= sms && item_tiles <= 8) || (2 * items >= sms && item_tiles <= 12);
     // no more CTAs than the page tables could fill with tiles
     const int ctas = static_cast<int>(std::min<long long>(sms, items * item_tiles));

@@ -6,7 +6,9 @@
 // Streaming work, a few operations an element: the bound is memory traffic, each row read once and
 // written once.  16301 tokens with 32 heads of 64 rotary channels, bf16: 35.5 us, 4.94 TB/s (a copy of the queries'
 // bytes alone, 128 of every 384, reaches 5.5); a pass of 16 tokens with 16 heads 2.8 us, the latency of its
-// chain of loads (slot and position, table row).
+// chain of loads (slot and position, table row).  The same for fp32: 76 us, 4.55 TB/s, and 3.4; bf16 rows into an fp32 cache
+// 39 us, 4.96 TB/s.  Rows that are not 16-byte pieces take a warp each, an element or two to a lane at a
+// time: 109 us in bf16 (1.6 TB/s), 115 in fp32 (3.0), a pass of 16 tokens 5.3.
 #include "latent_args.cuh"
 #include "row_common.cuh"
 

@@ -8,7 +8,7 @@
 // they are: its bound is memory traffic, each row read once and written once.
 //
 // 24 branches given up, forked and grown by 24 copies of 14 rows in 48 layers of 4 heads of 128 (132 MB): 24 us,
-// 15.5 of them the copies; 128 branches in a pool of 40,000 pages, where 10 MB move: 19 us, the four kernels'
+// 15.5 of them the copies; 128 branches in a pool of 40,000 pages, where 10 MB move: 17.6 us, the four kernels'
 // chains of loads; 16 sequences' paths of up to 6 rows in 48 layers reserved and accepted: 12 us.
 #include <algorithm>
 
