@@ -694,8 +694,8 @@ typedef struct {
  * s / page): the latent channels, normalised when norm is not NULL,
  *     y_i = c_i norm_i / sqrt(mean_j(c_j^2) + eps),
  * and the rotary channels, turned by the token's position when rotary is not NULL (rotary->rot
- * <= rope; channels from rot on are copied), in fp32, the sum of squares too, rounded once to the cache's type.  When q is not
- * NULL (with rotary), its rows of rope channels are rotated into q_out in the same launch, for every
+ * <= rope; channels from rot on are copied), in fp32, the sum of squares too, rounded once to the cache's
+ * type.  When q is not NULL (with rotary), its rows of rope channels are rotated into q_out in the same launch, for every
  * token, whatever its slot.  A negative slot takes nothing; one beyond the cache is recorded and takes
  * nothing; slots that are not negative must differ.  A token whose position is outside the table is
  * recorded and nothing of it is written.
@@ -783,9 +783,9 @@ size_t moe_pages_workspace_bytes(const moe_page_pool_t *pool);
  * need[b] > 0, that page is replaced by a new one and its rows below the length are copied, in every
  * cache; of several sequences that share it in one call, each in order takes a copy as long as
  * others still hold it.  Pages held behind it (of a sequence whose length was lowered) that the need[b] tokens
- * reach and others hold too, as the call finds them, are replaced and nothing is copied.  From the first sequence on that the free pages do not suffice for, none that
- * needs a page gets any: got[b] = 0 and it is left as it was, otherwise 1 (0 also for one that is
- * recorded).
+ * reach and others hold too, as the call finds them, are replaced and nothing is copied.  From the first
+ * sequence on that the free pages do not suffice for, none that needs a page gets any: got[b] = 0 and it is
+ * left as it was, otherwise 1 (0 also for one that is recorded).
  *   length, need [dev] int32 [seqs]: need[b] >= 0, 0 <= length[b] <= held[b] * page; got [dev] int32
  *   [seqs] or NULL.  seqs <= MOE_MAX_POOL_SEQS.  ws of moe_pages_workspace_bytes.  Asynchronous on s.
  */

@@ -342,7 +342,6 @@ __global__ void __launch_bounds__(256) pages_accept_kernel(const __grid_constant
 // A thread takes one column of a row (16 bytes, 4 of scales) through all of a sequence's moves in order: the
 // path ascends, so target i is at or before source i and before every later one, and no row is written
 // before it was read.  Eight rows' loads are in flight together.
-
 __global__ void __launch_bounds__(kMove) pages_move_kernel(const __grid_constant__ PageArgs a, const __grid_constant__ PageRows p, int columns, int slices, int settle) {
     __shared__ int source_s[MOE_MAX_TREE_TOKENS][2], target_s[MOE_MAX_TREE_TOKENS][2];   // page, row
     pdl_wait();
